@@ -14,6 +14,9 @@
  *                       in "LLM long-context inference: managing the KV cache with an
  *                       INT4 state machine", pwwt.cn/news/4219524, section 5 step 5);
  *   dequantize          the inverse map code * scale (section 2.1 of the 4-bit page).
+ * Around them: attention that adds up the positions' weights, eviction by those weights, and
+ * differential attention (each described at its declaration; no passage of the pages has a
+ * counterpart).
  *
  * Conventions
  *   - Every pointer argument except `cfg` and host outputs is a DEVICE pointer on the
@@ -414,6 +417,140 @@ int kvq_mixed_decode_attention(const kvq_cache_config *cfg, const void *pool, co
                                int32_t batch, int32_t num_q_heads, int32_t max_len, int32_t residual,
                                float softmax_scale, float *out, void *workspace, size_t workspace_bytes,
                                kvq_stream_t stream);
+
+/*
+ * Decode attention with the positions' weights: kvq_decode_attention that also adds up how
+ * much softmax weight each cached position received, the measure by which kvq_evict_select
+ * cuts a cache to a budget.  With p_g(t) the softmax weight of position t for query head g,
+ *   weights[b][h][t] = decay * weights[b][h][t] + sum of p_g(t) over the query heads g of
+ *                      kv head h,   for t < seq_lens[b];
+ * positions behind the sequence keep what they held.  The sum runs over the query heads in
+ * order, so repeated calls agree bit for bit.
+ *   decay           in [0, 1]: 1 accumulates, 0 keeps this call's weights alone (what weights
+ *                   held is not read then), a value between lets older weight fade.
+ *   weights         device fp32 [batch, num_kv_heads, weights_stride], updated in place.
+ *   weights_stride  floats per kv head, >= max_len.
+ *   max_len         as in kvq_decode_attention; a longer seq_lens[b] raises
+ *                   KVQ_FLAG_BAD_POSITION and max_len positions are attended to.
+ *   workspace       >= kvq_decode_weights_workspace_bytes(...): beside the partial results it
+ *                   holds the scores of the call (4 bytes per position and query head).
+ *   other arguments, shapes and the launch overlap as in kvq_decode_attention (weights is
+ *   read and written after the kernel ahead has finished).
+ * kvq_decode_step_weights: the same with one new token per sequence appended first, as
+ *   kvq_decode_step; weights at the token's position is zero before unless the caller wants
+ *   it to start with more (kvq_evict_compact leaves zeros behind the kept positions).
+ * kvq_int8_decode_attention_weights: over the INT8 per-row cache (head_dim 128).
+ * Returns as kvq_decode_attention; KVQ_EINVAL also for a decay or stride out of range.
+ */
+size_t kvq_decode_weights_workspace_bytes(const kvq_cache_config *cfg, int32_t batch, int32_t num_q_heads,
+                                          int32_t max_len);
+int kvq_decode_attention_weights(const kvq_cache_config *cfg, const void *pool, const void *q,
+                                 const int32_t *block_table, int32_t max_blocks, const int32_t *seq_lens,
+                                 int32_t batch, int32_t num_q_heads, int32_t max_len, float softmax_scale,
+                                 float decay, float *weights, int32_t weights_stride, float *out, void *workspace,
+                                 size_t workspace_bytes, kvq_stream_t stream);
+int kvq_decode_step_weights(const kvq_cache_config *cfg, void *pool, const void *k_new, const void *v_new,
+                            const int32_t *append_pos, const void *q, const int32_t *block_table,
+                            int32_t max_blocks, const int32_t *seq_lens, int32_t batch, int32_t num_q_heads,
+                            int32_t max_len, float softmax_scale, float decay, float *weights,
+                            int32_t weights_stride, float *out, void *workspace, size_t workspace_bytes,
+                            kvq_stream_t stream);
+size_t kvq_int8_decode_weights_workspace_bytes(const kvq_cache_config *cfg, int32_t batch, int32_t num_q_heads,
+                                               int32_t max_len);
+int kvq_int8_decode_attention_weights(const kvq_cache_config *cfg, const void *pool8, const void *q,
+                                      const int32_t *block_table, int32_t max_blocks, const int32_t *seq_lens,
+                                      int32_t batch, int32_t num_q_heads, int32_t max_len, float softmax_scale,
+                                      float decay, float *weights, int32_t weights_stride, float *out,
+                                      void *workspace, size_t workspace_bytes, kvq_stream_t stream);
+
+/*
+ * Eviction from a cache, step one: which positions each (sequence, kv head) keeps when its
+ * cache is cut to `keep` positions.  Of n = seq_lens[b] > keep positions stay
+ *   the first `sinks` and the last `recent`, whatever their weights;
+ *   of the others, the keep - sinks - recent of largest weight (NaN counts as -infinity,
+ *   equal weights: the lower position first).
+ * With n <= keep every position stays.
+ *   cfg             only num_kv_heads matters (the rest must be a valid geometry).
+ *   weights         device fp32 [batch, num_kv_heads, weights_stride], as accumulated by
+ *                   kvq_decode_attention_weights; weights_stride >= max_len.
+ *   seq_lens        device int32 [batch]; one beyond max_len raises KVQ_FLAG_BAD_POSITION and
+ *                   counts as max_len.
+ *   keep            >= 1 and >= sinks + recent.
+ *   kept            device int32 [batch, num_kv_heads, keep]: the positions kept, ascending,
+ *                   then -1 up to keep.
+ *   new_lens        device int32 [batch]: min(n, keep).  May be seq_lens itself only when no
+ *                   kvq_evict_compact of this cut follows (it needs the old lengths).
+ *   status          device uint32 status word or NULL.
+ * Returns KVQ_OK, KVQ_EINVAL, KVQ_EUNSUPPORTED or KVQ_ECUDA.
+ */
+int kvq_evict_select(const kvq_cache_config *cfg, const float *weights, int32_t weights_stride,
+                     const int32_t *seq_lens, int32_t batch, int32_t max_len, int32_t keep, int32_t sinks,
+                     int32_t recent, int32_t *kept, int32_t *new_lens, uint32_t *status, kvq_stream_t stream);
+
+/*
+ * Eviction, step two: the kept rows of every (sequence, kv head) moved to positions 0, 1, ..
+ * as they are stored (codes and scales unchanged): row kept[b][h][i] of block_table goes to
+ * position i of dst_table, for i < min(seq_lens[b], keep).  Each kv head keeps positions of
+ * its own, so after the call position i of two heads may hold different tokens; attention
+ * over new_lens positions of dst_table is attention over the kept ones.
+ *   dst_table       device int32 [batch, dst_max_blocks].  block_table itself: in place, the
+ *                   pages from ceil(new_lens / page_size) on are then free.  Else pages that
+ *                   no row of the call is read from (for sequences whose pages are shared).
+ *                   In place, no two sequences may share a page that rows are written to.
+ *   seq_lens        device int32 [batch]: the lengths before the cut.
+ *   kept, keep      as written by kvq_evict_select: strictly ascending, kept[i] < seq_lens[b].
+ *   weights         device fp32 [batch, num_kv_heads, weights_stride] or NULL: weights of the
+ *                   kept positions move along, the ones behind them up to seq_lens[b] become 0.
+ *   status          device uint32 status word or NULL.
+ * A kept position outside the sequence, a position outside a table (KVQ_FLAG_BAD_POSITION) or
+ * a page id out of range (KVQ_FLAG_BAD_PAGE) is skipped and flagged; nothing outside the
+ * arguments is read or written.  A length beyond the table (or beyond weights_stride) is cut
+ * to it and flagged.  The slots of dst_table's pages that no row is moved to keep their bytes.
+ * kvq_int8_evict_compact: the same over the INT8 per-row cache (head_dim 64, 128 or 256).
+ * Returns KVQ_OK, KVQ_EINVAL, KVQ_EUNSUPPORTED or KVQ_ECUDA.
+ */
+int kvq_evict_compact(const kvq_cache_config *cfg, void *pool, const int32_t *block_table, int32_t max_blocks,
+                      const int32_t *dst_table, int32_t dst_max_blocks, const int32_t *seq_lens, int32_t batch,
+                      const int32_t *kept, int32_t keep, float *weights, int32_t weights_stride, uint32_t *status,
+                      kvq_stream_t stream);
+int kvq_int8_evict_compact(const kvq_cache_config *cfg, void *pool8, const int32_t *block_table, int32_t max_blocks,
+                           const int32_t *dst_table, int32_t dst_max_blocks, const int32_t *seq_lens, int32_t batch,
+                           const int32_t *kept, int32_t keep, float *weights, int32_t weights_stride,
+                           uint32_t *status, kvq_stream_t stream);
+
+/*
+ * Differential decode attention: the difference of two softmax maps over one cache.  A K row
+ * is two keys, k1 its first head_dim / 2 elements and k2 the rest, and a q row two queries;
+ * a V row belongs to both maps.  With a_i = softmax_t(softmax_scale * q_i . k_i[t]),
+ *   o   = sum_t (a_1[t] - lambda[hq] a_2[t]) v[t]
+ *   out = out_scale * o                                    without norm_weight
+ *   out = out_scale * norm_weight * o / sqrt(mean(o^2) + norm_eps)   with it (the mean over
+ *         the head's head_dim outputs).
+ * Both maps come from one pass over the packed pages.
+ *   lambda       device fp32 [num_q_heads]: the learned weight of the second map.
+ *   norm_weight  device fp32 [head_dim], 16-byte aligned, or NULL.
+ *   norm_eps     >= 0, finite (read with norm_weight only).
+ *   workspace    >= kvq_diff_decode_workspace_bytes(...).
+ *   other arguments and the launch overlap as in kvq_decode_attention (lambda and norm_weight
+ *   are read after the kernel ahead has finished); a length of 0 gives zeros.
+ * group_k may be at most head_dim / 2; num_q_heads / num_kv_heads at most 4 (2 at head_dim
+ * 256, where group_k must be 64 or 128): KVQ_EUNSUPPORTED otherwise.
+ * kvq_diff_decode_step: the same with one new token per sequence appended first, as
+ *   kvq_decode_step.
+ * Returns as kvq_decode_attention.
+ */
+size_t kvq_diff_decode_workspace_bytes(const kvq_cache_config *cfg, int32_t batch, int32_t num_q_heads,
+                                       int32_t max_len);
+int kvq_diff_decode_attention(const kvq_cache_config *cfg, const void *pool, const void *q,
+                              const int32_t *block_table, int32_t max_blocks, const int32_t *seq_lens,
+                              int32_t batch, int32_t num_q_heads, int32_t max_len, float softmax_scale,
+                              const float *lambda, const float *norm_weight, float norm_eps, float out_scale,
+                              float *out, void *workspace, size_t workspace_bytes, kvq_stream_t stream);
+int kvq_diff_decode_step(const kvq_cache_config *cfg, void *pool, const void *k_new, const void *v_new,
+                         const int32_t *append_pos, const void *q, const int32_t *block_table, int32_t max_blocks,
+                         const int32_t *seq_lens, int32_t batch, int32_t num_q_heads, int32_t max_len,
+                         float softmax_scale, const float *lambda, const float *norm_weight, float norm_eps,
+                         float out_scale, float *out, void *workspace, size_t workspace_bytes, kvq_stream_t stream);
 
 /*
  * Decode attention that allocates nothing, for callers that cannot provide a

@@ -28,7 +28,11 @@ ABI_SYMBOLS = ("kvq_block_bytes", "kvq_pool_bytes", "kvq_quantize_append", "kvq_
                "kvq_int8_decode_workspace_bytes", "kvq_int8_decode_attention", "kvq_wht4_codebook",
                "kvq_wht4_pool_bytes", "kvq_wht4_quantize_append", "kvq_wht4_dequantize",
                "kvq_wht4_decode_workspace_bytes", "kvq_wht4_decode_attention", "kvq_decode_step_host",
-               "kvq_decode_step_host_pipelined", "kvq_test_decode_wait_timeout")
+               "kvq_decode_step_host_pipelined", "kvq_test_decode_wait_timeout",
+               "kvq_decode_weights_workspace_bytes", "kvq_decode_attention_weights", "kvq_decode_step_weights",
+               "kvq_int8_decode_weights_workspace_bytes", "kvq_int8_decode_attention_weights", "kvq_evict_select",
+               "kvq_evict_compact", "kvq_int8_evict_compact", "kvq_diff_decode_workspace_bytes",
+               "kvq_diff_decode_attention", "kvq_diff_decode_step")
 
 
 class KvqError(RuntimeError):
@@ -126,6 +130,25 @@ def lib() -> C.CDLL:
         L.kvq_wht4_decode_workspace_bytes.restype = SZ
         L.kvq_wht4_decode_attention.argtypes = [cfgp, P, P, P, I32, P, I32, I32, I32, C.c_float, P, P, SZ, P]
         L.kvq_wht4_decode_attention.restype = C.c_int
+        F = C.c_float
+        for name in ("kvq_decode_weights_workspace_bytes", "kvq_int8_decode_weights_workspace_bytes",
+                     "kvq_diff_decode_workspace_bytes"):
+            getattr(L, name).argtypes = [cfgp, I32, I32, I32]
+            getattr(L, name).restype = SZ
+        for name in ("kvq_decode_attention_weights", "kvq_int8_decode_attention_weights"):
+            getattr(L, name).argtypes = [cfgp, P, P, P, I32, P, I32, I32, I32, F, F, P, I32, P, P, SZ, P]
+            getattr(L, name).restype = C.c_int
+        L.kvq_decode_step_weights.argtypes = [cfgp, P, P, P, P, P, P, I32, P, I32, I32, I32, F, F, P, I32, P, P, SZ, P]
+        L.kvq_decode_step_weights.restype = C.c_int
+        L.kvq_evict_select.argtypes = [cfgp, P, I32, P, I32, I32, I32, I32, I32, P, P, P, P]
+        L.kvq_evict_select.restype = C.c_int
+        for name in ("kvq_evict_compact", "kvq_int8_evict_compact"):
+            getattr(L, name).argtypes = [cfgp, P, P, I32, P, I32, P, I32, P, I32, P, I32, P, P]
+            getattr(L, name).restype = C.c_int
+        L.kvq_diff_decode_attention.argtypes = [cfgp, P, P, P, I32, P, I32, I32, I32, F, P, P, F, F, P, P, SZ, P]
+        L.kvq_diff_decode_attention.restype = C.c_int
+        L.kvq_diff_decode_step.argtypes = [cfgp, P, P, P, P, P, P, I32, P, I32, I32, I32, F, P, P, F, F, P, P, SZ, P]
+        L.kvq_diff_decode_step.restype = C.c_int
         L.kvq_dequantize.argtypes = [cfgp, P, P, I32, I32, I32, I32, P, P, I32, P, P]
         L.kvq_dequantize.restype = C.c_int
         L.kvq_read_status.argtypes = [P, C.POINTER(C.c_uint32), P]
@@ -587,4 +610,247 @@ def kvq_test_decode_wait_timeout(cfg: CacheConfig, pool: torch.Tensor, q: torch.
         _dev(seq_lens, "seq_lens", torch.int32), B, Hq, int(max_len), float(softmax_scale),
         _dev(out, "out", torch.float32), _dev(workspace, "workspace", torch.uint8), workspace.numel(),
         int(wait_limit_ns), _stream(stream))
+    _check(rc)
+
+
+# ---------------------------------------------------------------------------
+# Attention weights of cached positions, eviction by them, differential attention
+# ---------------------------------------------------------------------------
+def _shaped(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: int) -> int:
+    """The address of a contiguous CUDA tensor on device `dev` (the current one), of that dtype and shape."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    p = _dev(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _bytes(t: torch.Tensor, name: str, at_least: int, dev: int) -> int:
+    p = _shaped(t, name, torch.uint8, getattr(t, "shape", ()), dev)
+    if t.numel() < at_least:
+        raise ValueError(f"{name} has {t.numel()} bytes, needs {at_least}")
+    return p
+
+
+def _table(t: torch.Tensor, name: str, batch: int, dev: int) -> tuple[int, int]:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be an int32 CUDA tensor [batch, blocks]")
+    blocks = t.shape[1]
+    return _shaped(t, name, torch.int32, (batch, blocks), dev), blocks
+
+
+def _batch_heads(q: torch.Tensor, d: int) -> tuple[int, int]:
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q must be a CUDA tensor [batch, num_q_heads, head_dim]")
+    return q.shape[0], q.shape[1]
+
+
+def _weights_of(weights: torch.Tensor, batch: int, heads: int, dev: int) -> tuple[int, int]:
+    if not isinstance(weights, torch.Tensor) or weights.dim() != 3:
+        raise ValueError("weights must be an fp32 CUDA tensor [batch, num_kv_heads, positions]")
+    stride = weights.shape[2]
+    return _shaped(weights, "weights", torch.float32, (batch, heads, stride), dev), stride
+
+
+def _new_rows(t: torch.Tensor, name: str, batch: int, cfg: CacheConfig, dev: int) -> int:
+    shape = (batch, cfg.num_kv_heads, cfg.head_dim)
+    if isinstance(t, torch.Tensor) and t.dim() == 4:
+        shape = (batch, 1, cfg.num_kv_heads, cfg.head_dim)
+    return _shaped(t, name, torch.float16, shape, dev)
+
+
+def _own_status(status: torch.Tensor | None, dev: int) -> int | None:
+    if status is None:
+        return None
+    p = _status(status)
+    if status.get_device() != dev:
+        raise ValueError(f"status is on {status.device}, the current device is cuda:{dev}")
+    return p
+
+
+def _mode_workspace_bytes(name: str, cfg: CacheConfig, batch: int, num_q_heads: int, max_len: int) -> int:
+    n = int(getattr(lib(), name)(C.byref(cfg), batch, num_q_heads, max_len))
+    if n == 0:
+        raise KvqError(KVQ_EUNSUPPORTED, kvq_last_error())
+    return n
+
+
+def kvq_decode_weights_workspace_bytes(cfg: CacheConfig, batch: int, num_q_heads: int, max_len: int) -> int:
+    return _mode_workspace_bytes("kvq_decode_weights_workspace_bytes", cfg, batch, num_q_heads, max_len)
+
+
+def kvq_int8_decode_weights_workspace_bytes(cfg: CacheConfig, batch: int, num_q_heads: int, max_len: int) -> int:
+    return _mode_workspace_bytes("kvq_int8_decode_weights_workspace_bytes", cfg, batch, num_q_heads, max_len)
+
+
+def kvq_diff_decode_workspace_bytes(cfg: CacheConfig, batch: int, num_q_heads: int, max_len: int) -> int:
+    return _mode_workspace_bytes("kvq_diff_decode_workspace_bytes", cfg, batch, num_q_heads, max_len)
+
+
+def new_weights_workspace(cfg: CacheConfig, batch: int, num_q_heads: int, max_len: int,
+                          device="cuda") -> torch.Tensor:
+    """A workspace of the decode calls with weights, its status word zeroed."""
+    return torch.zeros(kvq_decode_weights_workspace_bytes(cfg, batch, num_q_heads, max_len), dtype=torch.uint8,
+                       device=device)
+
+
+def new_int8_weights_workspace(cfg: CacheConfig, batch: int, num_q_heads: int, max_len: int,
+                               device="cuda") -> torch.Tensor:
+    return torch.zeros(kvq_int8_decode_weights_workspace_bytes(cfg, batch, num_q_heads, max_len), dtype=torch.uint8,
+                       device=device)
+
+
+def new_diff_workspace(cfg: CacheConfig, batch: int, num_q_heads: int, max_len: int, device="cuda") -> torch.Tensor:
+    """A workspace of the differential decode calls, its status word zeroed."""
+    return torch.zeros(kvq_diff_decode_workspace_bytes(cfg, batch, num_q_heads, max_len), dtype=torch.uint8,
+                       device=device)
+
+
+def _decode_head(cfg, pool, pool_bytes, q, block_table, seq_lens, out, dev):
+    """(batch, query heads), the C arguments pool, q, block_table, max_blocks, seq_lens, and out."""
+    d = cfg.head_dim
+    B, Hq = _batch_heads(q, d)
+    bt, blocks = _table(block_table, "block_table", B, dev)
+    return B, Hq, (_bytes(pool, "pool", pool_bytes, dev), _shaped(q, "q", torch.float16, (B, Hq, d), dev), bt, blocks,
+                   _shaped(seq_lens, "seq_lens", torch.int32, (B,), dev)), \
+        _shaped(out, "out", torch.float32, (B, Hq, d), dev)
+
+
+def kvq_decode_attention_weights(cfg: CacheConfig, pool: torch.Tensor, q: torch.Tensor, block_table: torch.Tensor,
+                                 seq_lens: torch.Tensor, max_len: int, softmax_scale: float, decay: float,
+                                 weights: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor,
+                                 stream=None) -> None:
+    """kvq_decode_attention that also updates weights (fp32 [B, Hkv, >= max_len]):
+    weights[b, h, t] = decay * weights[b, h, t] + the sum of position t's softmax weight over KV head h's query
+    heads, for t < seq_lens[b] (decay 0: the sum alone).  workspace as from new_weights_workspace."""
+    dev = torch.cuda.current_device()
+    B, Hq, (pp, qp, bt, blocks, sl), op = _decode_head(cfg, pool, kvq_pool_bytes(cfg), q, block_table, seq_lens, out,
+                                                       dev)
+    w, stride = _weights_of(weights, B, cfg.num_kv_heads, dev)
+    rc = lib().kvq_decode_attention_weights(
+        C.byref(cfg), pp, qp, bt, blocks, sl, B, Hq, int(max_len), float(softmax_scale), float(decay), w, stride,
+        op, _bytes(workspace, "workspace", 0, dev), workspace.numel(), _stream(stream))
+    _check(rc)
+
+
+def kvq_int8_decode_attention_weights(cfg: CacheConfig, pool: torch.Tensor, q: torch.Tensor,
+                                      block_table: torch.Tensor, seq_lens: torch.Tensor, max_len: int,
+                                      softmax_scale: float, decay: float, weights: torch.Tensor, out: torch.Tensor,
+                                      workspace: torch.Tensor, stream=None) -> None:
+    """kvq_decode_attention_weights over the INT8 per-row cache (workspace: new_int8_weights_workspace)."""
+    dev = torch.cuda.current_device()
+    B, Hq, (pp, qp, bt, blocks, sl), op = _decode_head(cfg, pool, kvq_int8_pool_bytes(cfg), q, block_table, seq_lens,
+                                                       out, dev)
+    w, stride = _weights_of(weights, B, cfg.num_kv_heads, dev)
+    rc = lib().kvq_int8_decode_attention_weights(
+        C.byref(cfg), pp, qp, bt, blocks, sl, B, Hq, int(max_len), float(softmax_scale), float(decay), w, stride,
+        op, _bytes(workspace, "workspace", 0, dev), workspace.numel(), _stream(stream))
+    _check(rc)
+
+
+def kvq_decode_step_weights(cfg: CacheConfig, pool: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                            append_pos: torch.Tensor, q: torch.Tensor, block_table: torch.Tensor,
+                            seq_lens: torch.Tensor, max_len: int, softmax_scale: float, decay: float,
+                            weights: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """kvq_decode_step (append k_new, v_new at append_pos, then attend) that also updates weights, as
+    kvq_decode_attention_weights."""
+    dev = torch.cuda.current_device()
+    B, Hq, (pp, qp, bt, blocks, sl), op = _decode_head(cfg, pool, kvq_pool_bytes(cfg), q, block_table, seq_lens, out,
+                                                       dev)
+    w, stride = _weights_of(weights, B, cfg.num_kv_heads, dev)
+    rc = lib().kvq_decode_step_weights(
+        C.byref(cfg), pp, _new_rows(k_new, "k_new", B, cfg, dev), _new_rows(v_new, "v_new", B, cfg, dev),
+        _shaped(append_pos, "append_pos", torch.int32, (B,), dev), qp, bt, blocks, sl, B, Hq, int(max_len),
+        float(softmax_scale), float(decay), w, stride, op, _bytes(workspace, "workspace", 0, dev), workspace.numel(),
+        _stream(stream))
+    _check(rc)
+
+
+def kvq_evict_select(cfg: CacheConfig, weights: torch.Tensor, seq_lens: torch.Tensor, max_len: int, keep: int,
+                     sinks: int, recent: int, kept: torch.Tensor, new_lens: torch.Tensor,
+                     status: torch.Tensor | None = None, stream=None) -> None:
+    """The positions each KV head keeps of a cache cut to `keep`: the first `sinks`, the last `recent`, the rest by
+    largest weight (ties: the lower position).  weights fp32 [B, Hkv, >= max_len]; seq_lens int32 [B];
+    kept int32 [B, Hkv, keep] (ascending, then -1) and new_lens int32 [B] are written."""
+    if not isinstance(seq_lens, torch.Tensor) or seq_lens.dim() != 1:
+        raise ValueError("seq_lens must be an int32 CUDA tensor [batch]")
+    B, H, dev = int(seq_lens.shape[0]), cfg.num_kv_heads, torch.cuda.current_device()
+    w, stride = _weights_of(weights, B, H, dev)
+    rc = lib().kvq_evict_select(
+        C.byref(cfg), w, stride, _shaped(seq_lens, "seq_lens", torch.int32, (B,), dev), B, int(max_len), int(keep), int(sinks),
+        int(recent), _shaped(kept, "kept", torch.int32, (B, H, int(keep)), dev),
+        _shaped(new_lens, "new_lens", torch.int32, (B,), dev), _own_status(status, dev), _stream(stream))
+    _check(rc)
+
+
+def _evict_compact(fn, cfg, pool, pool_bytes, block_table, dst_table, seq_lens, kept, weights, status, stream) -> None:
+    if not isinstance(kept, torch.Tensor) or kept.dim() != 3:
+        raise ValueError("kept must be an int32 CUDA tensor [batch, num_kv_heads, keep]")
+    B, H, keep = int(kept.shape[0]), cfg.num_kv_heads, int(kept.shape[2])
+    dev = torch.cuda.current_device()
+    bt, blocks = _table(block_table, "block_table", B, dev)
+    dt, dblocks = _table(dst_table, "dst_table", B, dev)
+    w, stride = (None, 0) if weights is None else _weights_of(weights, B, H, dev)
+    rc = fn(C.byref(cfg), _bytes(pool, "pool", pool_bytes, dev), bt, blocks, dt, dblocks,
+            _shaped(seq_lens, "seq_lens", torch.int32, (B,), dev), B, _shaped(kept, "kept", torch.int32, (B, H, keep), dev), keep, w,
+            stride, _own_status(status, dev), _stream(stream))
+    _check(rc)
+
+
+def kvq_evict_compact(cfg: CacheConfig, pool: torch.Tensor, block_table: torch.Tensor, dst_table: torch.Tensor,
+                      seq_lens: torch.Tensor, kept: torch.Tensor, weights: torch.Tensor | None = None,
+                      status: torch.Tensor | None = None, stream=None) -> None:
+    """Rows kept[b, h, i] (as from kvq_evict_select) of block_table moved to position i of dst_table (block_table
+    itself: in place), with their weights; seq_lens: the lengths before the cut."""
+    _evict_compact(lib().kvq_evict_compact, cfg, pool, kvq_pool_bytes(cfg), block_table, dst_table, seq_lens, kept,
+                   weights, status, stream)
+
+
+def kvq_int8_evict_compact(cfg: CacheConfig, pool: torch.Tensor, block_table: torch.Tensor, dst_table: torch.Tensor,
+                           seq_lens: torch.Tensor, kept: torch.Tensor, weights: torch.Tensor | None = None,
+                           status: torch.Tensor | None = None, stream=None) -> None:
+    """kvq_evict_compact over the INT8 per-row cache."""
+    _evict_compact(lib().kvq_int8_evict_compact, cfg, pool, kvq_int8_pool_bytes(cfg), block_table, dst_table, seq_lens,
+                   kept, weights, status, stream)
+
+
+def kvq_diff_decode_attention(cfg: CacheConfig, pool: torch.Tensor, q: torch.Tensor, block_table: torch.Tensor,
+                              seq_lens: torch.Tensor, max_len: int, softmax_scale: float, lam: torch.Tensor,
+                              norm_weight: torch.Tensor | None, norm_eps: float, out_scale: float, out: torch.Tensor,
+                              workspace: torch.Tensor, stream=None) -> None:
+    """Differential attention: softmax over the first halves of q and K minus lam (fp32 [Hq]) times softmax over the
+    second halves, applied to V; then an RMS norm over the head with norm_weight (fp32 [d]; None: no norm), times
+    out_scale, into out (fp32 [B, Hq, d]).  workspace as from new_diff_workspace."""
+    dev = torch.cuda.current_device()
+    B, Hq, (pp, qp, bt, blocks, sl), op = _decode_head(cfg, pool, kvq_pool_bytes(cfg), q, block_table, seq_lens, out,
+                                                       dev)
+    d = cfg.head_dim
+    rc = lib().kvq_diff_decode_attention(
+        C.byref(cfg), pp, qp, bt, blocks, sl, B, Hq, int(max_len), float(softmax_scale),
+        _shaped(lam, "lam", torch.float32, (Hq,), dev),
+        None if norm_weight is None else _shaped(norm_weight, "norm_weight", torch.float32, (d,), dev), float(norm_eps),
+        float(out_scale), op, _bytes(workspace, "workspace", 0, dev), workspace.numel(), _stream(stream))
+    _check(rc)
+
+
+def kvq_diff_decode_step(cfg: CacheConfig, pool: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                         append_pos: torch.Tensor, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                         max_len: int, softmax_scale: float, lam: torch.Tensor, norm_weight: torch.Tensor | None,
+                         norm_eps: float, out_scale: float, out: torch.Tensor, workspace: torch.Tensor,
+                         stream=None) -> None:
+    """kvq_diff_decode_attention with k_new, v_new appended at append_pos first, as kvq_decode_step."""
+    dev = torch.cuda.current_device()
+    B, Hq, (pp, qp, bt, blocks, sl), op = _decode_head(cfg, pool, kvq_pool_bytes(cfg), q, block_table, seq_lens, out,
+                                                       dev)
+    d = cfg.head_dim
+    rc = lib().kvq_diff_decode_step(
+        C.byref(cfg), pp, _new_rows(k_new, "k_new", B, cfg, dev), _new_rows(v_new, "v_new", B, cfg, dev),
+        _shaped(append_pos, "append_pos", torch.int32, (B,), dev), qp, bt, blocks, sl, B, Hq, int(max_len),
+        float(softmax_scale), _shaped(lam, "lam", torch.float32, (Hq,), dev),
+        None if norm_weight is None else _shaped(norm_weight, "norm_weight", torch.float32, (d,), dev), float(norm_eps),
+        float(out_scale), op, _bytes(workspace, "workspace", 0, dev), workspace.numel(), _stream(stream))
     _check(rc)

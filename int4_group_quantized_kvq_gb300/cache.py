@@ -10,6 +10,12 @@ nothing) around the C ABI calls of a decode step:
 With ``window > 0`` the attention is restricted to the last ``window`` positions and
 the first ``sinks`` (``kvq_decode_attention_window`` / ``kvq_decode_step_window``).
 
+With ``track_weights`` the cache also accumulates the attention weight each cached position
+receives (``kvq_decode_attention_weights`` / ``kvq_decode_step_weights``), and ``evict`` cuts it
+by that measure to a budget of positions, each KV head keeping its own
+(``kvq_evict_select``, ``kvq_evict_compact``).  ``attend_diff`` and ``decode_step_diff`` read the
+same pool as differential attention, for a cache made with ``diff`` (``kvq_diff_decode_attention`` / ``kvq_diff_decode_step``).
+
 ``decode_step_host`` is the same step driven from pinned host buffers (``HostStaging``)
 in one kvq_decode_step_host call: the step's q, K and V are copied in with one transfer
 and the output copied back, on the same stream; ``HostPipeline`` overlaps those copies
@@ -26,7 +32,8 @@ from . import binding as B
 
 class PagedKVCache:
     def __init__(self, cfg: B.CacheConfig, block_table: torch.Tensor, num_q_heads: int, max_len: int,
-                 device="cuda", pool: torch.Tensor | None = None, window: int = 0, sinks: int = 0):
+                 device="cuda", pool: torch.Tensor | None = None, window: int = 0, sinks: int = 0,
+                 track_weights: bool = False, decay: float = 1.0, diff: bool = False):
         self.cfg = cfg
         self.window = int(window)
         self.sinks = int(sinks)
@@ -41,7 +48,19 @@ class PagedKVCache:
         if pool.numel() < nbytes:
             raise ValueError(f"pool has {pool.numel()} bytes, needs {nbytes}")
         self.pool = pool
-        self.workspace = B.new_workspace(cfg, self.batch, self.num_q_heads, self.max_len, device=self.device)
+        self.decay = float(decay)
+        self.weights = None
+        self.diff_workspace = B.new_diff_workspace(cfg, self.batch, self.num_q_heads, self.max_len,
+                                                   device=self.device) if diff else None
+        if track_weights:
+            if self.window > 0:
+                raise ValueError("a cache with a window does not track weights")
+            self.weights = torch.zeros(self.batch, cfg.num_kv_heads, self.max_len, dtype=torch.float32,
+                                       device=self.device)
+            self.workspace = B.new_weights_workspace(cfg, self.batch, self.num_q_heads, self.max_len,
+                                                     device=self.device)
+        else:
+            self.workspace = B.new_workspace(cfg, self.batch, self.num_q_heads, self.max_len, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.softmax_scale = 1.0 / math.sqrt(cfg.head_dim)
 
@@ -52,7 +71,11 @@ class PagedKVCache:
 
     def attend(self, q: torch.Tensor, seq_lens: torch.Tensor, out: torch.Tensor, stream=None) -> None:
         """Decode attention of q [B, Hq, d] fp16 over positions 0 .. seq_lens[b]-1 into out (fp32)."""
-        if self.window > 0:
+        if self.weights is not None:
+            B.kvq_decode_attention_weights(self.cfg, self.pool, q, self.block_table, seq_lens, self.max_len,
+                                           self.softmax_scale, self.decay, self.weights, out, self.workspace,
+                                           stream=stream)
+        elif self.window > 0:
             B.kvq_decode_attention_window(self.cfg, self.pool, q, self.block_table, seq_lens, self.max_len,
                                           self.softmax_scale, self.window, self.sinks, out, self.workspace,
                                           stream=stream)
@@ -63,7 +86,11 @@ class PagedKVCache:
     def decode_step(self, q, k_new, v_new, append_pos, seq_lens, out, stream=None) -> None:
         """Append one token per sequence at append_pos, then attend over seq_lens (which include it):
         one kvq_decode_step call."""
-        if self.window > 0:
+        if self.weights is not None:
+            B.kvq_decode_step_weights(self.cfg, self.pool, k_new, v_new, append_pos, q, self.block_table, seq_lens,
+                                      self.max_len, self.softmax_scale, self.decay, self.weights, out, self.workspace,
+                                      stream=stream)
+        elif self.window > 0:
             B.kvq_decode_step_window(self.cfg, self.pool, k_new, v_new, append_pos, q, self.block_table, seq_lens,
                                      self.max_len, self.softmax_scale, self.window, self.sinks, out, self.workspace,
                                      stream=stream)
@@ -76,19 +103,66 @@ class PagedKVCache:
         self.append(k_new, v_new, append_pos, stream)
         self.attend(q, seq_lens, out, stream)
 
+    def evict(self, seq_lens, keep: int, sinks: int = 0, recent: int = 0, dst_table: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+        """Cut every sequence to at most `keep` positions: the first `sinks`, the last `recent` and the ones of
+        largest accumulated weight, each KV head its own.  The rows move to the front of the sequence's pages, or
+        into dst_table's (int32 [B, blocks]), which then becomes the cache's block table.  Returns the new lengths
+        (int32 [B]); pages from ceil(new length / page_size) on are free.  Allocates its small results on the
+        current stream, so `stream` is that one or one that waits for it."""
+        if self.weights is None:
+            raise ValueError("evict needs a cache with track_weights")
+        dst = self.block_table if dst_table is None else dst_table
+        if int(dst.shape[1]) * self.cfg.page_size < min(int(keep), self.max_len):
+            raise ValueError(f"dst_table has {int(dst.shape[1])} pages a sequence, too few for {keep} positions")
+        kept = torch.empty(self.batch, self.cfg.num_kv_heads, int(keep), dtype=torch.int32, device=self.device)
+        new_lens = torch.empty(self.batch, dtype=torch.int32, device=self.device)
+        B.kvq_evict_select(self.cfg, self.weights, seq_lens, self.max_len, keep, sinks, recent, kept, new_lens,
+                           status=self.status, stream=stream)
+        B.kvq_evict_compact(self.cfg, self.pool, self.block_table, dst, seq_lens, kept, self.weights,
+                            status=self.status, stream=stream)
+        if stream is not None and isinstance(stream, torch.cuda.Stream):
+            kept.record_stream(stream)
+            new_lens.record_stream(stream)
+        self.block_table = dst
+        return new_lens
+
+    def attend_diff(self, q, lam, seq_lens, out, norm_weight=None, norm_eps: float = 1e-5, out_scale: float = 1.0,
+                    stream=None) -> None:
+        """Differential decode attention: softmax over the first halves of q and K minus lam (fp32 [Hq]) times
+        softmax over the second halves, scaled by 1 / sqrt(head_dim / 2), then the optional RMS norm and scale.
+        For a cache made with `diff`."""
+        if self.diff_workspace is None:
+            raise ValueError("attend_diff needs a cache made with diff")
+        B.kvq_diff_decode_attention(self.cfg, self.pool, q, self.block_table, seq_lens, self.max_len,
+                                    self.softmax_scale * math.sqrt(2.0), lam, norm_weight, norm_eps, out_scale, out,
+                                    self.diff_workspace, stream=stream)
+
+    def decode_step_diff(self, q, k_new, v_new, lam, append_pos, seq_lens, out, norm_weight=None,
+                         norm_eps: float = 1e-5, out_scale: float = 1.0, stream=None) -> None:
+        """Append one token per sequence at append_pos, then attend_diff over seq_lens: one kvq_diff_decode_step."""
+        if self.diff_workspace is None:
+            raise ValueError("decode_step_diff needs a cache made with diff")
+        B.kvq_diff_decode_step(self.cfg, self.pool, k_new, v_new, append_pos, q, self.block_table, seq_lens,
+                               self.max_len, self.softmax_scale * math.sqrt(2.0), lam, norm_weight, norm_eps,
+                               out_scale, out, self.diff_workspace, stream=stream)
+
     def decode_step_host(self, staging: "HostStaging", append_pos, seq_lens, stream=None) -> None:
         """The decode step from pinned host memory in one kvq_decode_step_host call: one H2D copy of
         the step's q, K and V (staged back to back), the step, one D2H copy of the output, all
         asynchronous on the step's stream."""
         if self.window > 0:
             raise ValueError("the host step attends to every position (no window)")
+        if self.weights is not None:
+            raise ValueError("the host step does not track weights")
         B.kvq_decode_step_host(self.cfg, self.pool, staging.host, staging.dev, append_pos, self.block_table, seq_lens,
                                self.batch, self.num_q_heads, self.max_len, self.softmax_scale, staging.out,
                                staging.out_host, self.workspace, stream=stream)
 
     def flags(self) -> int:
         """Status flags of the last calls (synchronizes)."""
-        return B.kvq_read_status(self.status) | B.kvq_read_status(self.workspace)
+        f = B.kvq_read_status(self.status) | B.kvq_read_status(self.workspace)
+        return f if self.diff_workspace is None else f | B.kvq_read_status(self.diff_workspace)
 
 
 class HostStaging:
@@ -153,6 +227,8 @@ class HostPipeline:
         st = self.slots[i % 2]
         if cache.window > 0:
             raise ValueError("the pipelined host step attends to every position (no window)")
+        if cache.weights is not None:
+            raise ValueError("the pipelined host step does not track weights")
         B.kvq_decode_step_host_pipelined(cache.cfg, cache.pool, st.host, st.dev, append_pos, cache.block_table,
                                          seq_lens, cache.batch, cache.num_q_heads, cache.max_len,
                                          cache.softmax_scale, st.out, st.out_host, cache.workspace, self.compute,

@@ -28,6 +28,13 @@ struct CParams {
     float* out;
     float* out_host;  // device address of mapped pinned host memory that also receives out, or nullptr
     int32_t B, Hq, lg_p;
+    // MODE 1: (max, 1 / sum) of each row, and the bound the lengths are cut to
+    float2* stat;
+    int32_t len_max;
+    // MODE 2 (Hq counts virtual heads, two per output row)
+    const float* lambda;
+    const float* norm_weight;
+    float norm_eps, out_scale;
 };
 
 constexpr int kCombineMaxWarps = 16;
@@ -50,7 +57,11 @@ constexpr int kCombineLocalB = 256;   // up to this batch the row metadata is co
 // register file and keep the next call's decode CTAs off that SM until it leaves; at 64
 // it holds half.  Rows of 4- and 8-warp CTAs (up to 64 partials) load 8 at a time, in
 // one round.
-template <int D, int NSRC, int NB>
+// MODE 1 also writes each row's maximum and reciprocal sum for the weights kernel behind it.
+// MODE 2 (differential attention) has one CTA per query head: the rows of its two maps are
+// merged one after the other, then o = o1 - lambda o2, the optional RMS norm over the row,
+// which warp 0 holds whole, and the output scale.
+template <int D, int NSRC, int NB, int MODE = 0>
 __global__ void __launch_bounds__(kCombineMaxWarps * 32, NB == 8 || D == 256 ? 1 : 2)
 combine_kernel(CParams p) {
     static_assert(D == 64 || D == 128 || D == 256, "head_dim 64, 128 or 256");
@@ -67,12 +78,16 @@ combine_kernel(CParams p) {
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int nw = blockDim.x >> 5;
-    const int b = static_cast<int>(blockIdx.x / p.Hq);
-    const int hq = static_cast<int>(blockIdx.x - static_cast<long long>(b) * p.Hq);
+    const int rows_b = MODE == 2 ? p.Hq / 2 : p.Hq;  // output rows per sequence
+    const int b = static_cast<int>(blockIdx.x / rows_b);
+    const int hrow = static_cast<int>(blockIdx.x - static_cast<long long>(b) * rows_b);
+    const int hq = MODE == 2 ? 2 * hrow : hrow;  // (both maps' virtual heads share a segment)
 
     // Pages of sequence i as source s listed them, and the row's range of partials.
     auto pages_of = [&](const CSource& s, int i) {
-        return seq_span(p.seq_lens[i] - s.len_sub, p.lg_p, s.max_blocks, s.window, s.sinks).np;
+        int L = p.seq_lens[i] - s.len_sub;
+        if constexpr (MODE == 1) L = min(L, p.len_max);
+        return seq_span(L, p.lg_p, s.max_blocks, s.window, s.sinks).np;
     };
     auto row_range = [&](const CSource& s, int pb_, int np_, int tot_, long long& cf_, long long& base_,
                          long long& U_) {
@@ -135,114 +150,160 @@ combine_kernel(CParams p) {
         }
     }
 
-    float M = -INFINITY, L = 0.f;
-    float4 acc[NV][NA];
+    __shared__ float4 s_first[MODE == 2 ? D / 4 : 1];  // MODE 2: map 1's output row
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int map = 0; map < (MODE == 2 ? 2 : 1); ++map) {
+        if (MODE == 2 && map == 1) __syncthreads();  // warp 0 has read map 1's results
+        float M = -INFINITY, L = 0.f;
+        float4 acc[NV][NA];
 #pragma unroll
-        for (int a = 0; a < NA; ++a) acc[v][a] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
-    for (int si = 0; si < NSRC; ++si) {
-        const CSource& s = p.src[si];
-        const int sl = hq - (hq / s.ns) * s.ns;
-        const bool dense = U[si] >= s.C;  // every CTA slice holds units
-        const long long stride_ml = static_cast<long long>(s.ns) * 2;
-        const long long stride_o = static_cast<long long>(s.ns) * D;
-        const float* ml0 = s.ws_ml + (base[si] * s.ns + sl) * 2;
-        const float* o0 = s.ws_o + (base[si] * s.ns + sl) * D + 4 * lane;
-        for (int j0 = warp; j0 < n[si]; j0 += NB * nw) {
-            float2 ml[NB];
-            float4 ov[NB][NV];
+            for (int a = 0; a < NA; ++a) acc[v][a] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int kk = 0; kk < NB; ++kk) {
-                const int j = j0 + kk * nw;
-                bool have = j < n[si];
-                if (have && !dense) {
-                    const long long k = cf[si] + j / s.W;
-                    have = slice_start(k, U[si], s.C) < slice_start(k + 1, U[si], s.C);
-                }
-                ml[kk] = have ? __ldcg(reinterpret_cast<const float2*>(ml0 + j * stride_ml)) : make_float2(-INFINITY, 0.f);
+        for (int si = 0; si < NSRC; ++si) {
+            const CSource& s = p.src[si];
+            const int sl = hq - (hq / s.ns) * s.ns + map;
+            const bool dense = U[si] >= s.C;  // every CTA slice holds units
+            const long long stride_ml = static_cast<long long>(s.ns) * 2;
+            const long long stride_o = static_cast<long long>(s.ns) * D;
+            const float* ml0 = s.ws_ml + (base[si] * s.ns + sl) * 2;
+            const float* o0 = s.ws_o + (base[si] * s.ns + sl) * D + 4 * lane;
+            for (int j0 = warp; j0 < n[si]; j0 += NB * nw) {
+                float2 ml[NB];
+                float4 ov[NB][NV];
 #pragma unroll
-                for (int v = 0; v < NV; ++v)
-                    ov[kk][v] = have && lane_has(lane, v) ? __ldcg(reinterpret_cast<const float4*>(o0 + j * stride_o) + 32 * v)
-                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            float mb = M;
-#pragma unroll
-            for (int kk = 0; kk < NB; ++kk) mb = fmaxf(mb, ml[kk].x);
-            if (mb == -INFINITY) continue;  // only empty partials so far
-            if (mb > M) {  // a larger running maximum: rescale what has been summed
-                const float f = fast_exp2(M - mb);
-                L *= f;
-#pragma unroll
-                for (int v = 0; v < NV; ++v)
-#pragma unroll
-                    for (int a = 0; a < NA; ++a) {
-                        acc[v][a].x *= f;
-                        acc[v][a].y *= f;
-                        acc[v][a].z *= f;
-                        acc[v][a].w *= f;
+                for (int kk = 0; kk < NB; ++kk) {
+                    const int j = j0 + kk * nw;
+                    bool have = j < n[si];
+                    if (have && !dense) {
+                        const long long k = cf[si] + j / s.W;
+                        have = slice_start(k, U[si], s.C) < slice_start(k + 1, U[si], s.C);
                     }
-                M = mb;
-            }
+                    ml[kk] = have ? __ldcg(reinterpret_cast<const float2*>(ml0 + j * stride_ml)) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int kk = 0; kk < NB; ++kk) {
-                const float f = fast_exp2(ml[kk].x - M);
-                L = fmaf(f, ml[kk].y, L);
+                    for (int v = 0; v < NV; ++v)
+                        ov[kk][v] = have && lane_has(lane, v) ? __ldcg(reinterpret_cast<const float4*>(o0 + j * stride_o) + 32 * v)
+                                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                float mb = M;
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    float4& A = acc[v][kk % NA];
-                    A.x = fmaf(f, ov[kk][v].x, A.x);
-                    A.y = fmaf(f, ov[kk][v].y, A.y);
-                    A.z = fmaf(f, ov[kk][v].z, A.z);
-                    A.w = fmaf(f, ov[kk][v].w, A.w);
+                for (int kk = 0; kk < NB; ++kk) mb = fmaxf(mb, ml[kk].x);
+                if (mb == -INFINITY) continue;  // only empty partials so far
+                if (mb > M) {  // a larger running maximum: rescale what has been summed
+                    const float f = fast_exp2(M - mb);
+                    L *= f;
+#pragma unroll
+                    for (int v = 0; v < NV; ++v)
+#pragma unroll
+                        for (int a = 0; a < NA; ++a) {
+                            acc[v][a].x *= f;
+                            acc[v][a].y *= f;
+                            acc[v][a].z *= f;
+                            acc[v][a].w *= f;
+                        }
+                    M = mb;
+                }
+#pragma unroll
+                for (int kk = 0; kk < NB; ++kk) {
+                    const float f = fast_exp2(ml[kk].x - M);
+                    L = fmaf(f, ml[kk].y, L);
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                        float4& A = acc[v][kk % NA];
+                        A.x = fmaf(f, ov[kk][v].x, A.x);
+                        A.y = fmaf(f, ov[kk][v].y, A.y);
+                        A.z = fmaf(f, ov[kk][v].z, A.z);
+                        A.w = fmaf(f, ov[kk][v].w, A.w);
+                    }
                 }
             }
         }
-    }
-    if (lane == 0) {
-        s_m[warp] = M;
-        s_l[warp] = L;
-    }
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        float4 t = acc[v][0];
-#pragma unroll
-        for (int a = 1; a < NA; ++a) {
-            t.x += acc[v][a].x;
-            t.y += acc[v][a].y;
-            t.z += acc[v][a].z;
-            t.w += acc[v][a].w;
+        if (lane == 0) {
+            s_m[warp] = M;
+            s_l[warp] = L;
         }
-        if (lane_has(lane, v)) s_o[warp][lane + 32 * v] = t;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        float Mx = -INFINITY;
-        for (int w = 0; w < nw; ++w) Mx = fmaxf(Mx, s_m[w]);
-        float Ls = 0.f;
-        if (Mx != -INFINITY)
-            for (int w = 0; w < nw; ++w) Ls = fmaf(fast_exp2(s_m[w] - Mx), s_l[w], Ls);
-        const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
-        const long long row = static_cast<long long>(b) * p.Hq + hq;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            if (!lane_has(lane, v)) continue;
-            const int f4 = lane + 32 * v;
-            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (Mx != -INFINITY) {
-                for (int w = 0; w < nw; ++w) {
-                    const float f = fast_exp2(s_m[w] - Mx);
-                    const float4 ow = s_o[w][f4];
-                    O.x = fmaf(f, ow.x, O.x);
-                    O.y = fmaf(f, ow.y, O.y);
-                    O.z = fmaf(f, ow.z, O.z);
-                    O.w = fmaf(f, ow.w, O.w);
+            float4 t = acc[v][0];
+#pragma unroll
+            for (int a = 1; a < NA; ++a) {
+                t.x += acc[v][a].x;
+                t.y += acc[v][a].y;
+                t.z += acc[v][a].z;
+                t.w += acc[v][a].w;
+            }
+            if (lane_has(lane, v)) s_o[warp][lane + 32 * v] = t;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            float Mx = -INFINITY;
+            for (int w = 0; w < nw; ++w) Mx = fmaxf(Mx, s_m[w]);
+            float Ls = 0.f;
+            if (Mx != -INFINITY)
+                for (int w = 0; w < nw; ++w) Ls = fmaf(fast_exp2(s_m[w] - Mx), s_l[w], Ls);
+            const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+            const long long row = static_cast<long long>(b) * rows_b + hrow;
+            if constexpr (MODE == 1) {
+                if (lane == 0) p.stat[row] = make_float2(Mx, inv);
+            }
+            float4 res[NV];
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                res[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (!lane_has(lane, v)) continue;
+                const int f4 = lane + 32 * v;
+                float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (Mx != -INFINITY) {
+                    for (int w = 0; w < nw; ++w) {
+                        const float f = fast_exp2(s_m[w] - Mx);
+                        const float4 ow = s_o[w][f4];
+                        O.x = fmaf(f, ow.x, O.x);
+                        O.y = fmaf(f, ow.y, O.y);
+                        O.z = fmaf(f, ow.z, O.z);
+                        O.w = fmaf(f, ow.w, O.w);
+                    }
+                }
+                res[v] = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
+            }
+            if constexpr (MODE == 2) {
+                if (map == 0) {
+#pragma unroll
+                    for (int v = 0; v < NV; ++v)
+                        if (lane_has(lane, v)) s_first[lane + 32 * v] = res[v];
+                    continue;
+                }
+                const float lam = p.lambda[hrow];
+                float ss = 0.f;
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    if (!lane_has(lane, v)) continue;
+                    const float4 f1 = s_first[lane + 32 * v];  // (this lane's own store)
+                    res[v] = make_float4(fmaf(-lam, res[v].x, f1.x), fmaf(-lam, res[v].y, f1.y),
+                                         fmaf(-lam, res[v].z, f1.z), fmaf(-lam, res[v].w, f1.w));
+                    ss += res[v].x * res[v].x + res[v].y * res[v].y + res[v].z * res[v].z + res[v].w * res[v].w;
+                }
+                float f = p.out_scale;
+                if (p.norm_weight != nullptr) {
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+                    f *= rsqrtf(ss * (1.f / D) + p.norm_eps);
+                }
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    if (!lane_has(lane, v)) continue;
+                    float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
+                    if (p.norm_weight != nullptr) w = reinterpret_cast<const float4*>(p.norm_weight)[lane + 32 * v];
+                    res[v] = n[0] > 0 ? make_float4(res[v].x * f * w.x, res[v].y * f * w.y, res[v].z * f * w.z, res[v].w * f * w.w)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);  // no positions: zeros, whatever norm_eps is
                 }
             }
-            const float4 r = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
-            reinterpret_cast<float4*>(p.out + row * D)[f4] = r;
-            if (p.out_host != nullptr) reinterpret_cast<float4*>(p.out_host + row * D)[f4] = r;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                if (!lane_has(lane, v)) continue;
+                reinterpret_cast<float4*>(p.out + row * D)[lane + 32 * v] = res[v];
+                if (p.out_host != nullptr) reinterpret_cast<float4*>(p.out_host + row * D)[lane + 32 * v] = res[v];
+            }
         }
     }
 }
@@ -268,8 +329,21 @@ decode::CSource source_of(const DecodeArgs& a, const DecodePlan& plan) {
     return s;
 }
 
-cudaError_t launch(const decode::CParams& p, int d, int warps, cudaStream_t stream) {
-    const long long rows = static_cast<long long>(p.B) * p.Hq;
+template <int MODE>
+cudaError_t launch_one(const cudaLaunchConfig_t& cfg, const decode::CParams& p, int d, bool light) {
+    switch (d) {
+        case 64: return light ? cudaLaunchKernelEx(&cfg, decode::combine_kernel<64, 1, 4, MODE>, p)
+                              : cudaLaunchKernelEx(&cfg, decode::combine_kernel<64, 1, 8, MODE>, p);
+        case 128: return light ? cudaLaunchKernelEx(&cfg, decode::combine_kernel<128, 1, 4, MODE>, p)
+                               : cudaLaunchKernelEx(&cfg, decode::combine_kernel<128, 1, 8, MODE>, p);
+        case 256: return light ? cudaLaunchKernelEx(&cfg, decode::combine_kernel<256, 1, 4, MODE>, p)
+                               : cudaLaunchKernelEx(&cfg, decode::combine_kernel<256, 1, 8, MODE>, p);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch(const decode::CParams& p, DecodeMode mode, int d, int warps, cudaStream_t stream) {
+    const long long rows = static_cast<long long>(p.B) * (mode == DecodeMode::kDiff ? p.Hq / 2 : p.Hq);
     if (rows <= 0) return cudaSuccess;
     if (rows > 0x7fffffffLL) return cudaErrorInvalidValue;
     // Launched while the decode grid runs (programmatic dependent launch); the kernel
@@ -287,13 +361,9 @@ cudaError_t launch(const decode::CParams& p, int d, int warps, cudaStream_t stre
     cudaError_t err;
     const bool light = warps == 16;  // the 64-register instance
     if (p.nsrc == 2) err = cudaLaunchKernelEx(&cfg, decode::combine_kernel<128, 2, 8>, p);  // mixed: head_dim 128 only
-    else if (d == 64) err = light ? cudaLaunchKernelEx(&cfg, decode::combine_kernel<64, 1, 4>, p)
-                                  : cudaLaunchKernelEx(&cfg, decode::combine_kernel<64, 1, 8>, p);
-    else if (d == 256) err = light ? cudaLaunchKernelEx(&cfg, decode::combine_kernel<256, 1, 4>, p)
-                                   : cudaLaunchKernelEx(&cfg, decode::combine_kernel<256, 1, 8>, p);
-    else if (d == 128) err = light ? cudaLaunchKernelEx(&cfg, decode::combine_kernel<128, 1, 4>, p)
-                                   : cudaLaunchKernelEx(&cfg, decode::combine_kernel<128, 1, 8>, p);
-    else return cudaErrorInvalidValue;
+    else if (mode == DecodeMode::kWeights) err = launch_one<1>(cfg, p, d, light);
+    else if (mode == DecodeMode::kDiff) err = launch_one<2>(cfg, p, d, light);
+    else err = launch_one<0>(cfg, p, d, light);
     if (err != cudaSuccess) return err;
     return cudaGetLastError();
 }
@@ -316,7 +386,13 @@ cudaError_t launch_combine(const DecodeArgs& a, const DecodePlan& plan, cudaStre
     p.B = a.B;
     p.Hq = a.Hq;
     p.lg_p = lg2(a.L.P);
-    return launch(p, a.L.d, plan.combine_warps, stream);
+    p.stat = reinterpret_cast<float2*>(a.workspace + plan.ws_stat_offset);
+    p.len_max = a.max_len;
+    p.lambda = a.lambda;
+    p.norm_weight = a.norm_weight;
+    p.norm_eps = a.norm_eps;
+    p.out_scale = a.out_scale;
+    return launch(p, a.mode, a.L.d, plan.combine_warps, stream);
 }
 
 // The mixed-precision decode: the partials of the INT4 grid (a0, plan0) and of the FP16
@@ -333,7 +409,7 @@ cudaError_t launch_combine2(const DecodeArgs& a0, const DecodePlan& plan0, const
     p.Hq = a0.Hq;
     p.lg_p = lg2(a0.L.P);
     const int warps = std::max(plan0.combine_warps, plan1.combine_warps);
-    return launch(p, a0.L.d, warps, stream);
+    return launch(p, DecodeMode::kPlain, a0.L.d, warps, stream);
 }
 
 }  // namespace kvq

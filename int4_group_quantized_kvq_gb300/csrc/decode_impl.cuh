@@ -55,6 +55,8 @@
 //    only the weights are exchanged (four shuffles per chunk and V group).  With HK = 1
 //    chunks are taken two at a time (two 16-token pages, or two chunks of a larger
 //    page): the two score chains interleave and one softmax reduction covers both.
+//    Two further forms of the call are modes of this kernel (MODE 1 and 2 below): attention
+//    that also leaves every score for the accumulated weights, and differential attention.
 //  * Split combine.  At the end of each segment (sequence, head group) every warp writes
 //    its own partial (running max, running sum and unnormalised output per slot) to the
 //    workspace, straight from its accumulators; no warp waits for another, and nothing is counted or fenced on the streaming path, so a warp that
@@ -135,6 +137,10 @@ struct KParams {
     // q is written by the kernel ahead on the stream (the host-buffer step's copy kernel):
     // read it only after griddepcontrol.wait
     bool q_after_wait;
+    // MODE 1: every attended position's score (log2 units) goes to scores[b][kv head][t][query
+    // head of the kv head], score_ld positions per kv head; lengths are cut to score_ld
+    float* scores;
+    int32_t score_ld;
 };
 
 // a / b for a >= 0, b > 0, with 32-bit division when both fit (the usual case).
@@ -188,8 +194,9 @@ __device__ __forceinline__ int span_index(const SeqSpan& sp, int r) {
 }
 
 // Exclusive prefix sums of pages per sequence into pre[0..B], the lengths (negative ones
-// as 0) into lens[0..B-1] and the append positions (-1: none) into aps[0..B-1]; run by
-// one warp.
+// as 0, with CUT those past score_ld as score_ld) into lens[0..B-1] and the append positions
+// (-1: none) into aps[0..B-1]; run by one warp.
+template <bool CUT = false>
 __device__ __forceinline__ void page_prefix(const KParams& p, int32_t* pre, int32_t* lens, int32_t* aps, int lane) {
     int carry = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -198,6 +205,12 @@ __device__ __forceinline__ void page_prefix(const KParams& p, int32_t* pre, int3
         if (b < p.B) {
             int L = p.seq_lens[b] - p.len_sub;
             L = L < 0 ? 0 : L;
+            if constexpr (CUT) {
+                if (L > p.score_ld) {
+                    raise_flag(p.status, KVQ_FLAG_BAD_POSITION);
+                    L = p.score_ld;
+                }
+            }
             lens[b] = L;
             aps[b] = p.k_new != nullptr ? p.append_pos[b] : -1;
             if (((static_cast<long long>(L) + p.P - 1) >> p.lg_p) > p.max_blocks) raise_flag(p.status, KVQ_FLAG_BAD_POSITION);
@@ -393,17 +406,37 @@ __device__ __forceinline__ void load_scales(const uint8_t* p, float (&a)[N], flo
 // section 3.1): K codes P x D int8, V codes P x D int8, K scales P fp32, V scales P fp32
 // per block, a value being code * scale; it runs with one group per row (GK = GV = D) and
 // one-head units, and has no fused append.
-template <int D, int GK, int GV, int HK, int HS, bool WIN, bool P16, int CODEC = 0>
+// MODE 0: plain attention.  MODE 1: attention that also stores each position's scores, from
+// which the weights kernel (decode_weights.cu) takes the positions' softmax weights once the
+// combine knows each row's maximum and sum.  MODE 2: differential attention's two maps: a
+// query head is two rows of score columns ("virtual heads" 2 h and 2 h + 1), the first
+// carrying the lower half of q, the second the upper half, zeros elsewhere; their outputs are
+// subtracted by the combine.  Modes 1 and 2 feed the score MMA centred codes (n - 8, one more
+// instruction per pair of codes than the f16 subnormals of MODE 0): the offset form's partial
+// sums are of the size of 8 sum |q| whatever the codes are, and the MMA's fp32 accumulation
+// rounds at that size, which with K groups stretched by an outlier channel moves a score by
+// some 1e-5.  The plain output tolerates it; the weights are fp32 results of their own, and a
+// difference of two maps keeps only what does not cancel.
+template <int D, int GK, int GV, int HK, int HS, bool WIN, bool P16, int CODEC = 0, int MODE = 0>
 __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decode_splitkv_kernel(KParams p) {
     static_assert(D == 64 || D == 128 || D == 256, "head_dim 64, 128 or 256");
     static_assert(CODEC == 0 || (CODEC == 1 && D == 128 && GK == D && GV == D && HK == 1), "INT8: d 128, rows");
     static_assert(D <= 128 || (HK == 1 && HS == 1), "head_dim 256: one-head units, up to 4 query heads each");
     static_assert(HK == 1 || HS == 1, "several kv heads per unit only with one query head each");
     static_assert(HK == 1 || P16, "four-head units only for 16-token pages");
+    static_assert(MODE == 0 || !WIN, "the weights and differential modes attend to every position");
+    static_assert(MODE != 2 || (HK == 1 && CODEC == 0 && 2 * GK <= D), "differential: one-head INT4 units, K groups within a half");
     static_assert(4 * HS + 2 * HK <= kQRows, "q rows and the appended token's K and V rows fit a q buffer");
     constexpr int NGK = D / GK;               // K groups per row
     constexpr int NGV = D / GV;               // V groups per row
     constexpr bool I8 = CODEC == 1;
+    constexpr bool CENTRED = MODE != 0;       // codes enter the score MMA without their offset
+    // Modes 1 and 2 hold the softmax terms as 2^kUp p: the weights p * v_scale become f16 high
+    // and low parts, and small ones would lose bits as f16 subnormals.  A quantized row's scale
+    // is at most 65504 / 7 (INT8: 65504 / 127), so 2^kUp p v_scale stays a finite f16.  (INT8
+    // rows of unit-normal values have scales of about 0.03: without it the output's error
+    // against fp64 was 6.5e-6 of its norm.)
+    constexpr float kUp = MODE == 0 ? 0.f : (I8 ? 6.f : 2.f);
     constexpr int KW = I8 ? D / 16 : D / 32;  // K code words per thread per token row
     constexpr int KSTEPS = D / 16;            // MMA k-steps over head_dim
     constexpr int NTQ = (HS * NGK + 1) / 2;   // score n-tiles
@@ -450,7 +483,7 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
     // Until griddepcontrol.wait below, the kernel ahead of this one on the stream may still be
     // running.  Only the read-only inputs are read before it: seq_lens, the block table and
     // q.  The pool (written by quantize-append), the output and the workspace come after.
-    if (warp == 0) page_prefix(p, pre, lens, aps, lane);
+    if (warp == 0) page_prefix<MODE == 1>(p, pre, lens, aps, lane);
     const uint32_t qfree0 = smem_u32(&ctl->qfree[0]);
     if (threadIdx.x == 0) {
         mbar_init(qbar0, 1);
@@ -552,7 +585,9 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
     // rows of the segment's HK kv heads after them (rows ns .. ns + 2 HK - 1): the warp that
     // streams the page quantizes them from there, instead of loading them from global memory
     // in the middle of the stream, where a load waits behind the SM's page copies in flight.
-    const uint32_t q_bytes = static_cast<uint32_t>(p.ns) * D * 2;
+    // (MODE 2: ns virtual heads are ns / 2 query heads)
+    const int nq = MODE == 2 ? p.ns / 2 : p.ns;  // q rows of a segment
+    const uint32_t q_bytes = static_cast<uint32_t>(nq) * D * 2;
     auto issue_q = [&](int sb, int shg, int k) {
         const uint32_t bar = qbar0 + 8 * (k & 1);
         __half* dst = qbuf + (k & 1) * kQRows * D;
@@ -560,7 +595,7 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
         const uint32_t r_bytes = HK * D * 2;
         fence_proxy_async_smem();
         mbar_arrive_expect_tx(bar, q_bytes + (rows ? 2 * r_bytes : 0));
-        bulk_g2s(smem_u32(dst), p.q + (static_cast<long long>(sb) * p.Hq + shg * p.ns) * D, q_bytes, bar);
+        bulk_g2s(smem_u32(dst), p.q + (static_cast<long long>(sb) * (MODE == 2 ? p.Hq / 2 : p.Hq) + shg * nq) * D, q_bytes, bar);
         if (rows) {
             const long long row = static_cast<long long>(sb) * p.Hkv + static_cast<long long>(shg) * HK;
             bulk_g2s(smem_u32(dst + p.ns * D), p.k_new + row * D, r_bytes, bar);
@@ -599,6 +634,10 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
     int Leff = 0;  // positions of the segment's sequence (clamped to its block table)
     int wlo = 0;   // its first window position (0: all attended)
     SeqSpan sspan{};  // attended positions and listed pages of the segment's sequence
+
+    // MODE 1: this thread's scores of the segment's position 0, and the step from a position to the next
+    float* sc = nullptr;
+    const int sc_step = HK == 1 ? p.ns : 1;
 
     // the kv head (within the unit) of this thread's score slot, and of its B-fragment
     // column (HK > 1 only when every slot is its own kv head)
@@ -670,8 +709,16 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
 #pragma unroll
                     for (int X = 0; X < TG; ++X) {
                         const uint32_t x = kg[X][0][j] ^ 0x80808080u, y = kg8[X][0][j] ^ 0x80808080u;
-                        const uint32_t a0 = prmt(x, 0u, 0x5140u), a1 = prmt(y, 0u, 0x5140u);
-                        const uint32_t a2 = prmt(x, 0u, 0x7362u), a3 = prmt(y, 0u, 0x7362u);
+                        // (centred: 1024 + c + 128, minus 1152)
+                        constexpr uint32_t e = CENTRED ? 0x64646464u : 0u;
+                        uint32_t a0 = prmt(x, e, 0x5140u), a1 = prmt(y, e, 0x5140u);
+                        uint32_t a2 = prmt(x, e, 0x7362u), a3 = prmt(y, e, 0x7362u);
+                        if constexpr (CENTRED) {
+                            a0 = h2_sub(a0, 0x64806480u);
+                            a1 = h2_sub(a1, 0x64806480u);
+                            a2 = h2_sub(a2, 0x64806480u);
+                            a3 = h2_sub(a3, 0x64806480u);
+                        }
 #pragma unroll
                         for (int t = 0; t < NTQ; ++t) mma_f16_16816(acc[X][0][t], a0, a1, a2, a3, qb[j][t][0], qb[j][t][1]);
                     }
@@ -688,8 +735,11 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
                                 // n * 2^-24, the high ones 16 n * 2^-24
                                 const uint32_t x = kg[X][a][wi] >> (8 * e);
                                 const uint32_t y = kg8[X][a][wi] >> (8 * e);
-                                const uint32_t a0 = x & 0x000F000Fu, a1 = y & 0x000F000Fu;
-                                const uint32_t a2 = x & 0x00F000F0u, a3 = y & 0x00F000F0u;
+                                // (centred: the codes n - 8 themselves)
+                                const uint32_t a0 = CENTRED ? unpack_lo(x) : x & 0x000F000Fu;
+                                const uint32_t a1 = CENTRED ? unpack_lo(y) : y & 0x000F000Fu;
+                                const uint32_t a2 = CENTRED ? unpack_hi(x) : x & 0x00F000F0u;
+                                const uint32_t a3 = CENTRED ? unpack_hi(y) : y & 0x00F000F0u;
 #pragma unroll
                                 for (int t = 0; t < NTQ; ++t)
                                     mma_f16_16816(acc[X][a][t], a0, a1, a2, a3, qb[2 * wi + e][t][0],
@@ -722,12 +772,24 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
                     // the group's code dot product sum (n - off) q = 2^24 S - off sum q
                     const int pi = s * NGK + R;
                     // (times softmax_scale * log2 e, folded into both terms)
-                    const float qo = q8[pi >> 1][pi & 1];
-                    z0 = fmaf(skg[R], fmaf(sacc[pi >> 1][pi & 1], s24, -qo), z0);
-                    z1 = fmaf(skg8[R], fmaf(sacc[pi >> 1][2 + (pi & 1)], s24, -qo), z1);
+                    if constexpr (CENTRED) {
+                        z0 = fmaf(skg[R], sacc[pi >> 1][pi & 1], z0);
+                        z1 = fmaf(skg8[R], sacc[pi >> 1][2 + (pi & 1)], z1);
+                    } else {
+                        const float qo = q8[pi >> 1][pi & 1];
+                        z0 = fmaf(skg[R], fmaf(sacc[pi >> 1][pi & 1], s24, -qo), z0);
+                        z1 = fmaf(skg8[R], fmaf(sacc[pi >> 1][2 + (pi & 1)], s24, -qo), z1);
+                    }
                 }
-                z[X][s][0] = z0;
-                z[X][s][1] = z1;
+                z[X][s][0] = CENTRED ? z0 * p.scale_log2 : z0;
+                z[X][s][1] = CENTRED ? z1 * p.scale_log2 : z1;
+                if constexpr (MODE == 1) {
+                    if (HK > 1 || c + 4 * s < p.ns) {
+                        float* at = sc + static_cast<long long>(t0[X] + g) * sc_step + 4 * s;
+                        if (!MASKED || vg[X]) at[0] = z[X][s][0];
+                        if (!MASKED || vg8[X]) at[8 * sc_step] = z[X][s][1];
+                    }
+                }
                 if (MASKED) {
                     z[X][s][0] = vg[X] ? z[X][s][0] : -INFINITY;
                     z[X][s][1] = vg8[X] ? z[X][s][1] : -INFINITY;
@@ -770,8 +832,8 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
         for (int s = 0; s < HS; ++s) {
 #pragma unroll
             for (int X = 0; X < TG; ++X) {
-                pr[X][s][0] = fast_exp2(z[X][s][0] - m[s]);
-                pr[X][s][1] = fast_exp2(z[X][s][1] - m[s]);
+                pr[X][s][0] = fast_exp2(z[X][s][0] - (m[s] - kUp));
+                pr[X][s][1] = fast_exp2(z[X][s][1] - (m[s] - kUp));
                 l[s] += pr[X][s][0] + pr[X][s][1];
             }
         }
@@ -967,6 +1029,10 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
                     my_app = u >= fu && u < ue && (u - fu) % kWarps == 0;
                 }
             }
+            if constexpr (MODE == 1) {
+                const long long head = static_cast<long long>(b) * p.Hkv + static_cast<long long>(hg) * HK + a_row;
+                sc = p.scores + head * p.score_ld * sc_step + (HK == 1 ? c : 0);
+            }
             const __half* qseg = qbuf + (segk & 1) * kQRows * D;
 #pragma unroll
             for (int t = 0; t < NTQ; ++t) {
@@ -975,7 +1041,7 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
                 const int R = pi % NGK;
                 const int j = (g >> 1) + 4 * sigma;
                 const bool colv = sigma < HS && j < p.ns;
-                const __half* qrow = qseg + (colv ? j : 0) * D;
+                const __half* qrow = qseg + (colv ? (MODE == 2 ? j / 2 : j) : 0) * D;
                 float qs = 0.f;  // this thread's part of the column's sum of q
                 if constexpr (I8) {
                     // k-step j: dimensions c (D / 4) + 4 j .. + 3, in order
@@ -994,7 +1060,8 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
                 for (int wi = 0; wi < (I8 ? 0 : KW); ++wi) {
                     const int dbase = c * (D / 4) + 8 * wi;
                     uint4 w4 = make_uint4(0, 0, 0, 0);
-                    if (colv && dbase / GK == R) w4 = *reinterpret_cast<const uint4*>(qrow + dbase);
+                    // (MODE 2: virtual head j carries half j % 2 of the query head's row)
+                    if (colv && dbase / GK == R && (MODE != 2 || dbase / (D / 2) == (j & 1))) w4 = *reinterpret_cast<const uint4*>(qrow + dbase);
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&(&w4.x)[h]));
@@ -1002,16 +1069,20 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
                     }
                     // the entries meeting high nibbles (odd dimensions) are divided by 16
                     qb[2 * wi][t][0] = prmt(w4.x, w4.z, 0x5410u);
-                    qb[2 * wi][t][1] = h2_mul(prmt(w4.x, w4.z, 0x7632u), 0x2C002C00u /* 1/16 */);
+                    // (centred codes: as they are)
+                    const uint32_t odd0 = prmt(w4.x, w4.z, 0x7632u), odd1 = prmt(w4.y, w4.w, 0x7632u);
+                    qb[2 * wi][t][1] = CENTRED ? odd0 : h2_mul(odd0, 0x2C002C00u /* 1/16 */);
                     qb[2 * wi + 1][t][0] = prmt(w4.y, w4.w, 0x5410u);
-                    qb[2 * wi + 1][t][1] = h2_mul(prmt(w4.y, w4.w, 0x7632u), 0x2C002C00u);
+                    qb[2 * wi + 1][t][1] = CENTRED ? odd1 : h2_mul(odd1, 0x2C002C00u);
                 }
                 // column g of n-tile t: its sum over the row group's four threads; this
                 // thread's score columns 2c and 2c + 1 are those of the threads with g = 2c, 2c + 1
-                qs += __shfl_xor_sync(0xffffffffu, qs, 1);
-                qs += __shfl_xor_sync(0xffffffffu, qs, 2);
-                q8[t][0] = (kOff * p.scale_log2) * __shfl_sync(0xffffffffu, qs, 8 * c);
-                q8[t][1] = (kOff * p.scale_log2) * __shfl_sync(0xffffffffu, qs, 8 * c + 4);
+                if constexpr (!CENTRED) {
+                    qs += __shfl_xor_sync(0xffffffffu, qs, 1);
+                    qs += __shfl_xor_sync(0xffffffffu, qs, 2);
+                    q8[t][0] = (kOff * p.scale_log2) * __shfl_sync(0xffffffffu, qs, 8 * c);
+                    q8[t][1] = (kOff * p.scale_log2) * __shfl_sync(0xffffffffu, qs, 8 * c + 4);
+                }
             }
         }
         // this warp is done with the segment's q buffer (a warp with units here has waited
@@ -1164,7 +1235,7 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
                             }
                     }
                     if (g == 0 && c < nsr)
-                        *reinterpret_cast<float2*>(p.ws_ml + (piece * p.ns + 4 * s + c) * 2) = make_float2(m[s], lt[s]);
+                        *reinterpret_cast<float2*>(p.ws_ml + (piece * p.ns + 4 * s + c) * 2) = make_float2(m[s] - kUp, lt[s]);
                 }
             } else {
                 // no units of this segment here (or a failed wait): an empty partial
@@ -1223,11 +1294,11 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
 
 // Raise the kernel's dynamic shared-memory limit once to the largest size asked for,
 // so repeated calls (and calls under stream capture) only launch.
-template <int D, int GK, int GV, int HK, int HS, bool WIN, bool P16, int CODEC = 0>
+template <int D, int GK, int GV, int HK, int HS, bool WIN, bool P16, int CODEC = 0, int MODE = 0>
 cudaError_t ensure_smem_attr(size_t smem) {
     static std::atomic<long long> granted{-1};
     if (static_cast<long long>(smem) <= granted.load(std::memory_order_acquire)) return cudaSuccess;
-    const cudaError_t err = cudaFuncSetAttribute(decode_splitkv_kernel<D, GK, GV, HK, HS, WIN, P16, CODEC>,
+    const cudaError_t err = cudaFuncSetAttribute(decode_splitkv_kernel<D, GK, GV, HK, HS, WIN, P16, CODEC, MODE>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (err != cudaSuccess) cudaGetLastError();  // a refused size must not linger as the last error
     if (err == cudaSuccess) {
@@ -1240,7 +1311,7 @@ cudaError_t ensure_smem_attr(size_t smem) {
 
 // Resident CTAs per SM for a given shared-memory size, memoised per size (a few sizes
 // per shape are asked for; the slots fill once and later calls only read them).
-template <int D, int GK, int GV, int HK, int HS, bool WIN, bool P16, int CODEC = 0>
+template <int D, int GK, int GV, int HK, int HS, bool WIN, bool P16, int CODEC = 0, int MODE = 0>
 int occupancy(size_t smem) {
     constexpr int kSlots = 32;
     static std::atomic<long long> memo[kSlots];  // (smem << 8) | ctas, 0 = empty
@@ -1249,9 +1320,9 @@ int occupancy(size_t smem) {
         if (m == 0) break;
         if ((m >> 8) == static_cast<long long>(smem)) return static_cast<int>(m & 0xff);
     }
-    if (ensure_smem_attr<D, GK, GV, HK, HS, WIN, P16, CODEC>(smem) != cudaSuccess) return 0;
+    if (ensure_smem_attr<D, GK, GV, HK, HS, WIN, P16, CODEC, MODE>(smem) != cudaSuccess) return 0;
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_splitkv_kernel<D, GK, GV, HK, HS, WIN, P16, CODEC>, cta_warps<HS>() * 32,
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_splitkv_kernel<D, GK, GV, HK, HS, WIN, P16, CODEC, MODE>, cta_warps<HS>() * 32,
                                                       smem) != cudaSuccess)
         return 0;
     const long long entry = (static_cast<long long>(smem) << 8) | (n & 0xff);
@@ -1262,7 +1333,7 @@ int occupancy(size_t smem) {
     return n;
 }
 
-template <int D, int GK, int GV, int HK, int HS, bool WIN, bool P16, int CODEC = 0>
+template <int D, int GK, int GV, int HK, int HS, bool WIN, bool P16, int CODEC = 0, int MODE = 0>
 cudaError_t run(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream) {
     KParams p;
     p.pool = a.pool;
@@ -1297,6 +1368,8 @@ cudaError_t run(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream
         p.v_scales = 2 * a.L.P * D + 4 * a.L.P;
     }
     p.unit_bytes = p.block_bytes * HK;
+    p.scores = MODE == 1 ? reinterpret_cast<float*>(a.workspace + plan.ws_score_offset) : nullptr;
+    p.score_ld = a.max_len;
     p.stages = plan.stages;
     p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
     p.k_new = a.k_new;
@@ -1311,7 +1384,7 @@ cudaError_t run(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream
     while ((8 << p.lg_lk) < a.L.Gk) ++p.lg_lk;
     p.lg_lv = 0;
     while ((8 << p.lg_lv) < a.L.Gv) ++p.lg_lv;
-    cudaError_t err = ensure_smem_attr<D, GK, GV, HK, HS, WIN, P16, CODEC>(plan.smem_bytes);
+    cudaError_t err = ensure_smem_attr<D, GK, GV, HK, HS, WIN, P16, CODEC, MODE>(plan.smem_bytes);
     if (err != cudaSuccess) return err;
     // The launch may start before the kernel ahead of it on the stream finishes
     // (programmatic dependent launch); the kernel waits with griddepcontrol.wait before
@@ -1326,7 +1399,7 @@ cudaError_t run(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, decode_splitkv_kernel<D, GK, GV, HK, HS, WIN, P16, CODEC>, p);
+    err = cudaLaunchKernelEx(&cfg, decode_splitkv_kernel<D, GK, GV, HK, HS, WIN, P16, CODEC, MODE>, p);
     if (err != cudaSuccess) return err;
     return cudaGetLastError();
 }
@@ -1377,18 +1450,30 @@ int decode_occupancy_d256_win(const DecodeArgs& a, const DecodePlan& plan, size_
 #define KVQ_DECODE_RUN(D_, GK_, GV_, HK_, HS_, W_, P16_) decode::run<D_, GK_, GV_, HK_, HS_, W_, P16_>(a, plan, s)
 #define KVQ_DECODE_OCC(D_, GK_, GV_, HK_, HS_, W_, P16_) decode::occupancy<D_, GK_, GV_, HK_, HS_, W_, P16_>(smem)
 // One translation unit's entry points over the cases CASES(CALL) lists.
-#define KVQ_DECODE_TU(CASES, RUN_NAME, OCC_NAME)                                                     \
+#define KVQ_DECODE_TU(CASES, RUN_NAME, OCC_NAME) \
+    KVQ_DECODE_TU_OF(CASES, KVQ_DECODE_RUN, KVQ_DECODE_OCC, RUN_NAME, OCC_NAME)
+// The same for another mode of the kernel, RUN and OCC naming its instances.
+#define KVQ_DECODE_TU_OF(CASES, RUN, OCC, RUN_NAME, OCC_NAME)                                        \
     namespace kvq {                                                                                  \
     cudaError_t RUN_NAME(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t s) {              \
         switch (KVQ_DECODE_KEY(a.L.Gk, a.L.Gv, plan.hk, plan.hs, a.L.P == 16 ? 1 : 0)) {             \
-            CASES(KVQ_DECODE_RUN)                                                                    \
+            CASES(RUN)                                                                               \
             default: return cudaErrorInvalidValue;                                                   \
         }                                                                                            \
     }                                                                                                \
     int OCC_NAME(const DecodeArgs& a, const DecodePlan& plan, size_t smem) {                         \
         switch (KVQ_DECODE_KEY(a.L.Gk, a.L.Gv, plan.hk, plan.hs, a.L.P == 16 ? 1 : 0)) {             \
-            CASES(KVQ_DECODE_OCC)                                                                    \
+            CASES(OCC)                                                                               \
             default: return 0;                                                                       \
         }                                                                                            \
     }                                                                                                \
     }
+// Attention with weights (MODE 1) and differential attention (MODE 2, one-head units only).
+#define KVQ_WEIGHTS_RUN(D_, GK_, GV_, HK_, HS_, W_, P16_) decode::run<D_, GK_, GV_, HK_, HS_, W_, P16_, 0, 1>(a, plan, s)
+#define KVQ_WEIGHTS_OCC(D_, GK_, GV_, HK_, HS_, W_, P16_) decode::occupancy<D_, GK_, GV_, HK_, HS_, W_, P16_, 0, 1>(smem)
+#define KVQ_DIFF_RUN(D_, GK_, GV_, HK_, HS_, W_, P16_) decode::run<D_, GK_, GV_, HK_, HS_, W_, P16_, 0, 2>(a, plan, s)
+#define KVQ_DIFF_OCC(D_, GK_, GV_, HK_, HS_, W_, P16_) decode::occupancy<D_, GK_, GV_, HK_, HS_, W_, P16_, 0, 2>(smem)
+#define KVQ_DIFF_CASES(D_, GK_, GV_, W_, CALL)          \
+    KVQ_DECODE_CASES_1H(D_, GK_, GV_, W_, CALL)         \
+    case KVQ_DECODE_KEY(GK_, GV_, 1, 2, 1): return CALL(D_, GK_, GV_, 1, 2, W_, true);  \
+    case KVQ_DECODE_KEY(GK_, GV_, 1, 2, 0): return CALL(D_, GK_, GV_, 1, 2, W_, false);

@@ -39,6 +39,26 @@ int decode_occupancy_d64(const DecodeArgs& a, const DecodePlan& plan, size_t sme
 int decode_occupancy_d64_win(const DecodeArgs& a, const DecodePlan& plan, size_t smem);
 int decode_occupancy_d256(const DecodeArgs& a, const DecodePlan& plan, size_t smem);
 int decode_occupancy_d256_win(const DecodeArgs& a, const DecodePlan& plan, size_t smem);
+cudaError_t decode_run_wt_gk32(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t s);
+cudaError_t decode_run_wt_gk64(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t s);
+cudaError_t decode_run_wt_gk128(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t s);
+cudaError_t decode_run_wt_d64(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t s);
+cudaError_t decode_run_wt_d256(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t s);
+cudaError_t decode_run_wt_int8(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t s);
+cudaError_t decode_run_diff_gk32(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t s);
+cudaError_t decode_run_diff_gk64(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t s);
+cudaError_t decode_run_diff_d64(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t s);
+cudaError_t decode_run_diff_d256(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t s);
+int decode_occupancy_wt_gk32(const DecodeArgs& a, const DecodePlan& plan, size_t smem);
+int decode_occupancy_wt_gk64(const DecodeArgs& a, const DecodePlan& plan, size_t smem);
+int decode_occupancy_wt_gk128(const DecodeArgs& a, const DecodePlan& plan, size_t smem);
+int decode_occupancy_wt_d64(const DecodeArgs& a, const DecodePlan& plan, size_t smem);
+int decode_occupancy_wt_d256(const DecodeArgs& a, const DecodePlan& plan, size_t smem);
+int decode_occupancy_wt_int8(const DecodeArgs& a, const DecodePlan& plan, size_t smem);
+int decode_occupancy_diff_gk32(const DecodeArgs& a, const DecodePlan& plan, size_t smem);
+int decode_occupancy_diff_gk64(const DecodeArgs& a, const DecodePlan& plan, size_t smem);
+int decode_occupancy_diff_d64(const DecodeArgs& a, const DecodePlan& plan, size_t smem);
+int decode_occupancy_diff_d256(const DecodeArgs& a, const DecodePlan& plan, size_t smem);
 cudaError_t launch_combine(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t s);
 cudaError_t decode_run_fp16(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t s);
 int decode_occupancy_fp16(const DecodeArgs& a, const DecodePlan& plan, size_t smem);
@@ -52,6 +72,29 @@ constexpr int kMinUnitsPerWarp = 2;
 constexpr size_t kAlign = 256;
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// The weights and differential modes' entry points for a shape (nullptr: none).
+struct ModeEntry {
+    cudaError_t (*run)(const DecodeArgs&, const DecodePlan&, cudaStream_t);
+    int (*occ)(const DecodeArgs&, const DecodePlan&, size_t);
+};
+ModeEntry mode_entry(const DecodeArgs& a) {
+    if (a.mode == DecodeMode::kWeights) {
+        if (a.int8) return {decode_run_wt_int8, decode_occupancy_wt_int8};
+        if (a.fp16) return {nullptr, nullptr};
+        if (a.L.d == 64) return {decode_run_wt_d64, decode_occupancy_wt_d64};
+        if (a.L.d == 256) return {decode_run_wt_d256, decode_occupancy_wt_d256};
+        if (a.L.Gk == 32) return {decode_run_wt_gk32, decode_occupancy_wt_gk32};
+        if (a.L.Gk == 64) return {decode_run_wt_gk64, decode_occupancy_wt_gk64};
+        if (a.L.Gk == 128) return {decode_run_wt_gk128, decode_occupancy_wt_gk128};
+    } else if (a.mode == DecodeMode::kDiff && !a.fp16) {
+        if (a.L.d == 64) return {decode_run_diff_d64, decode_occupancy_diff_d64};
+        if (a.L.d == 256) return {decode_run_diff_d256, decode_occupancy_diff_d256};
+        if (a.L.Gk == 32) return {decode_run_diff_gk32, decode_occupancy_diff_gk32};
+        if (a.L.Gk == 64) return {decode_run_diff_gk64, decode_occupancy_diff_gk64};
+    }
+    return {nullptr, nullptr};
+}
 }  // namespace
 
 cudaError_t plan_decode(const DecodeArgs& a, DecodePlan* plan) {
@@ -85,6 +128,10 @@ cudaError_t plan_decode(const DecodeArgs& a, DecodePlan* plan) {
                kCtlBytes + round_up(static_cast<size_t>(3 * a.B + 1) * 4, 16);
     };
     auto occ_for = [&](size_t smem) {
+        if (a.mode != DecodeMode::kPlain) {
+            const ModeEntry e = mode_entry(a);
+            return e.occ ? e.occ(a, *plan, smem) : 0;
+        }
         if (a.int8) return decode_occupancy_int8(a, *plan, smem);
         if (a.fp16) return decode_occupancy_fp16(a, *plan, smem);
         const bool w = a.window > 0;
@@ -143,10 +190,21 @@ cudaError_t plan_decode(const DecodeArgs& a, DecodePlan* plan) {
     plan->ws_ml_offset = plan->ws_pre_offset + round_up((static_cast<size_t>(a.B) + 1) * sizeof(int32_t), kAlign);
     plan->ws_o_offset = plan->ws_ml_offset + round_up(pieces * ns * 2 * sizeof(float), kAlign);
     plan->ws_bytes = plan->ws_o_offset + round_up(pieces * ns * a.L.d * sizeof(float), kAlign);
+    plan->ws_stat_offset = plan->ws_score_offset = plan->ws_bytes;
+    if (a.mode == DecodeMode::kWeights) {
+        const size_t rows = static_cast<size_t>(a.B) * a.Hq;
+        plan->ws_score_offset += round_up(rows * 2 * sizeof(float), kAlign);
+        plan->ws_bytes = plan->ws_score_offset +
+                         round_up(rows * static_cast<size_t>(std::max(a.max_len, 0)) * sizeof(float), kAlign);
+    }
     return cudaSuccess;
 }
 
 cudaError_t launch_decode_grid(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream) {
+    if (a.mode != DecodeMode::kPlain) {
+        const ModeEntry e = mode_entry(a);
+        return e.run ? e.run(a, plan, stream) : cudaErrorInvalidValue;
+    }
     if (a.int8) return decode_run_int8(a, plan, stream);
     if (a.fp16) return decode_run_fp16(a, plan, stream);
     const bool w = a.window > 0;
@@ -163,7 +221,9 @@ cudaError_t launch_decode_grid(const DecodeArgs& a, const DecodePlan& plan, cuda
 cudaError_t launch_decode(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream) {
     cudaError_t e = launch_decode_grid(a, plan, stream);
     if (e != cudaSuccess) return e;
-    return launch_combine(a, plan, stream);
+    e = launch_combine(a, plan, stream);
+    if (e != cudaSuccess || a.mode != DecodeMode::kWeights) return e;
+    return launch_accumulate_weights(a, plan, stream);
 }
 
 }  // namespace kvq

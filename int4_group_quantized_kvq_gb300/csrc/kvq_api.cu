@@ -3,6 +3,7 @@
 // except a per-thread error string.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
@@ -60,6 +61,18 @@ int check_decode_shape(const kvq_cache_config* c, int r, int codec) {
     if (c->head_dim == 256 && c->group_k < 64)
         return fail(KVQ_EUNSUPPORTED, "head_dim 256: group_k %d < 64", c->group_k);
     return KVQ_OK;
+}
+
+// Differential attention: the halves of a K row are two keys, so a K group may not span both,
+// and a query head is two virtual heads of the decode kernel.
+int check_diff_shape(const kvq_cache_config* c, int r) {
+    if (2 * c->group_k > c->head_dim)
+        return fail(KVQ_EUNSUPPORTED, "differential attention: group_k %d > head_dim / 2 = %d", c->group_k, c->head_dim / 2);
+    const int most = c->head_dim == 256 ? 2 : 4;
+    if (r > most)
+        return fail(KVQ_EUNSUPPORTED, "differential attention at head_dim %d: query heads per KV head %d > %d", c->head_dim,
+                    r, most);
+    return check_decode_shape(c, 2 * r, 0);
 }
 
 int cuda_fail(cudaError_t e, const char* what) {
@@ -168,16 +181,20 @@ namespace {
 // codec: 0 the INT4 cache, 1 the FP16 cache, 2 the INT8 per-row cache, 3 the rotated
 // 4-bit cache
 size_t workspace_bytes_impl(const kvq_cache_config* cfg, int32_t batch, int32_t num_q_heads, int32_t max_len,
-                            int codec) {
+                            int codec, kvq::DecodeMode mode = kvq::DecodeMode::kPlain) {
+    const bool diff = mode == kvq::DecodeMode::kDiff;
     if (check_cfg(cfg) != KVQ_OK) return 0;
     if (batch < 1 || num_q_heads < 1 || max_len < 0 || num_q_heads % cfg->num_kv_heads) {
         fail(KVQ_EINVAL, "invalid batch / num_q_heads / max_len");
         return 0;
     }
-    if (check_decode_shape(cfg, num_q_heads / cfg->num_kv_heads, codec) != KVQ_OK) return 0;
+    if ((diff ? check_diff_shape(cfg, num_q_heads / cfg->num_kv_heads)
+              : check_decode_shape(cfg, num_q_heads / cfg->num_kv_heads, codec)) != KVQ_OK)
+        return 0;
     kvq::DecodeArgs a{};
+    a.mode = mode;
     a.B = batch;
-    a.Hq = num_q_heads;
+    a.Hq = diff ? 2 * num_q_heads : num_q_heads;
     a.Hkv = cfg->num_kv_heads;
     a.max_len = max_len;
     a.fp16 = codec != 0;
@@ -482,6 +499,286 @@ int kvq_decode_step_window(const kvq_cache_config* cfg, void* pool, const void* 
     return decode_step_impl(cfg, pool, k_new, v_new, append_pos, q, block_table, max_blocks, seq_lens, batch,
                             num_q_heads, max_len, softmax_scale, window, sinks, out, workspace, workspace_bytes,
                             stream);
+}
+
+namespace {
+// The decode calls with more than plain attention: with weights (x.weights set) and
+// differential ones (x.lambda set); k_new, v_new and append_pos NULL: no append.
+struct ModeArgs {
+    float* weights = nullptr;
+    int32_t weights_stride = 0;
+    float decay = 1.f;
+    const float* lambda = nullptr;
+    const float* norm_weight = nullptr;
+    float norm_eps = 0.f;
+    float out_scale = 1.f;
+};
+int decode_mode_impl(const char* name, kvq::DecodeMode mode, const ModeArgs& x, const kvq_cache_config* cfg, void* pool,
+                     bool append, const void* k_new, const void* v_new, const int32_t* append_pos, const void* q,
+                     const int32_t* block_table, int32_t max_blocks, const int32_t* seq_lens, int32_t batch,
+                     int32_t num_q_heads, int32_t max_len, float softmax_scale, float* out, void* workspace,
+                     size_t workspace_bytes, kvq_stream_t stream, int codec = 0) {
+    const bool diff = mode == kvq::DecodeMode::kDiff;
+    if (int e = check_cfg(cfg)) return e;
+    if (batch < 0 || num_q_heads < 1 || max_len < 0)
+        return fail(KVQ_EINVAL, "batch %d, num_q_heads %d, max_len %d", batch, num_q_heads, max_len);
+    if (num_q_heads % cfg->num_kv_heads)
+        return fail(KVQ_EINVAL, "num_q_heads %d not a multiple of num_kv_heads %d", num_q_heads, cfg->num_kv_heads);
+    const int r = num_q_heads / cfg->num_kv_heads;
+    if (r > 8) return fail(KVQ_EUNSUPPORTED, "query heads per KV head %d > 8", r);
+    if (int e = diff ? check_diff_shape(cfg, r) : check_decode_shape(cfg, r, codec)) return e;
+    if (batch > 4096) return fail(KVQ_EUNSUPPORTED, "batch %d > 4096", batch);
+    if (cfg->num_kv_heads > 65535) return fail(KVQ_EUNSUPPORTED, "num_kv_heads %d > 65535", cfg->num_kv_heads);
+    if (diff) {
+        if (x.norm_weight && !(x.norm_eps >= 0.f && std::isfinite(x.norm_eps)))
+            return fail(KVQ_EINVAL, "norm_eps must be finite and not negative");
+    } else {
+        if (!(x.decay >= 0.f && x.decay <= 1.f)) return fail(KVQ_EINVAL, "decay must be in [0, 1]");
+        if (x.weights_stride < max_len)
+            return fail(KVQ_EINVAL, "weights_stride %d < max_len %d", x.weights_stride, max_len);
+    }
+    if (batch == 0) return ok();
+    if (max_blocks < 1) return fail(KVQ_EINVAL, "max_blocks %d < 1", max_blocks);
+    if (!pool || !q || !block_table || !seq_lens || !out || !workspace || (append && (!k_new || !v_new || !append_pos)) ||
+        (diff ? !x.lambda : !x.weights))
+        return fail(KVQ_EINVAL, "NULL device pointer");
+    if (!aligned(pool, 16) || !aligned(q, 16) || !aligned(out, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) ||
+        !aligned(x.norm_weight, 16))
+        return fail(KVQ_EINVAL, "pool, q, out, the new rows and norm_weight must be 16-byte aligned");
+    if (!aligned(workspace, 256)) return fail(KVQ_EINVAL, "workspace must be 256-byte aligned");
+    if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(append_pos, 4) || !aligned(x.weights, 4) ||
+        !aligned(x.lambda, 4))
+        return fail(KVQ_EINVAL, "int32 and float arguments must be 4-byte aligned");
+    kvq::DecodeArgs a;
+    a.mode = mode;
+    a.weights = x.weights;
+    a.weights_ld = x.weights_stride;
+    a.decay = x.decay;
+    a.lambda = x.lambda;
+    a.norm_weight = x.norm_weight;
+    a.norm_eps = x.norm_eps;
+    a.out_scale = x.out_scale;
+    a.pool = static_cast<const uint8_t*>(pool);
+    a.q = static_cast<const __half*>(q);
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.out = out;
+    a.workspace = static_cast<uint8_t*>(workspace);
+    a.max_blocks = max_blocks;
+    a.B = batch;
+    a.Hq = diff ? 2 * num_q_heads : num_q_heads;
+    a.Hkv = cfg->num_kv_heads;
+    a.num_pages = cfg->num_pages;
+    a.max_len = max_len;
+    a.softmax_scale = softmax_scale;
+    a.fp16 = codec != 0;
+    a.int8 = codec == 2;
+    a.L = kvq::block_layout(*cfg);
+    if (append) {
+        a.k_new = static_cast<const __half*>(k_new);
+        a.v_new = static_cast<const __half*>(v_new);
+        a.append_pos = append_pos;
+        a.pool_w = static_cast<uint8_t*>(pool);
+    }
+    kvq::DecodePlan plan;
+    cudaError_t e = kvq::plan_decode(a, &plan);
+    if (e == cudaErrorInvalidValue) return fail(KVQ_EUNSUPPORTED, "no decode kernel for this shape");
+    if (e != cudaSuccess) return cuda_fail(e, name);
+    if (workspace_bytes < plan.ws_bytes)
+        return fail(KVQ_EWORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, plan.ws_bytes);
+    e = kvq::launch_decode(a, plan, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, name);
+    return ok();
+}
+}  // namespace
+
+size_t kvq_decode_weights_workspace_bytes(const kvq_cache_config* cfg, int32_t batch, int32_t num_q_heads,
+                                          int32_t max_len) {
+    return workspace_bytes_impl(cfg, batch, num_q_heads, max_len, 0, kvq::DecodeMode::kWeights);
+}
+
+size_t kvq_int8_decode_weights_workspace_bytes(const kvq_cache_config* cfg, int32_t batch, int32_t num_q_heads,
+                                               int32_t max_len) {
+    return workspace_bytes_impl(cfg, batch, num_q_heads, max_len, 2, kvq::DecodeMode::kWeights);
+}
+
+size_t kvq_diff_decode_workspace_bytes(const kvq_cache_config* cfg, int32_t batch, int32_t num_q_heads,
+                                       int32_t max_len) {
+    return workspace_bytes_impl(cfg, batch, num_q_heads, max_len, 0, kvq::DecodeMode::kDiff);
+}
+
+int kvq_decode_attention_weights(const kvq_cache_config* cfg, const void* pool, const void* q,
+                                 const int32_t* block_table, int32_t max_blocks, const int32_t* seq_lens,
+                                 int32_t batch, int32_t num_q_heads, int32_t max_len, float softmax_scale, float decay,
+                                 float* weights, int32_t weights_stride, float* out, void* workspace,
+                                 size_t workspace_bytes, kvq_stream_t stream) {
+    ModeArgs x;
+    x.weights = weights;
+    x.weights_stride = weights_stride;
+    x.decay = decay;
+    return decode_mode_impl("kvq_decode_attention_weights", kvq::DecodeMode::kWeights, x, cfg, const_cast<void*>(pool),
+                            false, nullptr, nullptr, nullptr, q, block_table, max_blocks, seq_lens, batch, num_q_heads,
+                            max_len, softmax_scale, out, workspace, workspace_bytes, stream);
+}
+
+int kvq_int8_decode_attention_weights(const kvq_cache_config* cfg, const void* pool8, const void* q,
+                                      const int32_t* block_table, int32_t max_blocks, const int32_t* seq_lens,
+                                      int32_t batch, int32_t num_q_heads, int32_t max_len, float softmax_scale,
+                                      float decay, float* weights, int32_t weights_stride, float* out, void* workspace,
+                                      size_t workspace_bytes, kvq_stream_t stream) {
+    ModeArgs x;
+    x.weights = weights;
+    x.weights_stride = weights_stride;
+    x.decay = decay;
+    return decode_mode_impl("kvq_int8_decode_attention_weights", kvq::DecodeMode::kWeights, x, cfg,
+                            const_cast<void*>(pool8), false, nullptr, nullptr, nullptr, q, block_table, max_blocks,
+                            seq_lens, batch, num_q_heads, max_len, softmax_scale, out, workspace, workspace_bytes,
+                            stream, 2);
+}
+
+int kvq_decode_step_weights(const kvq_cache_config* cfg, void* pool, const void* k_new, const void* v_new,
+                            const int32_t* append_pos, const void* q, const int32_t* block_table, int32_t max_blocks,
+                            const int32_t* seq_lens, int32_t batch, int32_t num_q_heads, int32_t max_len,
+                            float softmax_scale, float decay, float* weights, int32_t weights_stride, float* out,
+                            void* workspace, size_t workspace_bytes, kvq_stream_t stream) {
+    ModeArgs x;
+    x.weights = weights;
+    x.weights_stride = weights_stride;
+    x.decay = decay;
+    return decode_mode_impl("kvq_decode_step_weights", kvq::DecodeMode::kWeights, x, cfg, pool, true, k_new, v_new,
+                            append_pos, q, block_table, max_blocks, seq_lens, batch, num_q_heads, max_len,
+                            softmax_scale, out, workspace, workspace_bytes, stream);
+}
+
+int kvq_diff_decode_attention(const kvq_cache_config* cfg, const void* pool, const void* q, const int32_t* block_table,
+                              int32_t max_blocks, const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,
+                              int32_t max_len, float softmax_scale, const float* lambda, const float* norm_weight,
+                              float norm_eps, float out_scale, float* out, void* workspace, size_t workspace_bytes,
+                              kvq_stream_t stream) {
+    ModeArgs x;
+    x.lambda = lambda;
+    x.norm_weight = norm_weight;
+    x.norm_eps = norm_eps;
+    x.out_scale = out_scale;
+    return decode_mode_impl("kvq_diff_decode_attention", kvq::DecodeMode::kDiff, x, cfg, const_cast<void*>(pool), false,
+                            nullptr, nullptr, nullptr, q, block_table, max_blocks, seq_lens, batch, num_q_heads,
+                            max_len, softmax_scale, out, workspace, workspace_bytes, stream);
+}
+
+int kvq_diff_decode_step(const kvq_cache_config* cfg, void* pool, const void* k_new, const void* v_new,
+                         const int32_t* append_pos, const void* q, const int32_t* block_table, int32_t max_blocks,
+                         const int32_t* seq_lens, int32_t batch, int32_t num_q_heads, int32_t max_len,
+                         float softmax_scale, const float* lambda, const float* norm_weight, float norm_eps,
+                         float out_scale, float* out, void* workspace, size_t workspace_bytes, kvq_stream_t stream) {
+    ModeArgs x;
+    x.lambda = lambda;
+    x.norm_weight = norm_weight;
+    x.norm_eps = norm_eps;
+    x.out_scale = out_scale;
+    return decode_mode_impl("kvq_diff_decode_step", kvq::DecodeMode::kDiff, x, cfg, pool, true, k_new, v_new,
+                            append_pos, q, block_table, max_blocks, seq_lens, batch, num_q_heads, max_len,
+                            softmax_scale, out, workspace, workspace_bytes, stream);
+}
+
+int kvq_evict_select(const kvq_cache_config* cfg, const float* weights, int32_t weights_stride, const int32_t* seq_lens,
+                     int32_t batch, int32_t max_len, int32_t keep, int32_t sinks, int32_t recent, int32_t* kept,
+                     int32_t* new_lens, uint32_t* status, kvq_stream_t stream) {
+    if (int e = check_cfg(cfg)) return e;
+    if (batch < 0 || max_len < 0) return fail(KVQ_EINVAL, "batch %d / max_len %d negative", batch, max_len);
+    if (keep < 1 || sinks < 0 || recent < 0 || static_cast<int64_t>(sinks) + recent > keep)
+        return fail(KVQ_EINVAL, "keep %d, sinks %d, recent %d: keep must be at least 1 and sinks + recent", keep, sinks,
+                    recent);
+    if (weights_stride < max_len) return fail(KVQ_EINVAL, "weights_stride %d < max_len %d", weights_stride, max_len);
+    if (batch > 65535) return fail(KVQ_EUNSUPPORTED, "batch %d > 65535", batch);
+    if (cfg->num_kv_heads > 65535) return fail(KVQ_EUNSUPPORTED, "num_kv_heads %d > 65535", cfg->num_kv_heads);
+    if (batch == 0) return ok();
+    if (!weights || !seq_lens || !kept || !new_lens) return fail(KVQ_EINVAL, "NULL device pointer");
+    if (!aligned(weights, 4) || !aligned(seq_lens, 4) || !aligned(kept, 4) || !aligned(new_lens, 4) || !aligned(status, 4))
+        return fail(KVQ_EINVAL, "arguments must be 4-byte aligned");
+    kvq::EvictSelectArgs a;
+    a.weights = weights;
+    a.seq_lens = seq_lens;
+    a.kept = kept;
+    a.new_lens = new_lens;
+    a.status = status;
+    a.weights_ld = weights_stride;
+    a.max_len = max_len;
+    a.B = batch;
+    a.Hkv = cfg->num_kv_heads;
+    a.keep = keep;
+    a.sinks = sinks;
+    a.recent = recent;
+    cudaError_t e = kvq::launch_evict_select(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kvq_evict_select launch");
+    return ok();
+}
+
+namespace {
+int evict_compact_impl(const kvq_cache_config* cfg, void* pool, const int32_t* block_table, int32_t max_blocks,
+                       const int32_t* dst_table, int32_t dst_max_blocks, const int32_t* seq_lens, int32_t batch,
+                       const int32_t* kept, int32_t keep, float* weights, int32_t weights_stride, uint32_t* status,
+                       kvq_stream_t stream, bool int8) {
+    if (int e = check_cfg(cfg)) return e;
+    if (batch < 0) return fail(KVQ_EINVAL, "batch %d negative", batch);
+    if (keep < 1) return fail(KVQ_EINVAL, "keep %d < 1", keep);
+    if (batch > 65535) return fail(KVQ_EUNSUPPORTED, "batch %d > 65535", batch);
+    if (cfg->num_kv_heads > 65535) return fail(KVQ_EUNSUPPORTED, "num_kv_heads %d > 65535", cfg->num_kv_heads);
+    if (batch == 0) return ok();
+    if (max_blocks < 1 || dst_max_blocks < 1)
+        return fail(KVQ_EINVAL, "max_blocks %d / dst_max_blocks %d < 1", max_blocks, dst_max_blocks);
+    if (!pool || !block_table || !dst_table || !seq_lens || !kept) return fail(KVQ_EINVAL, "NULL device pointer");
+    if (weights && weights_stride < 0) return fail(KVQ_EINVAL, "weights_stride %d negative", weights_stride);
+    if (!aligned(pool, 16)) return fail(KVQ_EINVAL, "pool must be 16-byte aligned");
+    if (!aligned(block_table, 4) || !aligned(dst_table, 4) || !aligned(seq_lens, 4) || !aligned(kept, 4) ||
+        !aligned(weights, 4) || !aligned(status, 4))
+        return fail(KVQ_EINVAL, "arguments must be 4-byte aligned");
+    kvq::EvictCompactArgs a;
+    a.pool = static_cast<uint8_t*>(pool);
+    a.block_table = block_table;
+    a.dst_table = dst_table;
+    a.seq_lens = seq_lens;
+    a.kept = kept;
+    a.weights = weights;
+    a.status = status;
+    a.max_blocks = max_blocks;
+    a.dst_max_blocks = dst_max_blocks;
+    a.weights_ld = weights_stride;
+    a.B = batch;
+    a.Hkv = cfg->num_kv_heads;
+    a.num_pages = cfg->num_pages;
+    a.keep = keep;
+    a.lg_p = 0;
+    while ((1 << a.lg_p) < cfg->page_size) ++a.lg_p;
+    const int d = cfg->head_dim;
+    a.row_bytes[0] = a.row_bytes[1] = int8 ? d : d / 2;
+    a.row_bytes[2] = int8 ? 4 : 2 * (d / cfg->group_k);
+    a.row_bytes[3] = int8 ? 4 : 2 * (d / cfg->group_v);
+    int off = 0;
+    for (int i = 0; i < 4; ++i) {
+        a.sec_off[i] = off;
+        off += cfg->page_size * a.row_bytes[i];
+    }
+    a.block_bytes = (off + 15) / 16 * 16;
+    cudaError_t e = kvq::launch_evict_compact(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, int8 ? "kvq_int8_evict_compact launch" : "kvq_evict_compact launch");
+    return ok();
+}
+}  // namespace
+
+int kvq_evict_compact(const kvq_cache_config* cfg, void* pool, const int32_t* block_table, int32_t max_blocks,
+                      const int32_t* dst_table, int32_t dst_max_blocks, const int32_t* seq_lens, int32_t batch,
+                      const int32_t* kept, int32_t keep, float* weights, int32_t weights_stride, uint32_t* status,
+                      kvq_stream_t stream) {
+    return evict_compact_impl(cfg, pool, block_table, max_blocks, dst_table, dst_max_blocks, seq_lens, batch, kept,
+                              keep, weights, weights_stride, status, stream, false);
+}
+
+int kvq_int8_evict_compact(const kvq_cache_config* cfg, void* pool8, const int32_t* block_table, int32_t max_blocks,
+                           const int32_t* dst_table, int32_t dst_max_blocks, const int32_t* seq_lens, int32_t batch,
+                           const int32_t* kept, int32_t keep, float* weights, int32_t weights_stride, uint32_t* status,
+                           kvq_stream_t stream) {
+    return evict_compact_impl(cfg, pool8, block_table, max_blocks, dst_table, dst_max_blocks, seq_lens, batch, kept,
+                              keep, weights, weights_stride, status, stream, true);
 }
 
 int kvq_dequantize(const kvq_cache_config* cfg, const void* pool, const int32_t* block_table, int32_t max_blocks,

@@ -99,7 +99,16 @@ struct DecodePlan {
     size_t ws_pre_offset; // pages prefix per sequence, published by the decode grid
     size_t ws_ml_offset;  // (max, sum) of the warp partials
     size_t ws_o_offset;   // unnormalised outputs of the warp partials
+    size_t ws_stat_offset;  // attention with weights: (max, 1 / sum) of each output row
+    size_t ws_score_offset; // attention with weights: the scores of every attended position
     size_t ws_bytes;      // total workspace bytes
+};
+
+// What a decode call computes besides, or instead of, plain attention.
+enum class DecodeMode : int32_t {
+    kPlain = 0,
+    kWeights = 1,  // the positions' attention weights are added to an accumulator too
+    kDiff = 2,     // the difference of two softmax maps (Hq counts virtual heads, two per query head)
 };
 
 struct DecodeArgs {
@@ -140,6 +149,18 @@ struct DecodeArgs {
     // of that bound (each warp's first page copy announced 16 bytes larger than it is)
     uint64_t wait_ns = 0;
     bool withhold_first_copy = false;
+    DecodeMode mode = DecodeMode::kPlain;
+    // kWeights: weights[b][kv head][t] = decay * weights + the sum over the kv head's query
+    // heads of position t's softmax weight (decay 0: the sum alone); weights_ld floats per kv head
+    float* weights = nullptr;
+    int32_t weights_ld = 0;
+    float decay = 1.f;
+    // kDiff: out = out_scale * norm(map 1 - lambda[query head] * map 2), norm an RMS norm over
+    // head_dim with gain norm_weight and norm_eps (norm_weight nullptr: none)
+    const float* lambda = nullptr;
+    const float* norm_weight = nullptr;
+    float norm_eps = 0.f;
+    float out_scale = 1.f;
 };
 
 // The FP16 cache of the latency comparison: block (page, kv head) holds K rows P x d fp16,
@@ -189,5 +210,34 @@ cudaError_t launch_decode(const DecodeArgs& a, const DecodePlan& plan, cudaStrea
 cudaError_t launch_decode_grid(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream);
 cudaError_t launch_combine2(const DecodeArgs& a0, const DecodePlan& plan0, const DecodeArgs& a1,
                             const DecodePlan& plan1, cudaStream_t stream);
+// the accumulation of the positions' weights, behind the combine (kWeights)
+cudaError_t launch_accumulate_weights(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream);
+
+// Eviction from a cache (evict.cu).  Select: of each (sequence, kv head), the positions kept.
+struct EvictSelectArgs {
+    const float* weights;
+    const int32_t* seq_lens;
+    int32_t* kept;      // [B][Hkv][keep], ascending, -1 behind the kept ones
+    int32_t* new_lens;  // [B]
+    uint32_t* status;
+    int32_t weights_ld, max_len, B, Hkv, keep, sinks, recent;
+};
+cudaError_t launch_evict_select(const EvictSelectArgs& a, cudaStream_t stream);
+
+// Compact: the kept rows of each (sequence, kv head) to positions 0 .. of dst_table's pages.
+// A block's row of a token is four pieces (K and V codes, K and V scales), piece i of
+// row_bytes[i] bytes at sec_off[i] + slot * row_bytes[i].
+struct EvictCompactArgs {
+    uint8_t* pool;
+    const int32_t* block_table;
+    const int32_t* dst_table;
+    const int32_t* seq_lens;
+    const int32_t* kept;
+    float* weights;     // or nullptr
+    uint32_t* status;
+    int32_t max_blocks, dst_max_blocks, weights_ld, B, Hkv, num_pages, keep, lg_p, block_bytes;
+    int32_t sec_off[4], row_bytes[4];
+};
+cudaError_t launch_evict_compact(const EvictCompactArgs& a, cudaStream_t stream);
 
 }  // namespace kvq

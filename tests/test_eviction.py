@@ -1,0 +1,483 @@
+"""Decode attention with accumulated position weights, the selection by them and the compaction, against fp64 and
+plain numpy; the three together as a serving loop runs them."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from conftest import cuda_available
+from eviction_testlib import EPS32, Pool, errors, score_error, softmax64
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not cuda_available(), reason="needs a CUDA GPU")]
+
+
+def make_q(B, Hq, d, seed):
+    return torch.from_numpy(np.random.default_rng(seed).standard_normal((B, Hq, d)).astype(np.float16)).cuda()
+
+
+def call_weights(kvq, pool, x, q, decay, weights, max_len=None, ws=None, lens=None, stream=None):
+    cfg = pool.cfg(kvq)
+    B, Hq, d = q.shape
+    max_len = max(pool.lens) if max_len is None else max_len
+    new, fn = (kvq.new_int8_weights_workspace, kvq.kvq_int8_decode_attention_weights) if pool.codec == "int8" else \
+        (kvq.new_weights_workspace, kvq.kvq_decode_attention_weights)
+    ws = new(cfg, B, Hq, max_len) if ws is None else ws
+    out = torch.full((B, Hq, d), float("nan"), device="cuda")
+    fn(cfg, x, q, pool.table_gpu(), pool.lens_gpu() if lens is None else lens, max_len, d ** -0.5, decay, weights, out,
+       ws, stream=stream)
+    return out, ws
+
+
+def check_weights(pool, q, decay, before, out, after, lens=None):
+    """out and the updated weights against fp64, each within its derived bound."""
+    q = q.cpu().numpy().astype(np.float64)
+    out, before, after = out.cpu().numpy(), before.cpu().numpy(), after.cpu().numpy()
+    B, Hq, d = q.shape
+    r = Hq // pool.Hkv
+    for b, n in enumerate(pool.lens if lens is None else lens):
+        assert np.array_equal(after[b, :, n:], before[b, :, n:], equal_nan=True), "positions behind the sequence"
+        if n == 0:
+            assert not out[b].any()
+            continue
+        K, V = pool.values(b, n)
+        for h in range(pool.Hkv):
+            qh = q[b, h * r:(h + 1) * r]
+            z = qh @ K[h].T * d ** -0.5
+            dz = score_error(qh, K[h], d ** -0.5)
+            p = softmax64(z)
+            mass, slack = np.zeros(n), np.zeros(n)
+            for g in range(r):
+                tol, rel = errors(z[g], V[h], dz, pool.codec)
+                err = np.abs(out[b, h * r + g] - p[g] @ V[h])
+                assert err.max() <= tol, (b, h, g, err.max(), tol)
+                mass += p[g]
+                slack += rel * p[g]
+            want = mass if decay == 0.0 else decay * before[b, h, :n].astype(np.float64) + mass
+            slack += 2 * (r + 2) * EPS32 * np.abs(want) + 1e-37
+            assert (np.abs(after[b, h, :n] - want) <= slack).all(), (b, h, np.max(np.abs(after[b, h, :n] - want) / slack))
+
+
+@pytest.mark.parametrize("Hkv,r,d,P,Gk,Gv,lens", [
+    (8, 1, 128, 16, 64, 128, [513]),                     # four kv heads a unit
+    (3, 1, 128, 16, 64, 64, [1, 0, 16, 17, 700]),        # one head a unit, one query head
+    (4, 2, 128, 16, 32, 32, [15, 33, 1024]),
+    (2, 4, 128, 16, 128, 128, [2049, 5]),
+    (2, 5, 128, 16, 64, 128, [300, 31]),                 # two slots a thread, three of them empty
+    (1, 8, 128, 16, 64, 32, [777]),
+    (2, 3, 128, 32, 64, 128, [64, 65, 999]),
+    (4, 1, 128, 64, 64, 128, [63, 128, 1]),
+    (2, 8, 128, 64, 128, 64, [500, 0]),
+    (4, 1, 64, 16, 32, 64, [255, 1]),
+    (2, 7, 64, 32, 64, 32, [400]),
+    (2, 4, 256, 16, 64, 128, [300, 17]),
+    (3, 1, 256, 64, 128, 32, [129, 0, 640]),
+])
+@pytest.mark.parametrize("decay", [1.0, 0.0, 0.75])
+def test_attention_and_weights_match_fp64(kvq, Hkv, r, d, P, Gk, Gv, lens, decay):
+    pool = Pool("int4", Hkv, d, lens, P, Gk, Gv, seed=d + r)
+    q = make_q(len(lens), Hkv * r, d, 3)
+    before = torch.rand(len(lens), Hkv, max(lens) + 5, device="cuda")
+    if decay == 0.0:
+        before.fill_(float("nan"))  # not read
+    weights = before.clone()
+    out, ws = call_weights(kvq, pool, pool.gpu(), q, decay, weights)
+    assert kvq.kvq_read_status(ws) == 0
+    check_weights(pool, q, decay, before, out, weights)
+
+
+@pytest.mark.parametrize("Hkv,r,P,lens", [(4, 1, 16, [1, 0, 513]), (2, 4, 64, [64, 700]), (2, 6, 32, [33, 250]),
+                                          (1, 8, 16, [1025])])
+def test_int8_attention_and_weights_match_fp64(kvq, Hkv, r, P, lens):
+    pool = Pool("int8", Hkv, 128, lens, P, 128, 128, seed=r)
+    q = make_q(len(lens), Hkv * r, 128, 4)
+    before = torch.rand(len(lens), Hkv, max(lens), device="cuda")
+    weights = before.clone()
+    out, ws = call_weights(kvq, pool, pool.gpu(), q, 0.5, weights)
+    assert kvq.kvq_read_status(ws) == 0
+    check_weights(pool, q, 0.5, before, out, weights)
+
+
+def test_many_sequences_and_a_long_one(kvq):
+    # over 256 sequences the combine reads the published page prefix
+    lens = [(7 * b) % 40 for b in range(300)] + [9000]
+    pool = Pool("int4", 2, 64, lens, 16, 32, 64, seed=9)
+    q = make_q(len(lens), 4, 64, 5)
+    before = torch.rand(len(lens), 2, max(lens), device="cuda")
+    weights = before.clone()
+    out, ws = call_weights(kvq, pool, pool.gpu(), q, 1.0, weights)
+    assert kvq.kvq_read_status(ws) == 0
+    check_weights(pool, q, 1.0, before, out, weights)
+
+
+def test_equal_bits_on_repeat_side_stream_and_replayed_graph(kvq):
+    pool = Pool("int4", 4, 128, [600, 77], 16, 64, 128, seed=2)
+    x, q = pool.gpu(), make_q(2, 16, 128, 6)
+    start = torch.rand(2, 4, 600, device="cuda")
+    w0 = start.clone()
+    out0, ws = call_weights(kvq, pool, x, q, 0.5, w0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    w1 = start.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out1, _ = call_weights(kvq, pool, x, q, 0.5, w1)
+    side.synchronize()
+    assert torch.equal(out0, out1) and torch.equal(w0, w1)
+    w2, out2 = start.clone(), torch.empty_like(out0)
+    table, lens, cfg = pool.table_gpu(), pool.lens_gpu(), pool.cfg(kvq)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kvq.kvq_decode_attention_weights(cfg, x, q, table, lens, 600, 128 ** -0.5, 0.5, w2, out2, ws)
+    for _ in range(2):
+        w2.copy_(start)
+        graph.replay()
+        assert torch.equal(out0, out2) and torch.equal(w0, w2)
+
+
+def test_agrees_with_plain_decode_attention(kvq):
+    pool = Pool("int4", 8, 128, [1000, 3], 16, 64, 128, seed=12)
+    x, q, cfg = pool.gpu(), make_q(2, 8, 128, 7), pool.cfg(kvq)
+    out, _ = call_weights(kvq, pool, x, q, 1.0, torch.zeros(2, 8, 1000, device="cuda"))
+    plain = torch.empty_like(out)
+    kvq.kvq_decode_attention(cfg, x, q, pool.table_gpu(), pool.lens_gpu(), 1000, 128 ** -0.5, plain,
+                             kvq.new_workspace(cfg, 2, 8, 1000))
+    # both are within 2e-4 of the exact result, the framework's tolerance of decode attention
+    assert (out - plain).abs().max().item() <= 4e-4
+
+
+def test_step_is_append_then_attention(kvq):
+    for Hkv, r, d, P in ((8, 1, 128, 16), (2, 4, 128, 32), (2, 3, 256, 16)):
+        pool = Pool("int4", Hkv, d, [64, 17, 200], P, 64, 64, seed=21, spare=4, blocks=16)
+        x1, q, cfg = pool.gpu(), make_q(3, Hkv * r, d, 8), pool.cfg(kvq)
+        x2 = x1.clone()
+        k, v = make_q(3, Hkv, d, 30), make_q(3, Hkv, d, 31)
+        pos = torch.tensor([63, 16, -1], dtype=torch.int32, device="cuda")  # the last sequence appends nothing
+        start = torch.rand(3, Hkv, 200, device="cuda")
+        w1, w2 = start.clone(), start.clone()
+        ws = kvq.new_weights_workspace(cfg, 3, Hkv * r, 200)
+        o1, o2 = torch.empty_like(q, dtype=torch.float32), torch.empty_like(q, dtype=torch.float32)
+        kvq.kvq_decode_step_weights(cfg, x1, k, v, pos, q, pool.table_gpu(), pool.lens_gpu(), 200, d ** -0.5, 1.0, w1,
+                                    o1, ws)
+        for b in (0, 1):
+            kvq.kvq_quantize_append(cfg, x2, k[b:b + 1, None].contiguous(), v[b:b + 1, None].contiguous(),
+                                    pool.table_gpu()[b:b + 1].contiguous(), pos[b:b + 1].contiguous())
+        kvq.kvq_decode_attention_weights(cfg, x2, q, pool.table_gpu(), pool.lens_gpu(), 200, d ** -0.5, 1.0, w2, o2, ws)
+        assert kvq.kvq_read_status(ws) == 0
+        assert torch.equal(x1, x2) and torch.equal(o1, o2) and torch.equal(w1, w2)
+
+
+def test_bad_page_and_overlong_sequence_are_flagged(kvq):
+    pool = Pool("int4", 2, 128, [100, 50], 16, 64, 128, seed=5)
+    x, q, cfg = pool.gpu(), make_q(2, 4, 128, 9), pool.cfg(kvq)
+    table = pool.table_gpu()
+    table[0, 2] = pool.num_pages + 7
+    w, out = torch.zeros(2, 2, 100, device="cuda"), torch.empty(2, 4, 128, device="cuda")
+    ws = kvq.new_weights_workspace(cfg, 2, 4, 100)
+    kvq.kvq_decode_attention_weights(cfg, x, q, table, pool.lens_gpu(), 100, 0.1, 1.0, w, out, ws)
+    assert kvq.kvq_read_status(ws) == kvq.KVQ_FLAG_BAD_PAGE
+    # a length beyond max_len: cut to it and flagged, nothing behind max_len touched
+    start = torch.rand(2, 2, 100, device="cuda")
+    w = start.clone()
+    out, ws = call_weights(kvq, pool, x, q, 1.0, w, max_len=40)
+    assert kvq.kvq_read_status(ws) == kvq.KVQ_FLAG_BAD_POSITION
+    check_weights(pool, q, 1.0, start, out, w, lens=[40, 40])
+    # and one beyond the block table
+    lens = torch.tensor([100, 5000], dtype=torch.int32, device="cuda")
+    w = start.clone()
+    out, ws = call_weights(kvq, pool, x, q, 1.0, w, lens=lens)
+    assert kvq.kvq_read_status(ws) & kvq.KVQ_FLAG_BAD_POSITION
+
+
+# ---- select --------------------------------------------------------------------------------------
+
+def plain_select(w, lens, keep, sinks, recent):
+    B, H, _ = w.shape
+    kept = np.full((B, H, keep), -1, np.int32)
+    for b, n in enumerate(lens):
+        for h in range(H):
+            x = w[b, h, :n].astype(np.float64)
+            x[np.isnan(x)] = -np.inf
+            always = np.zeros(n, bool)
+            always[:sinks] = True
+            always[max(0, n - recent):] = True
+            order = np.lexsort((np.arange(n), -x, ~always))
+            pick = np.sort(order[:keep])
+            kept[b, h, :len(pick)] = pick
+    return kept, np.minimum(lens, keep).astype(np.int32)
+
+
+def run_select(kvq, w, lens, max_len, keep, sinks, recent, status=None):
+    B, H, _ = w.shape
+    kept = torch.full((B, H, keep), -7, dtype=torch.int32, device="cuda")
+    new = torch.full((B,), -7, dtype=torch.int32, device="cuda")
+    kvq.kvq_evict_select(kvq.config(H, 128), w, torch.tensor(lens, dtype=torch.int32, device="cuda"), max_len, keep,
+                         sinks, recent, kept, new, status=status)
+    return kept.cpu().numpy(), new.cpu().numpy()
+
+
+@pytest.mark.parametrize("lens,keep,sinks,recent", [
+    ([1, 0, 2, 5], 1, 0, 0), ([1, 0, 2, 5], 1, 1, 0), ([3, 9, 10, 11], 10, 4, 6), ([100, 7, 64], 64, 4, 16),
+    ([1025, 1024, 1023], 511, 0, 1), ([5000, 4097, 33], 33, 1, 31), ([20000, 3], 4096, 4, 512),
+    ([70001], 65000, 3, 100), ([131072], 1, 0, 0), ([300, 299], 400, 2, 2),
+])
+@pytest.mark.parametrize("kind", ["spread", "ties", "equal", "odd"])
+def test_select_matches_numpy(kvq, lens, keep, sinks, recent, kind):
+    rng = np.random.default_rng(keep + len(kind))
+    B, H, S = len(lens), 3, max(lens) + 3
+    w = np.exp(2 * rng.standard_normal((B, H, S))).astype(np.float32)
+    if kind == "ties":
+        w = np.floor(w)  # many zeros and small whole numbers
+    elif kind == "equal":
+        w[:] = 0.25
+    elif kind == "odd":
+        some = rng.integers(0, 12, w.shape)
+        for i, v in enumerate((np.nan, np.inf, -np.inf, 0.0, -0.0, -1.5, 1e-42, -1e-42)):
+            w[some == i] = v
+    got, new = run_select(kvq, torch.from_numpy(w).cuda(), lens, max(lens), keep, sinks, recent)
+    want, want_new = plain_select(w, lens, keep, sinks, recent)
+    assert np.array_equal(got, want) and np.array_equal(new, want_new)
+
+
+def test_select_over_long_and_negative_lengths(kvq):
+    w = torch.rand(2, 2, 50, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got, new = run_select(kvq, w, [60, -4], 40, 8, 1, 2, status=status)
+    want, want_new = plain_select(w.cpu().numpy(), [40, 0], 8, 1, 2)
+    assert np.array_equal(got, want) and np.array_equal(new, want_new)
+    assert status.item() == kvq.KVQ_FLAG_BAD_POSITION
+
+
+# ---- compact -------------------------------------------------------------------------------------
+
+def random_kept(pool, keep, seed):
+    rng = np.random.default_rng(seed)
+    kept = np.full((len(pool.lens), pool.Hkv, keep), -1, np.int32)
+    for b, n in enumerate(pool.lens):
+        for h in range(pool.Hkv):
+            m = min(n, keep)
+            kept[b, h, :m] = np.sort(rng.permutation(n)[:m])
+    return kept
+
+
+def plain_compact(pool, x, table, dst, kept, w):
+    """The pool and weights after the move, row by row from a copy of the pool."""
+    y, u = x.copy(), w.copy()
+    P = pool.P
+    for b, n in enumerate(pool.lens):
+        for h in range(pool.Hkv):
+            m = min(n, kept.shape[2])
+            for i in range(m):
+                t = kept[b, h, i]
+                for o, rb in zip(pool.off, pool.row):
+                    src = x[table[b, t // P], h, o + t % P * rb:o + (t % P + 1) * rb]
+                    y[dst[b, i // P], h, o + i % P * rb:o + (i % P + 1) * rb] = src
+            u[b, h, :n] = 0
+            u[b, h, :m] = w[b, h, kept[b, h, :m]]
+    return y, u
+
+
+def run_compact(kvq, pool, table, dst, kept, w, status=None):
+    x, u = pool.gpu(), torch.from_numpy(w.copy()).cuda()
+    t = torch.from_numpy(table).cuda()
+    fn = kvq.kvq_int8_evict_compact if pool.codec == "int8" else kvq.kvq_evict_compact
+    fn(pool.cfg(kvq), x, t, t if dst is table else torch.from_numpy(dst).cuda(), pool.lens_gpu(),
+       torch.from_numpy(kept).cuda(), u, status=status)
+    return x.cpu().numpy().reshape(pool.bytes.shape), u.cpu().numpy()
+
+
+@pytest.mark.parametrize("codec,Hkv,d,P,Gk,Gv,lens,keep", [
+    ("int4", 4, 128, 16, 64, 128, [600, 0, 1, 77], 64), ("int4", 3, 64, 32, 32, 64, [500, 33], 100),
+    ("int4", 1, 64, 16, 64, 64, [1000], 999), ("int4", 2, 256, 64, 128, 32, [700, 64], 65),
+    ("int4", 2, 128, 16, 32, 32, [4000], 1500), ("int4", 2, 128, 16, 64, 128, [40, 30], 200),
+    ("int8", 2, 128, 64, 128, 128, [300, 5], 77), ("int8", 3, 64, 16, 64, 64, [200], 1),
+    ("int8", 2, 256, 32, 128, 128, [3000, 100], 1111),
+])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_compact_moves_rows_bit_for_bit(kvq, codec, Hkv, d, P, Gk, Gv, lens, keep, in_place):
+    blocks = (keep + P - 1) // P
+    pool = Pool(codec, Hkv, d, lens, P, Gk, Gv, seed=keep, spare=1 if in_place else len(lens) * blocks)
+    dst = pool.table if in_place else pool.spare[:len(lens) * blocks].reshape(len(lens), blocks).copy()
+    kept = random_kept(pool, keep, 3)
+    w = np.random.default_rng(1).random((len(lens), Hkv, max(lens) + 2)).astype(np.float32)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x, u = run_compact(kvq, pool, pool.table, dst, kept, w, status)
+    want_x, want_u = plain_compact(pool, pool.bytes, pool.table, dst, kept, w)
+    assert status.item() == 0
+    assert np.array_equal(x, want_x) and np.array_equal(u, want_u)
+
+
+def test_compact_skips_and_flags_bad_positions_and_pages(kvq):
+    pool = Pool("int4", 2, 128, [100, 90], 16, 64, 128, seed=4)
+    kept = random_kept(pool, 40, 8)
+    w = np.random.default_rng(1).random((2, 2, 100)).astype(np.float32)
+    bad = kept.copy()
+    bad[0, 1, 39] = 100  # outside the sequence
+    bad[1, 0, 0] = -3
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x, _ = run_compact(kvq, pool, pool.table, pool.table, bad, w, status)
+    assert status.item() == kvq.KVQ_FLAG_BAD_POSITION
+    want, _ = plain_compact(pool, pool.bytes, pool.table, pool.table, kept, w)
+    ours = pool.table[0, :3], pool.table[1, :3]
+    for b, h, rows in ((0, 0, 40), (0, 1, 39), (1, 1, 40)):
+        for i in range(rows):
+            at = (ours[b][i // 16], h, i % 16)
+            assert pool.stored(x, *at) == pool.stored(want, *at)
+    # a bad source page and a bad destination page
+    status.zero_()
+    table = pool.table.copy()
+    table[0, 0] = -1
+    x, _ = run_compact(kvq, pool, table, table, kept, w, status)
+    assert status.item() == kvq.KVQ_FLAG_BAD_PAGE
+    untouched = np.setdiff1d(np.arange(pool.num_pages), np.concatenate([table[0, :3], table[1, :3]]))
+    assert np.array_equal(x[untouched], pool.bytes[untouched])
+    # a destination table that is too short for the rows kept
+    status.zero_()
+    x, _ = run_compact(kvq, pool, pool.table, np.ascontiguousarray(pool.table[:, :2]), kept, w, status)
+    assert status.item() == kvq.KVQ_FLAG_BAD_POSITION
+
+
+def test_compact_without_weights(kvq):
+    pool = Pool("int4", 2, 128, [100], 16, 64, 128, seed=4)
+    kept = random_kept(pool, 30, 8)
+    x, table = pool.gpu(), pool.table_gpu()
+    kvq.kvq_evict_compact(pool.cfg(kvq), x, table, table, pool.lens_gpu(), torch.from_numpy(kept).cuda())
+    want, _ = plain_compact(pool, pool.bytes, pool.table, pool.table, kept, np.zeros((1, 2, 100), np.float32))
+    assert np.array_equal(x.cpu().numpy().reshape(want.shape), want)
+
+
+# ---- together ------------------------------------------------------------------------------------
+
+def test_serving_loop_with_eviction(kvq):
+    """Append a history, decode with tracked weights, cut the cache, decode on: after the cut each KV head attends to
+    exactly the positions it kept, and the next tokens follow behind them."""
+    from int4_group_quantized_kvq_gb300.cache import PagedKVCache
+    B, H, r, d, P, n0 = 2, 3, 2, 128, 16, [150, 90]
+    blocks = 16
+    cfg = kvq.config(H, d, P, 64, 128, B * blocks)
+    table = torch.randperm(B * blocks, generator=torch.Generator().manual_seed(1)).to(torch.int32).view(B, blocks)
+    cache = PagedKVCache(cfg, table, H * r, blocks * P, track_weights=True, decay=0.9)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=gen, device="cuda").half()
+
+    for b in range(B):  # histories of different lengths
+        one = PagedKVCache(cfg, cache.block_table[b:b + 1], H * r, blocks * P, pool=cache.pool)
+        one.append(rand(1, n0[b], H, d), rand(1, n0[b], H, d), torch.zeros(1, dtype=torch.int32, device="cuda"))
+    lens = torch.tensor(n0, dtype=torch.int32, device="cuda")
+    out = torch.empty(B, H * r, d, device="cuda")
+
+    def step():
+        nonlocal lens
+        q, k, v = rand(B, H * r, d), rand(B, H, d), rand(B, H, d)
+        lens = lens + 1
+        cache.decode_step(q, k, v, lens - 1, lens, out)
+        return q
+
+    def rows(b, n):
+        k, v = torch.empty(n, H, d, device="cuda"), torch.empty(n, H, d, device="cuda")
+        kvq.kvq_dequantize(cfg, cache.pool, cache.block_table, b, 0, n, k, v)
+        return k.double().cpu().numpy().transpose(1, 0, 2), v.double().cpu().numpy().transpose(1, 0, 2)
+
+    for _ in range(5):
+        step()
+    keep, sinks, recent = 100, 4, 20
+    weights = cache.weights.cpu().numpy()
+    old = [rows(b, n0[b] + 5) for b in range(B)]
+    lens = cache.evict(lens, keep, sinks, recent)
+    assert lens.tolist() == [100, 95] and cache.flags() == 0
+    kept, _ = plain_select(weights, [n0[0] + 5, n0[1] + 5], keep, sinks, recent)
+    for b in range(B):
+        m = int(lens[b])
+        k, v = rows(b, m)
+        for h in range(H):
+            at = kept[b, h, :m]
+            assert np.array_equal(k[h], old[b][0][h][at]) and np.array_equal(v[h], old[b][1][h][at])
+            assert np.array_equal(cache.weights[b, h, :m].cpu().numpy(), weights[b, h, at])
+            assert not cache.weights[b, h, m:].any()
+    q = step()
+    for b in range(B):
+        K, V = rows(b, int(lens[b]))
+        for hq in range(H * r):
+            z = q[b, hq].double().cpu().numpy() @ K[hq // r].T * d ** -0.5
+            dz = score_error(q[b, hq:hq + 1].double().cpu().numpy(), K[hq // r], d ** -0.5)
+            tol, _ = errors(z, V[hq // r], dz)
+            assert np.abs(out[b, hq].cpu().numpy() - softmax64(z) @ V[hq // r]).max() <= tol
+    # a second cut, into other pages
+    other = torch.arange(B * blocks, dtype=torch.int32, device="cuda")
+    used = torch.cat([cache.block_table[b, :(int(lens[b]) + P - 1) // P] for b in range(B)])
+    spare = other[~torch.isin(other, used)][:B * 4].view(B, 4).contiguous()
+    before = [rows(b, int(lens[b])) for b in range(B)]
+    weights = cache.weights.cpu().numpy()
+    old_lens = lens.tolist()
+    lens = cache.evict(lens, 60, 4, 20, dst_table=spare)
+    kept, _ = plain_select(weights, old_lens, 60, 4, 20)
+    assert lens.tolist() == [60, 60] and cache.flags() == 0
+    for b in range(B):
+        k, v = rows(b, 60)
+        for h in range(H):
+            assert np.array_equal(k[h], before[b][0][h][kept[b, h]]) and np.array_equal(v[h], before[b][1][h][kept[b, h]])
+
+
+def test_decode_right_behind_select_and_compact(kvq):
+    """Decode attention launched directly behind the two kernels reads the lengths and rows that they wrote."""
+    pool = Pool("int4", 2, 128, [3000, 2500], 16, 64, 128, seed=6)
+    cfg, q = pool.cfg(kvq), make_q(2, 8, 128, 2)
+    w = torch.rand(2, 2, 3000, device="cuda")
+    kept = torch.empty(2, 2, 700, dtype=torch.int32, device="cuda")
+    ws, table, lens = kvq.new_workspace(cfg, 2, 8, 3000), pool.table_gpu(), pool.lens_gpu()
+
+    def go(wait):
+        x, new = pool.gpu(), torch.full((2,), 3000, dtype=torch.int32, device="cuda")
+        out, u = torch.zeros(2, 8, 128, device="cuda"), w.clone()
+        torch.cuda.synchronize()
+        kvq.kvq_evict_select(cfg, u, lens, 3000, 700, 4, 64, kept, new)
+        if wait:
+            torch.cuda.synchronize()
+        kvq.kvq_evict_compact(cfg, x, table, table, lens, kept, u)
+        if wait:
+            torch.cuda.synchronize()
+        kvq.kvq_decode_attention(cfg, x, q, table, new, 3000, 128 ** -0.5, out, ws)
+        return out.clone()
+
+    want = go(True)
+    for _ in range(5):
+        assert torch.equal(go(False), want)
+
+
+def test_tensors_are_checked(kvq):
+    pool = Pool("int4", 2, 128, [100, 50], 16, 64, 128, seed=5)
+    x, q, cfg = pool.gpu(), make_q(2, 4, 128, 9), pool.cfg(kvq)
+    table, lens = pool.table_gpu(), pool.lens_gpu()
+    w, out = torch.zeros(2, 2, 100, device="cuda"), torch.empty(2, 4, 128, device="cuda")
+    ws = kvq.new_weights_workspace(cfg, 2, 4, 100)
+
+    def call(**k):
+        a = dict(cfg=cfg, pool=x, q=q, block_table=table, seq_lens=lens, max_len=100, softmax_scale=0.1, decay=1.0,
+                 weights=w, out=out, workspace=ws)
+        a.update(k)
+        kvq.kvq_decode_attention_weights(**a)
+
+    call()
+    for bad in (dict(q=q.float()), dict(q=q[:1]), dict(q=q.cpu()), dict(pool=x[:-1]), dict(block_table=table[:1]),
+                dict(seq_lens=lens.long()), dict(seq_lens=lens[:1]), dict(weights=w[:, :1].contiguous()),
+                dict(weights=w.transpose(0, 1)), dict(weights=w.double()), dict(out=out[:1]), dict(out=None),
+                dict(weights=w[:, :, ::2])):
+        with pytest.raises(ValueError):
+            call(**bad)
+    for bad in (dict(decay=1.5), dict(decay=float("nan")), dict(max_len=101), dict(max_len=-1),
+                dict(workspace=ws[:256].clone())):
+        with pytest.raises(kvq.KvqError):
+            call(**bad)
+    kept, new = torch.empty(2, 2, 10, dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    for bad in (dict(kept=kept[:1]), dict(kept=kept.long()), dict(new_lens=new[:1]), dict(weights=w[:1]),
+                dict(status=torch.zeros(1))):
+        a = dict(cfg=cfg, weights=w, seq_lens=lens, max_len=100, keep=10, sinks=1, recent=1, kept=kept, new_lens=new)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            kvq.kvq_evict_select(**a)
+    with pytest.raises(ValueError):
+        kvq.kvq_evict_compact(cfg, x, table, table, lens, kept[:1].contiguous(), w)
+    with pytest.raises(ValueError):
+        kvq.kvq_evict_compact(cfg, x, table, table[:1].contiguous(), lens, kept, w)
