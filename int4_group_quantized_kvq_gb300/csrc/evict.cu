@@ -1,8 +1,13 @@
 // evict.cu -- eviction from a paged cache by accumulated attention weight: the choice of the
 // positions each kv head keeps, and the move of their rows to the front of the sequence.
 //
-// Neither kernel signals its dependents early: the lengths and the pool they write may be the
-// inputs that the next decode call reads before its own wait.
+// Both kernels give one thread-block cluster to each (sequence, kv head), so that a few long
+// sequences still fill the device, and are launched while the kernel ahead on the stream
+// finishes (programmatic dependent launch, with a wait before anything is read).  Neither
+// signals its own dependents early: the lengths and the pool they write may be the inputs
+// that the next decode call reads before its own wait.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "kvq_device.cuh"
@@ -10,6 +15,8 @@
 
 namespace kvq {
 namespace {
+
+namespace cg = cooperative_groups;
 
 // ---------------------------------------------------------------------------
 // Select
@@ -21,152 +28,284 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 
-constexpr int kSelectThreads = 1024;
+constexpr int kSelKeys = 8;     // keys a thread holds in registers; a longer slice is read again in each pass
+constexpr int kSelBins = 2048;  // 11 bits a pass
 
-// One CTA per (sequence, kv head).  Of n > keep positions the first `sinks` and the last
-// `recent` stay, and of those between, the k = keep - sinks - recent of largest weight: a
-// radix descent over the keys finds the k-th largest T and how many keys equal to T belong
-// (four passes, a histogram of 8 bits each), then one pass in position order writes the
-// positions with key > T and the first ones with key == T.
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(EvictSelectArgs p) {
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t s_prefix, s_left;
-    __shared__ uint32_t s_gt[32], s_eq[32];
-    const int h = blockIdx.x % p.Hkv, b = blockIdx.x / p.Hkv;
+// Of n > keep positions the first `sinks` and the last `recent` stay, and of the ones between
+// (lo .. hi - 1) the k = keep - sinks - recent of largest weight.  A radix descent finds the
+// k-th largest key T and how many keys equal to T belong: three passes over digits of 11, 11
+// and 10 bits from the top, each a histogram of the keys that share the digits found so far.
+// Then the positions with key > T and the first ones with key == T are written in order.
+//
+// The cluster's CTAs take equal slices of the positions.  A thread holds its keys in registers,
+// read once; the CTAs' histograms are added through distributed shared memory by every CTA for
+// itself, one cluster barrier per pass (a histogram per pass, so none is cleared while another
+// CTA may read it).  The first digit spans sign, exponent and two mantissa bits: accumulated
+// weights lie within a few binades, and with 8 bits almost all keys of a warp would meet in
+// one or two counters.  Bound by latency (the chain of barriers and passes, not the bytes):
+// 4 x 8 rows of 32768 positions 69.7 us with one CTA a row and four 8-bit passes over the L2.
+template <int CL, int T>
+__global__ void __launch_bounds__(T) evict_select_kernel(EvictSelectArgs p) {
+    constexpr int kWarps = T / 32;
+    static_assert(kWarps >= kSelKeys && kWarps <= 32, "a warp per round of keys, a lane per warp");
+    __shared__ __align__(16) uint32_t hist[3][kSelBins];
+    __shared__ uint32_t s_warp[32], s_digit, s_left;
+    __shared__ uint32_t s_gt[kSelKeys][kWarps], s_eq[kSelKeys][kWarps];
+    __shared__ uint32_t s_cta[2];
+    const int rank = CL > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
+    const int row = blockIdx.x / CL;
+    const int h = row % p.Hkv, b = row / p.Hkv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < 3 * kSelBins; i += T) hist[0][i] = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     int n = p.seq_lens[b];
     n = n < 0 ? 0 : n;
+    const bool first = h == 0 && rank == 0 && tid == 0;
     if (n > p.max_len) {
         n = p.max_len;
-        if (h == 0 && tid == 0) raise_flag(p.status, KVQ_FLAG_BAD_POSITION);
+        if (first) raise_flag(p.status, KVQ_FLAG_BAD_POSITION);
     }
-    if (h == 0 && tid == 0) p.new_lens[b] = min(n, p.keep);
-    const float* w = p.weights + static_cast<long long>(blockIdx.x) * p.weights_ld;
-    int32_t* kept = p.kept + static_cast<long long>(blockIdx.x) * p.keep;
-    if (n <= p.keep) {
-        for (int i = tid; i < p.keep; i += kSelectThreads) kept[i] = i < n ? i : -1;
+    const float* w = p.weights + static_cast<long long>(row) * p.weights_ld;
+    int32_t* kept = p.kept + static_cast<long long>(row) * p.keep;
+    const int all = CL * T, me = rank * T + tid;
+    if (n <= p.keep) {  // (the whole cluster)
+        for (int i = me; i < p.keep; i += all) kept[i] = i < n ? i : -1;
+        if (first) p.new_lens[b] = n;
         return;
     }
+    if (first) p.new_lens[b] = p.keep;
     const int lo = p.sinks, hi = n - p.recent;
     const int k = p.keep - p.sinks - p.recent;
-    for (int i = tid; i < lo; i += kSelectThreads) kept[i] = i;
-    for (int i = tid; i < p.recent; i += kSelectThreads) kept[lo + k + i] = hi + i;
-    if (k == 0) return;
+    for (int i = me; i < lo; i += all) kept[i] = i;
+    for (int i = me; i < p.recent; i += all) kept[lo + k + i] = hi + i;
+    if (k == 0) return;  // (the whole cluster)
+
+    const int slice = (hi - lo + CL - 1) / CL;
+    const int t0 = min(lo + rank * slice, hi), t1 = min(t0 + slice, hi);
+    uint32_t key[kSelKeys];
+#pragma unroll
+    for (int j = 0; j < kSelKeys; ++j) {
+        const int t = t0 + j * T + tid;
+        key[j] = t < t1 ? weight_key(w[t]) : 0u;
+    }
+    const int rest = t0 + kSelKeys * T + tid;  // this thread's first position past its registers
+    __syncthreads();
 
     uint32_t prefix = 0, left = static_cast<uint32_t>(k);
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        const uint32_t above = shift == 24 ? 0u : ~0u << (shift + 8);
-        for (int t = lo + tid; t < hi; t += kSelectThreads) {
-            const uint32_t key = weight_key(w[t]);
-            if ((key & above) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
-        }
-        __syncthreads();
-        if (warp == 0) {
-            // lane l holds digits 255 - 8 l down to 248 - 8 l; the digit where the count from
-            // the top reaches `left`
-            uint32_t c[8], sum = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum += c[j] = hist[255 - 8 * lane - j];
-            uint32_t before = sum;
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+        const int bins = pass == 2 ? 1024 : kSelBins;
+        const int above = pass == 0 ? 32 : (pass == 1 ? 21 : 10);  // bits above this pass's digit start here
+        auto count = [&](uint32_t x) {
+            if (pass == 0 || (x >> above) == (prefix >> above)) atomicAdd(&hist[pass][(x >> shift) & (bins - 1)], 1u);
+        };
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xffffffffu, before, off);
-                if (lane >= off) before += y;
-            }
-            before -= sum;
-            if (before < left && before + sum >= left) {
-                uint32_t need = left - before;
+        for (int j = 0; j < kSelKeys; ++j)
+            if (t0 + j * T + tid < t1) count(key[j]);
+        for (int t = rest; t < t1; t += T) count(weight_key(w[t]));
+        if (CL > 1) cg::this_cluster().sync();
+        else __syncthreads();
+        // thread i holds NB bins, the i-th NB from the top; c[j] counts the j-th of them from the top
+        constexpr int NB = kSelBins / T;
+        uint32_t c[NB], sum = 0;
+        const int top = bins - 1 - tid * NB;  // (the last pass has half as many bins: the upper threads none)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (need > 0 && need <= c[j]) {
-                        s_prefix = prefix | (static_cast<uint32_t>(255 - 8 * lane - j) << shift);
-                        s_left = need;
-                        need = 0;
-                    } else if (need > 0) {
-                        need -= c[j];
-                    }
+        for (int j = 0; j < NB; ++j) c[j] = 0;
+        if (top > 0) {
+#pragma unroll
+            for (int r = 0; r < CL; ++r) {
+                const uint32_t* from = CL > 1 ? cg::this_cluster().map_shared_rank(&hist[pass][0], r) : &hist[pass][0];
+#pragma unroll
+                for (int j = 0; j < NB; j += 2) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(from + top - j - 1);
+                    c[j] += v.y;
+                    c[j + 1] += v.x;
                 }
             }
+#pragma unroll
+            for (int j = 0; j < NB; ++j) sum += c[j];
+        }
+        uint32_t before = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, before, off);
+            if (lane >= off) before += y;
+        }
+        if (lane == 31) s_warp[warp] = before;
+        before -= sum;
+        __syncthreads();
+        uint32_t x = lane < kWarps ? s_warp[lane] : 0u;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        if (warp > 0) before += __shfl_sync(0xffffffffu, x, warp - 1);
+        if (before < left && before + sum >= left) {  // exactly one thread
+            uint32_t need = left - before;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                if (need > 0 && need <= c[j]) {
+                    s_digit = static_cast<uint32_t>(top - j);
+                    s_left = need;
+                }
+                need = need > c[j] ? need - c[j] : 0;
+            }
         }
         __syncthreads();
-        prefix = s_prefix;
+        prefix |= s_digit << shift;
         left = s_left;
     }
 
-    // in position order: keys above T, and the first `left` equal to it
-    uint32_t gt_done = 0, eq_done = 0;
-    for (int t0 = lo; t0 < hi; t0 += kSelectThreads) {
-        const int t = t0 + tid;
-        const uint32_t key = t < hi ? weight_key(w[t]) : 0u;
-        const bool gt = t < hi && key > prefix, eq = t < hi && key == prefix;
-        const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
+    // how many of this CTA's keys are above T and equal to it, and the same of the CTAs before it
+    uint32_t g = 0, e = 0;
+#pragma unroll
+    for (int j = 0; j < kSelKeys; ++j) {
+        const bool in = t0 + j * T + tid < t1;
+        const uint32_t mg = __ballot_sync(0xffffffffu, in && key[j] > prefix);
+        const uint32_t m2 = __ballot_sync(0xffffffffu, in && key[j] == prefix);
         if (lane == 0) {
-            s_gt[warp] = __popc(mg);
-            s_eq[warp] = __popc(me);
+            s_gt[j][warp] = __popc(mg);
+            s_eq[j][warp] = __popc(m2);
+        }
+    }
+    uint32_t done_gt = 0, done_eq = 0;  // before this CTA, then before the chunk being written
+    if (CL > 1) {
+        for (int t = rest; t < t1; t += T) {
+            const uint32_t x = weight_key(w[t]);
+            g += x > prefix;
+            e += x == prefix;
+        }
+        if (tid < 2) s_cta[tid] = 0;
+        __syncthreads();
+        if (warp < kSelKeys && lane < kWarps) {
+            g += s_gt[warp][lane];
+            e += s_eq[warp][lane];
+        }
+        g = __reduce_add_sync(0xffffffffu, g);
+        e = __reduce_add_sync(0xffffffffu, e);
+        if (lane == 0 && (g | e) != 0) {
+            atomicAdd(&s_cta[0], g);
+            atomicAdd(&s_cta[1], e);
+        }
+        cg::this_cluster().sync();
+        for (int r = 0; r < rank; ++r) {
+            const uint32_t* from = cg::this_cluster().map_shared_rank(&s_cta[0], r);
+            done_gt += from[0];
+            done_eq += from[1];
+        }
+    }
+    // in position order, kSelKeys rounds of T positions at a time: an entry of
+    // s_gt, s_eq counts a warp's 32 positions, entries ordered as positions are
+    for (int c0 = t0;; c0 += kSelKeys * T) {
+        uint32_t mg[kSelKeys], m2[kSelKeys];
+#pragma unroll
+        for (int j = 0; j < kSelKeys; ++j) {
+            const int t = c0 + j * T + tid;
+            const uint32_t x = c0 == t0 ? key[j] : (t < t1 ? weight_key(w[t]) : 0u);
+            mg[j] = __ballot_sync(0xffffffffu, t < t1 && x > prefix);
+            m2[j] = __ballot_sync(0xffffffffu, t < t1 && x == prefix);
+            if (c0 != t0 && lane == 0) {
+                s_gt[j][warp] = __popc(mg[j]);
+                s_eq[j][warp] = __popc(m2[j]);
+            }
         }
         __syncthreads();
-        uint32_t bg = gt_done, be = eq_done, ag = 0, ae = 0;
-        for (int v = 0; v < 32; ++v) {
-            const uint32_t xg = s_gt[v], xe = s_eq[v];
-            if (v < warp) {
-                bg += xg;
-                be += xe;
+        // warps 0 .. kSelKeys - 1 turn a round's counts into sums before each warp, lane order;
+        // the rounds' totals are added by every thread below
+        if (warp < kSelKeys) {
+            uint32_t a = lane < kWarps ? s_gt[warp][lane] : 0u, q = lane < kWarps ? s_eq[warp][lane] : 0u;
+            const uint32_t a0 = a, q0 = q;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t ya = __shfl_up_sync(0xffffffffu, a, off), yq = __shfl_up_sync(0xffffffffu, q, off);
+                if (lane >= off) {
+                    a += ya;
+                    q += yq;
+                }
             }
-            ag += xg;
-            ae += xe;
+            if (lane < kWarps) {
+                s_gt[warp][lane] = a - a0;
+                s_eq[warp][lane] = q - q0;
+            }
+            if (lane == 31) {
+                s_warp[warp] = a;
+                s_warp[kSelKeys + warp] = q;
+            }
         }
+        __syncthreads();
         const uint32_t below = (1u << lane) - 1u;
-        bg += __popc(mg & below);
-        be += __popc(me & below);
-        if (gt || (eq && be < left)) kept[lo + bg + min(be, left)] = t;
-        gt_done += ag;
-        eq_done += ae;
+#pragma unroll
+        for (int j = 0; j < kSelKeys; ++j) {
+            const bool gt = (mg[j] >> lane) & 1u, eq = (m2[j] >> lane) & 1u;
+            const uint32_t bg = done_gt + s_gt[j][warp] + __popc(mg[j] & below);
+            const uint32_t be = done_eq + s_eq[j][warp] + __popc(m2[j] & below);
+            if (gt || (eq && be < left)) kept[lo + bg + min(be, left)] = c0 + j * T + tid;
+            done_gt += s_warp[j];
+            done_eq += s_warp[kSelKeys + j];
+        }
+        if (c0 + kSelKeys * T >= t1) break;
         __syncthreads();
     }
+    if (CL > 1) cg::this_cluster().sync();  // no CTA leaves while another may read its shared memory
 }
 
 // ---------------------------------------------------------------------------
 // Compact
 // ---------------------------------------------------------------------------
-constexpr int kCompactThreads = 512;
-constexpr int kCompactRows = 64;  // rows moved together
+constexpr int kCmpThreads = 256;
+constexpr int kCmpWords = 16;      // 16-byte code words a thread holds between its loads and its stores
+constexpr int kCmpMaxRows = 1024;  // rows a CTA moves in a round (head_dim 64, the shortest rows)
+constexpr int kCmpScaleBytes = 8192;
 
-// One CTA per (sequence, kv head), kCompactRows rows at a time through shared memory: every
-// row of the chunk is read before one is written.  The kept positions ascend, so kept[i] >= i
-// and a chunk's writes (positions below its own end) never reach a row that a later chunk
-// still has to read; in place and other pages are one path.
-__global__ void __launch_bounds__(kCompactThreads) evict_compact_kernel(EvictCompactArgs p) {
-    extern __shared__ __align__(16) uint8_t buf[];
-    __shared__ long long s_src[kCompactRows], s_dst[kCompactRows];
-    __shared__ float s_w[kCompactRows];
-    const int h = blockIdx.x % p.Hkv, b = blockIdx.x / p.Hkv;
+// A cluster moves the kept rows of its (sequence, kv head) in rounds: every CTA loads its share
+// of the round's rows (codes into registers, scales into shared memory), the cluster's barrier,
+// then the stores.  Kept positions ascend, so kept[i] >= i: a round's stores reach only
+// positions below the round's end, no row that a later round has to read, and within the round
+// everything has been read; the move in place needs no second buffer, and the move into other
+// pages is the same path.  The bound is HBM: every row is read once (its scales with the
+// sectors of their neighbours, 32 bytes for a few) and written once, in whole lines.  One CTA
+// per (sequence, kv head) with chunks of 64 rows through shared memory took 173 us for
+// 8 x 32 x 2048 rows of 134 bytes (its chain of small round trips), and 332 us for 4 x 8 x 4095
+// of 264.
+__global__ void __launch_bounds__(kCmpThreads, 2) evict_compact_kernel(EvictCompactArgs p, int32_t rows_cta, int32_t lg_w) {
+    __shared__ long long s_src[kCmpMaxRows], s_dst[kCmpMaxRows];  // a row's block * 64 + slot; -1: stays
+    __shared__ __align__(16) uint8_t s_scale[kCmpScaleBytes];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = static_cast<int>(cluster.block_rank()), size = static_cast<int>(cluster.num_blocks());
+    const int row = blockIdx.x / size;
+    const int h = row % p.Hkv, b = row / p.Hkv;
     const int tid = threadIdx.x;
     const int P = 1 << p.lg_p;
-    const bool first = h == 0 && tid == 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     long long n = p.seq_lens[b];
     n = n < 0 ? 0 : n;
     long long cap = static_cast<long long>(p.max_blocks) << p.lg_p;
     if (p.weights && cap > p.weights_ld) cap = p.weights_ld;
     if (n > cap) {
         n = cap;
-        if (first) raise_flag(p.status, KVQ_FLAG_BAD_POSITION);
+        if (h == 0 && rank == 0 && tid == 0) raise_flag(p.status, KVQ_FLAG_BAD_POSITION);
     }
     const int m = static_cast<int>(min(n, static_cast<long long>(p.keep)));
-    const int32_t* kept = p.kept + static_cast<long long>(blockIdx.x) * p.keep;
-    float* w = p.weights ? p.weights + static_cast<long long>(blockIdx.x) * p.weights_ld : nullptr;
+    const int32_t* kept = p.kept + static_cast<long long>(row) * p.keep;
+    float* w = p.weights ? p.weights + static_cast<long long>(row) * p.weights_ld : nullptr;
     const int32_t* table = p.block_table + static_cast<long long>(b) * p.max_blocks;
     const int32_t* dtable = p.dst_table + static_cast<long long>(b) * p.dst_max_blocks;
-    int row = 0;
-    for (int i = 0; i < 4; ++i) row += p.row_bytes[i];
-    const int row_pad = (row + 15) & ~15;
-    for (int i0 = 0; i0 < m; i0 += kCompactRows) {
-        const int rows = min(kCompactRows, m - i0);
-        if (tid < rows) {
-            const int i = i0 + tid, t = kept[i];
+    // a row's code words: 2^lg_w of K, then as many of V
+    const int word_mask = (2 << lg_w) - 1;
+    const int scale_row = p.row_bytes[2] + p.row_bytes[3];
+    for (long long base = 0; base < m; base += static_cast<long long>(size) * rows_cta) {
+        const long long r0 = base + static_cast<long long>(rank) * rows_cta;
+        const int rows = r0 < m ? static_cast<int>(min(static_cast<long long>(rows_cta), m - r0)) : 0;
+        float wv[kCmpMaxRows / kCmpThreads];
+#pragma unroll
+        for (int k = 0; k < kCmpMaxRows / kCmpThreads; ++k) {
+            const int rr = tid + k * kCmpThreads;
+            wv[k] = 0.f;
+            if (rr >= rows) continue;
+            const int i = static_cast<int>(r0) + rr, t = kept[i];
             long long src = -1, dst = -1;
-            float x = 0.f;
             if (t < 0 || t >= n || (i >> p.lg_p) >= p.dst_max_blocks) {
                 raise_flag(p.status, KVQ_FLAG_BAD_POSITION);
             } else {
@@ -177,62 +316,114 @@ __global__ void __launch_bounds__(kCompactThreads) evict_compact_kernel(EvictCom
                     src = ((static_cast<long long>(sp) * p.Hkv + h) << 6) | (t & (P - 1));
                     dst = ((static_cast<long long>(dp) * p.Hkv + h) << 6) | (i & (P - 1));
                 }
-                if (w) x = w[t];
+                if (w) wv[k] = w[t];
             }
-            s_src[tid] = src;
-            s_dst[tid] = dst;
-            s_w[tid] = x;
+            s_src[rr] = src;
+            s_dst[rr] = dst;
         }
         __syncthreads();
-        // codes in 16-byte words, scales in 2-byte ones
-        for (int pass = 0; pass < 2; ++pass) {
-            int off = 0;
-            for (int sec = 0; sec < 4; ++sec) {
-                const int rb = p.row_bytes[sec];
-                const int unit = sec < 2 ? 16 : 2;
-                const int words = rb / unit;
-                for (int e = tid; e < rows * words; e += kCompactThreads) {
-                    const int rr = e / words, ww = e - rr * words;
-                    const long long at = pass == 0 ? s_src[rr] : s_dst[rr];
-                    if (at < 0) continue;
-                    uint8_t* g = p.pool + (at >> 6) * p.block_bytes + p.sec_off[sec] + (at & 63) * rb + ww * unit;
-                    uint8_t* s = buf + rr * row_pad + off + ww * unit;
-                    if (unit == 16) {
-                        if (pass == 0) *reinterpret_cast<uint4*>(s) = *reinterpret_cast<const uint4*>(g);
-                        else *reinterpret_cast<uint4*>(g) = *reinterpret_cast<const uint4*>(s);
-                    } else {
-                        if (pass == 0) *reinterpret_cast<uint16_t*>(s) = *reinterpret_cast<const uint16_t*>(g);
-                        else *reinterpret_cast<uint16_t*>(g) = *reinterpret_cast<const uint16_t*>(s);
-                    }
-                }
-                off += rb;
-            }
-            if (pass == 0) __syncthreads();
+        auto address = [&](long long at, int off, int bytes) {
+            return p.pool + (at >> 6) * p.block_bytes + off + (at & 63) * bytes;
+        };
+        // word ww of a row: K's first (section 0 at offset 0), then V's
+        auto word = [&](long long at, int ww) {
+            return reinterpret_cast<uint4*>(address(at, (ww >> lg_w) * p.sec_off[1], p.row_bytes[0]) +
+                                            ((ww & (word_mask >> 1)) << 4));
+        };
+        uint4 v[kCmpWords];
+#pragma unroll
+        for (int k = 0; k < kCmpWords; ++k) {
+            const int e = tid + k * kCmpThreads, rr = e >> (lg_w + 1), ww = e & word_mask;
+            v[k] = make_uint4(0, 0, 0, 0);
+            if (rr < rows && s_src[rr] >= 0)
+                v[k] = *word(s_src[rr], ww);
         }
-        if (w && tid < rows) w[i0 + tid] = s_w[tid];
+        // scales: 2-byte pieces, a row's K scales then its V scales in s_scale
+        auto scales = [&](bool load) {
+#pragma unroll
+            for (int sec = 2; sec < 4; ++sec) {
+                const int words = p.row_bytes[sec] >> 1, lg = 31 - __clz(words);  // a power of two
+                for (int e = tid; e < rows * words; e += kCmpThreads) {
+                    const int rr = e >> lg, ww = e & (words - 1);
+                    const long long at = load ? s_src[rr] : s_dst[rr];
+                    if (at < 0) continue;
+                    uint16_t* g = reinterpret_cast<uint16_t*>(address(at, p.sec_off[sec], p.row_bytes[sec])) + ww;
+                    uint16_t* s = reinterpret_cast<uint16_t*>(s_scale + rr * scale_row + (sec == 3 ? p.row_bytes[2] : 0)) + ww;
+                    if (load) *s = *g;
+                    else *g = *s;
+                }
+            }
+        };
+        scales(true);
+        cluster.sync();  // the round has been read
+#pragma unroll
+        for (int k = 0; k < kCmpWords; ++k) {
+            const int e = tid + k * kCmpThreads, rr = e >> (lg_w + 1), ww = e & word_mask;
+            if (rr < rows && s_dst[rr] >= 0)
+                *word(s_dst[rr], ww) = v[k];
+        }
+        scales(false);
+        if (w) {
+#pragma unroll
+            for (int k = 0; k < kCmpMaxRows / kCmpThreads; ++k)
+                if (tid + k * kCmpThreads < rows) w[r0 + tid + k * kCmpThreads] = wv[k];
+        }
         __syncthreads();
     }
+    // (every round's weights have been read: the last barrier)
     if (w)
-        for (long long i = m + tid; i < n; i += kCompactThreads) w[i] = 0.f;
+        for (long long i = m + rank * kCmpThreads + tid; i < n; i += static_cast<long long>(size) * kCmpThreads) w[i] = 0.f;
+}
+
+// A launch of `rows` clusters of `cluster` CTAs behind the kernel ahead on the stream.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), long long rows, int cluster, int threads, cudaStream_t stream,
+                            Args... args) {
+    if (rows * cluster > 0x7fffffffLL) return cudaErrorInvalidValue;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_evict_select(const EvictSelectArgs& a, cudaStream_t stream) {
     const long long rows = static_cast<long long>(a.B) * a.Hkv;
-    if (rows > 0x7fffffffLL) return cudaErrorInvalidValue;
-    evict_select_kernel<<<static_cast<unsigned>(rows), kSelectThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    // Rows that 256 threads hold in registers take a CTA of that size, several to an SM.
+    // Longer ones take CTAs of 1024 threads, one to an SM, and the largest cluster that leaves
+    // them all resident at once (152 SMs) and every thread a position.
+    if (a.max_len <= 256 * kSelKeys) return launch_clusters(evict_select_kernel<1, 256>, rows, 1, 256, stream, a);
+    int cl = 1;
+    while (cl < 8 && rows * cl * 2 <= 152 && a.max_len > 1024 * cl) cl *= 2;
+    switch (cl) {
+        case 1: return launch_clusters(evict_select_kernel<1, 1024>, rows, 1, 1024, stream, a);
+        case 2: return launch_clusters(evict_select_kernel<2, 1024>, rows, 2, 1024, stream, a);
+        case 4: return launch_clusters(evict_select_kernel<4, 1024>, rows, 4, 1024, stream, a);
+        default: return launch_clusters(evict_select_kernel<8, 1024>, rows, 8, 1024, stream, a);
+    }
 }
 
 cudaError_t launch_evict_compact(const EvictCompactArgs& a, cudaStream_t stream) {
-    const long long rows = static_cast<long long>(a.B) * a.Hkv;
-    if (rows > 0x7fffffffLL) return cudaErrorInvalidValue;
-    int row = 0;
-    for (int i = 0; i < 4; ++i) row += a.row_bytes[i];
-    const int smem = kCompactRows * ((row + 15) & ~15);
-    evict_compact_kernel<<<static_cast<unsigned>(rows), kCompactThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    // rows a CTA holds: its threads' code words over a row's (K and V, 16 bytes each)
+    int lg_w = 0;
+    while ((16 << lg_w) < a.row_bytes[0]) ++lg_w;
+    int rows_cta = (kCmpThreads * kCmpWords) >> (lg_w + 1);
+    rows_cta = std::min({rows_cta, kCmpMaxRows, kCmpScaleBytes / (a.row_bytes[2] + a.row_bytes[3])});
+    // the smallest cluster that moves a sequence in one round, at most 8 (the portable size)
+    int cl = 1;
+    while (cl < 8 && cl * rows_cta < a.keep) cl *= 2;
+    return launch_clusters(evict_compact_kernel, static_cast<long long>(a.B) * a.Hkv, cl, kCmpThreads, stream, a,
+                           static_cast<int32_t>(rows_cta), static_cast<int32_t>(lg_w));
 }
 
 }  // namespace kvq
