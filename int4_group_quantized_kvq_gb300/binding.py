@@ -616,6 +616,7 @@ def kvq_test_decode_wait_timeout(cfg: CacheConfig, pool: torch.Tensor, q: torch.
 # ---------------------------------------------------------------------------
 # Attention weights of cached positions, eviction by them, differential attention
 # ---------------------------------------------------------------------------
+# These calls run once per layer and token, so their checks are kept to a few attribute reads per tensor.
 def _shaped(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: int) -> int:
     """The address of a contiguous CUDA tensor on device `dev` (the current one), of that dtype and shape."""
     try:
@@ -623,44 +624,47 @@ def _shaped(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: i
             return t.data_ptr()
     except AttributeError:
         pass
-    p = _dev(t, name, dtype)
+    _dev(t, name, dtype)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
-def _bytes(t: torch.Tensor, name: str, at_least: int, dev: int) -> int:
-    p = _shaped(t, name, torch.uint8, getattr(t, "shape", ()), dev)
-    if t.numel() < at_least:
-        raise ValueError(f"{name} has {t.numel()} bytes, needs {at_least}")
+def _dims(t: torch.Tensor, name: str, n: int) -> tuple:
+    """The shape of a tensor of n dimensions."""
+    shape = getattr(t, "shape", ())
+    if len(shape) != n:
+        raise ValueError(f"{name} must be a CUDA tensor of {n} dimensions")
+    return shape
+
+
+def _bytes(t: torch.Tensor, name: str, dev: int) -> tuple[int, int]:
+    """Address and size of a uint8 buffer."""
+    return _shaped(t, name, torch.uint8, getattr(t, "shape", ()), dev), t.numel()
+
+
+def _pool_at(t: torch.Tensor, need: int, dev: int) -> int:
+    p, n = _bytes(t, "pool", dev)
+    if need == 0:
+        raise KvqError(KVQ_EINVAL, kvq_last_error())
+    if n < need:
+        raise ValueError(f"pool has {n} bytes, needs {need}")
     return p
-
-
-def _table(t: torch.Tensor, name: str, batch: int, dev: int) -> tuple[int, int]:
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise ValueError(f"{name} must be an int32 CUDA tensor [batch, blocks]")
-    blocks = t.shape[1]
-    return _shaped(t, name, torch.int32, (batch, blocks), dev), blocks
-
-
-def _batch_heads(q: torch.Tensor, d: int) -> tuple[int, int]:
-    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[2] != d:
-        raise ValueError("q must be a CUDA tensor [batch, num_q_heads, head_dim]")
-    return q.shape[0], q.shape[1]
-
-
-def _weights_of(weights: torch.Tensor, batch: int, heads: int, dev: int) -> tuple[int, int]:
-    if not isinstance(weights, torch.Tensor) or weights.dim() != 3:
-        raise ValueError("weights must be an fp32 CUDA tensor [batch, num_kv_heads, positions]")
-    stride = weights.shape[2]
-    return _shaped(weights, "weights", torch.float32, (batch, heads, stride), dev), stride
 
 
 def _new_rows(t: torch.Tensor, name: str, batch: int, cfg: CacheConfig, dev: int) -> int:
     shape = (batch, cfg.num_kv_heads, cfg.head_dim)
-    if isinstance(t, torch.Tensor) and t.dim() == 4:
+    if len(getattr(t, "shape", ())) == 4:
         shape = (batch, 1, cfg.num_kv_heads, cfg.head_dim)
     return _shaped(t, name, torch.float16, shape, dev)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, dev: int) -> int:
+    """_stream, without building a Stream object for the current one where torch can name it directly."""
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def _own_status(status: torch.Tensor | None, dev: int) -> int | None:
@@ -710,14 +714,31 @@ def new_diff_workspace(cfg: CacheConfig, batch: int, num_q_heads: int, max_len: 
                        device=device)
 
 
-def _decode_head(cfg, pool, pool_bytes, q, block_table, seq_lens, out, dev):
+def _decode_head(cfg, pool, pool_need, q, block_table, seq_lens, out, dev):
     """(batch, query heads), the C arguments pool, q, block_table, max_blocks, seq_lens, and out."""
-    d = cfg.head_dim
-    B, Hq = _batch_heads(q, d)
-    bt, blocks = _table(block_table, "block_table", B, dev)
-    return B, Hq, (_bytes(pool, "pool", pool_bytes, dev), _shaped(q, "q", torch.float16, (B, Hq, d), dev), bt, blocks,
+    shape = _dims(q, "q", 3)
+    B, Hq, d = shape
+    if d != cfg.head_dim:
+        raise ValueError(f"q must be [batch, num_q_heads, {cfg.head_dim}], got {list(shape)}")
+    blocks = _dims(block_table, "block_table", 2)[1]
+    return B, Hq, (_pool_at(pool, pool_need, dev), _shaped(q, "q", torch.float16, shape, dev),
+                   _shaped(block_table, "block_table", torch.int32, (B, blocks), dev), blocks,
                    _shaped(seq_lens, "seq_lens", torch.int32, (B,), dev)), \
-        _shaped(out, "out", torch.float32, (B, Hq, d), dev)
+        _shaped(out, "out", torch.float32, shape, dev)
+
+
+def _weights_call(fn, pool_bytes, cfg, pool, q, block_table, seq_lens, max_len, softmax_scale, decay, weights, out,
+                  workspace, stream, step=None) -> None:
+    dev = torch.cuda.current_device()
+    ref = C.byref(cfg)
+    B, Hq, (pp, qp, bt, blocks, sl), op = _decode_head(cfg, pool, pool_bytes(ref), q, block_table, seq_lens, out, dev)
+    stride = _dims(weights, "weights", 3)[2]
+    w = _shaped(weights, "weights", torch.float32, (B, cfg.num_kv_heads, stride), dev)
+    new = () if step is None else (_new_rows(step[0], "k_new", B, cfg, dev), _new_rows(step[1], "v_new", B, cfg, dev),
+                                   _shaped(step[2], "append_pos", torch.int32, (B,), dev))
+    rc = fn(ref, pp, *new, qp, bt, blocks, sl, B, Hq, int(max_len), float(softmax_scale), float(decay), w, stride, op,
+            *_bytes(workspace, "workspace", dev), _stream_on(stream, dev))
+    _check(rc)
 
 
 def kvq_decode_attention_weights(cfg: CacheConfig, pool: torch.Tensor, q: torch.Tensor, block_table: torch.Tensor,
@@ -727,14 +748,9 @@ def kvq_decode_attention_weights(cfg: CacheConfig, pool: torch.Tensor, q: torch.
     """kvq_decode_attention that also updates weights (fp32 [B, Hkv, >= max_len]):
     weights[b, h, t] = decay * weights[b, h, t] + the sum of position t's softmax weight over KV head h's query
     heads, for t < seq_lens[b] (decay 0: the sum alone).  workspace as from new_weights_workspace."""
-    dev = torch.cuda.current_device()
-    B, Hq, (pp, qp, bt, blocks, sl), op = _decode_head(cfg, pool, kvq_pool_bytes(cfg), q, block_table, seq_lens, out,
-                                                       dev)
-    w, stride = _weights_of(weights, B, cfg.num_kv_heads, dev)
-    rc = lib().kvq_decode_attention_weights(
-        C.byref(cfg), pp, qp, bt, blocks, sl, B, Hq, int(max_len), float(softmax_scale), float(decay), w, stride,
-        op, _bytes(workspace, "workspace", 0, dev), workspace.numel(), _stream(stream))
-    _check(rc)
+    L = lib()
+    _weights_call(L.kvq_decode_attention_weights, L.kvq_pool_bytes, cfg, pool, q, block_table, seq_lens, max_len,
+                  softmax_scale, decay, weights, out, workspace, stream)
 
 
 def kvq_int8_decode_attention_weights(cfg: CacheConfig, pool: torch.Tensor, q: torch.Tensor,
@@ -742,14 +758,9 @@ def kvq_int8_decode_attention_weights(cfg: CacheConfig, pool: torch.Tensor, q: t
                                       softmax_scale: float, decay: float, weights: torch.Tensor, out: torch.Tensor,
                                       workspace: torch.Tensor, stream=None) -> None:
     """kvq_decode_attention_weights over the INT8 per-row cache (workspace: new_int8_weights_workspace)."""
-    dev = torch.cuda.current_device()
-    B, Hq, (pp, qp, bt, blocks, sl), op = _decode_head(cfg, pool, kvq_int8_pool_bytes(cfg), q, block_table, seq_lens,
-                                                       out, dev)
-    w, stride = _weights_of(weights, B, cfg.num_kv_heads, dev)
-    rc = lib().kvq_int8_decode_attention_weights(
-        C.byref(cfg), pp, qp, bt, blocks, sl, B, Hq, int(max_len), float(softmax_scale), float(decay), w, stride,
-        op, _bytes(workspace, "workspace", 0, dev), workspace.numel(), _stream(stream))
-    _check(rc)
+    L = lib()
+    _weights_call(L.kvq_int8_decode_attention_weights, L.kvq_int8_pool_bytes, cfg, pool, q, block_table, seq_lens,
+                  max_len, softmax_scale, decay, weights, out, workspace, stream)
 
 
 def kvq_decode_step_weights(cfg: CacheConfig, pool: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -758,16 +769,9 @@ def kvq_decode_step_weights(cfg: CacheConfig, pool: torch.Tensor, k_new: torch.T
                             weights: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """kvq_decode_step (append k_new, v_new at append_pos, then attend) that also updates weights, as
     kvq_decode_attention_weights."""
-    dev = torch.cuda.current_device()
-    B, Hq, (pp, qp, bt, blocks, sl), op = _decode_head(cfg, pool, kvq_pool_bytes(cfg), q, block_table, seq_lens, out,
-                                                       dev)
-    w, stride = _weights_of(weights, B, cfg.num_kv_heads, dev)
-    rc = lib().kvq_decode_step_weights(
-        C.byref(cfg), pp, _new_rows(k_new, "k_new", B, cfg, dev), _new_rows(v_new, "v_new", B, cfg, dev),
-        _shaped(append_pos, "append_pos", torch.int32, (B,), dev), qp, bt, blocks, sl, B, Hq, int(max_len),
-        float(softmax_scale), float(decay), w, stride, op, _bytes(workspace, "workspace", 0, dev), workspace.numel(),
-        _stream(stream))
-    _check(rc)
+    L = lib()
+    _weights_call(L.kvq_decode_step_weights, L.kvq_pool_bytes, cfg, pool, q, block_table, seq_lens, max_len,
+                  softmax_scale, decay, weights, out, workspace, stream, (k_new, v_new, append_pos))
 
 
 def kvq_evict_select(cfg: CacheConfig, weights: torch.Tensor, seq_lens: torch.Tensor, max_len: int, keep: int,
@@ -776,28 +780,32 @@ def kvq_evict_select(cfg: CacheConfig, weights: torch.Tensor, seq_lens: torch.Te
     """The positions each KV head keeps of a cache cut to `keep`: the first `sinks`, the last `recent`, the rest by
     largest weight (ties: the lower position).  weights fp32 [B, Hkv, >= max_len]; seq_lens int32 [B];
     kept int32 [B, Hkv, keep] (ascending, then -1) and new_lens int32 [B] are written."""
-    if not isinstance(seq_lens, torch.Tensor) or seq_lens.dim() != 1:
-        raise ValueError("seq_lens must be an int32 CUDA tensor [batch]")
-    B, H, dev = int(seq_lens.shape[0]), cfg.num_kv_heads, torch.cuda.current_device()
-    w, stride = _weights_of(weights, B, H, dev)
-    rc = lib().kvq_evict_select(
-        C.byref(cfg), w, stride, _shaped(seq_lens, "seq_lens", torch.int32, (B,), dev), B, int(max_len), int(keep), int(sinks),
-        int(recent), _shaped(kept, "kept", torch.int32, (B, H, int(keep)), dev),
-        _shaped(new_lens, "new_lens", torch.int32, (B,), dev), _own_status(status, dev), _stream(stream))
+    L = lib()
+    B, H, dev = _dims(seq_lens, "seq_lens", 1)[0], cfg.num_kv_heads, torch.cuda.current_device()
+    stride = _dims(weights, "weights", 3)[2]
+    rc = L.kvq_evict_select(
+        C.byref(cfg), _shaped(weights, "weights", torch.float32, (B, H, stride), dev), stride,
+        _shaped(seq_lens, "seq_lens", torch.int32, (B,), dev), B, int(max_len), int(keep), int(sinks), int(recent),
+        _shaped(kept, "kept", torch.int32, (B, H, keep), dev), _shaped(new_lens, "new_lens", torch.int32, (B,), dev),
+        _own_status(status, dev), _stream_on(stream, dev))
     _check(rc)
 
 
-def _evict_compact(fn, cfg, pool, pool_bytes, block_table, dst_table, seq_lens, kept, weights, status, stream) -> None:
-    if not isinstance(kept, torch.Tensor) or kept.dim() != 3:
-        raise ValueError("kept must be an int32 CUDA tensor [batch, num_kv_heads, keep]")
-    B, H, keep = int(kept.shape[0]), cfg.num_kv_heads, int(kept.shape[2])
+def _compact_call(fn, pool_bytes, cfg, pool, block_table, dst_table, seq_lens, kept, weights, status, stream) -> None:
     dev = torch.cuda.current_device()
-    bt, blocks = _table(block_table, "block_table", B, dev)
-    dt, dblocks = _table(dst_table, "dst_table", B, dev)
-    w, stride = (None, 0) if weights is None else _weights_of(weights, B, H, dev)
-    rc = fn(C.byref(cfg), _bytes(pool, "pool", pool_bytes, dev), bt, blocks, dt, dblocks,
-            _shaped(seq_lens, "seq_lens", torch.int32, (B,), dev), B, _shaped(kept, "kept", torch.int32, (B, H, keep), dev), keep, w,
-            stride, _own_status(status, dev), _stream(stream))
+    ref = C.byref(cfg)
+    shape = _dims(kept, "kept", 3)
+    B, H, keep = shape
+    if H != cfg.num_kv_heads:
+        raise ValueError(f"kept must be [batch, {cfg.num_kv_heads}, keep], got {list(shape)}")
+    blocks, dst_blocks = _dims(block_table, "block_table", 2)[1], _dims(dst_table, "dst_table", 2)[1]
+    stride = 0 if weights is None else _dims(weights, "weights", 3)[2]
+    rc = fn(ref, _pool_at(pool, pool_bytes(ref), dev),
+            _shaped(block_table, "block_table", torch.int32, (B, blocks), dev), blocks,
+            _shaped(dst_table, "dst_table", torch.int32, (B, dst_blocks), dev), dst_blocks,
+            _shaped(seq_lens, "seq_lens", torch.int32, (B,), dev), B, _shaped(kept, "kept", torch.int32, shape, dev),
+            keep, None if weights is None else _shaped(weights, "weights", torch.float32, (B, H, stride), dev), stride,
+            _own_status(status, dev), _stream_on(stream, dev))
     _check(rc)
 
 
@@ -806,16 +814,33 @@ def kvq_evict_compact(cfg: CacheConfig, pool: torch.Tensor, block_table: torch.T
                       status: torch.Tensor | None = None, stream=None) -> None:
     """Rows kept[b, h, i] (as from kvq_evict_select) of block_table moved to position i of dst_table (block_table
     itself: in place), with their weights; seq_lens: the lengths before the cut."""
-    _evict_compact(lib().kvq_evict_compact, cfg, pool, kvq_pool_bytes(cfg), block_table, dst_table, seq_lens, kept,
-                   weights, status, stream)
+    L = lib()
+    _compact_call(L.kvq_evict_compact, L.kvq_pool_bytes, cfg, pool, block_table, dst_table, seq_lens, kept, weights,
+                  status, stream)
 
 
 def kvq_int8_evict_compact(cfg: CacheConfig, pool: torch.Tensor, block_table: torch.Tensor, dst_table: torch.Tensor,
                            seq_lens: torch.Tensor, kept: torch.Tensor, weights: torch.Tensor | None = None,
                            status: torch.Tensor | None = None, stream=None) -> None:
     """kvq_evict_compact over the INT8 per-row cache."""
-    _evict_compact(lib().kvq_int8_evict_compact, cfg, pool, kvq_int8_pool_bytes(cfg), block_table, dst_table, seq_lens,
-                   kept, weights, status, stream)
+    L = lib()
+    _compact_call(L.kvq_int8_evict_compact, L.kvq_int8_pool_bytes, cfg, pool, block_table, dst_table, seq_lens, kept,
+                  weights, status, stream)
+
+
+def _diff_call(fn, cfg, pool, q, block_table, seq_lens, max_len, softmax_scale, lam, norm_weight, norm_eps, out_scale,
+               out, workspace, stream, step=None) -> None:
+    dev = torch.cuda.current_device()
+    ref = C.byref(cfg)
+    B, Hq, (pp, qp, bt, blocks, sl), op = _decode_head(cfg, pool, lib().kvq_pool_bytes(ref), q, block_table, seq_lens,
+                                                       out, dev)
+    new = () if step is None else (_new_rows(step[0], "k_new", B, cfg, dev), _new_rows(step[1], "v_new", B, cfg, dev),
+                                   _shaped(step[2], "append_pos", torch.int32, (B,), dev))
+    rc = fn(ref, pp, *new, qp, bt, blocks, sl, B, Hq, int(max_len), float(softmax_scale),
+            _shaped(lam, "lam", torch.float32, (Hq,), dev),
+            None if norm_weight is None else _shaped(norm_weight, "norm_weight", torch.float32, (cfg.head_dim,), dev),
+            float(norm_eps), float(out_scale), op, *_bytes(workspace, "workspace", dev), _stream_on(stream, dev))
+    _check(rc)
 
 
 def kvq_diff_decode_attention(cfg: CacheConfig, pool: torch.Tensor, q: torch.Tensor, block_table: torch.Tensor,
@@ -825,16 +850,8 @@ def kvq_diff_decode_attention(cfg: CacheConfig, pool: torch.Tensor, q: torch.Ten
     """Differential attention: softmax over the first halves of q and K minus lam (fp32 [Hq]) times softmax over the
     second halves, applied to V; then an RMS norm over the head with norm_weight (fp32 [d]; None: no norm), times
     out_scale, into out (fp32 [B, Hq, d]).  workspace as from new_diff_workspace."""
-    dev = torch.cuda.current_device()
-    B, Hq, (pp, qp, bt, blocks, sl), op = _decode_head(cfg, pool, kvq_pool_bytes(cfg), q, block_table, seq_lens, out,
-                                                       dev)
-    d = cfg.head_dim
-    rc = lib().kvq_diff_decode_attention(
-        C.byref(cfg), pp, qp, bt, blocks, sl, B, Hq, int(max_len), float(softmax_scale),
-        _shaped(lam, "lam", torch.float32, (Hq,), dev),
-        None if norm_weight is None else _shaped(norm_weight, "norm_weight", torch.float32, (d,), dev), float(norm_eps),
-        float(out_scale), op, _bytes(workspace, "workspace", 0, dev), workspace.numel(), _stream(stream))
-    _check(rc)
+    _diff_call(lib().kvq_diff_decode_attention, cfg, pool, q, block_table, seq_lens, max_len, softmax_scale, lam,
+               norm_weight, norm_eps, out_scale, out, workspace, stream)
 
 
 def kvq_diff_decode_step(cfg: CacheConfig, pool: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -843,14 +860,5 @@ def kvq_diff_decode_step(cfg: CacheConfig, pool: torch.Tensor, k_new: torch.Tens
                          norm_eps: float, out_scale: float, out: torch.Tensor, workspace: torch.Tensor,
                          stream=None) -> None:
     """kvq_diff_decode_attention with k_new, v_new appended at append_pos first, as kvq_decode_step."""
-    dev = torch.cuda.current_device()
-    B, Hq, (pp, qp, bt, blocks, sl), op = _decode_head(cfg, pool, kvq_pool_bytes(cfg), q, block_table, seq_lens, out,
-                                                       dev)
-    d = cfg.head_dim
-    rc = lib().kvq_diff_decode_step(
-        C.byref(cfg), pp, _new_rows(k_new, "k_new", B, cfg, dev), _new_rows(v_new, "v_new", B, cfg, dev),
-        _shaped(append_pos, "append_pos", torch.int32, (B,), dev), qp, bt, blocks, sl, B, Hq, int(max_len),
-        float(softmax_scale), _shaped(lam, "lam", torch.float32, (Hq,), dev),
-        None if norm_weight is None else _shaped(norm_weight, "norm_weight", torch.float32, (d,), dev), float(norm_eps),
-        float(out_scale), op, _bytes(workspace, "workspace", 0, dev), workspace.numel(), _stream(stream))
-    _check(rc)
+    _diff_call(lib().kvq_diff_decode_step, cfg, pool, q, block_table, seq_lens, max_len, softmax_scale, lam,
+               norm_weight, norm_eps, out_scale, out, workspace, stream, (k_new, v_new, append_pos))

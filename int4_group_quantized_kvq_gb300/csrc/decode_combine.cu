@@ -28,9 +28,14 @@ struct CParams {
     float* out;
     float* out_host;  // device address of mapped pinned host memory that also receives out, or nullptr
     int32_t B, Hq, lg_p;
-    // MODE 1: (max, 1 / sum) of each row, and the bound the lengths are cut to
+    // MODE 1: (max, 1 / sum) of each row, written by the combine; the decode grid's scores
+    // [B][Hq][score_ld], the accumulated weights [B][Hkv][weights_ld], the query heads per kv
+    // head, the chunks of positions a kv head is cut into, and the bound the lengths are cut to
     float2* stat;
-    int32_t len_max;
+    const float* scores;
+    float* weights;
+    float decay;
+    int32_t score_ld, weights_ld, r, chunks, len_max;
     // MODE 2 (Hq counts virtual heads, two per output row)
     const float* lambda;
     const float* norm_weight;
@@ -39,6 +44,57 @@ struct CParams {
 
 constexpr int kCombineMaxWarps = 16;
 constexpr int kCombineLocalB = 256;   // up to this batch the row metadata is computed before the wait
+
+// MODE 1's third kernel: CTA size, and the scores a thread has in flight; a chunk is one
+// position of one kv head per thread for every R of them, R the query heads per kv head
+// rounded up to 1, 2, 4 or 8.
+constexpr int kAddThreads = 256;
+constexpr int kAddScores = 16;
+__host__ __device__ constexpr int add_rows(int r) { return r <= 2 ? r : (r <= 4 ? 4 : 8); }
+__host__ __device__ constexpr int add_positions(int r) { return kAddThreads * (kAddScores / add_rows(r)); }
+
+// The attention weight of the positions, one CTA per kv head and chunk:
+//     weights[b][h][t] = decay * weights[b][h][t] + sum over the kv head's r rows of 2^(z - M) / L,
+// z the scores the decode grid stored, M and 1 / L from the combine, in row order (results do
+// not depend on timing).  Bound by latency and launch: a thread's scores, its old weights and
+// the rows' statistics are all in flight together, one round trip, and the scores, written
+// just before, mostly still lie in the L2.  8 x 32 heads of 8193 positions (25 MB): 6.7 us on
+// its own.  Tried and slower for the whole call on that shape (61.0 us): the same work in
+// further CTAs of the combine's launch, which then hold the register file of the combine
+// (67 us), and run beside the combine with M and L from the partials (63 us).
+template <int R>
+__global__ void __launch_bounds__(kAddThreads) add_weights_kernel(CParams p) {
+    constexpr int K = kAddScores / R;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const unsigned head = blockIdx.x / p.chunks, heads = p.Hq / p.r;
+    const int t0 = static_cast<int>(blockIdx.x - head * p.chunks) * (kAddThreads * K) + static_cast<int>(threadIdx.x);
+    const int b = head / heads;
+    const int Lb = min(min(p.seq_lens[b], p.len_max),
+                       static_cast<int>(min(static_cast<long long>(p.src[0].max_blocks) << p.lg_p, 0x7fffffffLL)));
+    float* w = p.weights + static_cast<long long>(head) * p.weights_ld + t0;
+    const float* zp = p.scores + static_cast<long long>(head) * p.r * p.score_ld + t0;
+    const float2* st = p.stat + static_cast<long long>(head) * p.r;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float z[K][R], old[K];
+    float2 ml[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) ml[i] = i < p.r ? __ldcg(st + i) : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const bool in = t0 + k * kAddThreads < Lb;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            z[k][i] = in && i < p.r ? __ldcg(zp + static_cast<long long>(i) * p.score_ld + k * kAddThreads) : 0.f;
+        old[k] = in && p.decay != 0.f ? w[k * kAddThreads] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < R; ++i) sum = fmaf(fast_exp2(z[k][i] - ml[i].x), ml[i].y, sum);
+        if (t0 + k * kAddThreads < Lb) w[k * kAddThreads] = fmaf(p.decay, old[k], sum);
+    }
+}
 
 // One CTA per output row (b, hq).  In source s the row's partials sit at W * (cf + seg) + j
 // for j < W * (cl - cf + 1), where CTAs cf..cl of that grid hold the units of segment
@@ -57,9 +113,10 @@ constexpr int kCombineLocalB = 256;   // up to this batch the row metadata is co
 // register file and keep the next call's decode CTAs off that SM until it leaves; at 64
 // it holds half.  Rows of 4- and 8-warp CTAs (up to 64 partials) load 8 at a time, in
 // one round.
-// MODE 1 also writes each row's maximum and reciprocal sum for the weights kernel behind it.
-// MODE 2 (differential attention) has one CTA per query head: the rows of its two maps are
-// merged one after the other, then o = o1 - lambda o2, the optional RMS norm over the row,
+// MODE 1 (attention with weights) also leaves each row's maximum and reciprocal sum for the
+// weights' kernel.
+// MODE 2 (differential attention) has one CTA per query head: even warps merge its first map's
+// row, odd warps the second's, then o = o1 - lambda o2, the optional RMS norm over the row,
 // which warp 0 holds whole, and the output scale.
 template <int D, int NSRC, int NB, int MODE = 0>
 __global__ void __launch_bounds__(kCombineMaxWarps * 32, NB == 8 || D == 256 ? 1 : 2)
@@ -82,6 +139,8 @@ combine_kernel(CParams p) {
     const int b = static_cast<int>(blockIdx.x / rows_b);
     const int hrow = static_cast<int>(blockIdx.x - static_cast<long long>(b) * rows_b);
     const int hq = MODE == 2 ? 2 * hrow : hrow;  // (both maps' virtual heads share a segment)
+    // the warps that merge this warp's row: all of them, or in MODE 2 every other one
+    const int map = MODE == 2 ? warp & 1 : 0, sub = MODE == 2 ? warp >> 1 : warp, nsub = MODE == 2 ? nw >> 1 : nw;
 
     // Pages of sequence i as source s listed them, and the row's range of partials.
     auto pages_of = [&](const CSource& s, int i) {
@@ -150,161 +209,165 @@ combine_kernel(CParams p) {
         }
     }
 
-    __shared__ float4 s_first[MODE == 2 ? D / 4 : 1];  // MODE 2: map 1's output row
+    float M = -INFINITY, L = 0.f;
+    float4 acc[NV][NA];
 #pragma unroll
-    for (int map = 0; map < (MODE == 2 ? 2 : 1); ++map) {
-        if (MODE == 2 && map == 1) __syncthreads();  // warp 0 has read map 1's results
-        float M = -INFINITY, L = 0.f;
-        float4 acc[NV][NA];
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
+        for (int a = 0; a < NA; ++a) acc[v][a] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int a = 0; a < NA; ++a) acc[v][a] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int si = 0; si < NSRC; ++si) {
+        const CSource& s = p.src[si];
+        const int sl = hq - (hq / s.ns) * s.ns + map;
+        const bool dense = U[si] >= s.C;  // every CTA slice holds units
+        const long long stride_ml = static_cast<long long>(s.ns) * 2;
+        const long long stride_o = static_cast<long long>(s.ns) * D;
+        const float* ml0 = s.ws_ml + (base[si] * s.ns + sl) * 2;
+        const float* o0 = s.ws_o + (base[si] * s.ns + sl) * D + 4 * lane;
+        for (int j0 = sub; j0 < n[si]; j0 += NB * nsub) {
+            float2 ml[NB];
+            float4 ov[NB][NV];
 #pragma unroll
-        for (int si = 0; si < NSRC; ++si) {
-            const CSource& s = p.src[si];
-            const int sl = hq - (hq / s.ns) * s.ns + map;
-            const bool dense = U[si] >= s.C;  // every CTA slice holds units
-            const long long stride_ml = static_cast<long long>(s.ns) * 2;
-            const long long stride_o = static_cast<long long>(s.ns) * D;
-            const float* ml0 = s.ws_ml + (base[si] * s.ns + sl) * 2;
-            const float* o0 = s.ws_o + (base[si] * s.ns + sl) * D + 4 * lane;
-            for (int j0 = warp; j0 < n[si]; j0 += NB * nw) {
-                float2 ml[NB];
-                float4 ov[NB][NV];
-#pragma unroll
-                for (int kk = 0; kk < NB; ++kk) {
-                    const int j = j0 + kk * nw;
-                    bool have = j < n[si];
-                    if (have && !dense) {
-                        const long long k = cf[si] + j / s.W;
-                        have = slice_start(k, U[si], s.C) < slice_start(k + 1, U[si], s.C);
-                    }
-                    ml[kk] = have ? __ldcg(reinterpret_cast<const float2*>(ml0 + j * stride_ml)) : make_float2(-INFINITY, 0.f);
-#pragma unroll
-                    for (int v = 0; v < NV; ++v)
-                        ov[kk][v] = have && lane_has(lane, v) ? __ldcg(reinterpret_cast<const float4*>(o0 + j * stride_o) + 32 * v)
-                                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int kk = 0; kk < NB; ++kk) {
+                const int j = j0 + kk * nsub;
+                bool have = j < n[si];
+                if (have && !dense) {
+                    const long long k = cf[si] + j / s.W;
+                    have = slice_start(k, U[si], s.C) < slice_start(k + 1, U[si], s.C);
                 }
-                float mb = M;
+                ml[kk] = have ? __ldcg(reinterpret_cast<const float2*>(ml0 + j * stride_ml)) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-                for (int kk = 0; kk < NB; ++kk) mb = fmaxf(mb, ml[kk].x);
-                if (mb == -INFINITY) continue;  // only empty partials so far
-                if (mb > M) {  // a larger running maximum: rescale what has been summed
-                    const float f = fast_exp2(M - mb);
-                    L *= f;
+                for (int v = 0; v < NV; ++v)
+                    ov[kk][v] = have && lane_has(lane, v) ? __ldcg(reinterpret_cast<const float4*>(o0 + j * stride_o) + 32 * v)
+                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float mb = M;
 #pragma unroll
-                    for (int v = 0; v < NV; ++v)
+            for (int kk = 0; kk < NB; ++kk) mb = fmaxf(mb, ml[kk].x);
+            if (mb == -INFINITY) continue;  // only empty partials so far
+            if (mb > M) {  // a larger running maximum: rescale what has been summed
+                const float f = fast_exp2(M - mb);
+                L *= f;
 #pragma unroll
-                        for (int a = 0; a < NA; ++a) {
-                            acc[v][a].x *= f;
-                            acc[v][a].y *= f;
-                            acc[v][a].z *= f;
-                            acc[v][a].w *= f;
-                        }
-                    M = mb;
-                }
+                for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int kk = 0; kk < NB; ++kk) {
-                    const float f = fast_exp2(ml[kk].x - M);
-                    L = fmaf(f, ml[kk].y, L);
-#pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                        float4& A = acc[v][kk % NA];
-                        A.x = fmaf(f, ov[kk][v].x, A.x);
-                        A.y = fmaf(f, ov[kk][v].y, A.y);
-                        A.z = fmaf(f, ov[kk][v].z, A.z);
-                        A.w = fmaf(f, ov[kk][v].w, A.w);
+                    for (int a = 0; a < NA; ++a) {
+                        acc[v][a].x *= f;
+                        acc[v][a].y *= f;
+                        acc[v][a].z *= f;
+                        acc[v][a].w *= f;
                     }
+                M = mb;
+            }
+#pragma unroll
+            for (int kk = 0; kk < NB; ++kk) {
+                const float f = fast_exp2(ml[kk].x - M);
+                L = fmaf(f, ml[kk].y, L);
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    float4& A = acc[v][kk % NA];
+                    A.x = fmaf(f, ov[kk][v].x, A.x);
+                    A.y = fmaf(f, ov[kk][v].y, A.y);
+                    A.z = fmaf(f, ov[kk][v].z, A.z);
+                    A.w = fmaf(f, ov[kk][v].w, A.w);
                 }
             }
         }
-        if (lane == 0) {
-            s_m[warp] = M;
-            s_l[warp] = L;
+    }
+    if (lane == 0) {
+        s_m[warp] = M;
+        s_l[warp] = L;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        float4 t = acc[v][0];
+#pragma unroll
+        for (int a = 1; a < NA; ++a) {
+            t.x += acc[v][a].x;
+            t.y += acc[v][a].y;
+            t.z += acc[v][a].z;
+            t.w += acc[v][a].w;
+        }
+        if (lane_has(lane, v)) s_o[warp][lane + 32 * v] = t;
+    }
+    __syncthreads();
+    // the row of map `m` (lane l: float4 l, l + 32, ..)
+    auto merge = [&](int m, float4 (&res)[NV], float& Mx, float& inv) {
+        constexpr int step = MODE == 2 ? 2 : 1;
+        Mx = -INFINITY;
+        for (int w = m; w < nw; w += step) Mx = fmaxf(Mx, s_m[w]);
+        float Ls = 0.f;
+        if (Mx != -INFINITY)
+            for (int w = m; w < nw; w += step) Ls = fmaf(fast_exp2(s_m[w] - Mx), s_l[w], Ls);
+        inv = Ls > 0.f ? 1.f / Ls : 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            res[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!lane_has(lane, v) || Mx == -INFINITY) continue;
+            for (int w = m; w < nw; w += step) {
+                const float f = fast_exp2(s_m[w] - Mx);
+                const float4 ow = s_o[w][lane + 32 * v];
+                res[v].x = fmaf(f, ow.x, res[v].x);
+                res[v].y = fmaf(f, ow.y, res[v].y);
+                res[v].z = fmaf(f, ow.z, res[v].z);
+                res[v].w = fmaf(f, ow.w, res[v].w);
+            }
+            res[v] = make_float4(res[v].x * inv, res[v].y * inv, res[v].z * inv, res[v].w * inv);
+        }
+    };
+    float4 res[NV];
+    float Mx, inv;
+    if constexpr (MODE == 2) {
+        __shared__ float4 s_second[D / 4];
+        if (warp < 2) merge(warp, res, Mx, inv);
+        if (warp == 1) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                if (lane_has(lane, v)) s_second[lane + 32 * v] = res[v];
+        }
+        __syncthreads();
+        if (warp != 0) return;
+        const float lam = p.lambda[hrow];
+        float ss = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            if (!lane_has(lane, v)) continue;
+            const float4 o2 = s_second[lane + 32 * v];
+            res[v] = make_float4(fmaf(-lam, o2.x, res[v].x), fmaf(-lam, o2.y, res[v].y), fmaf(-lam, o2.z, res[v].z),
+                                 fmaf(-lam, o2.w, res[v].w));
+            ss += res[v].x * res[v].x + res[v].y * res[v].y + res[v].z * res[v].z + res[v].w * res[v].w;
+        }
+        float f = p.out_scale;
+        if (p.norm_weight != nullptr) {
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+            f *= rsqrtf(ss * (1.f / D) + p.norm_eps);
         }
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            float4 t = acc[v][0];
-#pragma unroll
-            for (int a = 1; a < NA; ++a) {
-                t.x += acc[v][a].x;
-                t.y += acc[v][a].y;
-                t.z += acc[v][a].z;
-                t.w += acc[v][a].w;
+            if (!lane_has(lane, v)) continue;
+            float4 w = make_float4(f, f, f, f);
+            if (p.norm_weight != nullptr) {
+                w = reinterpret_cast<const float4*>(p.norm_weight)[lane + 32 * v];
+                w = make_float4(w.x * f, w.y * f, w.z * f, w.w * f);
             }
-            if (lane_has(lane, v)) s_o[warp][lane + 32 * v] = t;
+            // no positions: zeros, whatever norm_eps is
+            res[v] = n[0] > 0 ? make_float4(res[v].x * w.x, res[v].y * w.y, res[v].z * w.z, res[v].w * w.w)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        __syncthreads();
-        if (warp == 0) {
-            float Mx = -INFINITY;
-            for (int w = 0; w < nw; ++w) Mx = fmaxf(Mx, s_m[w]);
-            float Ls = 0.f;
-            if (Mx != -INFINITY)
-                for (int w = 0; w < nw; ++w) Ls = fmaf(fast_exp2(s_m[w] - Mx), s_l[w], Ls);
-            const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
-            const long long row = static_cast<long long>(b) * rows_b + hrow;
-            if constexpr (MODE == 1) {
-                if (lane == 0) p.stat[row] = make_float2(Mx, inv);
-            }
-            float4 res[NV];
+    } else {
+        if (warp != 0) return;
+        merge(0, res, Mx, inv);
+    }
+    const long long row = static_cast<long long>(b) * rows_b + hrow;
+    if constexpr (MODE == 1) {
+        if (lane == 0) p.stat[row] = make_float2(Mx, inv);
+    }
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                res[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (!lane_has(lane, v)) continue;
-                const int f4 = lane + 32 * v;
-                float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (Mx != -INFINITY) {
-                    for (int w = 0; w < nw; ++w) {
-                        const float f = fast_exp2(s_m[w] - Mx);
-                        const float4 ow = s_o[w][f4];
-                        O.x = fmaf(f, ow.x, O.x);
-                        O.y = fmaf(f, ow.y, O.y);
-                        O.z = fmaf(f, ow.z, O.z);
-                        O.w = fmaf(f, ow.w, O.w);
-                    }
-                }
-                res[v] = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
-            }
-            if constexpr (MODE == 2) {
-                if (map == 0) {
-#pragma unroll
-                    for (int v = 0; v < NV; ++v)
-                        if (lane_has(lane, v)) s_first[lane + 32 * v] = res[v];
-                    continue;
-                }
-                const float lam = p.lambda[hrow];
-                float ss = 0.f;
-#pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    if (!lane_has(lane, v)) continue;
-                    const float4 f1 = s_first[lane + 32 * v];  // (this lane's own store)
-                    res[v] = make_float4(fmaf(-lam, res[v].x, f1.x), fmaf(-lam, res[v].y, f1.y),
-                                         fmaf(-lam, res[v].z, f1.z), fmaf(-lam, res[v].w, f1.w));
-                    ss += res[v].x * res[v].x + res[v].y * res[v].y + res[v].z * res[v].z + res[v].w * res[v].w;
-                }
-                float f = p.out_scale;
-                if (p.norm_weight != nullptr) {
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-                    f *= rsqrtf(ss * (1.f / D) + p.norm_eps);
-                }
-#pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    if (!lane_has(lane, v)) continue;
-                    float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
-                    if (p.norm_weight != nullptr) w = reinterpret_cast<const float4*>(p.norm_weight)[lane + 32 * v];
-                    res[v] = n[0] > 0 ? make_float4(res[v].x * f * w.x, res[v].y * f * w.y, res[v].z * f * w.z, res[v].w * f * w.w)
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);  // no positions: zeros, whatever norm_eps is
-                }
-            }
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                if (!lane_has(lane, v)) continue;
-                reinterpret_cast<float4*>(p.out + row * D)[lane + 32 * v] = res[v];
-                if (p.out_host != nullptr) reinterpret_cast<float4*>(p.out_host + row * D)[lane + 32 * v] = res[v];
-            }
-        }
+    for (int v = 0; v < NV; ++v) {
+        if (!lane_has(lane, v)) continue;
+        reinterpret_cast<float4*>(p.out + row * D)[lane + 32 * v] = res[v];
+        if (p.out_host != nullptr) reinterpret_cast<float4*>(p.out_host + row * D)[lane + 32 * v] = res[v];
     }
 }
 
@@ -343,7 +406,10 @@ cudaError_t launch_one(const cudaLaunchConfig_t& cfg, const decode::CParams& p, 
 }
 
 cudaError_t launch(const decode::CParams& p, DecodeMode mode, int d, int warps, cudaStream_t stream) {
-    const long long rows = static_cast<long long>(p.B) * (mode == DecodeMode::kDiff ? p.Hq / 2 : p.Hq);
+    long long rows = static_cast<long long>(p.B) * (mode == DecodeMode::kDiff ? p.Hq / 2 : p.Hq);
+    if (mode == DecodeMode::kDiff) {
+        warps = std::min(2 * warps, decode::kCombineMaxWarps);  // two rows
+    }
     if (rows <= 0) return cudaSuccess;
     if (rows > 0x7fffffffLL) return cudaErrorInvalidValue;
     // Launched while the decode grid runs (programmatic dependent launch); the kernel
@@ -387,12 +453,40 @@ cudaError_t launch_combine(const DecodeArgs& a, const DecodePlan& plan, cudaStre
     p.Hq = a.Hq;
     p.lg_p = lg2(a.L.P);
     p.stat = reinterpret_cast<float2*>(a.workspace + plan.ws_stat_offset);
+    p.scores = reinterpret_cast<const float*>(a.workspace + plan.ws_score_offset);
+    p.weights = a.weights;
+    p.decay = a.decay;
+    p.score_ld = plan.score_ld;
+    p.weights_ld = a.weights_ld;
+    p.r = a.Hq / a.Hkv;
+    p.chunks = static_cast<int32_t>((static_cast<long long>(a.max_len) + decode::add_positions(p.r) - 1) /
+                                    decode::add_positions(p.r));
     p.len_max = a.max_len;
     p.lambda = a.lambda;
     p.norm_weight = a.norm_weight;
     p.norm_eps = a.norm_eps;
     p.out_scale = a.out_scale;
-    return launch(p, a.mode, a.L.d, plan.combine_warps, stream);
+    cudaError_t err = launch(p, a.mode, a.L.d, plan.combine_warps, stream);
+    const long long adders = static_cast<long long>(a.B) * a.Hkv * p.chunks;
+    if (err != cudaSuccess || a.mode != DecodeMode::kWeights || adders == 0) return err;
+    if (adders > 0x7fffffffLL) return cudaErrorInvalidValue;
+    // launched while the combine runs; the kernel waits for it before it reads the workspace
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(adders));
+    cfg.blockDim = dim3(decode::kAddThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    switch (decode::add_rows(p.r)) {
+        case 1: err = cudaLaunchKernelEx(&cfg, decode::add_weights_kernel<1>, p); break;
+        case 2: err = cudaLaunchKernelEx(&cfg, decode::add_weights_kernel<2>, p); break;
+        case 4: err = cudaLaunchKernelEx(&cfg, decode::add_weights_kernel<4>, p); break;
+        default: err = cudaLaunchKernelEx(&cfg, decode::add_weights_kernel<8>, p); break;
+    }
+    return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 // The mixed-precision decode: the partials of the INT4 grid (a0, plan0) and of the FP16

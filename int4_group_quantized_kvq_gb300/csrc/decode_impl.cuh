@@ -87,7 +87,7 @@ constexpr uint64_t kWaitLimitNs = 250000000ull;   // a page copy that takes 250 
 // registers) when a thread carries one query-head slot of head_dim <= 128, else 2.
 template <int HS>
 constexpr int cta_warps() { return 4; }
-template <int HS, int D = 128>
+template <int HS, int D = 128, int MODE = 0>
 constexpr int min_ctas() { return HS == 1 && D <= 128 ? 3 : 2; }
 
 // CTA-wide bookkeeping in shared memory.
@@ -137,10 +137,10 @@ struct KParams {
     // q is written by the kernel ahead on the stream (the host-buffer step's copy kernel):
     // read it only after griddepcontrol.wait
     bool q_after_wait;
-    // MODE 1: every attended position's score (log2 units) goes to scores[b][kv head][t][query
-    // head of the kv head], score_ld positions per kv head; lengths are cut to score_ld
+    // MODE 1: every attended position's score (log2 units) goes to scores[b][query head][t],
+    // score_ld floats per query head; lengths are cut to len_max
     float* scores;
-    int32_t score_ld;
+    int32_t score_ld, len_max;
 };
 
 // a / b for a >= 0, b > 0, with 32-bit division when both fit (the usual case).
@@ -194,7 +194,7 @@ __device__ __forceinline__ int span_index(const SeqSpan& sp, int r) {
 }
 
 // Exclusive prefix sums of pages per sequence into pre[0..B], the lengths (negative ones
-// as 0, with CUT those past score_ld as score_ld) into lens[0..B-1] and the append positions
+// as 0, with CUT those past len_max as len_max) into lens[0..B-1] and the append positions
 // (-1: none) into aps[0..B-1]; run by one warp.
 template <bool CUT = false>
 __device__ __forceinline__ void page_prefix(const KParams& p, int32_t* pre, int32_t* lens, int32_t* aps, int lane) {
@@ -206,9 +206,9 @@ __device__ __forceinline__ void page_prefix(const KParams& p, int32_t* pre, int3
             int L = p.seq_lens[b] - p.len_sub;
             L = L < 0 ? 0 : L;
             if constexpr (CUT) {
-                if (L > p.score_ld) {
+                if (L > p.len_max) {
                     raise_flag(p.status, KVQ_FLAG_BAD_POSITION);
-                    L = p.score_ld;
+                    L = p.len_max;
                 }
             }
             lens[b] = L;
@@ -407,18 +407,18 @@ __device__ __forceinline__ void load_scales(const uint8_t* p, float (&a)[N], flo
 // per block, a value being code * scale; it runs with one group per row (GK = GV = D) and
 // one-head units, and has no fused append.
 // MODE 0: plain attention.  MODE 1: attention that also stores each position's scores, from
-// which the weights kernel (decode_weights.cu) takes the positions' softmax weights once the
-// combine knows each row's maximum and sum.  MODE 2: differential attention's two maps: a
-// query head is two rows of score columns ("virtual heads" 2 h and 2 h + 1), the first
-// carrying the lower half of q, the second the upper half, zeros elsewhere; their outputs are
-// subtracted by the combine.  Modes 1 and 2 feed the score MMA centred codes (n - 8, one more
+// which the weights' kernel behind the combine (decode_combine.cu) takes their softmax weights once
+// each row's maximum and sum are known.  MODE 2: differential attention's two maps: a
+// query head is two sets of score columns ("virtual heads" 2 h and 2 h + 1), the first with the
+// lower half of q and of the K groups, the second with the upper; their outputs are subtracted
+// by the combine.  Modes 1 and 2 feed the score MMA centred codes (n - 8, one more
 // instruction per pair of codes than the f16 subnormals of MODE 0): the offset form's partial
 // sums are of the size of 8 sum |q| whatever the codes are, and the MMA's fp32 accumulation
 // rounds at that size, which with K groups stretched by an outlier channel moves a score by
 // some 1e-5.  The plain output tolerates it; the weights are fp32 results of their own, and a
 // difference of two maps keeps only what does not cancel.
 template <int D, int GK, int GV, int HK, int HS, bool WIN, bool P16, int CODEC = 0, int MODE = 0>
-__global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decode_splitkv_kernel(KParams p) {
+__global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D, MODE>()) decode_splitkv_kernel(KParams p) {
     static_assert(D == 64 || D == 128 || D == 256, "head_dim 64, 128 or 256");
     static_assert(CODEC == 0 || (CODEC == 1 && D == 128 && GK == D && GV == D && HK == 1), "INT8: d 128, rows");
     static_assert(D <= 128 || (HK == 1 && HS == 1), "head_dim 256: one-head units, up to 4 query heads each");
@@ -430,6 +430,7 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
     constexpr int NGK = D / GK;               // K groups per row
     constexpr int NGV = D / GV;               // V groups per row
     constexpr bool I8 = CODEC == 1;
+    constexpr bool PAIRS = MODE == 2 && HS == 2;  // a thread's two slots are the maps of one query head
     constexpr bool CENTRED = MODE != 0;       // codes enter the score MMA without their offset
     // Modes 1 and 2 hold the softmax terms as 2^kUp p: the weights p * v_scale become f16 high
     // and low parts, and small ones would lose bits as f16 subnormals.  A quantized row's scale
@@ -439,7 +440,11 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
     constexpr float kUp = MODE == 0 ? 0.f : (I8 ? 6.f : 2.f);
     constexpr int KW = I8 ? D / 16 : D / 32;  // K code words per thread per token row
     constexpr int KSTEPS = D / 16;            // MMA k-steps over head_dim
-    constexpr int NTQ = (HS * NGK + 1) / 2;   // score n-tiles
+    // K groups a score slot sums over: all of a row's, in MODE 2 those of the slot's half.  In
+    // MODE 2 the slots are virtual heads (even: first map) when they are four at most; with more,
+    // a thread's slot c is query head c and its two slots are the two maps.
+    constexpr int NG = MODE == 2 ? NGK / 2 : NGK;
+    constexpr int NTQ = (HS * NG + 1) / 2;    // score n-tiles
     constexpr int VB = GV / 16;               // V code bytes per thread per group per row
     constexpr int MT = D / 16;                // output m-tiles
     constexpr int ROW = I8 ? D : D / 2;       // bytes of one token's codes
@@ -635,9 +640,7 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
     int wlo = 0;   // its first window position (0: all attended)
     SeqSpan sspan{};  // attended positions and listed pages of the segment's sequence
 
-    // MODE 1: this thread's scores of the segment's position 0, and the step from a position to the next
-    float* sc = nullptr;
-    const int sc_step = HK == 1 ? p.ns : 1;
+    float* sc = nullptr;  // MODE 1: the score of the segment's position 0 for this thread's slot c
 
     // the kv head (within the unit) of this thread's score slot, and of its B-fragment
     // column (HK > 1 only when every slot is its own kv head)
@@ -768,11 +771,15 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
             for (int s = 0; s < HS; ++s) {
                 float z0 = 0.f, z1 = 0.f;
 #pragma unroll
-                for (int R = 0; R < NGK; ++R) {
+                for (int R = 0; R < NG; ++R) {
                     // the group's code dot product sum (n - off) q = 2^24 S - off sum q
-                    const int pi = s * NGK + R;
+                    const int pi = s * NG + R;
                     // (times softmax_scale * log2 e, folded into both terms)
-                    if constexpr (CENTRED) {
+                    if constexpr (MODE == 2) {
+                        const bool second = HS == 2 ? s == 1 : (c & 1) != 0;  // the slot's map
+                        z0 = fmaf(second ? skg[NG + R] : skg[R], sacc[pi >> 1][pi & 1], z0);
+                        z1 = fmaf(second ? skg8[NG + R] : skg8[R], sacc[pi >> 1][2 + (pi & 1)], z1);
+                    } else if constexpr (CENTRED) {
                         z0 = fmaf(skg[R], sacc[pi >> 1][pi & 1], z0);
                         z1 = fmaf(skg8[R], sacc[pi >> 1][2 + (pi & 1)], z1);
                     } else {
@@ -784,10 +791,11 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
                 z[X][s][0] = CENTRED ? z0 * p.scale_log2 : z0;
                 z[X][s][1] = CENTRED ? z1 * p.scale_log2 : z1;
                 if constexpr (MODE == 1) {
+                    // (a slot's 8 tokens of a row group fill one 32-byte sector)
                     if (HK > 1 || c + 4 * s < p.ns) {
-                        float* at = sc + static_cast<long long>(t0[X] + g) * sc_step + 4 * s;
+                        float* at = sc + static_cast<long long>(4 * s) * p.score_ld + t0[X] + g;
                         if (!MASKED || vg[X]) at[0] = z[X][s][0];
-                        if (!MASKED || vg8[X]) at[8 * sc_step] = z[X][s][1];
+                        if (!MASKED || vg8[X]) at[8] = z[X][s][1];
                     }
                 }
                 if (MASKED) {
@@ -1030,18 +1038,23 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
                 }
             }
             if constexpr (MODE == 1) {
-                const long long head = static_cast<long long>(b) * p.Hkv + static_cast<long long>(hg) * HK + a_row;
-                sc = p.scores + head * p.score_ld * sc_step + (HK == 1 ? c : 0);
+                sc = p.scores + (static_cast<long long>(b) * p.Hq + hg * p.ns + c) * p.score_ld;
             }
             const __half* qseg = qbuf + (segk & 1) * kQRows * D;
 #pragma unroll
             for (int t = 0; t < NTQ; ++t) {
                 const int pi = 2 * t + (g & 1);
-                const int sigma = pi / NGK;
-                const int R = pi % NGK;
-                const int j = (g >> 1) + 4 * sigma;
-                const bool colv = sigma < HS && j < p.ns;
-                const __half* qrow = qseg + (colv ? (MODE == 2 ? j / 2 : j) : 0) * D;
+                const int sigma = pi / NG;
+                // slot, K group and q row of the column
+                int R = pi % NG, j = (g >> 1) + 4 * sigma;
+                if constexpr (MODE == 2) {
+                    const int slot = g >> 1;
+                    const int map = HS == 2 ? sigma : slot & 1;
+                    j = HS == 2 ? slot : slot >> 1;
+                    R += map * NG;
+                }
+                const bool colv = sigma < HS && j < nq;
+                const __half* qrow = qseg + (colv ? j : 0) * D;
                 float qs = 0.f;  // this thread's part of the column's sum of q
                 if constexpr (I8) {
                     // k-step j: dimensions c (D / 4) + 4 j .. + 3, in order
@@ -1060,8 +1073,7 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
                 for (int wi = 0; wi < (I8 ? 0 : KW); ++wi) {
                     const int dbase = c * (D / 4) + 8 * wi;
                     uint4 w4 = make_uint4(0, 0, 0, 0);
-                    // (MODE 2: virtual head j carries half j % 2 of the query head's row)
-                    if (colv && dbase / GK == R && (MODE != 2 || dbase / (D / 2) == (j & 1))) w4 = *reinterpret_cast<const uint4*>(qrow + dbase);
+                    if (colv && dbase / GK == R) w4 = *reinterpret_cast<const uint4*>(qrow + dbase);
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&(&w4.x)[h]));
@@ -1221,9 +1233,11 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
                 // segment end.)
 #pragma unroll
                 for (int s = 0; s < HS; ++s) {
-                    const int nsr = min(4, p.ns - 4 * s);  // slots in this round
+                    // slots in this round, and the row of slot c (MODE 2: virtual head 2 c + s)
+                    const int nsr = PAIRS ? nq : min(4, p.ns - 4 * s);
+                    const int srow = PAIRS ? 2 * c + s : 4 * s + c;
                     if (c < nsr) {
-                        float* orow = p.ws_o + (piece * p.ns + 4 * s + c) * D;
+                        float* orow = p.ws_o + (piece * p.ns + srow) * D;
 #pragma unroll
                         for (int R = 0; R < NGV; ++R)
 #pragma unroll
@@ -1235,7 +1249,7 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D>()) decod
                             }
                     }
                     if (g == 0 && c < nsr)
-                        *reinterpret_cast<float2*>(p.ws_ml + (piece * p.ns + 4 * s + c) * 2) = make_float2(m[s] - kUp, lt[s]);
+                        *reinterpret_cast<float2*>(p.ws_ml + (piece * p.ns + srow) * 2) = make_float2(m[s] - kUp, lt[s]);
                 }
             } else {
                 // no units of this segment here (or a failed wait): an empty partial
@@ -1369,7 +1383,8 @@ cudaError_t run(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream
     }
     p.unit_bytes = p.block_bytes * HK;
     p.scores = MODE == 1 ? reinterpret_cast<float*>(a.workspace + plan.ws_score_offset) : nullptr;
-    p.score_ld = a.max_len;
+    p.score_ld = plan.score_ld;
+    p.len_max = a.max_len;
     p.stages = plan.stages;
     p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
     p.k_new = a.k_new;

@@ -191,11 +191,14 @@ cudaError_t plan_decode(const DecodeArgs& a, DecodePlan* plan) {
     plan->ws_o_offset = plan->ws_ml_offset + round_up(pieces * ns * 2 * sizeof(float), kAlign);
     plan->ws_bytes = plan->ws_o_offset + round_up(pieces * ns * a.L.d * sizeof(float), kAlign);
     plan->ws_stat_offset = plan->ws_score_offset = plan->ws_bytes;
+    plan->score_ld = 0;
     if (a.mode == DecodeMode::kWeights) {
-        const size_t rows = static_cast<size_t>(a.B) * a.Hq;
-        plan->ws_score_offset += round_up(rows * 2 * sizeof(float), kAlign);
-        plan->ws_bytes = plan->ws_score_offset +
-                         round_up(rows * static_cast<size_t>(std::max(a.max_len, 0)) * sizeof(float), kAlign);
+        plan->ws_score_offset += round_up(static_cast<size_t>(a.B) * a.Hq * 2 * sizeof(float), kAlign);
+        // whole sectors per 8 positions of every query head
+        const size_t ld = round_up(static_cast<size_t>(std::max(a.max_len, 0)), 32);
+        if (ld > 0x7fffffff) return cudaErrorInvalidValue;
+        plan->score_ld = static_cast<int32_t>(ld);
+        plan->ws_bytes = plan->ws_score_offset + round_up(static_cast<size_t>(a.B) * a.Hq * ld * sizeof(float), kAlign);
     }
     return cudaSuccess;
 }
@@ -221,9 +224,7 @@ cudaError_t launch_decode_grid(const DecodeArgs& a, const DecodePlan& plan, cuda
 cudaError_t launch_decode(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream) {
     cudaError_t e = launch_decode_grid(a, plan, stream);
     if (e != cudaSuccess) return e;
-    e = launch_combine(a, plan, stream);
-    if (e != cudaSuccess || a.mode != DecodeMode::kWeights) return e;
-    return launch_accumulate_weights(a, plan, stream);
+    return launch_combine(a, plan, stream);
 }
 
 }  // namespace kvq

@@ -255,9 +255,9 @@ __global__ void __launch_bounds__(T) evict_select_kernel(EvictSelectArgs p) {
 // Compact
 // ---------------------------------------------------------------------------
 constexpr int kCmpThreads = 256;
-constexpr int kCmpWords = 16;      // 16-byte code words a thread holds between its loads and its stores
-constexpr int kCmpMaxRows = 1024;  // rows a CTA moves in a round (head_dim 64, the shortest rows)
-constexpr int kCmpScaleBytes = 8192;
+constexpr int kCmpWords = 8;       // 16-byte code words a thread holds between its loads and its stores
+constexpr int kCmpMaxRows = 512;   // rows a CTA moves in a round (head_dim 64, the shortest rows)
+constexpr int kCmpScaleBytes = 4096;
 
 // A cluster moves the kept rows of its (sequence, kv head) in rounds: every CTA loads its share
 // of the round's rows (codes into registers, scales into shared memory), the cluster's barrier,
@@ -269,7 +269,7 @@ constexpr int kCmpScaleBytes = 8192;
 // per (sequence, kv head) with chunks of 64 rows through shared memory took 173 us for
 // 8 x 32 x 2048 rows of 134 bytes (its chain of small round trips), and 332 us for 4 x 8 x 4095
 // of 264.
-__global__ void __launch_bounds__(kCmpThreads, 2) evict_compact_kernel(EvictCompactArgs p, int32_t rows_cta, int32_t lg_w) {
+__global__ void __launch_bounds__(kCmpThreads, 4) evict_compact_kernel(EvictCompactArgs p, int32_t rows_cta, int32_t lg_w) {
     __shared__ long long s_src[kCmpMaxRows], s_dst[kCmpMaxRows];  // a row's block * 64 + slot; -1: stays
     __shared__ __align__(16) uint8_t s_scale[kCmpScaleBytes];
     cg::cluster_group cluster = cg::this_cluster();

@@ -101,6 +101,7 @@ struct DecodePlan {
     size_t ws_o_offset;   // unnormalised outputs of the warp partials
     size_t ws_stat_offset;  // attention with weights: (max, 1 / sum) of each output row
     size_t ws_score_offset; // attention with weights: the scores of every attended position
+    int32_t score_ld;       //   ... floats from one query head's scores to the next's
     size_t ws_bytes;      // total workspace bytes
 };
 
@@ -210,8 +211,6 @@ cudaError_t launch_decode(const DecodeArgs& a, const DecodePlan& plan, cudaStrea
 cudaError_t launch_decode_grid(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream);
 cudaError_t launch_combine2(const DecodeArgs& a0, const DecodePlan& plan0, const DecodeArgs& a1,
                             const DecodePlan& plan1, cudaStream_t stream);
-// the accumulation of the positions' weights, behind the combine (kWeights)
-cudaError_t launch_accumulate_weights(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream);
 
 // Eviction from a cache (evict.cu).  Select: of each (sequence, kv head), the positions kept.
 struct EvictSelectArgs {
