@@ -254,24 +254,40 @@ __global__ void __launch_bounds__(T) evict_select_kernel(EvictSelectArgs p) {
 // ---------------------------------------------------------------------------
 // Compact
 // ---------------------------------------------------------------------------
-constexpr int kCmpThreads = 256;
-constexpr int kCmpWords = 8;       // 16-byte code words a thread holds between its loads and its stores
-constexpr int kCmpMaxRows = 512;   // rows a CTA moves in a round (head_dim 64, the shortest rows)
-constexpr int kCmpScaleBytes = 4096;
+constexpr int kCmpThreads = 512;
+constexpr int kCmpWords = 8;      // 16-byte code words a thread holds between its loads and its stores
+constexpr int kCmpMaxRows = kCmpThreads;  // rows a CTA moves in a round: one per thread
+
+// A row's scales of one kind: 2, 4, 8 or 16 bytes, as stored.
+__device__ __forceinline__ uint4 load_piece(const uint8_t* g, int bytes) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (bytes == 4) v.x = *reinterpret_cast<const uint32_t*>(g);
+    else if (bytes == 2) v.x = *reinterpret_cast<const uint16_t*>(g);
+    else if (bytes == 8) *reinterpret_cast<uint2*>(&v) = *reinterpret_cast<const uint2*>(g);
+    else v = *reinterpret_cast<const uint4*>(g);
+    return v;
+}
+__device__ __forceinline__ void store_piece(uint8_t* g, int bytes, const uint4& v) {
+    if (bytes == 4) *reinterpret_cast<uint32_t*>(g) = v.x;
+    else if (bytes == 2) *reinterpret_cast<uint16_t*>(g) = static_cast<uint16_t>(v.x);
+    else if (bytes == 8) *reinterpret_cast<uint2*>(g) = make_uint2(v.x, v.y);
+    else *reinterpret_cast<uint4*>(g) = v;
+}
 
 // A cluster moves the kept rows of its (sequence, kv head) in rounds: every CTA loads its share
-// of the round's rows (codes into registers, scales into shared memory), the cluster's barrier,
-// then the stores.  Kept positions ascend, so kept[i] >= i: a round's stores reach only
-// positions below the round's end, no row that a later round has to read, and within the round
-// everything has been read; the move in place needs no second buffer, and the move into other
-// pages is the same path.  The bound is HBM: every row is read once (its scales with the
-// sectors of their neighbours, 32 bytes for a few) and written once, in whole lines.  One CTA
-// per (sequence, kv head) with chunks of 64 rows through shared memory took 173 us for
-// 8 x 32 x 2048 rows of 134 bytes (its chain of small round trips), and 332 us for 4 x 8 x 4095
-// of 264.
-__global__ void __launch_bounds__(kCmpThreads, 4) evict_compact_kernel(EvictCompactArgs p, int32_t rows_cta, int32_t lg_w) {
-    __shared__ long long s_src[kCmpMaxRows], s_dst[kCmpMaxRows];  // a row's block * 64 + slot; -1: stays
-    __shared__ __align__(16) uint8_t s_scale[kCmpScaleBytes];
+// of the round's rows into registers, the cluster's barrier, then the stores.  Kept positions
+// ascend, so kept[i] >= i: a round's stores reach only positions below the round's end, no row
+// that a later round has to read, and within the round everything has been read; the move in
+// place needs no second buffer, and the move into other pages is the same path.  A thread owns
+// a row's lookups, scales and weight, and 16-byte words of codes across the CTA's rows, whose
+// source and destination it finds in shared memory as byte offsets.  The bound is HBM: every
+// row is read once (in 64-byte accesses that its 64 code bytes, not aligned to them, half fill:
+// 2.2 times its bytes on 8 x 32 x 2048 rows of 134 bytes, ncu) and written once.
+// One CTA per (sequence, kv head) with chunks of 64 rows through shared memory took 173 us for
+// those rows (its chain of small round trips), and 332 us for 4 x 8 x 4095 of 264.
+__global__ void __launch_bounds__(kCmpThreads, 2) evict_compact_kernel(EvictCompactArgs p, int32_t rows_cta, int32_t lg_w) {
+    // offset of a row's K codes in the pool, where it comes from and where it goes; -1: it stays
+    __shared__ long long s_src[kCmpMaxRows], s_dst[kCmpMaxRows];
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank()), size = static_cast<int>(cluster.num_blocks());
     const int row = blockIdx.x / size;
@@ -279,6 +295,7 @@ __global__ void __launch_bounds__(kCmpThreads, 4) evict_compact_kernel(EvictComp
     const int tid = threadIdx.x;
     const int P = 1 << p.lg_p;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int32_t* kept = p.kept + static_cast<long long>(row) * p.keep;
     long long n = p.seq_lens[b];
     n = n < 0 ? 0 : n;
     long long cap = static_cast<long long>(p.max_blocks) << p.lg_p;
@@ -288,86 +305,80 @@ __global__ void __launch_bounds__(kCmpThreads, 4) evict_compact_kernel(EvictComp
         if (h == 0 && rank == 0 && tid == 0) raise_flag(p.status, KVQ_FLAG_BAD_POSITION);
     }
     const int m = static_cast<int>(min(n, static_cast<long long>(p.keep)));
-    const int32_t* kept = p.kept + static_cast<long long>(row) * p.keep;
     float* w = p.weights ? p.weights + static_cast<long long>(row) * p.weights_ld : nullptr;
     const int32_t* table = p.block_table + static_cast<long long>(b) * p.max_blocks;
     const int32_t* dtable = p.dst_table + static_cast<long long>(b) * p.dst_max_blocks;
     // a row's code words: 2^lg_w of K, then as many of V
-    const int word_mask = (2 << lg_w) - 1;
-    const int scale_row = p.row_bytes[2] + p.row_bytes[3];
+    const int half_mask = (1 << lg_w) - 1;
+    // this thread's row of the round at `base`: its position and its two pages, looked up a round
+    // ahead (the kept list and the tables do not change); t -1: none, -2: a bad entry
+    int t_next = -1, sp_next = 0, dp_next = 0;
+    auto look_up = [&](long long base) {
+        const long long i = base + static_cast<long long>(rank) * rows_cta + tid;
+        t_next = -1;
+        if (tid >= rows_cta || i >= m) return;
+        const bool in = (i >> p.lg_p) < p.dst_max_blocks;
+        if (in) dp_next = dtable[i >> p.lg_p];
+        t_next = kept[i];
+        if (!in || t_next < 0 || t_next >= n) t_next = -2;
+        else sp_next = table[t_next >> p.lg_p];
+    };
+    look_up(0);
     for (long long base = 0; base < m; base += static_cast<long long>(size) * rows_cta) {
         const long long r0 = base + static_cast<long long>(rank) * rows_cta;
         const int rows = r0 < m ? static_cast<int>(min(static_cast<long long>(rows_cta), m - r0)) : 0;
-        float wv[kCmpMaxRows / kCmpThreads];
-#pragma unroll
-        for (int k = 0; k < kCmpMaxRows / kCmpThreads; ++k) {
-            const int rr = tid + k * kCmpThreads;
-            wv[k] = 0.f;
-            if (rr >= rows) continue;
-            const int i = static_cast<int>(r0) + rr, t = kept[i];
+        // this thread's row: its weight and scales, and where the scales go
+        float wv = 0.f;
+        uint4 ks = make_uint4(0, 0, 0, 0), vs = ks;
+        uint8_t* to = nullptr;  // the destination block, or nullptr
+        int to_slot = 0;
+        if (tid < rows) {
+            const int t = t_next, sp = sp_next, dp = dp_next;
             long long src = -1, dst = -1;
-            if (t < 0 || t >= n || (i >> p.lg_p) >= p.dst_max_blocks) {
+            if (t < 0) {
                 raise_flag(p.status, KVQ_FLAG_BAD_POSITION);
             } else {
-                const int sp = table[t >> p.lg_p], dp = dtable[i >> p.lg_p];
+                const int ss = t & (P - 1), ds = (static_cast<int>(r0) + tid) & (P - 1);
+                if (w) wv = w[t];
                 if (sp < 0 || sp >= p.num_pages || dp < 0 || dp >= p.num_pages) {
                     raise_flag(p.status, KVQ_FLAG_BAD_PAGE);
-                } else if (sp != dp || (t & (P - 1)) != (i & (P - 1))) {
-                    src = ((static_cast<long long>(sp) * p.Hkv + h) << 6) | (t & (P - 1));
-                    dst = ((static_cast<long long>(dp) * p.Hkv + h) << 6) | (i & (P - 1));
+                } else if (sp != dp || ss != ds) {
+                    src = (static_cast<long long>(sp) * p.Hkv + h) * p.block_bytes;
+                    dst = (static_cast<long long>(dp) * p.Hkv + h) * p.block_bytes;
+                    const uint8_t* from = p.pool + src;
+                    to = p.pool + dst;
+                    to_slot = ds;
+                    ks = load_piece(from + p.sec_off[2] + ss * p.row_bytes[2], p.row_bytes[2]);
+                    vs = load_piece(from + p.sec_off[3] + ss * p.row_bytes[3], p.row_bytes[3]);
+                    src += ss * p.row_bytes[0];
+                    dst += ds * p.row_bytes[0];
                 }
-                if (w) wv[k] = w[t];
             }
-            s_src[rr] = src;
-            s_dst[rr] = dst;
+            s_src[tid] = src;
+            s_dst[tid] = dst;
         }
         __syncthreads();
-        auto address = [&](long long at, int off, int bytes) {
-            return p.pool + (at >> 6) * p.block_bytes + off + (at & 63) * bytes;
-        };
-        // word ww of a row: K's first (section 0 at offset 0), then V's
-        auto word = [&](long long at, int ww) {
-            return reinterpret_cast<uint4*>(address(at, (ww >> lg_w) * p.sec_off[1], p.row_bytes[0]) +
-                                            ((ww & (word_mask >> 1)) << 4));
-        };
         uint4 v[kCmpWords];
 #pragma unroll
         for (int k = 0; k < kCmpWords; ++k) {
-            const int e = tid + k * kCmpThreads, rr = e >> (lg_w + 1), ww = e & word_mask;
+            const int e = tid + k * kCmpThreads, rr = e >> (lg_w + 1);
+            const int off = ((e >> lg_w) & 1) * p.sec_off[1] + ((e & half_mask) << 4);
             v[k] = make_uint4(0, 0, 0, 0);
-            if (rr < rows && s_src[rr] >= 0)
-                v[k] = *word(s_src[rr], ww);
+            if (rr < rows && s_src[rr] >= 0) v[k] = *reinterpret_cast<const uint4*>(p.pool + s_src[rr] + off);
         }
-        // scales: 2-byte pieces, a row's K scales then its V scales in s_scale
-        auto scales = [&](bool load) {
-#pragma unroll
-            for (int sec = 2; sec < 4; ++sec) {
-                const int words = p.row_bytes[sec] >> 1, lg = 31 - __clz(words);  // a power of two
-                for (int e = tid; e < rows * words; e += kCmpThreads) {
-                    const int rr = e >> lg, ww = e & (words - 1);
-                    const long long at = load ? s_src[rr] : s_dst[rr];
-                    if (at < 0) continue;
-                    uint16_t* g = reinterpret_cast<uint16_t*>(address(at, p.sec_off[sec], p.row_bytes[sec])) + ww;
-                    uint16_t* s = reinterpret_cast<uint16_t*>(s_scale + rr * scale_row + (sec == 3 ? p.row_bytes[2] : 0)) + ww;
-                    if (load) *s = *g;
-                    else *g = *s;
-                }
-            }
-        };
-        scales(true);
+        look_up(base + static_cast<long long>(size) * rows_cta);
         cluster.sync();  // the round has been read
 #pragma unroll
         for (int k = 0; k < kCmpWords; ++k) {
-            const int e = tid + k * kCmpThreads, rr = e >> (lg_w + 1), ww = e & word_mask;
-            if (rr < rows && s_dst[rr] >= 0)
-                *word(s_dst[rr], ww) = v[k];
+            const int e = tid + k * kCmpThreads, rr = e >> (lg_w + 1);
+            const int off = ((e >> lg_w) & 1) * p.sec_off[1] + ((e & half_mask) << 4);
+            if (rr < rows && s_dst[rr] >= 0) *reinterpret_cast<uint4*>(p.pool + s_dst[rr] + off) = v[k];
         }
-        scales(false);
-        if (w) {
-#pragma unroll
-            for (int k = 0; k < kCmpMaxRows / kCmpThreads; ++k)
-                if (tid + k * kCmpThreads < rows) w[r0 + tid + k * kCmpThreads] = wv[k];
+        if (to != nullptr) {
+            store_piece(to + p.sec_off[2] + to_slot * p.row_bytes[2], p.row_bytes[2], ks);
+            store_piece(to + p.sec_off[3] + to_slot * p.row_bytes[3], p.row_bytes[3], vs);
         }
+        if (w && tid < rows) w[r0 + tid] = wv;
         __syncthreads();
     }
     // (every round's weights have been read: the last barrier)
@@ -417,8 +428,7 @@ cudaError_t launch_evict_compact(const EvictCompactArgs& a, cudaStream_t stream)
     // rows a CTA holds: its threads' code words over a row's (K and V, 16 bytes each)
     int lg_w = 0;
     while ((16 << lg_w) < a.row_bytes[0]) ++lg_w;
-    int rows_cta = (kCmpThreads * kCmpWords) >> (lg_w + 1);
-    rows_cta = std::min({rows_cta, kCmpMaxRows, kCmpScaleBytes / (a.row_bytes[2] + a.row_bytes[3])});
+    const int rows_cta = std::min((kCmpThreads * kCmpWords) >> (lg_w + 1), kCmpMaxRows);
     // the smallest cluster that moves a sequence in one round, at most 8 (the portable size)
     int cl = 1;
     while (cl < 8 && cl * rows_cta < a.keep) cl *= 2;
