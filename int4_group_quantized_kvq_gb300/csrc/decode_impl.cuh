@@ -84,11 +84,22 @@ namespace decode {
 constexpr uint64_t kWaitLimitNs = 250000000ull;   // a page copy that takes 250 ms has failed
 
 // Warps per CTA, and resident CTAs per SM the register budget is tuned for: 3 (up to 168
-// registers) when a thread carries one query-head slot of head_dim <= 128, else 2.
+// registers) when a thread carries one query-head slot of head_dim <= 128, else 2.  Modes 1
+// and 2 take 3 with two slots too where that spills next to nothing: head_dim 64, and INT4
+// with one n-tile of scores (differential, K groups of 64, 4 x 32 / 8 heads of 131072
+// positions: 157 -> 143 us; with two tiles or the INT8 codes 60 to 600 bytes a thread spill,
+// and those shapes slow down by 8 to 75%).
 template <int HS>
 constexpr int cta_warps() { return 4; }
-template <int HS, int D = 128, int MODE = 0>
-constexpr int min_ctas() { return HS == 1 && D <= 128 ? 3 : 2; }
+template <int HS, int D = 128, int MODE = 0, int CODEC = 0, int TILES = 2>
+constexpr int min_ctas() {
+    return D <= 128 && (HS == 1 || (MODE != 0 && (D == 64 || (CODEC == 0 && TILES == 1)))) ? 3 : 2;
+}
+// K groups a score slot sums over, and n-tiles of scores, of a kernel instance
+template <int D, int GK, int MODE>
+constexpr int slot_groups() { return MODE == 2 ? D / GK / 2 : D / GK; }
+template <int D, int GK, int HS, int MODE>
+constexpr int score_tiles() { return (HS * slot_groups<D, GK, MODE>() + 1) / 2; }
 
 // CTA-wide bookkeeping in shared memory.
 struct CtaCtl {
@@ -418,7 +429,7 @@ __device__ __forceinline__ void load_scales(const uint8_t* p, float (&a)[N], flo
 // some 1e-5.  The plain output tolerates it; the weights are fp32 results of their own, and a
 // difference of two maps keeps only what does not cancel.
 template <int D, int GK, int GV, int HK, int HS, bool WIN, bool P16, int CODEC = 0, int MODE = 0>
-__global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D, MODE>()) decode_splitkv_kernel(KParams p) {
+__global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D, MODE, CODEC, score_tiles<D, GK, HS, MODE>()>()) decode_splitkv_kernel(KParams p) {
     static_assert(D == 64 || D == 128 || D == 256, "head_dim 64, 128 or 256");
     static_assert(CODEC == 0 || (CODEC == 1 && D == 128 && GK == D && GV == D && HK == 1), "INT8: d 128, rows");
     static_assert(D <= 128 || (HK == 1 && HS == 1), "head_dim 256: one-head units, up to 4 query heads each");
@@ -443,8 +454,8 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D, MODE>())
     // K groups a score slot sums over: all of a row's, in MODE 2 those of the slot's half.  In
     // MODE 2 the slots are virtual heads (even: first map) when they are four at most; with more,
     // a thread's slot c is query head c and its two slots are the two maps.
-    constexpr int NG = MODE == 2 ? NGK / 2 : NGK;
-    constexpr int NTQ = (HS * NG + 1) / 2;    // score n-tiles
+    constexpr int NG = slot_groups<D, GK, MODE>();
+    constexpr int NTQ = score_tiles<D, GK, HS, MODE>();  // score n-tiles
     constexpr int VB = GV / 16;               // V code bytes per thread per group per row
     constexpr int MT = D / 16;                // output m-tiles
     constexpr int ROW = I8 ? D : D / 2;       // bytes of one token's codes
