@@ -429,11 +429,12 @@ int kvq_mixed_decode_attention(const kvq_cache_config *cfg, const void *pool, co
  *   decay           in [0, 1]: 1 accumulates, 0 keeps this call's weights alone (what weights
  *                   held is not read then), a value between lets older weight fade.
  *   weights         device fp32 [batch, num_kv_heads, weights_stride], updated in place.
- *   weights_stride  floats per kv head, >= max_len.
+ *   weights_stride  floats per kv head, >= max_len (at most 2^30).
  *   max_len         as in kvq_decode_attention; a longer seq_lens[b] raises
  *                   KVQ_FLAG_BAD_POSITION and max_len positions are attended to.
  *   workspace       >= kvq_decode_weights_workspace_bytes(...): beside the partial results it
- *                   holds the scores of the call (4 bytes per position and query head).
+ *                   holds the scores of the call (4 bytes per position and query head).  Calls
+ *                   that share a workspace must not overlap on the GPU.
  *   other arguments, shapes and the launch overlap as in kvq_decode_attention (weights is
  *   read and written after the kernel ahead has finished).
  * kvq_decode_step_weights: the same with one new token per sequence appended first, as
@@ -478,8 +479,7 @@ int kvq_int8_decode_attention_weights(const kvq_cache_config *cfg, const void *p
  *   keep            >= 1 and >= sinks + recent.
  *   kept            device int32 [batch, num_kv_heads, keep]: the positions kept, ascending,
  *                   then -1 up to keep.
- *   new_lens        device int32 [batch]: min(n, keep).  May be seq_lens itself only when no
- *                   kvq_evict_compact of this cut follows (it needs the old lengths).
+ *   new_lens        device int32 [batch]: min(n, keep).  Not seq_lens itself (KVQ_EINVAL).
  *   status          device uint32 status word or NULL.
  * Returns KVQ_OK, KVQ_EINVAL, KVQ_EUNSUPPORTED or KVQ_ECUDA.
  */

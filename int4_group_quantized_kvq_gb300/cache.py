@@ -13,7 +13,8 @@ the first ``sinks`` (``kvq_decode_attention_window`` / ``kvq_decode_step_window`
 With ``track_weights`` the cache also accumulates the attention weight each cached position
 receives (``kvq_decode_attention_weights`` / ``kvq_decode_step_weights``), and ``evict`` cuts it
 by that measure to a budget of positions, each KV head keeping its own
-(``kvq_evict_select``, ``kvq_evict_compact``).  ``attend_diff`` and ``decode_step_diff`` read the
+(``kvq_evict_select``, ``kvq_evict_compact``).  A batch slot that takes a new sequence starts with
+``cache.weights[b] = 0``.  ``attend_diff`` and ``decode_step_diff`` read the
 same pool as differential attention, for a cache made with ``diff`` (``kvq_diff_decode_attention`` / ``kvq_diff_decode_step``).
 
 ``decode_step_host`` is the same step driven from pinned host buffers (``HostStaging``)

@@ -469,7 +469,6 @@ cudaError_t launch_combine(const DecodeArgs& a, const DecodePlan& plan, cudaStre
     cudaError_t err = launch(p, a.mode, a.L.d, plan.combine_warps, stream);
     const long long adders = static_cast<long long>(a.B) * a.Hkv * p.chunks;
     if (err != cudaSuccess || a.mode != DecodeMode::kWeights || adders == 0) return err;
-    if (adders > 0x7fffffffLL) return cudaErrorInvalidValue;
     // launched while the combine runs; the kernel waits for it before it reads the workspace
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -196,7 +196,8 @@ cudaError_t plan_decode(const DecodeArgs& a, DecodePlan* plan) {
         plan->ws_score_offset += round_up(static_cast<size_t>(a.B) * a.Hq * 2 * sizeof(float), kAlign);
         // whole sectors per 8 positions of every query head
         const size_t ld = round_up(static_cast<size_t>(std::max(a.max_len, 0)), 32);
-        if (ld > 0x7fffffff) return cudaErrorInvalidValue;
+        // (the weights' kernel: at least 512 positions of a kv head per CTA)
+        if (ld > 0x7fffffff || static_cast<size_t>(a.B) * a.Hkv * (ld / 512 + 1) > 0x7fffffff) return cudaErrorInvalidValue;
         plan->score_ld = static_cast<int32_t>(ld);
         plan->ws_bytes = plan->ws_score_offset + round_up(static_cast<size_t>(a.B) * a.Hq * ld * sizeof(float), kAlign);
     }

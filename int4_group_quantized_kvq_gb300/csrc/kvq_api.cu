@@ -63,6 +63,8 @@ int check_decode_shape(const kvq_cache_config* c, int r, int codec) {
     return KVQ_OK;
 }
 
+constexpr int32_t kMaxWeightLen = 1 << 30;  // positions of a kv head's weights (32-bit position arithmetic)
+
 // Differential attention: the halves of a K row are two keys, so a K group may not span both,
 // and a query head is two virtual heads of the decode kernel.
 int check_diff_shape(const kvq_cache_config* c, int r) {
@@ -536,11 +538,12 @@ int decode_mode_impl(const char* name, kvq::DecodeMode mode, const ModeArgs& x, 
         if (!(x.decay >= 0.f && x.decay <= 1.f)) return fail(KVQ_EINVAL, "decay must be in [0, 1]");
         if (x.weights_stride < max_len)
             return fail(KVQ_EINVAL, "weights_stride %d < max_len %d", x.weights_stride, max_len);
+        if (max_len > kMaxWeightLen) return fail(KVQ_EUNSUPPORTED, "max_len %d > 2^30", max_len);
     }
     if (batch == 0) return ok();
     if (max_blocks < 1) return fail(KVQ_EINVAL, "max_blocks %d < 1", max_blocks);
     if (!pool || !q || !block_table || !seq_lens || !out || !workspace || (append && (!k_new || !v_new || !append_pos)) ||
-        (diff ? !x.lambda : !x.weights))
+        (diff ? !x.lambda : !x.weights && max_len > 0))
         return fail(KVQ_EINVAL, "NULL device pointer");
     if (!aligned(pool, 16) || !aligned(q, 16) || !aligned(out, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) ||
         !aligned(x.norm_weight, 16))
@@ -689,10 +692,13 @@ int kvq_evict_select(const kvq_cache_config* cfg, const float* weights, int32_t 
         return fail(KVQ_EINVAL, "keep %d, sinks %d, recent %d: keep must be at least 1 and sinks + recent", keep, sinks,
                     recent);
     if (weights_stride < max_len) return fail(KVQ_EINVAL, "weights_stride %d < max_len %d", weights_stride, max_len);
+    if (max_len > kMaxWeightLen) return fail(KVQ_EUNSUPPORTED, "max_len %d > 2^30", max_len);
     if (batch > 65535) return fail(KVQ_EUNSUPPORTED, "batch %d > 65535", batch);
     if (cfg->num_kv_heads > 65535) return fail(KVQ_EUNSUPPORTED, "num_kv_heads %d > 65535", cfg->num_kv_heads);
     if (batch == 0) return ok();
-    if (!weights || !seq_lens || !kept || !new_lens) return fail(KVQ_EINVAL, "NULL device pointer");
+    if ((!weights && max_len > 0) || !seq_lens || !kept || !new_lens) return fail(KVQ_EINVAL, "NULL device pointer");
+    // every kv head reads the length of its sequence while one of them writes the new one
+    if (seq_lens == new_lens) return fail(KVQ_EINVAL, "new_lens must not be seq_lens");
     if (!aligned(weights, 4) || !aligned(seq_lens, 4) || !aligned(kept, 4) || !aligned(new_lens, 4) || !aligned(status, 4))
         return fail(KVQ_EINVAL, "arguments must be 4-byte aligned");
     kvq::EvictSelectArgs a;

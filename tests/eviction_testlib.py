@@ -11,9 +11,11 @@ EPS32 = 2.0 ** -24  # half a step of fp32
 class Pool:
     """A random pool of `codec` ("int4" or "int8") with a block table for sequences of `lens` positions.
 
-    Rows hold random codes over the whole code range and scales of a few binades, as the quantizers store them."""
+    Rows hold random codes over the whole code range and scales of a few binades, as the quantizers store them;
+    with `poison` every byte that no position owns is 0xFF, a NaN as a scale."""
 
-    def __init__(self, codec, Hkv, d, lens, P=16, Gk=64, Gv=64, seed=0, spare=2, blocks=None):
+    def __init__(self, codec, Hkv, d, lens, P=16, Gk=64, Gv=64, seed=0, spare=2, blocks=None,
+                 poison=False):
         self.codec, self.Hkv, self.d, self.P, self.Gk, self.Gv, self.lens = codec, Hkv, d, P, Gk, Gv, list(lens)
         rng = np.random.default_rng(seed)
         pages = [(n + P - 1) // P for n in self.lens]
@@ -43,6 +45,12 @@ class Pool:
                 s = base * np.exp2(rng.uniform(-2, 1, (self.num_pages, Hkv, n)))
                 v = s.astype(np.float32 if codec == "int8" else np.float16).view(np.uint8)
             x[:, :, self.off[i]:self.off[i] + v.shape[-1]] = v
+        if poison:  # slots behind each sequence's end, and spare pages: NaN scales and extreme codes
+            x[self.spare] = 0xFF
+            for b, n in enumerate(self.lens):
+                for slot in range(n % P if n else 0, P if n % P else 0):
+                    for o, r in zip(self.off, self.row):
+                        x[self.table[b, n // P], :, o + slot * r:o + (slot + 1) * r] = 0xFF
         self.bytes = x
 
     def cfg(self, kvq):

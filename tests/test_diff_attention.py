@@ -50,7 +50,7 @@ def check(pool, q, lam, gain, eps, scale, out, table=None, x=None):
 ])
 @pytest.mark.parametrize("norm", [False, True])
 def test_matches_fp64(kvq, Hkv, r, d, P, Gk, Gv, lens, norm):
-    pool = Pool("int4", Hkv, d, lens, P, Gk, Gv, seed=d + r)
+    pool = Pool("int4", Hkv, d, lens, P, Gk, Gv, seed=d + r, poison=True)
     q, cfg = make_q(len(lens), Hkv * r, d, 3), pool.cfg(kvq)
     lam = torch.linspace(-0.5, 1.2, Hkv * r, device="cuda")
     gain = torch.randn(d, device="cuda") if norm else None

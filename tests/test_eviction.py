@@ -75,7 +75,7 @@ def check_weights(pool, q, decay, before, out, after, lens=None):
 ])
 @pytest.mark.parametrize("decay", [1.0, 0.0, 0.75])
 def test_attention_and_weights_match_fp64(kvq, Hkv, r, d, P, Gk, Gv, lens, decay):
-    pool = Pool("int4", Hkv, d, lens, P, Gk, Gv, seed=d + r)
+    pool = Pool("int4", Hkv, d, lens, P, Gk, Gv, seed=d + r, poison=True)
     q = make_q(len(lens), Hkv * r, d, 3)
     before = torch.rand(len(lens), Hkv, max(lens) + 5, device="cuda")
     if decay == 0.0:
@@ -89,7 +89,7 @@ def test_attention_and_weights_match_fp64(kvq, Hkv, r, d, P, Gk, Gv, lens, decay
 @pytest.mark.parametrize("Hkv,r,P,lens", [(4, 1, 16, [1, 0, 513]), (2, 4, 64, [64, 700]), (2, 6, 32, [33, 250]),
                                           (1, 8, 16, [1025])])
 def test_int8_attention_and_weights_match_fp64(kvq, Hkv, r, P, lens):
-    pool = Pool("int8", Hkv, 128, lens, P, 128, 128, seed=r)
+    pool = Pool("int8", Hkv, 128, lens, P, 128, 128, seed=r, poison=True)
     q = make_q(len(lens), Hkv * r, 128, 4)
     before = torch.rand(len(lens), Hkv, max(lens), device="cuda")
     weights = before.clone()
@@ -444,6 +444,81 @@ def test_decode_right_behind_select_and_compact(kvq):
     want = go(True)
     for _ in range(5):
         assert torch.equal(go(False), want)
+
+
+def test_nothing_to_attend_and_no_positions(kvq):
+    pool = Pool("int4", 2, 128, [0, 0], 16, 64, 128, seed=6)
+    cfg, q = pool.cfg(kvq), make_q(2, 4, 128, 2)
+    w, out = torch.full((2, 2, 9), 3.0, device="cuda"), torch.full((2, 4, 128), 7.0, device="cuda")
+    ws = kvq.new_weights_workspace(cfg, 2, 4, 9)
+    kvq.kvq_decode_attention_weights(cfg, pool.gpu(), q, pool.table_gpu(), pool.lens_gpu(), 9, 0.1, 1.0, w, out, ws)
+    assert not out.any() and (w == 3.0).all() and kvq.kvq_read_status(ws) == 0
+    none = torch.empty(2, 2, 0, device="cuda")
+    kvq.kvq_decode_attention_weights(cfg, pool.gpu(), q, pool.table_gpu(), pool.lens_gpu(), 0, 0.1, 1.0, none, out, ws)
+    got, new = run_select(kvq, none, [0, 0], 0, 3, 1, 1)
+    assert (got == -1).all() and not new.any()
+    x, u = run_compact(kvq, pool, pool.table, pool.table, got, np.zeros((2, 2, 4), np.float32))
+    assert np.array_equal(x, pool.bytes) and not u.any()
+
+
+def test_a_row_of_nan_stays_in_its_row(kvq):
+    for Hkv, r in ((8, 1), (2, 4)):
+        pool = Pool("int4", Hkv, 128, [70, 90], 16, 64, 128, seed=6)
+        q = make_q(2, Hkv * r, 128, 2)
+        clean, w0 = q.clone(), torch.zeros(2, Hkv, 90, device="cuda")
+        out0, _ = call_weights(kvq, pool, pool.gpu(), clean, 1.0, w0)
+        q[0, 1, 5] = float("nan")
+        w1 = torch.zeros(2, Hkv, 90, device="cuda")
+        out1, _ = call_weights(kvq, pool, pool.gpu(), q, 1.0, w1)
+        rows = torch.ones(2, Hkv * r, dtype=torch.bool)
+        rows[0, 1] = False
+        heads = torch.ones(2, Hkv, dtype=torch.bool)
+        heads[0, 1 // r] = False
+        assert torch.equal(out0.cpu()[rows], out1.cpu()[rows]) and torch.equal(w0.cpu()[heads], w1.cpu()[heads])
+
+
+def test_select_and_compact_replayed_from_a_graph(kvq):
+    pool = Pool("int8", 2, 128, [3000, 40], 32, 128, 128, seed=6)
+    cfg, table, lens = pool.cfg(kvq), pool.table_gpu(), pool.lens_gpu()
+    x, w = pool.gpu(), torch.rand(2, 2, 3000, device="cuda")
+    x0, w0 = x.clone(), w.clone()
+    kept, new = torch.empty(2, 2, 500, dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+
+    def go():
+        kvq.kvq_evict_select(cfg, w, lens, 3000, 500, 4, 64, kept, new)
+        kvq.kvq_int8_evict_compact(cfg, x, table, table, lens, kept, w)
+
+    go()
+    want = x.clone(), w.clone(), kept.clone(), new.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go()
+    for _ in range(2):
+        x.copy_(x0)
+        w.copy_(w0)
+        kept.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(want, (x, w, kept, new)))
+
+
+def test_cache_refuses_what_it_does_not_track(kvq):
+    from int4_group_quantized_kvq_gb300.cache import HostPipeline, HostStaging, PagedKVCache
+    cfg = kvq.config(2, 128, 16, 64, 128, 8)
+    table = torch.arange(8, dtype=torch.int32).view(1, 8)
+    lens = torch.tensor([20], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        PagedKVCache(cfg, table, 4, 128, window=16, track_weights=True)
+    plain, tracked = PagedKVCache(cfg, table, 4, 128), PagedKVCache(cfg, table, 4, 128, track_weights=True)
+    with pytest.raises(ValueError):
+        plain.evict(lens, 10)
+    with pytest.raises(ValueError):
+        plain.attend_diff(None, None, lens, None)
+    with pytest.raises(ValueError):
+        tracked.evict(lens, 100, dst_table=table[:, :2].cuda().contiguous())
+    with pytest.raises(ValueError):
+        tracked.decode_step_host(HostStaging(1, 4, 2, 128, "cuda"), lens, lens)
+    with pytest.raises(ValueError):
+        HostPipeline(tracked).step(0, lens, lens)
 
 
 def test_tensors_are_checked(kvq):

@@ -29,7 +29,7 @@ def test_weights_calls_refuse(kvq):
                           (dict(decay=1.01), 1), (dict(decay=float("nan")), 1), (dict(pool=0x1008), 1),
                           (dict(out=None), 1), (dict(ws=0x7010), 1), (dict(Hq=12), 1), (dict(Hq=72), 2),
                           (dict(B=-1), 1), (dict(B=5000), 2), (dict(blocks=0), 1), (dict(max_len=-1), 1),
-                          (dict(lens=0x4002), 1)):
+                          (dict(max_len=(1 << 30) + 1, stride=(1 << 30) + 1), 2), (dict(lens=0x4002), 1)):
             assert fn(*weights_args(kvq, cfg, **bad)) == code, bad
             assert kvq.kvq_last_error()
         assert fn(*weights_args(kvq, cfg, B=0, w=None, pool=None)) == kvq.KVQ_OK
@@ -56,6 +56,7 @@ def test_select_refuses(kvq):
     for bad, code in ((dict(w=None), 1), (dict(kept=None), 1), (dict(new=None), 1), (dict(lens=None), 1),
                       (dict(stride=99), 1), (dict(keep=0), 1), (dict(keep=4), 1), (dict(sinks=-1), 1),
                       (dict(recent=-1), 1), (dict(recent=0x7fffffff, sinks=0x7fffffff), 1), (dict(B=-1), 1),
+                      (dict(new=0x2000), 1), (dict(max_len=(1 << 30) + 1, stride=(1 << 30) + 1), 2),
                       (dict(max_len=-1), 1), (dict(w=0x1001), 1), (dict(status=0x5001), 1), (dict(B=70000), 2)):
         assert call(**bad) == code, bad
         assert kvq.kvq_last_error()
