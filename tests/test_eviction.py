@@ -219,7 +219,8 @@ def run_select(kvq, w, lens, max_len, keep, sinks, recent, status=None):
 @pytest.mark.parametrize("lens,keep,sinks,recent", [
     ([1, 0, 2, 5], 1, 0, 0), ([1, 0, 2, 5], 1, 1, 0), ([3, 9, 10, 11], 10, 4, 6), ([100, 7, 64], 64, 4, 16),
     ([1025, 1024, 1023], 511, 0, 1), ([5000, 4097, 33], 33, 1, 31), ([20000, 3], 4096, 4, 512),
-    ([70001], 65000, 3, 100), ([131072], 1, 0, 0), ([300, 299], 400, 2, 2),
+    ([70001], 65000, 3, 100), ([131072], 1, 0, 0), ([300, 299], 400, 2, 2), ([32769, 32768, 2048], 9000, 1, 1),
+    ([300001], 50000, 7, 1000), ([2049], 2000, 0, 0),
 ])
 @pytest.mark.parametrize("kind", ["spread", "ties", "equal", "odd"])
 def test_select_matches_numpy(kvq, lens, keep, sinks, recent, kind):
