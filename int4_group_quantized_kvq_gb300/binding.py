@@ -616,6 +616,9 @@ def kvq_test_decode_wait_timeout(cfg: CacheConfig, pool: torch.Tensor, q: torch.
 # ---------------------------------------------------------------------------
 # Attention weights of cached positions, eviction by them, differential attention
 # ---------------------------------------------------------------------------
+_F16, _F32, _I32, _U8 = torch.float16, torch.float32, torch.int32, torch.uint8
+
+
 # These calls run once per layer and token, so their checks are kept to a few attribute reads per tensor.
 def _shaped(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: int) -> int:
     """The address of a contiguous CUDA tensor on device `dev` (the current one), of that dtype and shape."""
@@ -640,7 +643,7 @@ def _dims(t: torch.Tensor, name: str, n: int) -> tuple:
 
 def _bytes(t: torch.Tensor, name: str, dev: int) -> tuple[int, int]:
     """Address and size of a uint8 buffer."""
-    return _shaped(t, name, torch.uint8, getattr(t, "shape", ()), dev), t.numel()
+    return _shaped(t, name, _U8, getattr(t, "shape", ()), dev), t.numel()
 
 
 def _pool_at(t: torch.Tensor, need: int, dev: int) -> int:
@@ -656,7 +659,7 @@ def _new_rows(t: torch.Tensor, name: str, batch: int, cfg: CacheConfig, dev: int
     shape = (batch, cfg.num_kv_heads, cfg.head_dim)
     if len(getattr(t, "shape", ())) == 4:
         shape = (batch, 1, cfg.num_kv_heads, cfg.head_dim)
-    return _shaped(t, name, torch.float16, shape, dev)
+    return _shaped(t, name, _F16, shape, dev)
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -698,47 +701,67 @@ def kvq_diff_decode_workspace_bytes(cfg: CacheConfig, batch: int, num_q_heads: i
 def new_weights_workspace(cfg: CacheConfig, batch: int, num_q_heads: int, max_len: int,
                           device="cuda") -> torch.Tensor:
     """A workspace of the decode calls with weights, its status word zeroed."""
-    return torch.zeros(kvq_decode_weights_workspace_bytes(cfg, batch, num_q_heads, max_len), dtype=torch.uint8,
+    return torch.zeros(kvq_decode_weights_workspace_bytes(cfg, batch, num_q_heads, max_len), dtype=_U8,
                        device=device)
 
 
 def new_int8_weights_workspace(cfg: CacheConfig, batch: int, num_q_heads: int, max_len: int,
                                device="cuda") -> torch.Tensor:
-    return torch.zeros(kvq_int8_decode_weights_workspace_bytes(cfg, batch, num_q_heads, max_len), dtype=torch.uint8,
+    return torch.zeros(kvq_int8_decode_weights_workspace_bytes(cfg, batch, num_q_heads, max_len), dtype=_U8,
                        device=device)
 
 
 def new_diff_workspace(cfg: CacheConfig, batch: int, num_q_heads: int, max_len: int, device="cuda") -> torch.Tensor:
     """A workspace of the differential decode calls, its status word zeroed."""
-    return torch.zeros(kvq_diff_decode_workspace_bytes(cfg, batch, num_q_heads, max_len), dtype=torch.uint8,
+    return torch.zeros(kvq_diff_decode_workspace_bytes(cfg, batch, num_q_heads, max_len), dtype=_U8,
                        device=device)
 
 
-def _decode_head(cfg, pool, pool_need, q, block_table, seq_lens, out, dev):
-    """(batch, query heads), the C arguments pool, q, block_table, max_blocks, seq_lens, and out."""
+def _decode_args(cfg, ref, pool, pool_need, q, block_table, seq_lens, out, workspace, dev):
+    """batch, query heads, and the C arguments (pool, q, block_table, max_blocks, seq_lens), out, (workspace, bytes)."""
     shape = _dims(q, "q", 3)
     B, Hq, d = shape
     if d != cfg.head_dim:
         raise ValueError(f"q must be [batch, num_q_heads, {cfg.head_dim}], got {list(shape)}")
     blocks = _dims(block_table, "block_table", 2)[1]
-    return B, Hq, (_pool_at(pool, pool_need, dev), _shaped(q, "q", torch.float16, shape, dev),
-                   _shaped(block_table, "block_table", torch.int32, (B, blocks), dev), blocks,
-                   _shaped(seq_lens, "seq_lens", torch.int32, (B,), dev)), \
-        _shaped(out, "out", torch.float32, shape, dev)
+    try:  # everything as it should be, in one expression
+        if (q.dtype is _F16 and out.dtype is _F32 and out.shape == shape
+                and block_table.dtype is seq_lens.dtype is _I32 and block_table.shape[0] == B
+                and seq_lens.shape == (B,) and pool.dtype is workspace.dtype is _U8
+                and pool.numel() >= pool_need > 0
+                and q.get_device() == out.get_device() == block_table.get_device() == seq_lens.get_device()
+                == pool.get_device() == workspace.get_device() == dev
+                and q.is_contiguous() and out.is_contiguous() and block_table.is_contiguous()
+                and seq_lens.is_contiguous() and pool.is_contiguous() and workspace.is_contiguous()):
+            return B, Hq, (pool.data_ptr(), q.data_ptr(), block_table.data_ptr(), blocks, seq_lens.data_ptr()), \
+                out.data_ptr(), (workspace.data_ptr(), workspace.numel())
+    except AttributeError:
+        pass
+    # what is wrong, tensor by tensor
+    return B, Hq, (_pool_at(pool, pool_need, dev), _shaped(q, "q", _F16, shape, dev),
+                   _shaped(block_table, "block_table", _I32, (B, blocks), dev), blocks,
+                   _shaped(seq_lens, "seq_lens", _I32, (B,), dev)), \
+        _shaped(out, "out", _F32, shape, dev), _bytes(workspace, "workspace", dev)
 
 
 def _weights_call(fn, pool_bytes, cfg, pool, q, block_table, seq_lens, max_len, softmax_scale, decay, weights, out,
                   workspace, stream, step=None) -> None:
     dev = torch.cuda.current_device()
     ref = C.byref(cfg)
-    B, Hq, (pp, qp, bt, blocks, sl), op = _decode_head(cfg, pool, pool_bytes(ref), q, block_table, seq_lens, out, dev)
+    B, Hq, (pp, qp, bt, blocks, sl), op, (wp, wn) = _decode_args(cfg, ref, pool, pool_bytes(ref), q, block_table,
+                                                                 seq_lens, out, workspace, dev)
     stride = _dims(weights, "weights", 3)[2]
-    w = _shaped(weights, "weights", torch.float32, (B, cfg.num_kv_heads, stride), dev)
-    new = () if step is None else (_new_rows(step[0], "k_new", B, cfg, dev), _new_rows(step[1], "v_new", B, cfg, dev),
-                                   _shaped(step[2], "append_pos", torch.int32, (B,), dev))
-    rc = fn(ref, pp, *new, qp, bt, blocks, sl, B, Hq, int(max_len), float(softmax_scale), float(decay), w, stride, op,
-            *_bytes(workspace, "workspace", dev), _stream_on(stream, dev))
-    _check(rc)
+    w = _shaped(weights, "weights", _F32, (B, cfg.num_kv_heads, stride), dev)
+    st = _stream_on(stream, dev)
+    if step is None:
+        rc = fn(ref, pp, qp, bt, blocks, sl, B, Hq, int(max_len), float(softmax_scale), float(decay), w, stride, op, wp,
+                wn, st)
+    else:
+        rc = fn(ref, pp, _new_rows(step[0], "k_new", B, cfg, dev), _new_rows(step[1], "v_new", B, cfg, dev),
+                _shaped(step[2], "append_pos", _I32, (B,), dev), qp, bt, blocks, sl, B, Hq, int(max_len),
+                float(softmax_scale), float(decay), w, stride, op, wp, wn, st)
+    if rc:
+        _check(rc)
 
 
 def kvq_decode_attention_weights(cfg: CacheConfig, pool: torch.Tensor, q: torch.Tensor, block_table: torch.Tensor,
@@ -783,12 +806,24 @@ def kvq_evict_select(cfg: CacheConfig, weights: torch.Tensor, seq_lens: torch.Te
     L = lib()
     B, H, dev = _dims(seq_lens, "seq_lens", 1)[0], cfg.num_kv_heads, torch.cuda.current_device()
     stride = _dims(weights, "weights", 3)[2]
-    rc = L.kvq_evict_select(
-        C.byref(cfg), _shaped(weights, "weights", torch.float32, (B, H, stride), dev), stride,
-        _shaped(seq_lens, "seq_lens", torch.int32, (B,), dev), B, int(max_len), int(keep), int(sinks), int(recent),
-        _shaped(kept, "kept", torch.int32, (B, H, keep), dev), _shaped(new_lens, "new_lens", torch.int32, (B,), dev),
-        _own_status(status, dev), _stream_on(stream, dev))
-    _check(rc)
+    try:  # everything as it should be, in one expression
+        good = (weights.dtype is _F32 and weights.shape == (B, H, stride) and kept.shape == (B, H, keep)
+                and new_lens.shape == (B,) and seq_lens.dtype is kept.dtype is new_lens.dtype is _I32
+                and weights.get_device() == seq_lens.get_device() == kept.get_device() == new_lens.get_device() == dev
+                and weights.is_contiguous() and seq_lens.is_contiguous() and kept.is_contiguous()
+                and new_lens.is_contiguous())
+    except AttributeError:
+        good = False
+    if not good:  # what is wrong, tensor by tensor
+        _shaped(weights, "weights", _F32, (B, H, stride), dev)
+        _shaped(seq_lens, "seq_lens", _I32, (B,), dev)
+        _shaped(kept, "kept", _I32, (B, H, keep), dev)
+        _shaped(new_lens, "new_lens", _I32, (B,), dev)
+    rc = L.kvq_evict_select(C.byref(cfg), weights.data_ptr(), stride, seq_lens.data_ptr(), B, int(max_len), int(keep),
+                            int(sinks), int(recent), kept.data_ptr(), new_lens.data_ptr(),
+                            None if status is None else _own_status(status, dev), _stream_on(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def _compact_call(fn, pool_bytes, cfg, pool, block_table, dst_table, seq_lens, kept, weights, status, stream) -> None:
@@ -801,10 +836,10 @@ def _compact_call(fn, pool_bytes, cfg, pool, block_table, dst_table, seq_lens, k
     blocks, dst_blocks = _dims(block_table, "block_table", 2)[1], _dims(dst_table, "dst_table", 2)[1]
     stride = 0 if weights is None else _dims(weights, "weights", 3)[2]
     rc = fn(ref, _pool_at(pool, pool_bytes(ref), dev),
-            _shaped(block_table, "block_table", torch.int32, (B, blocks), dev), blocks,
-            _shaped(dst_table, "dst_table", torch.int32, (B, dst_blocks), dev), dst_blocks,
-            _shaped(seq_lens, "seq_lens", torch.int32, (B,), dev), B, _shaped(kept, "kept", torch.int32, shape, dev),
-            keep, None if weights is None else _shaped(weights, "weights", torch.float32, (B, H, stride), dev), stride,
+            _shaped(block_table, "block_table", _I32, (B, blocks), dev), blocks,
+            _shaped(dst_table, "dst_table", _I32, (B, dst_blocks), dev), dst_blocks,
+            _shaped(seq_lens, "seq_lens", _I32, (B,), dev), B, _shaped(kept, "kept", _I32, shape, dev),
+            keep, None if weights is None else _shaped(weights, "weights", _F32, (B, H, stride), dev), stride,
             _own_status(status, dev), _stream_on(stream, dev))
     _check(rc)
 
@@ -832,15 +867,20 @@ def _diff_call(fn, cfg, pool, q, block_table, seq_lens, max_len, softmax_scale, 
                out, workspace, stream, step=None) -> None:
     dev = torch.cuda.current_device()
     ref = C.byref(cfg)
-    B, Hq, (pp, qp, bt, blocks, sl), op = _decode_head(cfg, pool, lib().kvq_pool_bytes(ref), q, block_table, seq_lens,
-                                                       out, dev)
-    new = () if step is None else (_new_rows(step[0], "k_new", B, cfg, dev), _new_rows(step[1], "v_new", B, cfg, dev),
-                                   _shaped(step[2], "append_pos", torch.int32, (B,), dev))
-    rc = fn(ref, pp, *new, qp, bt, blocks, sl, B, Hq, int(max_len), float(softmax_scale),
-            _shaped(lam, "lam", torch.float32, (Hq,), dev),
-            None if norm_weight is None else _shaped(norm_weight, "norm_weight", torch.float32, (cfg.head_dim,), dev),
-            float(norm_eps), float(out_scale), op, *_bytes(workspace, "workspace", dev), _stream_on(stream, dev))
-    _check(rc)
+    B, Hq, (pp, qp, bt, blocks, sl), op, (wp, wn) = _decode_args(cfg, ref, pool, lib().kvq_pool_bytes(ref), q,
+                                                                 block_table, seq_lens, out, workspace, dev)
+    lp = _shaped(lam, "lam", _F32, (Hq,), dev)
+    gp = None if norm_weight is None else _shaped(norm_weight, "norm_weight", _F32, (cfg.head_dim,), dev)
+    st = _stream_on(stream, dev)
+    if step is None:
+        rc = fn(ref, pp, qp, bt, blocks, sl, B, Hq, int(max_len), float(softmax_scale), lp, gp, float(norm_eps),
+                float(out_scale), op, wp, wn, st)
+    else:
+        rc = fn(ref, pp, _new_rows(step[0], "k_new", B, cfg, dev), _new_rows(step[1], "v_new", B, cfg, dev),
+                _shaped(step[2], "append_pos", _I32, (B,), dev), qp, bt, blocks, sl, B, Hq, int(max_len),
+                float(softmax_scale), lp, gp, float(norm_eps), float(out_scale), op, wp, wn, st)
+    if rc:
+        _check(rc)
 
 
 def kvq_diff_decode_attention(cfg: CacheConfig, pool: torch.Tensor, q: torch.Tensor, block_table: torch.Tensor,

@@ -296,6 +296,23 @@ __global__ void __launch_bounds__(kCmpThreads, 2) evict_compact_kernel(EvictComp
     const int P = 1 << p.lg_p;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int32_t* kept = p.kept + static_cast<long long>(row) * p.keep;
+    const int32_t* table = p.block_table + static_cast<long long>(b) * p.max_blocks;
+    const int32_t* dtable = p.dst_table + static_cast<long long>(b) * p.dst_max_blocks;
+    // this thread's row of the round at `base`: its position and its two pages, looked up a round
+    // ahead (the kept list and the tables do not change); t -1: a bad entry.  Bounded by `keep`, so
+    // that the first lookup does not wait for the length.
+    int t_next = -1, sp_next = 0, dp_next = 0;
+    auto look_up = [&](long long base) {
+        const long long i = base + static_cast<long long>(rank) * rows_cta + tid;
+        t_next = -1;
+        if (tid >= rows_cta || i >= p.keep) return;
+        const bool in = (i >> p.lg_p) < p.dst_max_blocks;
+        if (in) dp_next = dtable[i >> p.lg_p];
+        t_next = kept[i];
+        if (!in || t_next < 0 || (t_next >> p.lg_p) >= p.max_blocks) t_next = -1;
+        else sp_next = table[t_next >> p.lg_p];
+    };
+    look_up(0);
     long long n = p.seq_lens[b];
     n = n < 0 ? 0 : n;
     long long cap = static_cast<long long>(p.max_blocks) << p.lg_p;
@@ -306,24 +323,8 @@ __global__ void __launch_bounds__(kCmpThreads, 2) evict_compact_kernel(EvictComp
     }
     const int m = static_cast<int>(min(n, static_cast<long long>(p.keep)));
     float* w = p.weights ? p.weights + static_cast<long long>(row) * p.weights_ld : nullptr;
-    const int32_t* table = p.block_table + static_cast<long long>(b) * p.max_blocks;
-    const int32_t* dtable = p.dst_table + static_cast<long long>(b) * p.dst_max_blocks;
     // a row's code words: 2^lg_w of K, then as many of V
     const int half_mask = (1 << lg_w) - 1;
-    // this thread's row of the round at `base`: its position and its two pages, looked up a round
-    // ahead (the kept list and the tables do not change); t -1: none, -2: a bad entry
-    int t_next = -1, sp_next = 0, dp_next = 0;
-    auto look_up = [&](long long base) {
-        const long long i = base + static_cast<long long>(rank) * rows_cta + tid;
-        t_next = -1;
-        if (tid >= rows_cta || i >= m) return;
-        const bool in = (i >> p.lg_p) < p.dst_max_blocks;
-        if (in) dp_next = dtable[i >> p.lg_p];
-        t_next = kept[i];
-        if (!in || t_next < 0 || t_next >= n) t_next = -2;
-        else sp_next = table[t_next >> p.lg_p];
-    };
-    look_up(0);
     for (long long base = 0; base < m; base += static_cast<long long>(size) * rows_cta) {
         const long long r0 = base + static_cast<long long>(rank) * rows_cta;
         const int rows = r0 < m ? static_cast<int>(min(static_cast<long long>(rows_cta), m - r0)) : 0;
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(kCmpThreads, 2) evict_compact_kernel(EvictComp
         if (tid < rows) {
             const int t = t_next, sp = sp_next, dp = dp_next;
             long long src = -1, dst = -1;
-            if (t < 0) {
+            if (t < 0 || t >= n) {
                 raise_flag(p.status, KVQ_FLAG_BAD_POSITION);
             } else {
                 const int ss = t & (P - 1), ds = (static_cast<int>(r0) + tid) & (P - 1);
