@@ -425,7 +425,10 @@ cudaError_t launch(const decode::CParams& p, DecodeMode mode, int d, int warps, 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cudaError_t err;
-    const bool light = warps == 16;  // the 64-register instance
+    // The 64-register instance; in the weights and differential modes also where the rows' CTAs
+    // of the other one (16 warps on each of 152 SMs) would not all be resident at once
+    // (attention with weights, 32 x 8 kv heads of up to 4096 positions, 1024 rows: 39.3 -> 36.7 us).
+    const bool light = warps == 16 || (mode != DecodeMode::kPlain && rows * warps > 152 * 16);
     if (p.nsrc == 2) err = cudaLaunchKernelEx(&cfg, decode::combine_kernel<128, 2, 8>, p);  // mixed: head_dim 128 only
     else if (mode == DecodeMode::kWeights) err = launch_one<1>(cfg, p, d, light);
     else if (mode == DecodeMode::kDiff) err = launch_one<2>(cfg, p, d, light);
