@@ -45,7 +45,7 @@ struct CParams {
 constexpr int kCombineMaxWarps = 16;
 constexpr int kCombineLocalB = 256;   // up to this batch the row metadata is computed before the wait
 
-// MODE 1's third kernel: CTA size, and the scores a thread has in flight; a chunk is one
+// MODE 1: CTA size of the weights, and the scores a thread has in flight; a chunk is one
 // position of one kv head per thread for every R of them, R the query heads per kv head
 // rounded up to 1, 2, 4 or 8.
 constexpr int kAddThreads = 256;
@@ -53,32 +53,32 @@ constexpr int kAddScores = 16;
 __host__ __device__ constexpr int add_rows(int r) { return r <= 2 ? r : (r <= 4 ? 4 : 8); }
 __host__ __device__ constexpr int add_positions(int r) { return kAddThreads * (kAddScores / add_rows(r)); }
 
-// The attention weight of the positions, one CTA per kv head and chunk:
-//     weights[b][h][t] = decay * weights[b][h][t] + sum over the kv head's r rows of 2^(z - M) / L,
-// z the scores the decode grid stored, M and 1 / L from the combine, in row order (results do
-// not depend on timing).  Bound by latency and launch: a thread's scores, its old weights and
-// the rows' statistics are all in flight together, one round trip, and the scores, written
-// just before, mostly still lie in the L2.  8 x 32 heads of 8193 positions (25 MB): 6.7 us on
-// its own.  Tried and slower for the whole call on that shape (61.0 us): the same work in
-// further CTAs of the combine's launch, which then hold the register file of the combine
-// (67 us), and run beside the combine with M and L from the partials (63 us).
-template <int R>
-__global__ void __launch_bounds__(kAddThreads) add_weights_kernel(CParams p) {
+// Where a row's partials lie: n of them from `base` on, made by CTAs cf, cf + 1, .. of U units.
+struct RowPartials {
+    int n;
+    long long base, cf, U;
+};
+
+// The attention weight of one chunk of positions, from wt on, of kv head wh of sequence b:
+//     weights[b][wh][t] = decay * weights[b][wh][t] + sum over the kv head's r rows of 2^(z - M) / L,
+// z the scores the decode grid stored, in row order (results do not depend on timing).  M and
+// 1 / L of the rows come from the combine (stat), or with WITH_ROWS from the (max, sum) pairs of
+// their partials, by one warp per row.  Bound by latency: a thread's scores, its old weights and
+// the rows' statistics are all in flight together, and the scores, written just before, mostly
+// still lie in the L2.  s_m, s_inv: r floats each.
+template <int R, bool WITH_ROWS>
+__device__ __forceinline__ void add_weights(const CParams& p, int b, int wh, int wt, const RowPartials& rp, float* s_m,
+                                            float* s_inv) {
     constexpr int K = kAddScores / R;
-    asm volatile("griddepcontrol.launch_dependents;");
-    const unsigned head = blockIdx.x / p.chunks, heads = p.Hq / p.r;
-    const int t0 = static_cast<int>(blockIdx.x - head * p.chunks) * (kAddThreads * K) + static_cast<int>(threadIdx.x);
-    const int b = head / heads;
+    const CSource& s = p.src[0];
+    const int hq = wh * p.r;
     const int Lb = min(min(p.seq_lens[b], p.len_max),
-                       static_cast<int>(min(static_cast<long long>(p.src[0].max_blocks) << p.lg_p, 0x7fffffffLL)));
-    float* w = p.weights + static_cast<long long>(head) * p.weights_ld + t0;
-    const float* zp = p.scores + static_cast<long long>(head) * p.r * p.score_ld + t0;
-    const float2* st = p.stat + static_cast<long long>(head) * p.r;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+                       static_cast<int>(min(static_cast<long long>(s.max_blocks) << p.lg_p, 0x7fffffffLL)));
+    if (wt >= Lb) return;  // the whole CTA
+    const int t0 = wt + static_cast<int>(threadIdx.x);
+    float* w = p.weights + (static_cast<long long>(b) * (p.Hq / p.r) + wh) * p.weights_ld + t0;
+    const float* zp = p.scores + (static_cast<long long>(b) * p.Hq + hq) * p.score_ld + t0;
     float z[K][R], old[K];
-    float2 ml[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) ml[i] = i < p.r ? __ldcg(st + i) : make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const bool in = t0 + k * kAddThreads < Lb;
@@ -87,13 +87,62 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(CParams p) {
             z[k][i] = in && i < p.r ? __ldcg(zp + static_cast<long long>(i) * p.score_ld + k * kAddThreads) : 0.f;
         old[k] = in && p.decay != 0.f ? w[k * kAddThreads] : 0.f;
     }
+    if constexpr (WITH_ROWS) {
+        const int g = threadIdx.x >> 5, lane = threadIdx.x & 31;  // 8 warps, r <= 8 rows
+        if (g < p.r) {
+            const bool dense = rp.U >= s.C;  // every CTA slice of the decode grid holds units
+            const float* ml0 = s.ws_ml + (rp.base * s.ns + (hq + g) % s.ns) * 2;
+            float M = -INFINITY, L = 0.f;
+            for (int j = lane; j < rp.n; j += 32) {
+                const long long k = rp.cf + j / s.W;
+                if (!dense && slice_start(k, rp.U, s.C) >= slice_start(k + 1, rp.U, s.C)) continue;
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(ml0 + static_cast<long long>(j) * s.ns * 2));
+                const float mn = fmaxf(M, ml.x);
+                if (mn == -INFINITY) continue;
+                L = L * fast_exp2(M - mn) + ml.y * fast_exp2(ml.x - mn);
+                M = mn;
+            }
+            float Mx = M;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, off));
+            L = M == -INFINITY ? 0.f : L * fast_exp2(M - Mx);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+            if (lane == 0) {
+                s_m[g] = Mx;
+                s_inv[g] = L > 0.f ? 1.f / L : 0.f;
+            }
+        }
+    } else if (static_cast<int>(threadIdx.x) < p.r) {
+        const float2 st = __ldcg(p.stat + static_cast<long long>(b) * p.Hq + hq + threadIdx.x);
+        s_m[threadIdx.x] = st.x;
+        s_inv[threadIdx.x] = st.y;
+    }
+    __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < R; ++i) sum = fmaf(fast_exp2(z[k][i] - ml[i].x), ml[i].y, sum);
+        for (int i = 0; i < R; ++i)
+            if (i < p.r) sum = fmaf(fast_exp2(z[k][i] - s_m[i]), s_inv[i], sum);
         if (t0 + k * kAddThreads < Lb) w[k * kAddThreads] = fmaf(p.decay, old[k], sum);
     }
+}
+
+// The weights as a third kernel, one CTA per kv head and chunk.  8 x 32 heads of 8193 positions
+// (25 MB): 6.7 us on its own.  Tried and slower for the whole call on that shape (60 us): the
+// same work in further CTAs of the combine's launch, which then either hold the combine's
+// registers or hold the merge to theirs (65 to 78 us with 64 to 40 registers; see MODE 3 for
+// where it pays), and run beside the combine with M and L from the partials (63 us).
+template <int R>
+__global__ void __launch_bounds__(kAddThreads) add_weights_kernel(CParams p) {
+    __shared__ float s_m[8], s_inv[8];
+    asm volatile("griddepcontrol.launch_dependents;");
+    const unsigned head = blockIdx.x / p.chunks, heads = p.Hq / p.r;
+    const int wt = static_cast<int>(blockIdx.x - head * p.chunks) * add_positions(R);
+    const int b = static_cast<int>(head / heads), wh = static_cast<int>(head % heads);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    add_weights<R, false>(p, b, wh, wt, RowPartials{}, s_m, s_inv);
 }
 
 // One CTA per output row (b, hq).  In source s the row's partials sit at W * (cf + seg) + j
@@ -114,12 +163,16 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(CParams p) {
 // it holds half.  Rows of 4- and 8-warp CTAs (up to 64 partials) load 8 at a time, in
 // one round.
 // MODE 1 (attention with weights) also leaves each row's maximum and reciprocal sum for the
-// weights' kernel.
+// weights' kernel.  MODE 3 (the same, small calls) has the weights' CTAs in its own launch,
+// behind those of the rows: one launch less, which is what a call that leaves the device half
+// empty spends its time on (8 heads of 513 positions: 12.5 us a call in a stream, 14 with the
+// third launch; on the device 10.3 either way).
 // MODE 2 (differential attention) has one CTA per query head: even warps merge its first map's
 // row, odd warps the second's, then o = o1 - lambda o2, the optional RMS norm over the row,
 // which warp 0 holds whole, and the output scale.
 template <int D, int NSRC, int NB, int MODE = 0>
-__global__ void __launch_bounds__(kCombineMaxWarps * 32, NB == 8 || D == 256 ? 1 : 2)
+__global__ void __launch_bounds__(MODE == 3 ? kAddThreads : kCombineMaxWarps * 32,
+                                  MODE == 3 ? 2 : (NB == 8 || D == 256 ? 1 : 2))
 combine_kernel(CParams p) {
     static_assert(D == 64 || D == 128 || D == 256, "head_dim 64, 128 or 256");
     static_assert(NB == 8 || NB == 4, "8 partials a batch, or 4 for the 4-warp CTAs");
@@ -136,16 +189,25 @@ combine_kernel(CParams p) {
     const int lane = threadIdx.x & 31;
     const int nw = blockDim.x >> 5;
     const int rows_b = MODE == 2 ? p.Hq / 2 : p.Hq;  // output rows per sequence
-    const int b = static_cast<int>(blockIdx.x / rows_b);
-    const int hrow = static_cast<int>(blockIdx.x - static_cast<long long>(b) * rows_b);
-    const int hq = MODE == 2 ? 2 * hrow : hrow;  // (both maps' virtual heads share a segment)
+    int b = static_cast<int>(blockIdx.x / rows_b);
+    int hrow = static_cast<int>(blockIdx.x - static_cast<long long>(b) * rows_b);
+    const bool adds = MODE == 3 && b >= p.B;  // a CTA of the weights: kv head hrow / r, positions from wt on
+    int wt = 0;
+    if (adds) {
+        const unsigned k = blockIdx.x - static_cast<unsigned>(p.B) * rows_b;
+        const unsigned head = k / p.chunks, heads = p.Hq / p.r;
+        wt = static_cast<int>(k - head * p.chunks) * add_positions(p.r);
+        b = static_cast<int>(head / heads);
+        hrow = static_cast<int>(head % heads) * p.r;
+    }
+    const int hq = MODE == 2 ? 2 * hrow : hrow;  // (both maps' virtual heads, and a kv head's rows, share a segment)
     // the warps that merge this warp's row: all of them, or in MODE 2 every other one
     const int map = MODE == 2 ? warp & 1 : 0, sub = MODE == 2 ? warp >> 1 : warp, nsub = MODE == 2 ? nw >> 1 : nw;
 
     // Pages of sequence i as source s listed them, and the row's range of partials.
     auto pages_of = [&](const CSource& s, int i) {
         int L = p.seq_lens[i] - s.len_sub;
-        if constexpr (MODE == 1) L = min(L, p.len_max);
+        if constexpr (MODE == 1 || MODE == 3) L = min(L, p.len_max);
         return seq_span(L, p.lg_p, s.max_blocks, s.window, s.sinks).np;
     };
     auto row_range = [&](const CSource& s, int pb_, int np_, int tot_, long long& cf_, long long& base_,
@@ -206,6 +268,20 @@ combine_kernel(CParams p) {
             const int np = __ldcg(pre + b + 1) - pb;
             const int tot = __ldcg(pre + p.B);
             if (np > 0) n[si] = row_range(p.src[si], pb, np, tot, cf[si], base[si], U[si]);
+        }
+    }
+
+    if constexpr (MODE == 3) {
+        if (adds) {
+            const int wh = hrow / p.r;
+            const RowPartials rp{n[0], base[0], cf[0], U[0]};
+            switch (add_rows(p.r)) {
+                case 1: add_weights<1, true>(p, b, wh, wt, rp, s_m, s_l); break;
+                case 2: add_weights<2, true>(p, b, wh, wt, rp, s_m, s_l); break;
+                case 4: add_weights<4, true>(p, b, wh, wt, rp, s_m, s_l); break;
+                default: add_weights<8, true>(p, b, wh, wt, rp, s_m, s_l); break;
+            }
+            return;  // the whole CTA
         }
     }
 
@@ -394,20 +470,26 @@ decode::CSource source_of(const DecodeArgs& a, const DecodePlan& plan) {
 
 template <int MODE>
 cudaError_t launch_one(const cudaLaunchConfig_t& cfg, const decode::CParams& p, int d, bool light) {
+    constexpr int NB = MODE == 3 ? 4 : 8;  // (MODE 3: always the light one)
     switch (d) {
         case 64: return light ? cudaLaunchKernelEx(&cfg, decode::combine_kernel<64, 1, 4, MODE>, p)
-                              : cudaLaunchKernelEx(&cfg, decode::combine_kernel<64, 1, 8, MODE>, p);
+                              : cudaLaunchKernelEx(&cfg, decode::combine_kernel<64, 1, NB, MODE>, p);
         case 128: return light ? cudaLaunchKernelEx(&cfg, decode::combine_kernel<128, 1, 4, MODE>, p)
-                               : cudaLaunchKernelEx(&cfg, decode::combine_kernel<128, 1, 8, MODE>, p);
+                               : cudaLaunchKernelEx(&cfg, decode::combine_kernel<128, 1, NB, MODE>, p);
         case 256: return light ? cudaLaunchKernelEx(&cfg, decode::combine_kernel<256, 1, 4, MODE>, p)
-                               : cudaLaunchKernelEx(&cfg, decode::combine_kernel<256, 1, 8, MODE>, p);
+                               : cudaLaunchKernelEx(&cfg, decode::combine_kernel<256, 1, NB, MODE>, p);
         default: return cudaErrorInvalidValue;
     }
 }
 
-cudaError_t launch(const decode::CParams& p, DecodeMode mode, int d, int warps, cudaStream_t stream) {
+// with_weights: the weights' CTAs in the same launch (MODE 3)
+cudaError_t launch(const decode::CParams& p, DecodeMode mode, int d, int warps, cudaStream_t stream,
+                   bool with_weights = false) {
     long long rows = static_cast<long long>(p.B) * (mode == DecodeMode::kDiff ? p.Hq / 2 : p.Hq);
-    if (mode == DecodeMode::kDiff) {
+    if (with_weights) {
+        rows += static_cast<long long>(p.B) * (p.Hq / p.r) * p.chunks;
+        warps = decode::kAddThreads / 32;
+    } else if (mode == DecodeMode::kDiff) {
         warps = std::min(2 * warps, decode::kCombineMaxWarps);  // two rows
     }
     if (rows <= 0) return cudaSuccess;
@@ -430,6 +512,7 @@ cudaError_t launch(const decode::CParams& p, DecodeMode mode, int d, int warps, 
     // (attention with weights, 32 x 8 kv heads of up to 4096 positions, 1024 rows: 39.3 -> 36.7 us).
     const bool light = warps == 16 || (mode != DecodeMode::kPlain && rows * warps > 152 * 16);
     if (p.nsrc == 2) err = cudaLaunchKernelEx(&cfg, decode::combine_kernel<128, 2, 8>, p);  // mixed: head_dim 128 only
+    else if (with_weights) err = launch_one<3>(cfg, p, d, true);
     else if (mode == DecodeMode::kWeights) err = launch_one<1>(cfg, p, d, light);
     else if (mode == DecodeMode::kDiff) err = launch_one<2>(cfg, p, d, light);
     else err = launch_one<0>(cfg, p, d, light);
@@ -469,9 +552,12 @@ cudaError_t launch_combine(const DecodeArgs& a, const DecodePlan& plan, cudaStre
     p.norm_weight = a.norm_weight;
     p.norm_eps = a.norm_eps;
     p.out_scale = a.out_scale;
-    cudaError_t err = launch(p, a.mode, a.L.d, plan.combine_warps, stream);
     const long long adders = static_cast<long long>(a.B) * a.Hkv * p.chunks;
-    if (err != cudaSuccess || a.mode != DecodeMode::kWeights || adders == 0) return err;
+    const bool weights = a.mode == DecodeMode::kWeights && adders > 0;
+    // everything behind the decode grid in one launch where it leaves the device's 152 SMs a CTA each
+    const bool one = weights && static_cast<long long>(a.B) * a.Hq + adders <= 152;
+    cudaError_t err = launch(p, a.mode, a.L.d, plan.combine_warps, stream, one);
+    if (err != cudaSuccess || !weights || one) return err;
     // launched while the combine runs; the kernel waits for it before it reads the workspace
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
