@@ -509,8 +509,9 @@ cudaError_t launch(const decode::CParams& p, DecodeMode mode, int d, int warps, 
     cudaError_t err;
     // The 64-register instance; in the weights and differential modes also where the rows' CTAs
     // of the other one (16 warps on each of 152 SMs) would not all be resident at once
-    // (attention with weights, 32 x 8 kv heads of up to 4096 positions, 1024 rows: 39.3 -> 36.7 us).
-    const bool light = warps == 16 || (mode != DecodeMode::kPlain && rows * warps > 152 * 16);
+    // (attention with weights, 32 x 8 kv heads of up to 4096 positions, 1024 rows: 39.3 -> 36.7 us), and at head_dim 256
+    // (differential, 8 x 16 heads of 4097 positions: 40.3 -> 39.1 us; never slower).
+    const bool light = warps == 16 || (mode != DecodeMode::kPlain && (rows * warps > 152 * 16 || d == 256));
     if (p.nsrc == 2) err = cudaLaunchKernelEx(&cfg, decode::combine_kernel<128, 2, 8>, p);  // mixed: head_dim 128 only
     else if (with_weights) err = launch_one<3>(cfg, p, d, true);
     else if (mode == DecodeMode::kWeights) err = launch_one<1>(cfg, p, d, light);

@@ -432,11 +432,12 @@ template <int D, int GK, int GV, int HK, int HS, bool WIN, bool P16, int CODEC =
 __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D, MODE, CODEC, score_tiles<D, GK, HS, MODE>()>()) decode_splitkv_kernel(KParams p) {
     static_assert(D == 64 || D == 128 || D == 256, "head_dim 64, 128 or 256");
     static_assert(CODEC == 0 || (CODEC == 1 && D == 128 && GK == D && GV == D && HK == 1), "INT8: d 128, rows");
-    static_assert(D <= 128 || (HK == 1 && HS == 1), "head_dim 256: one-head units, up to 4 query heads each");
+    static_assert(D <= 128 || ((HK == 1 || (HK == 2 && MODE == 2)) && HS == 1), "head_dim 256: one-head units, up to 4 query heads each");
     static_assert(HK == 1 || HS == 1, "several kv heads per unit only with one query head each");
     static_assert(HK == 1 || P16, "four-head units only for 16-token pages");
     static_assert(MODE == 0 || !WIN, "the weights and differential modes attend to every position");
-    static_assert(MODE != 2 || (HK == 1 && CODEC == 0 && 2 * GK <= D), "differential: one-head INT4 units, K groups within a half");
+    static_assert(MODE != 2 || (HK <= 2 && CODEC == 0 && 2 * GK <= D), "differential: INT4, units of one or two heads, K groups within a half");
+    static_assert(HK == 1 || HK == 4 || (HK == 2 && MODE == 2), "two heads per unit: differential attention");
     static_assert(4 * HS + 2 * HK <= kQRows, "q rows and the appended token's K and V rows fit a q buffer");
     constexpr int NGK = D / GK;               // K groups per row
     constexpr int NGV = D / GV;               // V groups per row
@@ -655,8 +656,9 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D, MODE, CO
 
     // the kv head (within the unit) of this thread's score slot, and of its B-fragment
     // column (HK > 1 only when every slot is its own kv head)
-    const int a_row = HK == 1 ? 0 : c;
-    const int a_col = HK == 1 ? 0 : (g >> 1);
+    // (two heads of differential attention have two slots each, one per map)
+    const int a_row = HK == 1 ? 0 : (HK == 2 ? c >> 1 : c);
+    const int a_col = HK == 1 ? 0 : (HK == 2 ? g >> 2 : g >> 1);
     // per-thread byte offsets inside a unit buffer (chunk 0)
     const int k_off = g * ROW + c * (KW * 4);
     const int ks_off = a_row * bbytes + l_kscales + g * NGK * SB;
@@ -1494,12 +1496,16 @@ int decode_occupancy_d256_win(const DecodeArgs& a, const DecodePlan& plan, size_
         }                                                                                            \
     }                                                                                                \
     }
-// Attention with weights (MODE 1) and differential attention (MODE 2, one-head units only).
+// Attention with weights (MODE 1) and differential attention (MODE 2).
 #define KVQ_WEIGHTS_RUN(D_, GK_, GV_, HK_, HS_, W_, P16_) decode::run<D_, GK_, GV_, HK_, HS_, W_, P16_, 0, 1>(a, plan, s)
 #define KVQ_WEIGHTS_OCC(D_, GK_, GV_, HK_, HS_, W_, P16_) decode::occupancy<D_, GK_, GV_, HK_, HS_, W_, P16_, 0, 1>(smem)
 #define KVQ_DIFF_RUN(D_, GK_, GV_, HK_, HS_, W_, P16_) decode::run<D_, GK_, GV_, HK_, HS_, W_, P16_, 0, 2>(a, plan, s)
 #define KVQ_DIFF_OCC(D_, GK_, GV_, HK_, HS_, W_, P16_) decode::occupancy<D_, GK_, GV_, HK_, HS_, W_, P16_, 0, 2>(smem)
-#define KVQ_DIFF_CASES(D_, GK_, GV_, W_, CALL)          \
+// (up to four virtual heads: one-head units, or two heads of one query head each)
+#define KVQ_DIFF_CASES_4(D_, GK_, GV_, W_, CALL)        \
     KVQ_DECODE_CASES_1H(D_, GK_, GV_, W_, CALL)         \
+    case KVQ_DECODE_KEY(GK_, GV_, 2, 1, 1): return CALL(D_, GK_, GV_, 2, 1, W_, true);
+#define KVQ_DIFF_CASES(D_, GK_, GV_, W_, CALL)          \
+    KVQ_DIFF_CASES_4(D_, GK_, GV_, W_, CALL)            \
     case KVQ_DECODE_KEY(GK_, GV_, 1, 2, 1): return CALL(D_, GK_, GV_, 1, 2, W_, true);  \
     case KVQ_DECODE_KEY(GK_, GV_, 1, 2, 0): return CALL(D_, GK_, GV_, 1, 2, W_, false);

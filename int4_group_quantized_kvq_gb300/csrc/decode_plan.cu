@@ -107,6 +107,9 @@ cudaError_t plan_decode(const DecodeArgs& a, DecodePlan* plan) {
     // four kv heads per unit for 16-token pages (a 4-block unit then stays near the size
     // of one larger page); larger pages are big enough copies on their own
     plan->hk = (!a.fp16 && r == 1 && a.Hkv % 4 == 0 && a.L.P == 16 && a.L.d <= 128) ? 4 : 1;
+    // differential attention with one query head per kv head: its two virtual heads fill half of
+    // a unit's four slots, so two kv heads share one, for the same reason
+    if (a.mode == DecodeMode::kDiff && r == 2 && a.Hkv % 2 == 0 && a.L.P == 16) plan->hk = 2;
     plan->hs = (plan->hk == 1 && r > 4) ? 2 : 1;
     // CTA bookkeeping (128 bytes) and the two q buffers of 12 rows of head_dim fp16 (the q
     // rows of a segment and, in the decode step, the new token's K and V rows)
