@@ -152,6 +152,10 @@ struct KParams {
     // score_ld floats per query head; lengths are cut to len_max
     float* scores;
     int32_t score_ld, len_max;
+    // MODE 1 over INT8 pages of 64 tokens: a unit is half a page (P, lg_p and max_blocks count
+    // halves), its four sections copied one by one; page_ld is the block table's row and page_P
+    // the page's tokens.  (page_P == P: units are pages.)
+    int32_t page_ld, page_P;
 };
 
 // a / b for a >= 0, b > 0, with 32-bit division when both fit (the usual case).
@@ -312,6 +316,23 @@ __device__ __forceinline__ unsigned long long unit_addr_tagged(const KParams& p,
     return reinterpret_cast<unsigned long long>(
                p.pool + (static_cast<long long>(page) * p.Hkv + static_cast<long long>(hg) * HK) * p.block_bytes) |
            bad;
+}
+
+// The same for half-page units: bit 1 says which half.
+__device__ __forceinline__ unsigned long long half_unit_addr(const KParams& p, const int32_t* pre, const int32_t* lens,
+                                                             long long u) {
+    const int b = find_seq(pre, p.B, p.Hg, u);
+    const long long rem = u - static_cast<long long>(p.Hg) * pre[b];
+    const int np = pre[b + 1] - pre[b];
+    const int hg = static_cast<int>(rem / np);
+    const int half = static_cast<int>(rem - static_cast<long long>(hg) * np);
+    int page = p.block_table[static_cast<long long>(b) * p.page_ld + (half >> 1)];
+    if (page < 0 || page >= p.num_pages) {
+        raise_flag(p.status, KVQ_FLAG_BAD_PAGE);
+        page = 0;
+    }
+    return reinterpret_cast<unsigned long long>(p.pool + (static_cast<long long>(page) * p.Hkv + hg) * (2ll * p.block_bytes)) |
+           static_cast<unsigned long long>((half & 1) << 1);
 }
 
 // First unit of slice w of U units split over W slices.
@@ -578,22 +599,43 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D, MODE, CO
     // window's addresses are looked up one window ahead so their loads overlap work ----
     auto unit_of = [&](int i) { return c0 + warp + static_cast<long long>(kWarps) * i; };
     int wbase = 0;
-    unsigned long long waddr = lane < nm ? unit_addr_tagged<WIN>(p, pre, lens, unit_of(lane), HK) : 0ull;
-    unsigned long long wnext = 32 + lane < nm ? unit_addr_tagged<WIN>(p, pre, lens, unit_of(32 + lane), HK) : 0ull;
+    constexpr bool HALVES = MODE == 1 && I8 && !P16;  // an instance that takes half-page units
+    auto addr_of = [&](int i) -> unsigned long long {
+        if constexpr (HALVES) {
+            if (p.page_P != p.P) return half_unit_addr(p, pre, lens, unit_of(i));
+        }
+        return unit_addr_tagged<WIN>(p, pre, lens, unit_of(i), HK);
+    };
+    unsigned long long waddr = lane < nm ? addr_of(lane) : 0ull;
+    unsigned long long wnext = 32 + lane < nm ? addr_of(32 + lane) : 0ull;
     int issued = 0;
     const uint64_t l2_stream = l2_policy_evict_first();  // pages are read once per call
     auto issue = [&](int i, int st) {  // this warp's unit i into stage st; i increases call by call
         if (i - wbase >= 32) {
             wbase += 32;
             waddr = wnext;
-            wnext = wbase + 32 + lane < nm ? unit_addr_tagged<WIN>(p, pre, lens, unit_of(wbase + 32 + lane), HK) : 0ull;
+            wnext = wbase + 32 + lane < nm ? addr_of(wbase + 32 + lane) : 0ull;
         }
         const unsigned long long src = __shfl_sync(0xffffffffu, waddr, i - wbase);
         if (lane == 0) {
             uaddr[st] = src;
             const uint32_t bar = bar0 + 8 * st;
             mbar_arrive_expect_tx(bar, ubytes);
-            bulk_g2s_hint(ring0 + st * ubytes, reinterpret_cast<const void*>(src & ~1ull), ubytes, bar, l2_stream);
+            if constexpr (HALVES) {
+                if (p.page_P != p.P) {  // K codes, V codes, K scales, V scales of the half
+                    const uint8_t* from = reinterpret_cast<const uint8_t*>(src & ~15ull);
+                    const uint32_t to = ring0 + st * ubytes, half = (src >> 1) & 1u;
+                    const uint32_t codes = p.P * ROW, scales = p.P * SB;
+                    bulk_g2s_hint(to, from + half * codes, codes, bar, l2_stream);
+                    bulk_g2s_hint(to + codes, from + (2 + half) * codes, codes, bar, l2_stream);
+                    bulk_g2s_hint(to + 2 * codes, from + 4 * codes + half * scales, scales, bar, l2_stream);
+                    bulk_g2s_hint(to + 2 * codes + scales, from + 4 * codes + (2 + half) * scales, scales, bar, l2_stream);
+                } else {
+                    bulk_g2s_hint(ring0 + st * ubytes, reinterpret_cast<const void*>(src & ~1ull), ubytes, bar, l2_stream);
+                }
+            } else {
+                bulk_g2s_hint(ring0 + st * ubytes, reinterpret_cast<const void*>(src & ~1ull), ubytes, bar, l2_stream);
+            }
         }
         ++issued;
     };
@@ -1398,6 +1440,8 @@ cudaError_t run(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream
     p.scores = MODE == 1 ? reinterpret_cast<float*>(a.workspace + plan.ws_score_offset) : nullptr;
     p.score_ld = plan.score_ld;
     p.len_max = a.max_len;
+    p.page_ld = a.page_ld;
+    p.page_P = a.page_P != 0 ? a.page_P : a.L.P;
     p.stages = plan.stages;
     p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
     p.k_new = a.k_new;

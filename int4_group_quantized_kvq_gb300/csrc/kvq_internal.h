@@ -157,6 +157,9 @@ struct DecodeArgs {
     float* weights = nullptr;
     int32_t weights_ld = 0;
     float decay = 1.f;
+    // kWeights over INT8 pages of 64 tokens: half-page units; L.P and max_blocks then count halves,
+    // page_ld is the block table's row and page_P the page's tokens (0: units are pages)
+    int32_t page_ld = 0, page_P = 0;
     // kDiff: out = out_scale * norm(map 1 - lambda[query head] * map 2), norm an RMS norm over
     // head_dim with gain norm_weight and norm_eps (norm_weight nullptr: none)
     const float* lambda = nullptr;

@@ -189,6 +189,31 @@ def test_bad_page_and_overlong_sequence_are_flagged(kvq):
     assert kvq.kvq_read_status(ws) & kvq.KVQ_FLAG_BAD_POSITION
 
 
+def test_int8_half_pages_flag_bad_pages_and_lengths(kvq):
+    pool = Pool("int8", 2, 128, [150, 128], 64, 128, 128, seed=5)
+    x, q, cfg, table = pool.gpu(), make_q(2, 4, 128, 9), pool.cfg(kvq), pool.table_gpu()
+    ws, out = kvq.new_int8_weights_workspace(cfg, 2, 4, 300), torch.empty(2, 4, 128, device="cuda")
+
+    def go(table, lens):
+        start = torch.rand(2, 2, 300, device="cuda")
+        w = start.clone()
+        ws[:4] = 0
+        kvq.kvq_int8_decode_attention_weights(cfg, x, q, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                              300, 128 ** -0.5, 1.0, w, out, ws)
+        return start, w, kvq.kvq_read_status(ws)
+
+    for bad in (-1, pool.num_pages):
+        t = table.clone()
+        t[0, 1] = bad
+        assert go(t, [150, 128])[2] == kvq.KVQ_FLAG_BAD_PAGE
+    # a length beyond the table's three pages: cut to them and flagged (sequence 1 has two)
+    t = table.clone()
+    t[1, 2] = t[1, 1]
+    start, w, flags = go(t, [150, 200])
+    assert flags == kvq.KVQ_FLAG_BAD_POSITION
+    assert torch.equal(w[1, :, 192:], start[1, :, 192:]) and (w[1, :, :192] > start[1, :, :192]).all()
+
+
 # ---- select --------------------------------------------------------------------------------------
 
 def plain_select(w, lens, keep, sinks, recent):
