@@ -199,7 +199,7 @@ def test_int8_half_pages_flag_bad_pages_and_lengths(kvq):
         w = start.clone()
         ws[:4] = 0
         kvq.kvq_int8_decode_attention_weights(cfg, x, q, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
-                                              300, 128 ** -0.5, 1.0, w, out, ws)
+                                              300, 128 ** -0.5, 0.0, w, out, ws)
         return start, w, kvq.kvq_read_status(ws)
 
     for bad in (-1, pool.num_pages):
@@ -211,7 +211,10 @@ def test_int8_half_pages_flag_bad_pages_and_lengths(kvq):
     t[1, 2] = t[1, 1]
     start, w, flags = go(t, [150, 200])
     assert flags == kvq.KVQ_FLAG_BAD_POSITION
-    assert torch.equal(w[1, :, 192:], start[1, :, 192:]) and (w[1, :, :192] > start[1, :, :192]).all()
+    assert torch.equal(w[1, :, 192:], start[1, :, 192:])
+    # each kv head's weights of 192 positions add up to its two query heads' sums
+    assert torch.allclose(w[1, :, :192].double().sum(-1), torch.full((2,), 2.0, dtype=torch.float64, device="cuda"),
+                          rtol=1e-4)
 
 
 # ---- select --------------------------------------------------------------------------------------
