@@ -45,13 +45,15 @@ struct CParams {
 constexpr int kCombineMaxWarps = 16;
 constexpr int kCombineLocalB = 256;   // up to this batch the row metadata is computed before the wait
 
-// MODE 1: CTA size of the weights, and the scores a thread has in flight; a chunk is one
-// position of one kv head per thread for every R of them, R the query heads per kv head
-// rounded up to 1, 2, 4 or 8.
+// MODE 1: CTA size of the weights, and the scores a thread has in flight: 16, a position's R of
+// them for each of 16 / R positions, R the query heads per kv head rounded up to 1, 2, 4 or 8;
+// 8 positions at R = 1, where the old weights are as many loads again (8 x 32 heads of 8193
+// positions, a call: 59.4 us with 16, 58.5 with 8; at R = 4 45.6 with 16, 46.4 with 8).  A
+// chunk is what a CTA's threads cover.
 constexpr int kAddThreads = 256;
-constexpr int kAddScores = 16;
 __host__ __device__ constexpr int add_rows(int r) { return r <= 2 ? r : (r <= 4 ? 4 : 8); }
-__host__ __device__ constexpr int add_positions(int r) { return kAddThreads * (kAddScores / add_rows(r)); }
+__host__ __device__ constexpr int add_per_thread(int r) { return r == 1 ? 8 : 16 / add_rows(r); }
+__host__ __device__ constexpr int add_positions(int r) { return kAddThreads * add_per_thread(r); }
 
 // Where a row's partials lie: n of them from `base` on, made by CTAs cf, cf + 1, .. of U units.
 struct RowPartials {
@@ -69,7 +71,7 @@ struct RowPartials {
 template <int R, bool WITH_ROWS>
 __device__ __forceinline__ void add_weights(const CParams& p, int b, int wh, int wt, const RowPartials& rp, float* s_m,
                                             float* s_inv) {
-    constexpr int K = kAddScores / R;
+    constexpr int K = add_per_thread(R);
     const CSource& s = p.src[0];
     const int hq = wh * p.r;
     const int Lb = min(min(p.seq_lens[b], p.len_max),

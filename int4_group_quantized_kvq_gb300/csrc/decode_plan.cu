@@ -1,7 +1,8 @@
 // decode_plan.cu -- sizing of the persistent split-KV grid and of its workspace.
 //
 // A unit of work is one page of HK consecutive kv heads: HK = 4 when every query head
-// has its own kv head, Hkv is a multiple of 4 and pages hold 16 tokens, else HK = 1.
+// has its own kv head, Hkv is a multiple of 4 and pages hold 16 tokens, else HK = 1
+// (differential attention, two maps per query head: HK = 2 in that place).
 // The grid is C CTAs of 4 warps: C is the number of CTAs the device keeps resident (SMs
 // x resident CTAs), reduced for small problems so that a warp gets at least two units;
 // every CTA receives an equal contiguous slice of the flattened (sequence, head group,
