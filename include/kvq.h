@@ -177,8 +177,9 @@ size_t kvq_decode_workspace_bytes(const kvq_cache_config *cfg, int32_t batch, in
  * that kernel has signalled its dependents early, which this library's kernels do),
  * the decode grid may already read q, block_table and seq_lens; it reads the pool and
  * touches the workspace only after that kernel has finished, and out is written by
- * the combine grid after the decode grid has finished.  This library's kernels never
- * write q, block_table or seq_lens.
+ * the combine grid after the decode grid has finished.  This library's kernels that signal
+ * early never write q, block_table or seq_lens (kvq_evict_select, whose new lengths may be
+ * the next call's seq_lens, does not signal early).
  * Returns KVQ_OK, KVQ_EINVAL, KVQ_EUNSUPPORTED, KVQ_EWORKSPACE or KVQ_ECUDA.
  */
 int kvq_decode_attention(const kvq_cache_config *cfg, const void *pool, const void *q,
