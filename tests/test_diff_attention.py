@@ -74,6 +74,19 @@ def test_many_sequences(kvq):
     check(pool, q, lam, gain, 1e-6, 1.0, out)
 
 
+def test_thousands_of_short_sequences(kvq):
+    lens = [1 + (7 * b) % 40 for b in range(2100)]
+    for Hkv in (1, 2):  # one head to a unit, two heads to a unit
+        pool = Pool("int4", Hkv, 128, lens, 16, 64, 128, seed=9)
+        q, cfg = make_q(2100, Hkv, 128, 5), pool.cfg(kvq)
+        lam, out = torch.rand(Hkv, device="cuda"), torch.empty(2100, Hkv, 128, device="cuda")
+        ws = kvq.new_diff_workspace(cfg, 2100, Hkv, 40)
+        kvq.kvq_diff_decode_attention(cfg, pool.gpu(), q, pool.table_gpu(), pool.lens_gpu(), 40, 0.125, lam, None, 0.0,
+                                      1.0, out, ws)
+        assert kvq.kvq_read_status(ws) == 0
+        check(pool, q, lam, None, 0.0, 1.0, out)
+
+
 def test_empty_sequence_without_eps_gives_zeros(kvq):
     pool = Pool("int4", 2, 128, [0, 20], 16, 64, 128, seed=9)
     q, cfg = make_q(2, 2, 128, 5), pool.cfg(kvq)

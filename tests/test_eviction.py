@@ -135,6 +135,75 @@ def test_equal_bits_on_repeat_side_stream_and_replayed_graph(kvq):
         assert torch.equal(out0, out2) and torch.equal(w0, w2)
 
 
+def test_two_graphs_share_a_workspace(kvq):
+    pools = [Pool("int4", 4, 128, [600, 77], 16, 64, 128, seed=2), Pool("int4", 4, 128, [31, 400], 16, 64, 128, seed=3)]
+    cfg = [p.cfg(kvq) for p in pools]
+    ws = kvq.new_weights_workspace(cfg[0], 2, 16, 600)
+    sets, graphs, want = [], [], []
+    for p, c in zip(pools, cfg):
+        s = (p.gpu(), make_q(2, 16, 128, 6), p.table_gpu(), p.lens_gpu(), torch.zeros(2, 4, 600, device="cuda"),
+             torch.empty(2, 16, 128, device="cuda"))
+
+        def go(c=c, s=s):
+            kvq.kvq_decode_attention_weights(c, *s[:4], 600, 128 ** -0.5, 0.0, s[4], s[5], ws)
+
+        go()
+        want.append((s[4].clone(), s[5].clone()))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            go()
+        sets.append(s)
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1, 0):
+        sets[i][4].zero_()
+        sets[i][5].zero_()
+        graphs[i].replay()
+        assert torch.equal(sets[i][4], want[i][0]) and torch.equal(sets[i][5], want[i][1])
+
+
+@pytest.mark.parametrize("codec", ["int4", "int8"])
+def test_thousands_of_short_sequences(kvq, codec):
+    # segments of one page, many to a CTA: warps without units of a segment keep up with the others
+    lens = [1 + (7 * b) % 40 for b in range(2100)]
+    pool = Pool(codec, 1, 128, lens, 64 if codec == "int8" else 16, 64, 128, seed=9)
+    q = make_q(len(lens), 3, 128, 5)
+    before = torch.zeros(len(lens), 1, 40, device="cuda")
+    weights = before.clone()
+    out, ws = call_weights(kvq, pool, pool.gpu(), q, 1.0, weights)
+    assert kvq.kvq_read_status(ws) == 0
+    check_weights(pool, q, 1.0, before, out, weights)
+
+
+def test_pool_beyond_four_gigabytes(kvq):
+    """Pages whose byte offsets pass 32 bits: attention with weights, differential attention and compaction give what
+    the same pages give at the start of a small pool."""
+    pool = Pool("int4", 2, 128, [100, 60], 16, 64, 128, seed=8)
+    small, q = pool.gpu(), make_q(2, 4, 128, 3)
+    pages = 5 * 2 ** 30 // (2 * pool.block)
+    shift = pages - pool.num_pages
+    big_cfg = kvq.config(2, 128, 16, 64, 128, pages)
+    big = torch.zeros(kvq.kvq_pool_bytes(big_cfg), dtype=torch.uint8, device="cuda")
+    big[-small.numel():] = small
+    table = pool.table_gpu()
+    far = torch.where(table >= 0, table + shift, table)
+    kept = torch.from_numpy(random_kept(pool, 30, 2)).cuda()
+    lam = torch.tensor([0.1, 0.5, 0.7, 0.9], device="cuda")
+
+    def go(cfg, x, t):
+        w, out, o2 = torch.zeros(2, 2, 100, device="cuda"), torch.empty(2, 4, 128, device="cuda"), \
+            torch.empty(2, 4, 128, device="cuda")
+        kvq.kvq_decode_attention_weights(cfg, x, q, t, pool.lens_gpu(), 100, 0.1, 1.0, w, out,
+                                         kvq.new_weights_workspace(cfg, 2, 4, 100))
+        kvq.kvq_diff_decode_attention(cfg, x, q, t, pool.lens_gpu(), 100, 0.1, lam, None, 0.0, 1.0, o2,
+                                      kvq.new_diff_workspace(cfg, 2, 4, 100))
+        kvq.kvq_evict_compact(cfg, x, t, t, pool.lens_gpu(), kept, w)
+        return w, out, o2
+
+    want, got = go(pool.cfg(kvq), small, table), go(big_cfg, big, far)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert torch.equal(big[-small.numel():], small) and not big[:-small.numel()].any()
+
+
 def test_agrees_with_plain_decode_attention(kvq):
     pool = Pool("int4", 8, 128, [1000, 3], 16, 64, 128, seed=12)
     x, q, cfg = pool.gpu(), make_q(2, 8, 128, 7), pool.cfg(kvq)
