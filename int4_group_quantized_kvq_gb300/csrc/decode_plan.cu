@@ -4,7 +4,8 @@
 // has its own kv head, Hkv is a multiple of 4 and pages hold 16 tokens, else HK = 1
 // (differential attention, two maps per query head: HK = 2 in that place).
 // The grid is C CTAs of 4 warps: C is the number of CTAs the device keeps resident (SMs
-// x resident CTAs), reduced for small problems so that a warp gets at least two units;
+// x resident CTAs), reduced for small problems so that a warp gets at least two units (one
+// in the weights and differential modes);
 // every CTA receives an equal contiguous slice of the flattened (sequence, head group,
 // page) units.  Each warp writes one partial per segment (sequence, head group) its
 // CTA's slice touches, at index 4 * (CTA + segment) + warp, which is unique (CTA +
@@ -70,6 +71,10 @@ namespace {
 constexpr int kMaxStages = 8;           // deepest unit ring per warp
 constexpr size_t kMaxRingBytes = 8 * 2144;  // per warp: deeper rings gain nothing
 constexpr int kMinUnitsPerWarp = 2;
+// the weights and differential modes: a short call's pages spread over as many CTAs as they fill
+// (1 x 32 / 8 heads of 513 positions, 64-token pages, weights: 9.8 -> 8.0 us on the device; 4 x 32 / 8
+// of 300, differential: 12.3 -> 9.3 us)
+constexpr int kMinUnitsPerWarpModes = 1;
 constexpr size_t kAlign = 256;
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -177,7 +182,8 @@ cudaError_t plan_decode(const DecodeArgs& a, DecodePlan* plan) {
         pages_max = std::min(pages_max, sink_pages + a.window / a.L.P + 2);
     }
     const long long u_max = static_cast<long long>(hg) * a.B * pages_max;
-    const long long ctas = std::min(c_max, std::max<long long>(1, u_max / (kMinUnitsPerWarp * kWarpsPerCta)));
+    const int min_units = a.mode == DecodeMode::kPlain ? kMinUnitsPerWarp : kMinUnitsPerWarpModes;
+    const long long ctas = std::min(c_max, std::max<long long>(1, u_max / (min_units * kWarpsPerCta)));
     plan->ctas = static_cast<int32_t>(ctas);
     // Combine CTA size from the most partials a row can have: a segment of pages_max
     // units spans about pages_max / (u_max / ctas) + 2 CTA slices, 4 partials each; a
