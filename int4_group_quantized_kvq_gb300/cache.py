@@ -122,9 +122,10 @@ class PagedKVCache:
                            status=self.status, stream=stream)
         B.kvq_evict_compact(self.cfg, self.pool, self.block_table, dst, seq_lens, kept, self.weights,
                             status=self.status, stream=stream)
-        if stream is not None and isinstance(stream, torch.cuda.Stream):
-            kept.record_stream(stream)
-            new_lens.record_stream(stream)
+        if stream is not None:  # their memory is not handed out again before the stream has passed the calls
+            used = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+            kept.record_stream(used)
+            new_lens.record_stream(used)
         self.block_table = dst
         return new_lens
 

@@ -43,7 +43,8 @@ constexpr int kSelBins = 2048;  // 11 bits a pass
 // CTA may read it).  The first digit spans sign, exponent and two mantissa bits: accumulated
 // weights lie within a few binades, and with 8 bits almost all keys of a warp would meet in
 // one or two counters.  Bound by latency (the chain of barriers and passes, not the bytes):
-// 4 x 8 rows of 32768 positions 69.7 us with one CTA a row and four 8-bit passes over the L2.
+// 4 x 8 rows of 32768 positions 69.7 us a call with one CTA a row and four 8-bit passes over
+// the L2, 11.5 so, 17.9 with one CTA a row and 32 keys a thread.
 template <int CL, int T>
 __global__ void __launch_bounds__(T) evict_select_kernel(EvictSelectArgs p) {
     constexpr int kWarps = T / 32;
@@ -195,6 +196,8 @@ __global__ void __launch_bounds__(T) evict_select_kernel(EvictSelectArgs p) {
             done_gt += from[0];
             done_eq += from[1];
         }
+        // (this CTA has read the others' shared memory: the last wait below is for the rest)
+        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     }
     // in position order, kSelKeys rounds of T positions at a time: an entry of
     // s_gt, s_eq counts a warp's 32 positions, entries ordered as positions are
@@ -248,7 +251,8 @@ __global__ void __launch_bounds__(T) evict_select_kernel(EvictSelectArgs p) {
         if (c0 + kSelKeys * T >= t1) break;
         __syncthreads();
     }
-    if (CL > 1) cg::this_cluster().sync();  // no CTA leaves while another may read its shared memory
+    // no CTA leaves while another may read its shared memory
+    if (CL > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -284,7 +288,8 @@ __device__ __forceinline__ void store_piece(uint8_t* g, int bytes, const uint4& 
 // row is read once (in 64-byte accesses that its 64 code bytes, not aligned to them, half fill:
 // 2.2 times its bytes on 8 x 32 x 2048 rows of 134 bytes, ncu) and written once.
 // One CTA per (sequence, kv head) with chunks of 64 rows through shared memory took 173 us for
-// those rows (its chain of small round trips), and 332 us for 4 x 8 x 4095 of 264.
+// those rows (its chain of small round trips), and 332 us for 4 x 8 x 4095 of 264; so 42.7 and
+// 16.7 us.
 __global__ void __launch_bounds__(kCmpThreads, 2) evict_compact_kernel(EvictCompactArgs p, int32_t rows_cta, int32_t lg_w) {
     // offset of a row's K codes in the pool, where it comes from and where it goes; -1: it stays
     __shared__ long long s_src[kCmpMaxRows], s_dst[kCmpMaxRows];

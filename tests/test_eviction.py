@@ -599,6 +599,23 @@ def test_select_and_compact_replayed_from_a_graph(kvq):
         assert all(torch.equal(a, b) for a, b in zip(want, (x, w, kept, new)))
 
 
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_evict_on_a_side_stream(kvq, as_handle):
+    from int4_group_quantized_kvq_gb300.cache import PagedKVCache
+    pool = Pool("int4", 2, 128, [200, 90], 16, 64, 128, seed=4)
+    w = torch.rand(2, 2, 200, device="cuda")
+    caches = [PagedKVCache(pool.cfg(kvq), pool.table_gpu(), 4, 200, pool=pool.gpu(), track_weights=True) for _ in range(2)]
+    for c in caches:
+        c.weights.copy_(w)
+    want = caches[0].evict(pool.lens_gpu(), 50, 2, 8)
+    side, lens = torch.cuda.Stream(), pool.lens_gpu()
+    side.wait_stream(torch.cuda.current_stream())
+    got = caches[1].evict(lens, 50, 2, 8, stream=side.cuda_stream if as_handle else side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, want) and torch.equal(caches[0].pool, caches[1].pool)
+    assert torch.equal(caches[0].weights, caches[1].weights)
+
+
 def test_cache_refuses_what_it_does_not_track(kvq):
     from int4_group_quantized_kvq_gb300.cache import HostPipeline, HostStaging, PagedKVCache
     cfg = kvq.config(2, 128, 16, 64, 128, 8)
