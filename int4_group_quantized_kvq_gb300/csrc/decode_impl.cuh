@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D, MODE, CO
     static_assert(HK == 1 || P16, "four-head units only for 16-token pages");
     static_assert(MODE == 0 || !WIN, "the weights and differential modes attend to every position");
     static_assert(MODE != 2 || (HK <= 2 && CODEC == 0 && 2 * GK <= D), "differential: INT4, units of one or two heads, K groups within a half");
-    static_assert(HK == 1 || HK == 4 || (HK == 2 && MODE == 2), "two heads per unit: differential attention");
+    static_assert(HK == 1 || HK == 4 || (HK == 2 && MODE != 0), "two heads per unit: the weights and differential modes");
     static_assert(4 * HS + 2 * HK <= kQRows, "q rows and the appended token's K and V rows fit a q buffer");
     constexpr int NGK = D / GK;               // K groups per row
     constexpr int NGV = D / GV;               // V groups per row
@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D, MODE, CO
 
     // the kv head (within the unit) of this thread's score slot, and of its B-fragment
     // column (HK > 1 only when every slot is its own kv head)
-    // (two heads of differential attention have two slots each, one per map)
+    // (of two heads each has two slots: two query heads, or the two maps of one)
     const int a_row = HK == 1 ? 0 : (HK == 2 ? c >> 1 : c);
     const int a_col = HK == 1 ? 0 : (HK == 2 ? g >> 2 : g >> 1);
     // per-thread byte offsets inside a unit buffer (chunk 0)
@@ -1545,6 +1545,10 @@ int decode_occupancy_d256_win(const DecodeArgs& a, const DecodePlan& plan, size_
 #define KVQ_WEIGHTS_OCC(D_, GK_, GV_, HK_, HS_, W_, P16_) decode::occupancy<D_, GK_, GV_, HK_, HS_, W_, P16_, 0, 1>(smem)
 #define KVQ_DIFF_RUN(D_, GK_, GV_, HK_, HS_, W_, P16_) decode::run<D_, GK_, GV_, HK_, HS_, W_, P16_, 0, 2>(a, plan, s)
 #define KVQ_DIFF_OCC(D_, GK_, GV_, HK_, HS_, W_, P16_) decode::occupancy<D_, GK_, GV_, HK_, HS_, W_, P16_, 0, 2>(smem)
+// (with units of two kv heads of two query heads each)
+#define KVQ_WEIGHTS_CASES(D_, GK_, GV_, W_, CALL)       \
+    KVQ_DECODE_CASES(D_, GK_, GV_, W_, CALL)            \
+    case KVQ_DECODE_KEY(GK_, GV_, 2, 1, 1): return CALL(D_, GK_, GV_, 2, 1, W_, true);
 // (up to four virtual heads: one-head units, or two heads of one query head each)
 #define KVQ_DIFF_CASES_4(D_, GK_, GV_, W_, CALL)        \
     KVQ_DECODE_CASES_1H(D_, GK_, GV_, W_, CALL)         \

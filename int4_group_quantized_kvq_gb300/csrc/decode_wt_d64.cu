@@ -3,10 +3,10 @@
 #include "decode_impl.cuh"
 
 #define KVQ_WT_D64_CASES(CALL)                 \
-    KVQ_DECODE_CASES(64, 32, 32, false, CALL)  \
-    KVQ_DECODE_CASES(64, 32, 64, false, CALL)  \
-    KVQ_DECODE_CASES(64, 64, 32, false, CALL)  \
-    KVQ_DECODE_CASES(64, 64, 64, false, CALL)
+    KVQ_WEIGHTS_CASES(64, 32, 32, false, CALL)  \
+    KVQ_WEIGHTS_CASES(64, 32, 64, false, CALL)  \
+    KVQ_WEIGHTS_CASES(64, 64, 32, false, CALL)  \
+    KVQ_WEIGHTS_CASES(64, 64, 64, false, CALL)
 KVQ_DECODE_TU_OF(KVQ_WT_D64_CASES, KVQ_WEIGHTS_RUN, KVQ_WEIGHTS_OCC, decode_run_wt_d64, decode_occupancy_wt_d64)
 
 namespace kvq {

@@ -90,8 +90,8 @@ cudaError_t launch_stage_in(const void* src, void* dst, size_t n16, cudaStream_t
 
 // Decode attention: the persistent split-KV kernel with the split combine fused in.
 struct DecodePlan {
-    int32_t hk;           // kv heads per unit of work (4 when Hq == Hkv, Hkv % 4 == 0, P == 16; differential
-                          // attention 2 when Hkv % 2 == 0; else 1)
+    int32_t hk;           // kv heads per unit of work (4 when Hq == Hkv, Hkv % 4 == 0, P == 16; 2 for two
+                          // slots per kv head in the weights and differential modes; else 1)
     int32_t hs;           // query-head slots per score thread: 1 (up to 4 per unit) or 2 (up to 8)
     int32_t ctas;         // CTAs of the persistent grid (4 warps each)
     int32_t stages;       // bulk-copy ring depth per warp, in units

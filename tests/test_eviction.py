@@ -61,7 +61,9 @@ def check_weights(pool, q, decay, before, out, after, lens=None):
 @pytest.mark.parametrize("Hkv,r,d,P,Gk,Gv,lens", [
     (8, 1, 128, 16, 64, 128, [513]),                     # four kv heads a unit
     (3, 1, 128, 16, 64, 64, [1, 0, 16, 17, 700]),        # one head a unit, one query head
-    (4, 2, 128, 16, 32, 32, [15, 33, 1024]),
+    (4, 2, 128, 16, 32, 32, [15, 33, 1024]),             # two heads a unit
+    (6, 2, 64, 16, 64, 32, [5, 700, 0]),
+    (3, 2, 128, 16, 128, 64, [200, 1]),
     (2, 4, 128, 16, 128, 128, [2049, 5]),
     (2, 5, 128, 16, 64, 128, [300, 31]),                 # two slots a thread, three of them empty
     (1, 8, 128, 16, 64, 32, [777]),
@@ -216,7 +218,7 @@ def test_agrees_with_plain_decode_attention(kvq):
 
 
 def test_step_is_append_then_attention(kvq):
-    for Hkv, r, d, P in ((8, 1, 128, 16), (2, 4, 128, 32), (2, 3, 256, 16)):
+    for Hkv, r, d, P in ((8, 1, 128, 16), (2, 4, 128, 32), (2, 3, 256, 16), (4, 2, 128, 16), (2, 2, 64, 16)):
         pool = Pool("int4", Hkv, d, [64, 17, 200], P, 64, 64, seed=21, spare=4, blocks=16)
         x1, q, cfg = pool.gpu(), make_q(3, Hkv * r, d, 8), pool.cfg(kvq)
         x2 = x1.clone()
