@@ -480,7 +480,7 @@ int kvq_int8_decode_attention_weights(const kvq_cache_config *cfg, const void *p
  *   keep            >= 1 and >= sinks + recent.
  *   kept            device int32 [batch, num_kv_heads, keep]: the positions kept, ascending,
  *                   then -1 up to keep.
- *   new_lens        device int32 [batch]: min(n, keep).  Not seq_lens itself (KVQ_EINVAL).
+ *   new_lens        device int32 [batch]: min(n, keep).  Must not overlap seq_lens (KVQ_EINVAL).
  *   status          device uint32 status word or NULL.
  * Returns KVQ_OK, KVQ_EINVAL, KVQ_EUNSUPPORTED or KVQ_ECUDA.
  */

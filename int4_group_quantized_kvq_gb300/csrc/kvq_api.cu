@@ -711,7 +711,9 @@ int kvq_evict_select(const kvq_cache_config* cfg, const float* weights, int32_t 
     if (batch == 0) return ok();
     if ((!weights && max_len > 0) || !seq_lens || !kept || !new_lens) return fail(KVQ_EINVAL, "NULL device pointer");
     // every kv head reads the length of its sequence while one of them writes the new one
-    if (seq_lens == new_lens) return fail(KVQ_EINVAL, "new_lens must not be seq_lens");
+    const uintptr_t from = reinterpret_cast<uintptr_t>(seq_lens), to = reinterpret_cast<uintptr_t>(new_lens);
+    if ((from > to ? from - to : to - from) < sizeof(int32_t) * static_cast<uintptr_t>(batch))
+        return fail(KVQ_EINVAL, "new_lens must not overlap seq_lens");
     if (!aligned(weights, 4) || !aligned(seq_lens, 4) || !aligned(kept, 4) || !aligned(new_lens, 4) || !aligned(status, 4))
         return fail(KVQ_EINVAL, "arguments must be 4-byte aligned");
     kvq::EvictSelectArgs a;

@@ -120,3 +120,11 @@ def test_binding_refuses_host_tensors(kvq, monkeypatch):
         kvq.kvq_decode_attention_weights(cfg, torch.zeros(99999, dtype=torch.uint8), torch.zeros(1, 2, 128).half(),
                                          torch.zeros(1, 4, dtype=torch.int32), i, 16, 1.0, 1.0, z,
                                          torch.zeros(1, 2, 128), torch.zeros(9, dtype=torch.uint8))
+
+
+def test_select_refuses_lengths_that_overlap(kvq):
+    L, cfg = kvq.lib(), kvq.config(8, 128, 16, 64, 128, 10)
+    for off in (-12, -4, 0, 4, 12):  # of 4 lengths, 16 bytes
+        assert L.kvq_evict_select(C.byref(cfg), 0x1000, 100, 0x2000, 4, 100, 10, 2, 3, 0x3000, 0x2000 + off, None,
+                                  None) == kvq.KVQ_EINVAL
+        assert "overlap" in kvq.kvq_last_error()
