@@ -438,6 +438,9 @@ int kvq_mixed_decode_attention(const kvq_cache_config *cfg, const void *pool, co
  *                   that share a workspace must not overlap on the GPU.
  *   other arguments, shapes and the launch overlap as in kvq_decode_attention (weights is
  *   read and written after the kernel ahead has finished).
+ * A kv head of which a part did not arrive (KVQ_FLAG_WAIT_TIMEOUT; out is then not the
+ *   attention either) keeps its weights as they were, without the decay; the other heads get
+ *   theirs.  To repeat such a call, put back the weights from before it.
  * kvq_decode_step_weights: the same with one new token per sequence appended first, as
  *   kvq_decode_step; weights at the token's position is zero before unless the caller wants
  *   it to start with more (kvq_evict_compact leaves zeros behind the kept positions).
@@ -595,6 +598,17 @@ int kvq_test_decode_wait_timeout(const kvq_cache_config *cfg, const void *pool, 
                                  int32_t batch, int32_t num_q_heads, int32_t max_len, float softmax_scale,
                                  float *out, void *workspace, size_t workspace_bytes, uint64_t wait_limit_ns,
                                  kvq_stream_t stream);
+
+/*
+ * The same test of kvq_decode_attention_weights, only the first CTA's copies announced too
+ * large: the kv heads it holds a part of keep their weights, the others get theirs.
+ */
+int kvq_test_decode_weights_wait_timeout(const kvq_cache_config *cfg, const void *pool, const void *q,
+                                         const int32_t *block_table, int32_t max_blocks, const int32_t *seq_lens,
+                                         int32_t batch, int32_t num_q_heads, int32_t max_len, float softmax_scale,
+                                         float decay, float *weights, int32_t weights_stride, float *out,
+                                         void *workspace, size_t workspace_bytes, uint64_t wait_limit_ns,
+                                         kvq_stream_t stream);
 
 /*
  * Dequantize positions [start, start + n) of sequence b (section 2.1 of the 4-bit

@@ -32,7 +32,7 @@ ABI_SYMBOLS = ("kvq_block_bytes", "kvq_pool_bytes", "kvq_quantize_append", "kvq_
                "kvq_decode_weights_workspace_bytes", "kvq_decode_attention_weights", "kvq_decode_step_weights",
                "kvq_int8_decode_weights_workspace_bytes", "kvq_int8_decode_attention_weights", "kvq_evict_select",
                "kvq_evict_compact", "kvq_int8_evict_compact", "kvq_diff_decode_workspace_bytes",
-               "kvq_diff_decode_attention", "kvq_diff_decode_step")
+               "kvq_diff_decode_attention", "kvq_diff_decode_step", "kvq_test_decode_weights_wait_timeout")
 
 
 class KvqError(RuntimeError):
@@ -140,6 +140,9 @@ def lib() -> C.CDLL:
             getattr(L, name).restype = C.c_int
         L.kvq_decode_step_weights.argtypes = [cfgp, P, P, P, P, P, P, I32, P, I32, I32, I32, F, F, P, I32, P, P, SZ, P]
         L.kvq_decode_step_weights.restype = C.c_int
+        L.kvq_test_decode_weights_wait_timeout.argtypes = [cfgp, P, P, P, I32, P, I32, I32, I32, F, F, P, I32, P, P, SZ,
+                                                           C.c_uint64, P]
+        L.kvq_test_decode_weights_wait_timeout.restype = C.c_int
         L.kvq_evict_select.argtypes = [cfgp, P, I32, P, I32, I32, I32, I32, I32, P, P, P, P]
         L.kvq_evict_select.restype = C.c_int
         for name in ("kvq_evict_compact", "kvq_int8_evict_compact"):
@@ -784,6 +787,20 @@ def kvq_int8_decode_attention_weights(cfg: CacheConfig, pool: torch.Tensor, q: t
     L = lib()
     _weights_call(L.kvq_int8_decode_attention_weights, L.kvq_int8_pool_bytes, cfg, pool, q, block_table, seq_lens,
                   max_len, softmax_scale, decay, weights, out, workspace, stream)
+
+
+def kvq_test_decode_weights_wait_timeout(cfg: CacheConfig, pool: torch.Tensor, q: torch.Tensor,
+                                         block_table: torch.Tensor, seq_lens: torch.Tensor, max_len: int,
+                                         softmax_scale: float, decay: float, weights: torch.Tensor, out: torch.Tensor,
+                                         workspace: torch.Tensor, wait_limit_ns: int, stream=None) -> None:
+    """The bounded-wait test of kvq_decode_attention_weights (the test suite's): the first CTA's waits run out."""
+    L = lib()
+
+    def fn(*args):
+        return L.kvq_test_decode_weights_wait_timeout(*args[:-1], int(wait_limit_ns), args[-1])
+
+    _weights_call(fn, L.kvq_pool_bytes, cfg, pool, q, block_table, seq_lens, max_len, softmax_scale, decay, weights, out,
+                  workspace, stream)
 
 
 def kvq_decode_step_weights(cfg: CacheConfig, pool: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,

@@ -28,9 +28,10 @@ struct CParams {
     float* out;
     float* out_host;  // device address of mapped pinned host memory that also receives out, or nullptr
     int32_t B, Hq, lg_p;
-    // MODE 1: (max, 1 / sum) of each row, written by the combine; the decode grid's scores
-    // [B][Hq][score_ld], the accumulated weights [B][Hkv][weights_ld], the query heads per kv
-    // head, the chunks of positions a kv head is cut into, and the bound the lengths are cut to
+    // MODE 1: (max, 1 / sum) of each row, written by the combine (the second -1 where a part of the
+    // row failed); the decode grid's scores [B][Hq][score_ld], the accumulated weights
+    // [B][Hkv][weights_ld], the query heads per kv head, the chunks of positions a kv head is cut
+    // into, and the bound the lengths are cut to
     float2* stat;
     const float* scores;
     float* weights;
@@ -65,9 +66,10 @@ struct RowPartials {
 //     weights[b][wh][t] = decay * weights[b][wh][t] + sum over the kv head's r rows of 2^(z - M) / L,
 // z the scores the decode grid stored, in row order (results do not depend on timing).  M and
 // 1 / L of the rows come from the combine (stat), or with WITH_ROWS from the (max, sum) pairs of
-// their partials, by one warp per row.  Bound by latency: a thread's scores, its old weights and
-// the rows' statistics are all in flight together, and the scores, written just before, mostly
-// still lie in the L2.  s_m, s_inv: r floats each.
+// their partials, by one warp per row.  A kv head of which a part failed (a copy that did not
+// arrive: scores that were not stored) keeps its weights as they were.  Bound by latency: a
+// thread's scores, its old weights and the rows' statistics are all in flight together, and the
+// scores, written just before, mostly still lie in the L2.  s_m, s_inv: r floats each.
 template <int R, bool WITH_ROWS>
 __device__ __forceinline__ void add_weights(const CParams& p, int b, int wh, int wt, const RowPartials& rp, float* s_m,
                                             float* s_inv) {
@@ -95,11 +97,13 @@ __device__ __forceinline__ void add_weights(const CParams& p, int b, int wh, int
             const bool dense = rp.U >= s.C;  // every CTA slice of the decode grid holds units
             const float* ml0 = s.ws_ml + (rp.base * s.ns + (hq + g) % s.ns) * 2;
             float M = -INFINITY, L = 0.f;
+            bool failed = false;
             for (int j = lane; j < rp.n; j += 32) {
                 const long long k = rp.cf + j / s.W;
                 if (!dense && slice_start(k, rp.U, s.C) >= slice_start(k + 1, rp.U, s.C)) continue;
                 const float2 ml = __ldcg(reinterpret_cast<const float2*>(ml0 + static_cast<long long>(j) * s.ns * 2));
                 const float mn = fmaxf(M, ml.x);
+                failed |= ml.y < 0.f;
                 if (mn == -INFINITY) continue;
                 L = L * fast_exp2(M - mn) + ml.y * fast_exp2(ml.x - mn);
                 M = mn;
@@ -110,9 +114,10 @@ __device__ __forceinline__ void add_weights(const CParams& p, int b, int wh, int
             L = M == -INFINITY ? 0.f : L * fast_exp2(M - Mx);
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+            failed = __any_sync(0xffffffffu, failed);
             if (lane == 0) {
                 s_m[g] = Mx;
-                s_inv[g] = L > 0.f ? 1.f / L : 0.f;
+                s_inv[g] = failed ? -1.f : (L > 0.f ? 1.f / L : 0.f);
             }
         }
     } else if (static_cast<int>(threadIdx.x) < p.r) {
@@ -121,6 +126,7 @@ __device__ __forceinline__ void add_weights(const CParams& p, int b, int wh, int
         s_inv[threadIdx.x] = st.y;
     }
     __syncthreads();
+    if (s_inv[0] < 0.f) return;  // (a warp takes all rows of a kv head or fails for all of them)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         float sum = 0.f;
@@ -187,6 +193,7 @@ combine_kernel(CParams p) {
     __shared__ float s_m[kCombineMaxWarps], s_l[kCombineMaxWarps];
     __shared__ float4 s_o[kCombineMaxWarps][D / 4];
     __shared__ int s_red[2][2][kCombineMaxWarps];
+    __shared__ bool s_failed[kCombineMaxWarps];  // MODE 1: a partial that the warp took has failed
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int nw = blockDim.x >> 5;
@@ -288,6 +295,7 @@ combine_kernel(CParams p) {
     }
 
     float M = -INFINITY, L = 0.f;
+    bool failed = false;
     float4 acc[NV][NA];
 #pragma unroll
     for (int v = 0; v < NV; ++v)
@@ -321,7 +329,10 @@ combine_kernel(CParams p) {
             }
             float mb = M;
 #pragma unroll
-            for (int kk = 0; kk < NB; ++kk) mb = fmaxf(mb, ml[kk].x);
+            for (int kk = 0; kk < NB; ++kk) {
+                mb = fmaxf(mb, ml[kk].x);
+                if constexpr (MODE == 1) failed |= ml[kk].y < 0.f;
+            }
             if (mb == -INFINITY) continue;  // only empty partials so far
             if (mb > M) {  // a larger running maximum: rescale what has been summed
                 const float f = fast_exp2(M - mb);
@@ -355,6 +366,7 @@ combine_kernel(CParams p) {
     if (lane == 0) {
         s_m[warp] = M;
         s_l[warp] = L;
+        if constexpr (MODE == 1) s_failed[warp] = failed;
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -439,7 +451,8 @@ combine_kernel(CParams p) {
     }
     const long long row = static_cast<long long>(b) * rows_b + hrow;
     if constexpr (MODE == 1) {
-        if (lane == 0) p.stat[row] = make_float2(Mx, inv);
+        failed = __any_sync(0xffffffffu, lane < nw && s_failed[lane]);
+        if (lane == 0) p.stat[row] = make_float2(Mx, failed ? -1.f : inv);
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {

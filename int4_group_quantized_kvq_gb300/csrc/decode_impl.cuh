@@ -140,8 +140,8 @@ struct KParams {
     // positions attended: seq_lens[b] - len_sub (the INT4 part of the mixed-precision decode
     // stops len_sub positions short of the sequence's end; 0 otherwise)
     int32_t len_sub;
-    // bound of every wait on a copy, in ns; and a test of that bound: with withhold > 0 each
-    // warp announces its first page copy as `withhold` bytes larger than it is, so the wait
+    // bound of every wait on a copy, in ns; and a test of that bound: with withhold > 0 each warp
+    // (MODE 1: of the first CTA) announces its first page copy as `withhold` bytes larger than it is, so the wait
     // for it runs out
     uint64_t wait_ns;
     uint32_t withhold;
@@ -678,9 +678,10 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D, MODE, CO
     if (q_late) issue_first_q();
     publish_prefix();
     orphan_appends();
+    const bool withheld = p.withhold != 0 && (MODE != 1 || cta == 0);
     {
         const int pro = nm < stages ? nm : stages;
-        if (p.withhold != 0 && lane == 0 && pro > 0) mbar_expect_tx(bar0, p.withhold);  // before the copy is issued
+        if (withheld && lane == 0 && pro > 0) mbar_expect_tx(bar0, p.withhold);  // before the copy is issued
         for (int k = 0; k < pro; ++k) issue(k, k);
     }
 
@@ -1307,9 +1308,12 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D, MODE, CO
                         *reinterpret_cast<float2*>(p.ws_ml + (piece * p.ns + srow) * 2) = make_float2(m[s] - kUp, lt[s]);
                 }
             } else {
-                // no units of this segment here (or a failed wait): an empty partial
+                // no units of this segment here (or a failed wait): an empty partial.  In MODE 1 a
+                // failed one has a sum of -1, which the maximum -inf keeps out of the row's: its
+                // positions' scores were not stored, and the weights' kernel leaves the kv head alone
+                const float none = MODE == 1 && cnt > 0 ? -1.f : 0.f;
                 if (lane < p.ns)
-                    *reinterpret_cast<float2*>(p.ws_ml + (piece * p.ns + lane) * 2) = make_float2(-INFINITY, 0.f);
+                    *reinterpret_cast<float2*>(p.ws_ml + (piece * p.ns + lane) * 2) = make_float2(-INFINITY, none);
                 for (int k = 0; k < p.ns; ++k)
 #pragma unroll
                     for (int f = lane; f < D / 4; f += 32)
@@ -1347,7 +1351,7 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D, MODE, CO
     if (failed) {
         // the withheld bytes of the first copy's phase, as a 16-byte copy of its own, so that
         // the phase completes once both copies have landed
-        if (p.withhold != 0 && f_consumed == 0 && f_out > 0 && lane == 0)
+        if (withheld && f_consumed == 0 && f_out > 0 && lane == 0)
             bulk_g2s(ring0, p.pool, p.withhold, bar0);
         int st = f_st;
         uint32_t par = f_par;

@@ -531,7 +531,7 @@ int decode_mode_impl(const char* name, kvq::DecodeMode mode, const ModeArgs& x, 
                      bool append, const void* k_new, const void* v_new, const int32_t* append_pos, const void* q,
                      const int32_t* block_table, int32_t max_blocks, const int32_t* seq_lens, int32_t batch,
                      int32_t num_q_heads, int32_t max_len, float softmax_scale, float* out, void* workspace,
-                     size_t workspace_bytes, kvq_stream_t stream, int codec = 0) {
+                     size_t workspace_bytes, kvq_stream_t stream, int codec = 0, uint64_t test_wait_ns = 0) {
     const bool diff = mode == kvq::DecodeMode::kDiff;
     if (int e = check_cfg(cfg)) return e;
     if (batch < 0 || num_q_heads < 1 || max_len < 0)
@@ -590,6 +590,10 @@ int decode_mode_impl(const char* name, kvq::DecodeMode mode, const ModeArgs& x, 
     a.int8 = codec == 2;
     a.L = kvq::block_layout(*cfg);
     half_page_units(&a);
+    if (test_wait_ns != 0) {
+        a.wait_ns = test_wait_ns;
+        a.withhold_first_copy = true;
+    }
     if (append) {
         a.k_new = static_cast<const __half*>(k_new);
         a.v_new = static_cast<const __half*>(v_new);
@@ -664,6 +668,24 @@ int kvq_decode_step_weights(const kvq_cache_config* cfg, void* pool, const void*
     return decode_mode_impl("kvq_decode_step_weights", kvq::DecodeMode::kWeights, x, cfg, pool, true, k_new, v_new,
                             append_pos, q, block_table, max_blocks, seq_lens, batch, num_q_heads, max_len,
                             softmax_scale, out, workspace, workspace_bytes, stream);
+}
+
+int kvq_test_decode_weights_wait_timeout(const kvq_cache_config* cfg, const void* pool, const void* q,
+                                         const int32_t* block_table, int32_t max_blocks, const int32_t* seq_lens,
+                                         int32_t batch, int32_t num_q_heads, int32_t max_len, float softmax_scale,
+                                         float decay, float* weights, int32_t weights_stride, float* out,
+                                         void* workspace, size_t workspace_bytes, uint64_t wait_limit_ns,
+                                         kvq_stream_t stream) {
+    if (wait_limit_ns < 1000 || wait_limit_ns > 10000000)
+        return fail(KVQ_EINVAL, "wait_limit_ns %llu outside [1 us, 10 ms]", static_cast<unsigned long long>(wait_limit_ns));
+    ModeArgs x;
+    x.weights = weights;
+    x.weights_stride = weights_stride;
+    x.decay = decay;
+    return decode_mode_impl("kvq_test_decode_weights_wait_timeout", kvq::DecodeMode::kWeights, x, cfg,
+                            const_cast<void*>(pool), false, nullptr, nullptr, nullptr, q, block_table, max_blocks,
+                            seq_lens, batch, num_q_heads, max_len, softmax_scale, out, workspace, workspace_bytes,
+                            stream, 0, wait_limit_ns);
 }
 
 int kvq_diff_decode_attention(const kvq_cache_config* cfg, const void* pool, const void* q, const int32_t* block_table,

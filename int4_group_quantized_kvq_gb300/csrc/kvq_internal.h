@@ -148,7 +148,8 @@ struct DecodeArgs {
     // this grid start early: the grid reads q only after griddepcontrol.wait
     bool q_after_wait = false;
     // bound of the INT4 kernel's waits on copies in ns (0: the default, 250 ms), and the test
-    // of that bound (each warp's first page copy announced 16 bytes larger than it is)
+    // of that bound (each warp's, kWeights: each of the first CTA's, first page copy announced 16
+    // bytes larger than it is)
     uint64_t wait_ns = 0;
     bool withhold_first_copy = false;
     DecodeMode mode = DecodeMode::kPlain;

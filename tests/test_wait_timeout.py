@@ -50,3 +50,34 @@ def test_wait_limit_outside_its_range_is_rejected(kvq):
                                          case.q.cuda(), case.block_table.cuda(),
                                          torch.tensor([40], dtype=torch.int32, device="cuda"), 40, case.scale, out, ws,
                                          100)
+
+
+@pytest.mark.parametrize("B,Hkv,r,P,lens", [
+    (1, 1, 4, 16, [40]),                                  # one CTA: no head is complete
+    (2, 4, 4, 16, [600, 77]),                             # the weights in the combine's launch
+    (6, 8, 4, 16, [600, 77, 1, 33, 250, 0]),              # and in their own
+    (8, 32, 1, 16, [90, 77, 1, 33, 250, 0, 16, 17]),      # four kv heads a unit
+    (3, 4, 7, 64, [700, 130, 64]),
+])
+@pytest.mark.parametrize("decay", [1.0, 0.0, 0.5])
+def test_weights_of_heads_whose_copies_failed_stay(kvq, B, Hkv, r, P, lens, decay):
+    """The first CTA's copies fail: the kv heads it has part of keep their weights, the others get theirs."""
+    case = Case(B, Hkv * r, Hkv, 128, lens, P=P, seed=54)
+    cfg = case.cfg(kvq)
+    pool, q, table = torch.from_numpy(case.oracle_pool()).cuda(), case.q.cuda(), case.block_table.cuda()
+    n, ml = torch.tensor(lens, dtype=torch.int32, device="cuda"), max(lens)
+    ws = kvq.new_weights_workspace(cfg, B, case.Hq, ml)
+    out = torch.empty((B, case.Hq, 128), dtype=torch.float32, device="cuda")
+    before = torch.rand(B, Hkv, ml, device="cuda")
+    got, want = before.clone(), before.clone()
+    kvq.kvq_test_decode_weights_wait_timeout(cfg, pool, q, table, n, ml, case.scale, decay, got, out, ws, 5_000_000)
+    assert kvq.kvq_read_status(ws) == kvq.KVQ_FLAG_WAIT_TIMEOUT
+    ws[:4] = 0
+    kvq.kvq_decode_attention_weights(cfg, pool, q, table, n, ml, case.scale, decay, want, out, ws)
+    assert kvq.kvq_read_status(ws) == 0
+    stayed = {(b, h) for b in range(B) for h in range(Hkv) if lens[b] and torch.equal(got[b, h], before[b, h])}
+    for b in range(B):
+        for h in range(Hkv):
+            assert (b, h) in stayed or torch.equal(got[b, h], want[b, h]), (b, h)
+    assert (0, 0) in stayed
+    assert len(stayed) == 1 if B == 1 else len(stayed) < B * Hkv / 2
