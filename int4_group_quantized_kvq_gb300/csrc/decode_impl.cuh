@@ -1082,7 +1082,8 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D, MODE, CO
                 Leff = sspan.L;
                 wlo = sspan.wlo;
             } else {
-                Leff = min(lens[b], p.max_blocks * p.P);
+                // (the table's positions may pass 31 bits)
+                Leff = static_cast<int>(min(static_cast<long long>(lens[b]), static_cast<long long>(p.max_blocks) << p.lg_p));
             }
             apg_seg = -1;
             if constexpr (!I8) {

@@ -673,3 +673,37 @@ def test_tensors_are_checked(kvq):
         kvq.kvq_evict_compact(cfg, x, table, table, lens, kept[:1].contiguous(), w)
     with pytest.raises(ValueError):
         kvq.kvq_evict_compact(cfg, x, table, table[:1].contiguous(), lens, kept, w)
+
+
+@pytest.mark.parametrize("form", ["weights", "int8 weights", "differential", "plain"])
+def test_block_table_of_more_than_31_bits_of_positions(kvq, form):
+    """A table of 2^25 pages of 64 tokens: what a short table of the same pages gives."""
+    codec = "int8" if form == "int8 weights" else "int4"
+    pool = Pool(codec, 2, 128, [150], 64, 64, 128, seed=13)
+    x, q, cfg, lens = pool.gpu(), make_q(1, 8, 128, 14), pool.cfg(kvq), pool.lens_gpu()
+    short = pool.table_gpu()
+    long = torch.full((1, 1 << 25), -1, dtype=torch.int32, device="cuda")
+    long[:, :short.shape[1]] = short
+    lam = torch.full((8,), 0.4, device="cuda")
+
+    def go(table):
+        w, out = torch.rand(1, 2, 150, generator=torch.Generator("cuda").manual_seed(1), device="cuda"), \
+            torch.zeros(1, 8, 128, device="cuda")
+        args = cfg, x, q, table, lens, 150, 0.1
+        if form == "plain":
+            ws = kvq.new_workspace(cfg, 1, 8, 150)
+            kvq.kvq_decode_attention(*args, out, ws)
+        elif form == "differential":
+            ws = kvq.new_diff_workspace(cfg, 1, 8, 150)
+            kvq.kvq_diff_decode_attention(*args, lam, None, 0.0, 1.0, out, ws)
+        elif codec == "int8":
+            ws = kvq.new_int8_weights_workspace(cfg, 1, 8, 150)
+            kvq.kvq_int8_decode_attention_weights(*args, 1.0, w, out, ws)
+        else:
+            ws = kvq.new_weights_workspace(cfg, 1, 8, 150)
+            kvq.kvq_decode_attention_weights(*args, 1.0, w, out, ws)
+        assert kvq.kvq_read_status(ws) == 0
+        return w, out
+
+    (w0, o0), (w1, o1) = go(short), go(long)
+    assert o0.any() and torch.equal(w0, w1) and torch.equal(o0, o1)
