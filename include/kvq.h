@@ -507,9 +507,10 @@ int kvq_evict_select(const kvq_cache_config *cfg, const float *weights, int32_t 
  *                   kept positions move along, the ones behind them up to seq_lens[b] become 0.
  *   status          device uint32 status word or NULL.
  * A kept position outside the sequence, a position outside a table (KVQ_FLAG_BAD_POSITION) or
- * a page id out of range (KVQ_FLAG_BAD_PAGE) is skipped and flagged; nothing outside the
- * arguments is read or written.  A length beyond the table (or beyond weights_stride) is cut
- * to it and flagged.  The slots of dst_table's pages that no row is moved to keep their bytes.
+ * a page id out of range (KVQ_FLAG_BAD_PAGE) is skipped and flagged: no row goes to its
+ * position, whose weight becomes 0.  Nothing outside the arguments is read or written.  A
+ * length beyond the table (or beyond weights_stride) is cut to it and flagged.  The slots of
+ * dst_table's pages that no row is moved to keep their bytes.
  * kvq_int8_evict_compact: the same over the INT8 per-row cache (head_dim 64, 128 or 256).
  * Returns KVQ_OK, KVQ_EINVAL, KVQ_EUNSUPPORTED or KVQ_ECUDA.
  */

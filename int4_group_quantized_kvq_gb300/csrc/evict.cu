@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kCmpThreads, 2) evict_compact_kernel(EvictComp
     for (long long base = 0; base < m; base += static_cast<long long>(size) * rows_cta) {
         const long long r0 = base + static_cast<long long>(rank) * rows_cta;
         const int rows = r0 < m ? static_cast<int>(min(static_cast<long long>(rows_cta), m - r0)) : 0;
-        // this thread's row: its weight and scales, and where the scales go
+        // this thread's row: its weight (0 if it is skipped) and scales, and where the scales go
         float wv = 0.f;
         uint4 ks = make_uint4(0, 0, 0, 0), vs = ks;
         uint8_t* to = nullptr;  // the destination block, or nullptr
@@ -345,8 +345,9 @@ __global__ void __launch_bounds__(kCmpThreads, 2) evict_compact_kernel(EvictComp
                 raise_flag(p.status, KVQ_FLAG_BAD_POSITION);
             } else {
                 const int ss = t & (P - 1), ds = (static_cast<int>(r0) + tid) & (P - 1);
-                if (w) wv = w[t];
-                if (sp < 0 || sp >= p.num_pages || dp < 0 || dp >= p.num_pages) {
+                const bool pages = sp >= 0 && sp < p.num_pages && dp >= 0 && dp < p.num_pages;
+                if (w && pages) wv = w[t];
+                if (!pages) {
                     raise_flag(p.status, KVQ_FLAG_BAD_PAGE);
                 } else if (sp != dp || ss != ds) {
                     src = (static_cast<long long>(sp) * p.Hkv + h) * p.block_bytes;

@@ -707,3 +707,35 @@ def test_block_table_of_more_than_31_bits_of_positions(kvq, form):
 
     (w0, o0), (w1, o1) = go(short), go(long)
     assert o0.any() and torch.equal(w0, w1) and torch.equal(o0, o1)
+
+
+def test_a_row_that_is_not_moved_has_weight_zero(kvq):
+    pool = Pool("int4", 2, 128, [100, 90], 16, 64, 128, seed=4)
+    kept = random_kept(pool, 40, 8)
+    w = 1 + np.random.default_rng(1).random((2, 2, 100)).astype(np.float32)
+    _, want = plain_compact(pool, pool.bytes, pool.table, pool.table, kept, w)
+    # positions outside the sequence
+    bad, expect = kept.copy(), want.copy()
+    bad[0, 1, 39], expect[0, 1, 39] = 100, 0
+    bad[1, 0, 0], expect[1, 0, 0] = -3, 0
+    _, u = run_compact(kvq, pool, pool.table, pool.table, bad, w)
+    assert np.array_equal(u, expect)
+    # pages out of range: a source's (in place also a destination's), and a destination's alone
+    table = pool.table.copy()
+    table[0, 1] = pool.num_pages
+    _, u = run_compact(kvq, pool, table, table, kept, w)
+    expect = want.copy()
+    for h in range(2):
+        for i in range(40):
+            if kept[0, h, i] // 16 == 1 or i // 16 == 1:
+                expect[0, h, i] = 0
+    assert np.array_equal(u, expect) and (expect != want).any()
+    _, u = run_compact(kvq, pool, pool.table, table, kept, w)
+    expect = want.copy()
+    expect[0, :, 16:32] = 0
+    assert np.array_equal(u, expect)
+    # positions behind a short destination table
+    _, u = run_compact(kvq, pool, pool.table, np.ascontiguousarray(pool.table[:, :2]), kept, w)
+    expect = want.copy()
+    expect[:, :, 32:40] = 0
+    assert np.array_equal(u, expect)
