@@ -14,8 +14,9 @@ With ``track_weights`` the cache also accumulates the attention weight each cach
 receives (``kvq_decode_attention_weights`` / ``kvq_decode_step_weights``), and ``evict`` cuts it
 by that measure to a budget of positions, each KV head keeping its own
 (``kvq_evict_select``, ``kvq_evict_compact``).  A batch slot that takes a new sequence starts with
-``cache.weights[b] = 0``.  ``attend_diff`` and ``decode_step_diff`` read the
-same pool as differential attention, for a cache made with ``diff`` (``kvq_diff_decode_attention`` / ``kvq_diff_decode_step``).
+``cache.weights[b] = 0``.  ``attend_diff`` and ``decode_step_diff`` read the same pool as
+differential attention, for a cache made with ``diff`` (``kvq_diff_decode_attention`` /
+``kvq_diff_decode_step``); they know no window and add nothing to the weights.
 
 ``decode_step_host`` is the same step driven from pinned host buffers (``HostStaging``)
 in one kvq_decode_step_host call: the step's q, K and V are copied in with one transfer
@@ -51,6 +52,8 @@ class PagedKVCache:
         self.pool = pool
         self.decay = float(decay)
         self.weights = None
+        if diff and self.window > 0:
+            raise ValueError("differential attention attends to every position (no window)")
         self.diff_workspace = B.new_diff_workspace(cfg, self.batch, self.num_q_heads, self.max_len,
                                                    device=self.device) if diff else None
         if track_weights:

@@ -155,3 +155,10 @@ def test_tensors_are_checked(kvq):
     for bad in (dict(norm_eps=-1.0), dict(norm_eps=float("nan")), dict(workspace=base["workspace"][:512].clone())):
         with pytest.raises(kvq.KvqError):
             kvq.kvq_diff_decode_attention(**{**base, **bad})
+
+
+def test_a_cache_with_a_window_has_no_differential_attention(kvq):
+    from int4_group_quantized_kvq_gb300.cache import PagedKVCache
+    with pytest.raises(ValueError):
+        PagedKVCache(kvq.config(2, 128, 16, 64, 128, 8), torch.arange(8, dtype=torch.int32).view(1, 8), 4, 128,
+                     window=16, diff=True)
