@@ -117,7 +117,8 @@ class PagedKVCache:
         if self.weights is None:
             raise ValueError("evict needs a cache with track_weights")
         dst = self.block_table if dst_table is None else dst_table
-        if int(dst.shape[1]) * self.cfg.page_size < min(int(keep), self.max_len):
+        pages = int(self.block_table.shape[1])  # (a sequence is no longer than its pages)
+        if int(dst.shape[1]) * self.cfg.page_size < min(int(keep), self.max_len, pages * self.cfg.page_size):
             raise ValueError(f"dst_table has {int(dst.shape[1])} pages a sequence, too few for {keep} positions")
         kept = torch.empty(self.batch, self.cfg.num_kv_heads, int(keep), dtype=torch.int32, device=self.device)
         new_lens = torch.empty(self.batch, dtype=torch.int32, device=self.device)

@@ -739,3 +739,17 @@ def test_a_row_that_is_not_moved_has_weight_zero(kvq):
     expect = want.copy()
     expect[:, :, 32:40] = 0
     assert np.array_equal(u, expect)
+
+
+def test_evict_in_place_asks_for_no_more_pages_than_the_cache_has(kvq):
+    from int4_group_quantized_kvq_gb300.cache import PagedKVCache
+    pool = Pool("int4", 2, 128, [100, 60], 16, 64, 128, seed=4)  # 7 pages a sequence: 112 positions
+    cache = PagedKVCache(pool.cfg(kvq), pool.table_gpu(), 4, 200, pool=pool.gpu(), track_weights=True)
+    cache.weights.copy_(torch.rand(2, 2, 200, device="cuda"))
+    w = cache.weights.clone()
+    assert cache.evict(pool.lens_gpu(), 150, 2, 8).tolist() == [100, 60]
+    assert cache.flags() == 0
+    assert np.array_equal(cache.pool.cpu().numpy().reshape(pool.bytes.shape), pool.bytes)
+    assert torch.equal(cache.weights[0, :, :100], w[0, :, :100]) and torch.equal(cache.weights[1, :, :60], w[1, :, :60])
+    with pytest.raises(ValueError):  # 112 positions do not fit into 6 pages
+        cache.evict(pool.lens_gpu(), 150, 2, 8, dst_table=cache.block_table[:, :6].contiguous())
