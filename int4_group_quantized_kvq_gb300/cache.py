@@ -126,11 +126,14 @@ class PagedKVCache:
                            status=self.status, stream=stream)
         B.kvq_evict_compact(self.cfg, self.pool, self.block_table, dst, seq_lens, kept, self.weights,
                             status=self.status, stream=stream)
-        if stream is not None:  # their memory is not handed out again before the stream has passed the calls
+        # no tensor's memory is handed out again before the stream has passed the calls
+        if stream is not None:
             used = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
             kept.record_stream(used)
             new_lens.record_stream(used)
-        self.block_table = dst
+        if dst is not self.block_table:
+            self.block_table.record_stream(torch.cuda.current_stream() if stream is None else used)
+            self.block_table = dst
         return new_lens
 
     def attend_diff(self, q, lam, seq_lens, out, norm_weight=None, norm_eps: float = 1e-5, out_scale: float = 1.0,

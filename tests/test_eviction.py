@@ -753,3 +753,31 @@ def test_evict_in_place_asks_for_no_more_pages_than_the_cache_has(kvq):
     assert torch.equal(cache.weights[0, :, :100], w[0, :, :100]) and torch.equal(cache.weights[1, :, :60], w[1, :, :60])
     with pytest.raises(ValueError):  # 112 positions do not fit into 6 pages
         cache.evict(pool.lens_gpu(), 150, 2, 8, dst_table=cache.block_table[:, :6].contiguous())
+
+
+@pytest.mark.parametrize("current", [False, True])
+def test_evict_on_a_side_stream_holds_the_table_it_reads(kvq, current):
+    """The old block table's memory is not handed out while the side stream may still read it."""
+    from int4_group_quantized_kvq_gb300.cache import PagedKVCache
+    pool = Pool("int4", 2, 128, [200], 16, 64, 128, seed=4, spare=8)
+    wide = np.full((1, 1 << 20), -1, np.int32)  # 4 MB, found again by the next requests of its size
+    wide[:, :pool.blocks] = pool.table
+    cache = PagedKVCache(pool.cfg(kvq), torch.from_numpy(wide), 4, 200, pool=pool.gpu(), track_weights=True)
+    cache.weights.copy_(torch.rand(1, 2, 200, device="cuda"))
+    dst, lens = torch.from_numpy(pool.spare[:4][None].copy()).cuda(), pool.lens_gpu()
+    first = cache.block_table.data_ptr()
+    last = first + 4 * wide.size
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    if current:
+        with torch.cuda.stream(side):
+            cache.evict(lens, 60, 2, 8, dst_table=dst)
+    else:
+        cache.evict(lens, 60, 2, 8, dst_table=dst, stream=side)
+    assert not side.query(), "the side stream is still busy"
+    new = [torch.empty(1 << 20, dtype=torch.int32, device="cuda") for _ in range(16)]
+    assert all(t.data_ptr() + 4 * t.numel() <= first or t.data_ptr() >= last for t in new)
+    side.synchronize()
+    assert cache.flags() == 0
