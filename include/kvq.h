@@ -480,7 +480,7 @@ int kvq_int8_decode_attention_weights(const kvq_cache_config *cfg, const void *p
  *                   kvq_decode_attention_weights; weights_stride >= max_len.
  *   seq_lens        device int32 [batch]; one beyond max_len raises KVQ_FLAG_BAD_POSITION and
  *                   counts as max_len.
- *   keep            >= 1 and >= sinks + recent.
+ *   keep            >= 1 and >= sinks + recent; at most 2^30, as max_len.
  *   kept            device int32 [batch, num_kv_heads, keep]: the positions kept, ascending,
  *                   then -1 up to keep.
  *   new_lens        device int32 [batch]: min(n, keep).  Must not overlap seq_lens (KVQ_EINVAL).

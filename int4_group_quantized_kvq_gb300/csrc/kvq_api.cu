@@ -727,7 +727,8 @@ int kvq_evict_select(const kvq_cache_config* cfg, const float* weights, int32_t 
         return fail(KVQ_EINVAL, "keep %d, sinks %d, recent %d: keep must be at least 1 and sinks + recent", keep, sinks,
                     recent);
     if (weights_stride < max_len) return fail(KVQ_EINVAL, "weights_stride %d < max_len %d", weights_stride, max_len);
-    if (max_len > kMaxWeightLen) return fail(KVQ_EUNSUPPORTED, "max_len %d > 2^30", max_len);
+    if (max_len > kMaxWeightLen || keep > kMaxWeightLen)
+        return fail(KVQ_EUNSUPPORTED, "max_len %d or keep %d > 2^30", max_len, keep);
     if (batch > 65535) return fail(KVQ_EUNSUPPORTED, "batch %d > 65535", batch);
     if (cfg->num_kv_heads > 65535) return fail(KVQ_EUNSUPPORTED, "num_kv_heads %d > 65535", cfg->num_kv_heads);
     if (batch == 0) return ok();

@@ -128,3 +128,11 @@ def test_select_refuses_lengths_that_overlap(kvq):
         assert L.kvq_evict_select(C.byref(cfg), 0x1000, 100, 0x2000, 4, 100, 10, 2, 3, 0x3000, 0x2000 + off, None,
                                   None) == kvq.KVQ_EINVAL
         assert "overlap" in kvq.kvq_last_error()
+
+
+def test_select_refuses_budgets_past_its_position_arithmetic(kvq):
+    L, cfg = kvq.lib(), kvq.config(8, 128, 16, 64, 128, 10)
+    for keep in ((1 << 30) + 1, (1 << 31) - 8192, (1 << 31) - 1):
+        assert L.kvq_evict_select(C.byref(cfg), 0x1000, 100, 0x2000, 1, 100, keep, 2, 3, 0x3000, 0x4000, None,
+                                  None) == kvq.KVQ_EUNSUPPORTED
+        assert "keep" in kvq.kvq_last_error()
