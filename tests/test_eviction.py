@@ -781,3 +781,34 @@ def test_evict_on_a_side_stream_holds_the_table_it_reads(kvq, current):
     assert all(t.data_ptr() + 4 * t.numel() <= first or t.data_ptr() >= last for t in new)
     side.synchronize()
     assert cache.flags() == 0
+
+
+# Calls that leave the weights to a kernel of their own: more than 152 rows of the output and chunks of weights.
+@pytest.mark.parametrize("codec,Hkv,r,d,P,Gk,Gv,lens", [
+    ("int4", 32, 1, 128, 16, 64, 128, [300, 31, 0, 513, 17]),            # four kv heads a unit
+    ("int4", 32, 1, 128, 16, 64, 128, [(37 * b) % 200 for b in range(20)]),  # 640 rows: the light combine
+    ("int4", 7, 1, 128, 64, 32, 64, [64, 63, 1, 700] * 6),
+    ("int4", 16, 2, 128, 16, 32, 32, [2049, 5, 100, 16, 0]),             # two kv heads a unit
+    ("int4", 8, 5, 128, 16, 64, 128, [300, 31, 1, 700]),                 # two slots a thread
+    ("int4", 4, 8, 128, 32, 128, 64, [999, 64, 65, 1, 0]),
+    ("int4", 4, 4, 128, 16, 64, 128, [40001]),                           # rows of many partials, many chunks
+    ("int4", 8, 7, 64, 32, 64, 32, [400, 255, 1]),
+    ("int4", 16, 4, 256, 16, 64, 128, [300, 17, 129]),
+    ("int4", 33, 1, 256, 64, 128, 32, [129, 0, 640, 1, 2]),
+    ("int8", 8, 5, 128, 64, 128, 128, [300, 1291, 701, 65, 33]),         # half-page units, two slots a thread
+    ("int8", 4, 8, 128, 16, 128, 128, [513, 40, 1, 0, 200]),
+    ("int8", 40, 1, 128, 32, 128, 128, [33, 250, 64, 1]),
+])
+@pytest.mark.parametrize("decay", [1.0, 0.0, 0.75])
+def test_weights_in_a_launch_of_their_own_match_fp64(kvq, codec, Hkv, r, d, P, Gk, Gv, lens, decay):
+    chunk = 256 * (8 if r == 1 else 16 // (2 if r == 2 else 4 if r <= 4 else 8))
+    assert len(lens) * Hkv * (r + -(-max(lens) // chunk)) > 152
+    pool = Pool(codec, Hkv, d, lens, P, Gk, Gv, seed=d + r, poison=True)
+    q = make_q(len(lens), Hkv * r, d, 3)
+    before = torch.rand(len(lens), Hkv, max(lens) + 5, device="cuda")
+    if decay == 0.0:
+        before.fill_(float("nan"))  # not read
+    weights = before.clone()
+    out, ws = call_weights(kvq, pool, pool.gpu(), q, decay, weights)
+    assert kvq.kvq_read_status(ws) == 0
+    check_weights(pool, q, decay, before, out, weights)
