@@ -70,6 +70,7 @@
 
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <type_traits>
@@ -125,6 +126,7 @@ struct KParams {
     uint32_t* status;
     int32_t B, Hq, Hkv, Hg, r, ns;  // Hg = Hkv / HK head groups; ns = HK * r query heads per unit
     int32_t P, num_pages, max_blocks, block_bytes, unit_bytes, stages;
+    int32_t max_pos;  // positions a row of the block table holds, at most 2^31 - 1
     int32_t v_codes, k_scales, v_scales;
     float scale_log2;  // softmax_scale * log2(e)
     // fused append (decode step): one token per sequence, K and V rows [B, Hkv, D] fp16,
@@ -678,10 +680,10 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D, MODE, CO
     if (q_late) issue_first_q();
     publish_prefix();
     orphan_appends();
-    const bool withheld = p.withhold != 0 && (MODE != 1 || cta == 0);
+    auto withheld = [&]() { return p.withhold != 0 && (MODE != 1 || blockIdx.x == 0); };
     {
         const int pro = nm < stages ? nm : stages;
-        if (withheld && lane == 0 && pro > 0) mbar_expect_tx(bar0, p.withhold);  // before the copy is issued
+        if (withheld() && lane == 0 && pro > 0) mbar_expect_tx(bar0, p.withhold);  // before the copy is issued
         for (int k = 0; k < pro; ++k) issue(k, k);
     }
 
@@ -1082,8 +1084,7 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D, MODE, CO
                 Leff = sspan.L;
                 wlo = sspan.wlo;
             } else {
-                // (the table's positions may pass 31 bits)
-                Leff = static_cast<int>(min(static_cast<long long>(lens[b]), static_cast<long long>(p.max_blocks) << p.lg_p));
+                Leff = min(lens[b], p.max_pos);
             }
             apg_seg = -1;
             if constexpr (!I8) {
@@ -1352,7 +1353,7 @@ __global__ void __launch_bounds__(cta_warps<HS>() * 32, min_ctas<HS, D, MODE, CO
     if (failed) {
         // the withheld bytes of the first copy's phase, as a 16-byte copy of its own, so that
         // the phase completes once both copies have landed
-        if (withheld && f_consumed == 0 && f_out > 0 && lane == 0)
+        if (withheld() && f_consumed == 0 && f_out > 0 && lane == 0)
             bulk_g2s(ring0, p.pool, p.withhold, bar0);
         int st = f_st;
         uint32_t par = f_par;
@@ -1431,6 +1432,7 @@ cudaError_t run(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t stream
     p.P = a.L.P;
     p.num_pages = a.num_pages;
     p.max_blocks = a.max_blocks;
+    p.max_pos = static_cast<int32_t>(std::min<long long>(static_cast<long long>(a.max_blocks) * a.L.P, 0x7fffffff));
     p.block_bytes = a.L.bytes;
     p.v_codes = a.L.v_codes;
     p.k_scales = a.L.k_scales;
