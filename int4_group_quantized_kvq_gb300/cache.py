@@ -111,9 +111,11 @@ class PagedKVCache:
               stream=None) -> torch.Tensor:
         """Cut every sequence to at most `keep` positions: the first `sinks`, the last `recent` and the ones of
         largest accumulated weight, each KV head its own.  The rows move to the front of the sequence's pages, or
-        into dst_table's (int32 [B, blocks]), which then becomes the cache's block table.  Returns the new lengths
-        (int32 [B]); pages from ceil(new length / page_size) on are free.  Allocates its small results on the
-        current stream, so `stream` is that one or one that waits for it."""
+        into dst_table's (int32 [B, blocks]), which then becomes the cache's block table.  dst_table has to hold the
+        positions kept; a table with room for those alone is full, so a decode_step behind them appends nothing and
+        flags KVQ_FLAG_BAD_POSITION on the device.  A graph captured before holds the old table's address: it is to
+        be captured again, not replayed.  Returns the new lengths (int32 [B]); pages from ceil(new length / page_size) on are free.  Allocates
+        its small results on the current stream, so `stream` is that one or one that waits for it."""
         if self.weights is None:
             raise ValueError("evict needs a cache with track_weights")
         dst = self.block_table if dst_table is None else dst_table

@@ -570,7 +570,7 @@ cudaError_t launch_combine(const DecodeArgs& a, const DecodePlan& plan, cudaStre
     p.out_scale = a.out_scale;
     const long long adders = static_cast<long long>(a.B) * a.Hkv * p.chunks;
     const bool weights = a.mode == DecodeMode::kWeights && adders > 0;
-    // everything behind the decode grid in one launch where it leaves the device's 152 SMs a CTA each
+    // everything behind the decode grid in one launch where it is no more CTAs than the device's 152 SMs
     const bool one = weights && static_cast<long long>(a.B) * a.Hq + adders <= 152;
     cudaError_t err = launch(p, a.mode, a.L.d, plan.combine_warps, stream, one);
     if (err != cudaSuccess || !weights || one) return err;

@@ -418,8 +418,9 @@ cudaError_t launch_clusters(void (*kernel)(KArgs...), long long rows, int cluste
 cudaError_t launch_evict_select(const EvictSelectArgs& a, cudaStream_t stream) {
     const long long rows = static_cast<long long>(a.B) * a.Hkv;
     // Rows that 256 threads hold in registers take a CTA of that size, several to an SM.
-    // Longer ones take CTAs of 1024 threads, one to an SM, and the largest cluster that leaves
-    // them all resident at once (152 SMs) and every thread a position.
+    // Longer ones take CTAs of 1024 threads, one to an SM, and the largest cluster that leaves no
+    // more of them than the 152 SMs and every thread a position.  (A cluster's CTAs have to find
+    // their SMs in one GPC, so close to that bound the last clusters may start behind others.)
     if (a.max_len <= 256 * kSelKeys) return launch_clusters(evict_select_kernel<1, 256>, rows, 1, 256, stream, a);
     int cl = 1;
     while (cl < 8 && rows * cl * 2 <= 152 && a.max_len > 1024 * cl) cl *= 2;
