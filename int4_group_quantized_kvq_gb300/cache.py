@@ -114,8 +114,9 @@ class PagedKVCache:
         into dst_table's (int32 [B, blocks]), which then becomes the cache's block table.  dst_table has to hold the
         positions kept; a table with room for those alone is full, so a decode_step behind them appends nothing and
         flags KVQ_FLAG_BAD_POSITION on the device.  A graph captured before holds the old table's address: it is to
-        be captured again, not replayed.  Returns the new lengths (int32 [B]); pages from ceil(new length / page_size) on are free.  Allocates
-        its small results on the current stream, so `stream` is that one or one that waits for it."""
+        be captured again, not replayed (one of this call needs the old table kept).  Returns the new lengths
+        (int32 [B]); pages from ceil(new length / page_size) on are free.  Allocates its small results on the
+        current stream, so `stream` is that one or one that waits for it."""
         if self.weights is None:
             raise ValueError("evict needs a cache with track_weights")
         dst = self.block_table if dst_table is None else dst_table

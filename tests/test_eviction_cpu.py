@@ -136,3 +136,12 @@ def test_select_refuses_budgets_past_its_position_arithmetic(kvq):
         assert L.kvq_evict_select(C.byref(cfg), 0x1000, 100, 0x2000, 1, 100, keep, 2, 3, 0x3000, 0x4000, None,
                                   None) == kvq.KVQ_EUNSUPPORTED
         assert "keep" in kvq.kvq_last_error()
+
+
+def test_weights_wait_test_refuses(kvq):
+    L, cfg = kvq.lib(), kvq.config(8, 128, 16, 64, 128, 10)
+    args = weights_args(kvq, cfg)
+    for limit in (0, 999, 10_000_001):
+        assert L.kvq_test_decode_weights_wait_timeout(*args[:-1], limit, None) == kvq.KVQ_EINVAL
+        assert "wait_limit_ns" in kvq.kvq_last_error()
+    assert L.kvq_test_decode_weights_wait_timeout(*weights_args(kvq, cfg, w=None)[:-1], 1000, None) == kvq.KVQ_EINVAL
