@@ -14,8 +14,9 @@
  *                       in "LLM long-context inference: managing the KV cache with an
  *                       INT4 state machine", pwwt.cn/news/4219524, section 5 step 5);
  *   dequantize          the inverse map code * scale (section 2.1 of the 4-bit page).
- * Around them: attention that adds up the positions' weights, eviction by those weights, and
- * differential attention (each described at its declaration; no passage of the pages has a
+ * Around them: attention that adds up the positions' weights, eviction by those weights,
+ * differential attention, rotary positions applied on append, attention of many rows per sequence and
+ * a cache of shared latents (each described at its declaration; no passage of the pages has a
  * counterpart).
  *
  * Conventions
@@ -556,6 +557,166 @@ int kvq_diff_decode_step(const kvq_cache_config *cfg, void *pool, const void *k_
                          const int32_t *seq_lens, int32_t batch, int32_t num_q_heads, int32_t max_len,
                          float softmax_scale, const float *lambda, const float *norm_weight, float norm_eps,
                          float out_scale, float *out, void *workspace, size_t workspace_bytes, kvq_stream_t stream);
+
+/*
+ * Ragged batches of rows.  The calls below take any number of new tokens per sequence: prompts,
+ * parts of prompts, a few drafted tokens and single ones together.
+ *   cu_rows     device int32 [batch + 1], cu_rows[0] = 0, not descending: sequence b owns rows
+ *               cu_rows[b] .. cu_rows[b + 1] - 1 of the row arrays.  Rows from cu_rows[batch] up to
+ *               total_rows belong to no sequence (a batch padded for a captured graph): nothing is
+ *               written for them, and outputs keep what they held there.  Offsets that break the
+ *               rules give wrong rows but never an access outside the arguments.
+ *   start_pos   device int32 [batch]: row cu_rows[b] + t is position start_pos[b] + t.
+ *   batch       at most 65536.
+ *
+ * Rotary positions: a pair (a, b) of a head's first rotary_dim elements becomes
+ * (a c - b n, b c + a n) with the cosine c and sine n of its angle, in fp32 (each product and sum
+ * rounded once), then rounded to fp16.
+ *   rotary_dim   32, 64, 128 or 256, at most the head's size; the elements behind it stay.
+ *   interleaved  0: pair i is elements i and i + rotary_dim / 2; 1: elements 2 i and 2 i + 1.
+ *   axes         1 to 3 axes of position (time, height, width of a picture or video): of the
+ *                rotary_dim / 2 pairs the first sections[0] turn with axis 0's position, the next
+ *                sections[1] with axis 1's, and so on (sections is not read with one axis).
+ *   cos_sin      device fp32 [table_len, rotary_dim], 16-byte aligned: row p holds the cosines of
+ *                the rotary_dim / 2 angles of position p, then their sines.
+ *   positions    device int32 [axes, total_rows], or NULL with one axis: the row's position in the
+ *                cache.  A row with a position outside the table is skipped whole and raises
+ *                KVQ_FLAG_BAD_POSITION.
+ */
+typedef struct {
+    int32_t rotary_dim;
+    int32_t interleaved;
+    int32_t axes;
+    int32_t sections[3];
+} kvq_rope_config;
+
+/*
+ * Rotary positions and quantize-append in one pass over the rows of a projection: q rows turned into
+ * q_out, k rows turned, rounded to fp16 and, with the v rows, stored exactly as kvq_quantize_append
+ * stores them.
+ *   q, k, v      device fp16, 16-byte aligned: row i's heads [num_q_heads (num_kv_heads), head_dim]
+ *                start i * q_stride (k_stride, v_stride) values behind the first (multiples of 8; so
+ *                the parts of one fused projection need no copies).
+ *   q_out        as q, with rows q_out_stride values apart; q itself (with the same stride) turns in
+ *                place.  It must share no other memory with q, k or v.
+ *   num_q_heads  0: no queries (q and q_out are not read).
+ *   status       device uint32 status word or NULL.
+ * A row whose place in the cache is out of range stores no k and v and is flagged, as in
+ * kvq_quantize_append; its q is turned all the same.
+ * Returns KVQ_OK, KVQ_EINVAL, KVQ_EUNSUPPORTED or KVQ_ECUDA.
+ */
+int kvq_rope_append(const kvq_cache_config *cfg, const kvq_rope_config *rope, void *pool, const void *q,
+                    int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride, void *q_out,
+                    int64_t q_out_stride, int32_t num_q_heads, const float *cos_sin, int32_t table_len,
+                    const int32_t *positions, const int32_t *block_table, int32_t max_blocks,
+                    const int32_t *start_pos, const int32_t *cu_rows, int32_t batch, int32_t total_rows,
+                    uint32_t *status, kvq_stream_t stream);
+
+/*
+ * kvq_dequantize of a ragged batch in one launch: positions start_pos[b] + t of every sequence.
+ *   out_k, out_v  device [total_rows, num_kv_heads, head_dim], 16-byte aligned; out_dtype 0 = fp16,
+ *                 1 = fp32.  A position outside the block table gives zero rows, a bad page page 0's
+ *                 (both flagged), as kvq_dequantize.
+ * Returns KVQ_OK, KVQ_EINVAL, KVQ_EUNSUPPORTED or KVQ_ECUDA.
+ */
+int kvq_dequantize_varlen(const kvq_cache_config *cfg, const void *pool, const int32_t *block_table,
+                          int32_t max_blocks, const int32_t *start_pos, const int32_t *cu_rows, int32_t batch,
+                          int32_t total_rows, void *out_k, void *out_v, int32_t out_dtype, uint32_t *status,
+                          kvq_stream_t stream);
+
+/*
+ * Causal attention of a ragged batch of query rows over the packed cache, whose last rows they are:
+ * with n_b = cu_rows[b + 1] - cu_rows[b], row i of sequence b is position seq_lens[b] - n_b + i and
+ * attends to the positions up to its own (append the new tokens first).  A row before position 0
+ * (n_b > seq_lens[b]) attends to nothing and gives zeros.
+ *   q          device fp16 [total_rows, num_q_heads, head_dim], 16-byte aligned.
+ *   seq_lens   device int32 [batch]: positions in the cache, the new ones included.
+ *   max_len    host bound on every seq_lens[b] (at most 2^30); a longer one, or one beyond the block
+ *              table, raises KVQ_FLAG_BAD_POSITION and is cut to it.
+ *   out        device fp16 [total_rows, num_q_heads, head_dim], 16-byte aligned: sums and softmax
+ *              statistics in fp32; a dequantized element and a softmax weight are rounded to fp16
+ *              before their products, the output once.
+ *   workspace  >= kvq_chunk_workspace_bytes(...) bytes, 256-byte aligned; its first word is the status
+ *              word (zero it before the first call).  Nothing else in it has to be kept or cleared
+ *              between calls; calls that share one must not overlap on the GPU.
+ *   num_q_heads / num_kv_heads at most 8, head_dim 64 or 128.  A bad page reads as page 0 (flagged).
+ *   Slots behind a sequence may hold any bytes; rows inside it must be finite.
+ * Repeated calls agree bit for bit.
+ * Returns KVQ_OK, KVQ_EINVAL, KVQ_EUNSUPPORTED, KVQ_EWORKSPACE or KVQ_ECUDA.
+ */
+size_t kvq_chunk_workspace_bytes(const kvq_cache_config *cfg, int32_t batch, int32_t num_q_heads, int32_t max_len);
+int kvq_chunk_attention(const kvq_cache_config *cfg, const void *pool, const void *q, const int32_t *block_table,
+                        int32_t max_blocks, const int32_t *seq_lens, const int32_t *cu_rows, int32_t batch,
+                        int32_t total_rows, int32_t num_q_heads, int32_t max_len, float softmax_scale, void *out,
+                        void *workspace, size_t workspace_bytes, kvq_stream_t stream);
+
+/*
+ * The latent cache: per token one latent vector, from which a model expands the keys and values of
+ * all its heads, and one rotary key that all heads share.  A page is a block of
+ * kvq_latent_block_bytes(cfg) bytes and holds, for its P = page_size slots,
+ *   latent codes  P rows of latent_dim / 2 bytes (nibbles as in the INT4 cache)
+ *   scales        P rows of latent_dim / group fp16
+ *   rotary keys   P rows of rope_dim fp16.
+ * Quantization as in the INT4 cache (scale = fp16_rne(fp32(amax) / 7), zero -> 1; code =
+ * clamp(round_half_even(x / scale), -7, 7)), of fp32 values.
+ */
+typedef struct {
+    int32_t latent_dim; /* L: 256 or 512                      */
+    int32_t rope_dim;   /* R: 64                              */
+    int32_t page_size;  /* tokens per page: 16, 32 or 64      */
+    int32_t group;      /* quantization group: 32, 64 or 128  */
+    int32_t num_pages;  /* pages in the pool, >= 1            */
+} kvq_latent_config;
+
+size_t kvq_latent_block_bytes(const kvq_latent_config *cfg);
+size_t kvq_latent_pool_bytes(const kvq_latent_config *cfg);
+
+/*
+ * New rows into the latent cache, and the queries' rotary parts, in one pass:
+ *   y = (x * r) * norm_weight with r = 1 / sqrt(mean(x^2) + norm_eps) over the row's L latent values
+ *   (r rounded once to fp32 from an exact mean, then two fp32 products; y = x without norm_weight),
+ *   quantized; the row's last R values turned by its position and stored in fp16.
+ *   rope         rotary_dim = R, one axis.
+ *   rows         device fp16, 16-byte aligned, [total_rows] rows of L + R values row_stride apart.
+ *   norm_weight  device fp32 [L], 16-byte aligned, or NULL.
+ *   norm_eps     >= 0, finite (read with norm_weight only).
+ *   q_pe         device fp16, 16-byte aligned, [total_rows] rows of [num_heads, R] q_pe_stride values
+ *                apart: turned into the last R values of every head of
+ *   q_out        device fp16 [total_rows, num_heads, L + R], 16-byte aligned; its first L values (the
+ *                absorbed query, which the caller writes) stay.  num_heads 0: no queries.
+ *   other arguments as in kvq_rope_append.
+ * Returns KVQ_OK, KVQ_EINVAL, KVQ_EUNSUPPORTED or KVQ_ECUDA.
+ */
+int kvq_latent_append(const kvq_latent_config *cfg, const kvq_rope_config *rope, void *pool, const void *rows,
+                      int64_t row_stride, const float *norm_weight, float norm_eps, const void *q_pe,
+                      int64_t q_pe_stride, void *q_out, int32_t num_heads, const float *cos_sin, int32_t table_len,
+                      const int32_t *positions, const int32_t *block_table, int32_t max_blocks,
+                      const int32_t *start_pos, const int32_t *cu_rows, int32_t batch, int32_t total_rows,
+                      uint32_t *status, kvq_stream_t stream);
+
+/*
+ * Rows of the latent cache read back: out device fp16 [total_rows, L + R], 16-byte aligned (latent
+ * values code * scale rounded to fp16, rotary keys as stored), for the expanded form, whose keys and
+ * values are matrix products of these rows.  Positions and pages out of range as kvq_dequantize_varlen.
+ */
+int kvq_latent_dequantize(const kvq_latent_config *cfg, const void *pool, const int32_t *block_table,
+                          int32_t max_blocks, const int32_t *start_pos, const int32_t *cu_rows, int32_t batch,
+                          int32_t total_rows, void *out, uint32_t *status, kvq_stream_t stream);
+
+/*
+ * Attention over the latent cache in the absorbed form: every head's query is [q_latent, q_rotary], a
+ * token's key for all heads is its row [latent, rotary key], its value the latent:
+ *   out[i][h] = sum_t softmax_t(softmax_scale * (q_latent . c_t + q_rotary . k_t)) c_t.
+ * Rows, masks, max_len, workspace, precision and errors as in kvq_chunk_attention (one row per
+ * sequence: a decode step).
+ *   q    device fp16 [total_rows, num_heads, L + R], 16-byte aligned, num_heads 1 to 1024.
+ *   out  device fp16 [total_rows, num_heads, L], 16-byte aligned.
+ */
+size_t kvq_latent_workspace_bytes(const kvq_latent_config *cfg, int32_t batch, int32_t num_heads, int32_t max_len);
+int kvq_latent_attention(const kvq_latent_config *cfg, const void *pool, const void *q, const int32_t *block_table,
+                         int32_t max_blocks, const int32_t *seq_lens, const int32_t *cu_rows, int32_t batch,
+                         int32_t total_rows, int32_t num_heads, int32_t max_len, float softmax_scale, void *out,
+                         void *workspace, size_t workspace_bytes, kvq_stream_t stream);
 
 /*
  * Decode attention that allocates nothing, for callers that cannot provide a

@@ -32,7 +32,10 @@ ABI_SYMBOLS = ("kvq_block_bytes", "kvq_pool_bytes", "kvq_quantize_append", "kvq_
                "kvq_decode_weights_workspace_bytes", "kvq_decode_attention_weights", "kvq_decode_step_weights",
                "kvq_int8_decode_weights_workspace_bytes", "kvq_int8_decode_attention_weights", "kvq_evict_select",
                "kvq_evict_compact", "kvq_int8_evict_compact", "kvq_diff_decode_workspace_bytes",
-               "kvq_diff_decode_attention", "kvq_diff_decode_step", "kvq_test_decode_weights_wait_timeout")
+               "kvq_diff_decode_attention", "kvq_diff_decode_step", "kvq_test_decode_weights_wait_timeout",
+               "kvq_rope_append", "kvq_dequantize_varlen", "kvq_chunk_workspace_bytes", "kvq_chunk_attention",
+               "kvq_latent_block_bytes", "kvq_latent_pool_bytes", "kvq_latent_append", "kvq_latent_dequantize",
+               "kvq_latent_workspace_bytes", "kvq_latent_attention")
 
 
 class KvqError(RuntimeError):
@@ -50,6 +53,28 @@ class CacheConfig(C.Structure):
     def __repr__(self) -> str:
         return (f"CacheConfig(Hkv={self.num_kv_heads}, d={self.head_dim}, P={self.page_size}, "
                 f"Gk={self.group_k}, Gv={self.group_v}, pages={self.num_pages})")
+
+
+class RopeConfig(C.Structure):
+    """kvq_rope_config: rotary_dim, interleaved, axes, sections."""
+
+    _fields_ = [("rotary_dim", C.c_int32), ("interleaved", C.c_int32), ("axes", C.c_int32),
+                ("sections", C.c_int32 * 3)]
+
+    def __repr__(self) -> str:
+        return (f"RopeConfig(rotary_dim={self.rotary_dim}, interleaved={bool(self.interleaved)}, "
+                f"sections={list(self.sections)[:self.axes] if self.axes > 1 else None})")
+
+
+class LatentConfig(C.Structure):
+    """kvq_latent_config: latent_dim, rope_dim, page_size, group, num_pages."""
+
+    _fields_ = [("latent_dim", C.c_int32), ("rope_dim", C.c_int32), ("page_size", C.c_int32), ("group", C.c_int32),
+                ("num_pages", C.c_int32)]
+
+    def __repr__(self) -> str:
+        return (f"LatentConfig(L={self.latent_dim}, R={self.rope_dim}, P={self.page_size}, G={self.group}, "
+                f"pages={self.num_pages})")
 
 
 _lib: C.CDLL | None = None
@@ -152,6 +177,25 @@ def lib() -> C.CDLL:
         L.kvq_diff_decode_attention.restype = C.c_int
         L.kvq_diff_decode_step.argtypes = [cfgp, P, P, P, P, P, P, I32, P, I32, I32, I32, F, P, P, F, F, P, P, SZ, P]
         L.kvq_diff_decode_step.restype = C.c_int
+        I64, rcp, lcp = C.c_int64, C.POINTER(RopeConfig), C.POINTER(LatentConfig)
+        L.kvq_rope_append.argtypes = [cfgp, rcp, P, P, I64, P, I64, P, I64, P, I64, I32, P, I32, P, P, I32, P, P, I32,
+                                      I32, P, P]
+        L.kvq_dequantize_varlen.argtypes = [cfgp, P, P, I32, P, P, I32, I32, P, P, I32, P, P]
+        L.kvq_chunk_attention.argtypes = [cfgp, P, P, P, I32, P, P, I32, I32, I32, I32, F, P, P, SZ, P]
+        L.kvq_latent_append.argtypes = [lcp, rcp, P, P, I64, P, F, P, I64, P, I32, P, I32, P, P, I32, P, P, I32, I32, P,
+                                        P]
+        L.kvq_latent_dequantize.argtypes = [lcp, P, P, I32, P, P, I32, I32, P, P, P]
+        L.kvq_latent_attention.argtypes = [lcp, P, P, P, I32, P, P, I32, I32, I32, I32, F, P, P, SZ, P]
+        for name in ("kvq_rope_append", "kvq_dequantize_varlen", "kvq_chunk_attention", "kvq_latent_append",
+                     "kvq_latent_dequantize", "kvq_latent_attention"):
+            getattr(L, name).restype = C.c_int
+        L.kvq_chunk_workspace_bytes.argtypes = [cfgp, I32, I32, I32]
+        L.kvq_latent_workspace_bytes.argtypes = [lcp, I32, I32, I32]
+        L.kvq_latent_block_bytes.argtypes = [lcp]
+        L.kvq_latent_pool_bytes.argtypes = [lcp]
+        for name in ("kvq_chunk_workspace_bytes", "kvq_latent_workspace_bytes", "kvq_latent_block_bytes",
+                     "kvq_latent_pool_bytes"):
+            getattr(L, name).restype = SZ
         L.kvq_dequantize.argtypes = [cfgp, P, P, I32, I32, I32, I32, P, P, I32, P, P]
         L.kvq_dequantize.restype = C.c_int
         L.kvq_read_status.argtypes = [P, C.POINTER(C.c_uint32), P]
@@ -919,3 +963,237 @@ def kvq_diff_decode_step(cfg: CacheConfig, pool: torch.Tensor, k_new: torch.Tens
     """kvq_diff_decode_attention with k_new, v_new appended at append_pos first, as kvq_decode_step."""
     _diff_call(lib().kvq_diff_decode_step, cfg, pool, q, block_table, seq_lens, max_len, softmax_scale, lam,
                norm_weight, norm_eps, out_scale, out, workspace, stream, (k_new, v_new, append_pos))
+
+
+# ---------------------------------------------------------------------------
+# Ragged batches of rows: rotary append, read-back, chunk attention, the latent cache
+# ---------------------------------------------------------------------------
+def rope(rotary_dim: int, interleaved: bool = False, sections: list[int] | None = None) -> RopeConfig:
+    """Rotary positions of the first rotary_dim elements of a head: pairs (i, i + rotary_dim / 2), or (2 i, 2 i + 1)
+    when interleaved.  sections: the pairs that turn with each of two or three axes of position (None: one axis)."""
+    n = 1 if sections is None else len(sections)
+    if n > 3:
+        raise ValueError(f"sections must name at most 3 axes, got {n}")
+    if n == 1:
+        sections = (int(rotary_dim) // 2,)
+    return RopeConfig(int(rotary_dim), int(bool(interleaved)), n, (C.c_int32 * 3)(*[int(x) for x in sections]))
+
+
+def rope_table(length: int, rotary_dim: int, base: float = 10000.0, inv_freq: torch.Tensor | None = None,
+               device="cuda") -> torch.Tensor:
+    """The table of cosines and sines the rotary calls read, fp32 [length, rotary_dim]: angle = position * inv_freq[i]
+    (by default base^(-2 i / rotary_dim)), taken in fp64, since fp32 loses the angles of far positions."""
+    f = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim) if inv_freq is None else \
+        inv_freq.detach().to("cpu", torch.float64)
+    if f.shape != (rotary_dim // 2,):
+        raise ValueError(f"inv_freq must be [{rotary_dim // 2}], got {list(f.shape)}")
+    a = torch.arange(length, dtype=torch.float64)[:, None] * f
+    return torch.cat([a.cos(), a.sin()], dim=-1).to(torch.float32).to(device)
+
+
+def latent_config(latent_dim: int, rope_dim: int = 64, page_size: int = 64, group: int = 64,
+                  num_pages: int = 1) -> LatentConfig:
+    return LatentConfig(latent_dim, rope_dim, page_size, group, num_pages)
+
+
+def _rows_of(t: torch.Tensor, name: str, rows: int, heads: int, width: int, dev: int) -> tuple[int, int]:
+    """Address and row stride of fp16 [rows, heads, width] whose rows are whole but may lie apart."""
+    try:
+        s0, s1, s2 = t.stride()
+        if (t.dtype is _F16 and t.shape == (rows, heads, width) and t.get_device() == dev and s2 == 1
+                and (s1 == width or heads == 1)):
+            return t.data_ptr(), s0 if rows > 1 else heads * width
+    except (AttributeError, ValueError):
+        pass
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not _F16:
+        raise ValueError(f"{name} must be {_F16}, got {t.dtype}")
+    if tuple(t.shape) != (rows, heads, width):
+        raise ValueError(f"{name} must be {[rows, heads, width]}, got {list(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    raise ValueError(f"{name}: a row's values must be contiguous (strides {list(t.stride())})")
+
+
+def _ragged(block_table, per_seq, name, cu_rows, dev) -> tuple:
+    """batch, and the C arguments (block_table, max_blocks, per_seq, cu_rows, batch)."""
+    B, blocks = _dims(block_table, "block_table", 2)
+    try:  # everything as it should be, in one expression
+        if (block_table.dtype is per_seq.dtype is cu_rows.dtype is _I32 and per_seq.shape == (B,)
+                and cu_rows.shape == (B + 1,)
+                and block_table.get_device() == per_seq.get_device() == cu_rows.get_device() == dev
+                and block_table.is_contiguous() and per_seq.is_contiguous() and cu_rows.is_contiguous()):
+            return block_table.data_ptr(), blocks, per_seq.data_ptr(), cu_rows.data_ptr(), B
+    except AttributeError:
+        pass
+    return (_shaped(block_table, "block_table", _I32, (B, blocks), dev), blocks, _shaped(per_seq, name, _I32, (B,), dev),
+            _shaped(cu_rows, "cu_rows", _I32, (B + 1,), dev), B)
+
+
+def _angles(cos_sin, rope_cfg, positions, rows, dev) -> tuple:
+    """The C arguments (cos_sin, table_len, positions)."""
+    n, rot = _dims(cos_sin, "cos_sin", 2)
+    if rot != rope_cfg.rotary_dim:
+        raise ValueError(f"cos_sin must be [positions, {rope_cfg.rotary_dim}], got {[n, rot]}")
+    if positions is None:
+        return _shaped(cos_sin, "cos_sin", _F32, (n, rot), dev), n, None
+    shape = (rows,) if len(getattr(positions, "shape", ())) == 1 and rope_cfg.axes == 1 else (rope_cfg.axes, rows)
+    return _shaped(cos_sin, "cos_sin", _F32, (n, rot), dev), n, _shaped(positions, "positions", _I32, shape, dev)
+
+
+def kvq_rope_append(cfg: CacheConfig, rope: RopeConfig, pool: torch.Tensor, q: torch.Tensor | None, k: torch.Tensor,
+                    v: torch.Tensor, q_out: torch.Tensor | None, cos_sin: torch.Tensor, block_table: torch.Tensor,
+                    start_pos: torch.Tensor, cu_rows: torch.Tensor, positions: torch.Tensor | None = None,
+                    status: torch.Tensor | None = None, stream=None) -> None:
+    """Rotary positions and quantize-append of a ragged batch.  q: fp16 [T, Hq, d] (or None), k, v: fp16 [T, Hkv, d],
+    rows whole but possibly apart (parts of one projection); q_out: like q, or q itself.  cos_sin: fp32
+    [positions, rotary_dim], as from rope_table; positions: int32 [axes, T] (None: the rows' positions in the cache);
+    start_pos int32 [B]; cu_rows int32 [B + 1]."""
+    L, dev, ref = lib(), torch.cuda.current_device(), C.byref(cfg)
+    T, H, d = _dims(k, "k", 3)
+    kp, ks = _rows_of(k, "k", T, cfg.num_kv_heads, cfg.head_dim, dev)
+    vp, vs = _rows_of(v, "v", T, cfg.num_kv_heads, cfg.head_dim, dev)
+    Hq = qp = qs = op = os_ = 0
+    if q is not None:
+        Hq = _dims(q, "q", 3)[1]
+        qp, qs = _rows_of(q, "q", T, Hq, cfg.head_dim, dev)
+        op, os_ = _rows_of(q_out, "q_out", T, Hq, cfg.head_dim, dev)
+    table = _angles(cos_sin, rope, positions, T, dev)
+    bt, blocks, sp, cu, B = _ragged(block_table, start_pos, "start_pos", cu_rows, dev)
+    rc = L.kvq_rope_append(ref, C.byref(rope), _pool_at(pool, L.kvq_pool_bytes(ref), dev), qp, qs, kp, ks, vp, vs, op, os_,
+                           Hq, *table, bt, blocks, sp, cu, B, T, _own_status(status, dev), _stream_on(stream, dev))
+    if rc:
+        _check(rc)
+
+
+def kvq_dequantize_varlen(cfg: CacheConfig, pool: torch.Tensor, block_table: torch.Tensor, start_pos: torch.Tensor,
+                          cu_rows: torch.Tensor, out_k: torch.Tensor, out_v: torch.Tensor,
+                          status: torch.Tensor | None = None, stream=None) -> None:
+    """Positions start_pos[b] + t of a ragged batch read back into out_k, out_v (fp16 or fp32 [T, Hkv, d])."""
+    L, dev, ref = lib(), torch.cuda.current_device(), C.byref(cfg)
+    shape = _dims(out_k, "out_k", 3)
+    T = shape[0]
+    dtype = _F32 if out_k.dtype is _F32 else _F16
+    want = (T, cfg.num_kv_heads, cfg.head_dim)
+    bt, blocks, sp, cu, B = _ragged(block_table, start_pos, "start_pos", cu_rows, dev)
+    rc = L.kvq_dequantize_varlen(ref, _pool_at(pool, L.kvq_pool_bytes(ref), dev), bt, blocks, sp, cu, B, T,
+                                 _shaped(out_k, "out_k", dtype, want, dev), _shaped(out_v, "out_v", dtype, want, dev),
+                                 int(dtype is _F32), _own_status(status, dev), _stream_on(stream, dev))
+    if rc:
+        _check(rc)
+
+
+def kvq_chunk_workspace_bytes(cfg: CacheConfig, batch: int, num_q_heads: int, max_len: int) -> int:
+    return _mode_workspace_bytes("kvq_chunk_workspace_bytes", cfg, batch, num_q_heads, max_len)
+
+
+def new_chunk_workspace(cfg: CacheConfig, batch: int, num_q_heads: int, max_len: int, device="cuda") -> torch.Tensor:
+    """A workspace of kvq_chunk_attention, its status word zeroed."""
+    return _new_status_first(kvq_chunk_workspace_bytes(cfg, batch, num_q_heads, max_len), device)
+
+
+def _new_status_first(n: int, device) -> torch.Tensor:
+    w = torch.empty(n, dtype=_U8, device=device)
+    w[:256].zero_()
+    return w
+
+
+def _attend_rows(fn, ref, pool, need, q, width, block_table, seq_lens, cu_rows, max_len, softmax_scale, out, out_width,
+                 workspace, stream, dev) -> None:
+    T, H, n = _dims(q, "q", 3)
+    qp = _shaped(q, "q", _F16, (T, H, width), dev)
+    op = _shaped(out, "out", _F16, (T, H, out_width), dev)
+    bt, blocks, sl, cu, B = _ragged(block_table, seq_lens, "seq_lens", cu_rows, dev)
+    wp, wn = _bytes(workspace, "workspace", dev)
+    rc = fn(ref, _pool_at(pool, need, dev), qp, bt, blocks, sl, cu, B, T, H, int(max_len), float(softmax_scale), op, wp, wn,
+            _stream_on(stream, dev))
+    if rc:
+        _check(rc)
+
+
+def kvq_chunk_attention(cfg: CacheConfig, pool: torch.Tensor, q: torch.Tensor, block_table: torch.Tensor,
+                        seq_lens: torch.Tensor, cu_rows: torch.Tensor, max_len: int, softmax_scale: float,
+                        out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """Causal attention of the last rows of every sequence: q fp16 [T, Hq, d], rows cu_rows[b] .. cu_rows[b + 1] - 1 at the
+    last positions of sequence b's seq_lens[b]; out fp16 [T, Hq, d].  workspace as from new_chunk_workspace."""
+    L, ref = lib(), C.byref(cfg)
+    _attend_rows(L.kvq_chunk_attention, ref, pool, L.kvq_pool_bytes(ref), q, cfg.head_dim, block_table, seq_lens, cu_rows,
+                 max_len, softmax_scale, out, cfg.head_dim, workspace, stream, torch.cuda.current_device())
+
+
+def kvq_latent_block_bytes(cfg: LatentConfig) -> int:
+    n = lib().kvq_latent_block_bytes(C.byref(cfg))
+    if n == 0:
+        raise KvqError(KVQ_EINVAL, kvq_last_error())
+    return int(n)
+
+
+def kvq_latent_pool_bytes(cfg: LatentConfig) -> int:
+    n = lib().kvq_latent_pool_bytes(C.byref(cfg))
+    if n == 0:
+        raise KvqError(KVQ_EINVAL, kvq_last_error())
+    return int(n)
+
+
+def kvq_latent_append(cfg: LatentConfig, rope: RopeConfig, pool: torch.Tensor, rows: torch.Tensor,
+                      norm_weight: torch.Tensor | None, norm_eps: float, q_pe: torch.Tensor | None,
+                      q_out: torch.Tensor | None, cos_sin: torch.Tensor, block_table: torch.Tensor,
+                      start_pos: torch.Tensor, cu_rows: torch.Tensor, positions: torch.Tensor | None = None,
+                      status: torch.Tensor | None = None, stream=None) -> None:
+    """New rows of a latent cache.  rows: fp16 [T, L + R] (rows possibly apart): the latent part normalised with
+    norm_weight (fp32 [L]; None: as it is) and quantized, the rotary key turned; q_pe: fp16 [T, H, R] (or None), turned
+    into the last R values of q_out (fp16 [T, H, L + R])."""
+    L, dev, ref = lib(), torch.cuda.current_device(), C.byref(cfg)
+    T, width = _dims(rows, "rows", 2)
+    if width != cfg.latent_dim + cfg.rope_dim:
+        raise ValueError(f"rows must be [rows, {cfg.latent_dim + cfg.rope_dim}], got {[T, width]}")
+    rp, rs = _rows_of(rows.unsqueeze(1), "rows", T, 1, width, dev)
+    gp = None if norm_weight is None else _shaped(norm_weight, "norm_weight", _F32, (cfg.latent_dim,), dev)
+    H = qp = qs = 0
+    op = None
+    if q_pe is not None:
+        H = _dims(q_pe, "q_pe", 3)[1]
+        qp, qs = _rows_of(q_pe, "q_pe", T, H, cfg.rope_dim, dev)
+        op = _shaped(q_out, "q_out", _F16, (T, H, width), dev)
+    table = _angles(cos_sin, rope, positions, T, dev)
+    bt, blocks, sp, cu, B = _ragged(block_table, start_pos, "start_pos", cu_rows, dev)
+    rc = L.kvq_latent_append(ref, C.byref(rope), _pool_at(pool, L.kvq_latent_pool_bytes(ref), dev), rp, rs, gp,
+                             float(norm_eps), qp, qs, op, H, *table, bt, blocks, sp, cu, B, T, _own_status(status, dev),
+                             _stream_on(stream, dev))
+    if rc:
+        _check(rc)
+
+
+def kvq_latent_dequantize(cfg: LatentConfig, pool: torch.Tensor, block_table: torch.Tensor, start_pos: torch.Tensor,
+                          cu_rows: torch.Tensor, out: torch.Tensor, status: torch.Tensor | None = None,
+                          stream=None) -> None:
+    """Rows of a latent cache read back into out (fp16 [T, L + R])."""
+    L, dev, ref = lib(), torch.cuda.current_device(), C.byref(cfg)
+    T = _dims(out, "out", 2)[0]
+    bt, blocks, sp, cu, B = _ragged(block_table, start_pos, "start_pos", cu_rows, dev)
+    rc = L.kvq_latent_dequantize(ref, _pool_at(pool, L.kvq_latent_pool_bytes(ref), dev), bt, blocks, sp, cu, B, T,
+                                 _shaped(out, "out", _F16, (T, cfg.latent_dim + cfg.rope_dim), dev),
+                                 _own_status(status, dev), _stream_on(stream, dev))
+    if rc:
+        _check(rc)
+
+
+def kvq_latent_workspace_bytes(cfg: LatentConfig, batch: int, num_heads: int, max_len: int) -> int:
+    return _mode_workspace_bytes("kvq_latent_workspace_bytes", cfg, batch, num_heads, max_len)
+
+
+def new_latent_workspace(cfg: LatentConfig, batch: int, num_heads: int, max_len: int, device="cuda") -> torch.Tensor:
+    """A workspace of kvq_latent_attention, its status word zeroed."""
+    return _new_status_first(kvq_latent_workspace_bytes(cfg, batch, num_heads, max_len), device)
+
+
+def kvq_latent_attention(cfg: LatentConfig, pool: torch.Tensor, q: torch.Tensor, block_table: torch.Tensor,
+                         seq_lens: torch.Tensor, cu_rows: torch.Tensor, max_len: int, softmax_scale: float,
+                         out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """Attention over a latent cache in the absorbed form: q fp16 [T, H, L + R], rows as in kvq_chunk_attention; out fp16
+    [T, H, L].  workspace as from new_latent_workspace."""
+    L, ref = lib(), C.byref(cfg)
+    _attend_rows(L.kvq_latent_attention, ref, pool, L.kvq_latent_pool_bytes(ref), q, cfg.latent_dim + cfg.rope_dim,
+                 block_table, seq_lens, cu_rows, max_len, softmax_scale, out, cfg.latent_dim, workspace, stream,
+                 torch.cuda.current_device())

@@ -9,11 +9,14 @@
 #include <mutex>
 
 #include "kvq.h"
+#include "kvq_api.h"
 #include "kvq_internal.h"
 
 namespace {
-
 thread_local char g_err[512] = "";
+}
+
+namespace kvq {
 
 int fail(int code, const char* fmt, ...) {
     va_list ap;
@@ -28,11 +31,10 @@ int ok() {
     return KVQ_OK;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+int cuda_fail(cudaError_t e, const char* what) {
+    return fail(KVQ_ECUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
 
-bool is_pow2_in(int x, int lo, int hi) { return x >= lo && x <= hi && (x & (x - 1)) == 0; }
-
-// Geometry shared by every call.  Returns KVQ_OK or an error (with the message set).
 int check_cfg(const kvq_cache_config* c) {
     if (!c) return fail(KVQ_EINVAL, "cfg is NULL");
     if (c->num_kv_heads < 1) return fail(KVQ_EINVAL, "num_kv_heads %d < 1", c->num_kv_heads);
@@ -49,6 +51,17 @@ int check_cfg(const kvq_cache_config* c) {
         return fail(KVQ_EINVAL, "pool larger than 64 TiB");
     return KVQ_OK;
 }
+
+}  // namespace kvq
+
+namespace {
+
+using kvq::aligned;
+using kvq::check_cfg;
+using kvq::cuda_fail;
+using kvq::fail;
+using kvq::is_pow2_in;
+using kvq::ok;
 
 // Shapes the decode kernels take: the INT4 cache at head_dim 64, 128 or 256 (256: up to 4
 // query heads per kv head and K groups of 64 or 128, the register budget of one warp's
@@ -86,10 +99,6 @@ void half_page_units(kvq::DecodeArgs* a) {
     a->page_ld = a->max_blocks;
     a->L.P = 32;
     a->max_blocks = 2 * (a->max_blocks < (1 << 25) ? a->max_blocks : (1 << 25));  // beyond any length
-}
-
-int cuda_fail(cudaError_t e, const char* what) {
-    return fail(KVQ_ECUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
 // The device address of page-locked host memory (cudaHostAlloc / cudaHostRegister), or

@@ -244,4 +244,129 @@ struct EvictCompactArgs {
 };
 cudaError_t launch_evict_compact(const EvictCompactArgs& a, cudaStream_t stream);
 
+// ---- ragged batches of rows ------------------------------------------------------------------
+// Rows cu_rows[b] .. cu_rows[b + 1] - 1 belong to sequence b; row cu_rows[b] + t of it is position
+// start_pos[b] + t; rows from cu_rows[B] on belong to no sequence.
+
+// Rotary positions and quantize-append (rope_append.cu).
+struct RopeAppendArgs {
+    uint8_t* pool;
+    const __half* q;
+    const __half* k;
+    const __half* v;
+    __half* q_out;
+    const float* table;        // [table_len][rot]: rot / 2 cosines, then rot / 2 sines
+    const int32_t* positions;  // [axes][rows], or nullptr (one axis): the row's position in the cache
+    const int32_t* block_table;
+    const int32_t* start_pos;
+    const int32_t* cu_rows;
+    uint32_t* status;
+    long long q_stride, k_stride, v_stride, q_out_stride;  // values from one row to the next
+    int32_t rows, B, Hq, Hkv, max_blocks, num_pages, lg_p, table_len;
+    int32_t rot, inter, axes, bound0, bound1;  // pairs below bound0 turn with axis 0, below bound1 with axis 1
+    int32_t slices;                            // parts of a row's heads, each a warp's (set by the launcher)
+    BlockLayout L;
+};
+cudaError_t launch_rope_append(RopeAppendArgs a, cudaStream_t stream);
+
+struct DequantRowsArgs {
+    const uint8_t* pool;
+    const int32_t* block_table;
+    const int32_t* start_pos;
+    const int32_t* cu_rows;
+    void* out_k;
+    void* out_v;
+    uint32_t* status;
+    int32_t rows, B, Hkv, max_blocks, num_pages, lg_p, out_fp32, slices;
+    BlockLayout L;
+};
+cudaError_t launch_dequantize_rows(DequantRowsArgs a, cudaStream_t stream);
+
+// Blocks of 8 warps for `tasks` rows, each in `slices` parts: as many parts (at most most_slices) as
+// leave every warp of the device at most one.
+int rows_grid(long long tasks, int most_slices, int warps_per_sm, int* slices);
+// Launch with programmatic dependent launch (the kernel waits with griddepcontrol.wait).
+cudaError_t launch_rows(const void* kernel, int blocks, int threads, void** args, cudaStream_t stream);
+
+// A page of a latent cache: P rows of L / 2 bytes of codes, P rows of L / G fp16 scales, P rows of R
+// fp16 rotary keys (every part a multiple of 16 bytes).
+struct LatentLayout {
+    int32_t L, R, P, G;
+    int32_t scales, rope, bytes;  // offsets of the parts, bytes of a page
+};
+inline LatentLayout latent_layout(const kvq_latent_config& c) {
+    LatentLayout l;
+    l.L = c.latent_dim;
+    l.R = c.rope_dim;
+    l.P = c.page_size;
+    l.G = c.group;
+    l.scales = l.P * l.L / 2;
+    l.rope = l.scales + l.P * (l.L / l.G) * 2;
+    l.bytes = l.rope + l.P * l.R * 2;
+    return l;
+}
+
+struct LatentAppendArgs {
+    uint8_t* pool;
+    const __half* x;  // [rows][L + R], rows x_stride values apart
+    const float* gain;
+    const __half* q_pe;  // [rows][H][R], rows q_pe_stride values apart, or nullptr
+    __half* q_out;       // [rows][H][L + R]
+    const float* table;
+    const int32_t* positions;
+    const int32_t* block_table;
+    const int32_t* start_pos;
+    const int32_t* cu_rows;
+    uint32_t* status;
+    long long x_stride, q_pe_stride;
+    float eps;
+    int32_t rows, B, H, max_blocks, num_pages, lg_p, table_len, inter, slices;
+    LatentLayout lay;
+};
+cudaError_t launch_latent_append(LatentAppendArgs a, cudaStream_t stream);
+
+struct LatentDequantArgs {
+    const uint8_t* pool;
+    const int32_t* block_table;
+    const int32_t* start_pos;
+    const int32_t* cu_rows;
+    __half* out;
+    uint32_t* status;
+    int32_t rows, B, max_blocks, num_pages, lg_p;
+    LatentLayout lay;
+};
+cudaError_t launch_latent_dequantize(LatentDequantArgs a, cudaStream_t stream);
+
+// Attention of a ragged batch of query rows: row i of sequence b's n_b rows is position
+// seq_lens[b] - n_b + i and attends to the positions up to its own.
+struct ChunkArgs {
+    const uint8_t* pool;
+    const __half* q;
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    const int32_t* cu_rows;
+    __half* out;
+    uint8_t* workspace;
+    int32_t rows, B, Hq, Hkv, max_blocks, num_pages, lg_p, max_len;
+    float softmax_scale;
+    BlockLayout L;
+};
+size_t chunk_workspace_bytes(const ChunkArgs& a);
+cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t stream);
+
+struct LatentAttnArgs {
+    const uint8_t* pool;
+    const __half* q;  // [rows][H][L + R]
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    const int32_t* cu_rows;
+    __half* out;  // [rows][H][L]
+    uint8_t* workspace;
+    int32_t rows, B, H, max_blocks, num_pages, lg_p, max_len;
+    float softmax_scale;
+    LatentLayout lay;
+};
+size_t latent_workspace_bytes(const LatentAttnArgs& a);
+cudaError_t launch_latent_attention(const LatentAttnArgs& a, cudaStream_t stream);
+
 }  // namespace kvq
