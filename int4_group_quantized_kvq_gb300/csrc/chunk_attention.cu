@@ -1,80 +1,809 @@
 // chunk_attention.cu -- causal attention of a ragged batch of query rows (prompts, parts of prompts,
-// a few drafted tokens) over the packed INT4 cache.
+// a few drafted tokens) over the packed INT4 cache, on the tcgen05 tensor cores.
+//
+// For a row at position p:  z_t = scale q . k_t,  o = sum_{t <= p} softmax(z)_t v_t.
+//
+// Tiles.  128 rows of M are the r query heads of 128 / r tokens that share a kv head; 128 positions are
+// a key/value tile.  An item is two such row tiles of one (sequence, kv head), which share every key and
+// value tile (the dequantization is paid once for 256 rows); where an item has no second row tile, its
+// two streams take alternate key/value tiles instead and merge at the end.  A unit is one key/value
+// tile of an item; every CTA takes an equal run of the list of units, so causal prompts, uneven batches
+// and single long sequences spread evenly.  An item cut between CTAs leaves partial results (maximum,
+// sum, unnormalised output) that a second kernel merges in order.
+//
+// Warps of a CTA (one per SM):
+//   0-3, 4-7   softmax of stream 0 and 1: a thread has a row.  Scores come from tensor memory, weights go
+//              back there (as the f16 A operand of the second product, over the scores' columns).
+//   8-11       dequantize packed tiles into f16 operand tiles (shared memory, a ring of kRing).
+//   12         issues the MMAs: S = Q K^T (both from shared memory), O += P V (P from tensor memory).
+//   13         copies packed pages into shared memory (bulk copies, a ring of kPacked tiles).
 #include <cuda_fp16.h>
 
 #include <cmath>
 
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
-#include "kvq_rows.cuh"
+#include "kvq_tcgen05.cuh"
 
 namespace kvq {
 namespace {
 
-// One warp per (row, query head): a lane holds D / 32 dimensions, a position's score is a shuffle
-// reduction, the softmax runs online.
+constexpr int kThreads = 512;
+constexpr int kRing = 3;      // operand tiles (K or V) in shared memory
+constexpr int kPacked = 3;    // packed tiles in shared memory
+constexpr int kTile = 128;    // rows of M, positions of a tile
+constexpr uint32_t kTmem = 512;
+
+// Where a CTA's run of units starts, and how long it is.
+struct Start {
+    int b, h, j, k;
+    long long units;
+};
+
+// Merging of an item whose units lie in several CTAs, described by the CTA of its second part.
+struct MergeDesc {
+    int32_t parts;  // 0: nothing to merge
+    int32_t row0, tokens, h;
+};
+
+struct ChunkParams {
+    const uint8_t* pool;
+    const __half* q;
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    const int32_t* cu_rows;
+    __half* out;
+    uint32_t* status;
+    MergeDesc* desc;  // [gridDim.x]
+    float* part_ml;   // [2 gridDim.x][256][2]: maximum (of scale log2(e) z) and sum
+    float* part_o;    // [2 gridDim.x][256][D]
+    int32_t rows, B, Hq, Hkv, r, T, max_blocks, num_pages, lg_p, most;  // T: tokens of a row tile; most: longest sequence
+    float c;          // 2 |scale| log2(e): keys are held halved
+    uint32_t q_flip;  // sign bits of a negative scale
+    BlockLayout L;
+};
+
+struct Seq {
+    int row0, n, len;  // first row, rows, positions
+};
+__device__ __forceinline__ Seq sequence(const ChunkParams& p, int b) {
+    Seq s;
+    const int c0 = min(max(__ldg(p.cu_rows + b), 0), p.rows), c1 = min(max(__ldg(p.cu_rows + b + 1), 0), p.rows);
+    s.row0 = c0;
+    s.n = max(0, c1 - c0);
+    s.len = min(max(__ldg(p.seq_lens + b), 0), p.most);
+    return s;
+}
+// Positions the last row of item j can see, and the item's units (one at least: rows that see nothing
+// are written too).
+__device__ __forceinline__ int visible(const ChunkParams& p, const Seq& s, int j) {
+    return s.len - s.n + static_cast<int>(min(static_cast<long long>(j + 1) * 2 * p.T, static_cast<long long>(s.n)));
+}
+__device__ __forceinline__ int units_of(int vis) { return max(1, (vis + kTile - 1) / kTile); }
+
+// A segment: the units [k0, k1) of one item.
+struct Segment {
+    int b, h, j, k0, k1, nt, vis, tokens, tok0;
+    Seq s;
+    bool two;  // a second row tile (else the streams alternate)
+};
+
+// Walks a CTA's segments; every role of the CTA walks the same ones.
+struct Walk {
+    const ChunkParams& p;
+    long long left;
+    int b, h, j, k;
+    Seq s;
+    __device__ Walk(const ChunkParams& p_, const Start& st) : p(p_), left(st.units), b(st.b), h(st.h), j(st.j), k(st.k) {
+        s = sequence(p, b);
+    }
+    __device__ __forceinline__ bool next(Segment& g) {
+        if (left <= 0) return false;
+        const int step = 2 * p.T;
+        if (j * static_cast<long long>(step) >= s.n) {  // the next head or sequence
+            j = 0;
+            if (++h == p.Hkv) {
+                h = 0;
+                do {
+                    if (++b >= p.B) return false;
+                    s = sequence(p, b);
+                } while (s.n == 0);
+            }
+        }
+        g.b = b;
+        g.h = h;
+        g.j = j;
+        g.s = s;
+        g.vis = visible(p, s, j);
+        g.nt = units_of(g.vis);
+        g.k0 = k;
+        g.k1 = static_cast<int>(min(static_cast<long long>(g.nt), k + left));
+        g.tok0 = j * step;
+        g.tokens = min(step, s.n - g.tok0);
+        g.two = g.tokens > p.T;
+        left -= g.k1 - g.k0;
+        k = 0;
+        ++j;
+        return true;
+    }
+};
+
+struct Ctl {
+    uint64_t pk_full[kPacked], pk_empty[kPacked];
+    uint64_t kv_full[kRing], kv_empty[kRing];
+    uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
+    long long warp_sum[kThreads / 32];
+    Start start;
+    uint32_t tmem;
+    int stop;
+    float ml[2][kTile][2];
+};
+
+// The CTA's run of units: all threads.  The list is (sequence, kv head, item, tile); a thread counts the
+// units of a sequence per kv head.
+__device__ __forceinline__ void find_start(const ChunkParams& p, Ctl* ctl) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+    auto count = [&](int b) -> long long {
+        if (b >= p.B) return 0;
+        const Seq s = sequence(p, b);
+        long long u = 0;
+        for (int j = 0; j * 2ll * p.T < s.n; ++j) u += units_of(visible(p, s, j));
+        if (u > 0 && blockIdx.x == 0 && __ldg(p.seq_lens + b) > p.most) raise_flag(p.status, KVQ_FLAG_BAD_POSITION);
+        return u * p.Hkv;
+    };
+    long long mine = 0, first = 0;
+    for (int b = tid; b < p.B; b += kThreads) {
+        const long long u = count(b);
+        if (b == tid) first = u;
+        mine += u;
+    }
+    auto block_scan = [&](long long v, long long& total) -> long long {  // inclusive
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, v, off);
+            if (lane >= off) v += t;
+        }
+        if (lane == 31) ctl->warp_sum[warp] = v;
+        __syncthreads();
+        long long before = 0;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            const long long t = ctl->warp_sum[w];
+            if (w < warp) before += t;
+            total += t;
+        }
+        __syncthreads();
+        return v + before;
+    };
+    long long U;
+    block_scan(mine, U);
+    const long long C = min(static_cast<long long>(gridDim.x), U);
+    const long long cta = blockIdx.x;
+    if (tid == 0) {
+        ctl->start = Start{0, 0, 0, 0, 0};
+        p.desc[cta].parts = 0;
+    }
+    __syncthreads();
+    if (cta >= C) return;
+    const long long u0 = cta * U / C, u1 = (cta + 1) * U / C;
+    long long base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        const long long v = b0 == 0 ? first : count(b0 + tid);
+        long long total;
+        const long long incl = base + block_scan(v, total), excl = incl - v;
+        if (u0 >= excl && u0 < incl) {  // one thread
+            const int b = b0 + tid;
+            const Seq s = sequence(p, b);
+            const long long per = v / p.Hkv;
+            const int h = static_cast<int>((u0 - excl) / per);
+            long long rem = u0 - excl - h * per;
+            int j = 0;
+            while (true) {
+                const int nt = units_of(visible(p, s, j));
+                if (rem < nt) break;
+                rem -= nt;
+                ++j;
+            }
+            ctl->start = Start{b, h, j, static_cast<int>(rem), u1 - u0};
+            // this CTA starts inside an item: is its part the item's second one?
+            if (rem > 0) {
+                const long long i0 = u0 - rem, i1 = i0 + units_of(visible(p, s, j));
+                if ((cta - 1) * U / C <= i0) {
+                    int parts = 1;
+                    for (long long c = cta; c < C && c * U / C < i1; ++c) ++parts;
+                    p.desc[cta] = MergeDesc{parts, s.row0 + j * 2 * p.T, min(2 * p.T, s.n - j * 2 * p.T), h};
+                }
+            }
+        }
+        base += total;
+        if (base > u0) break;
+    }
+    __syncthreads();
+}
+
 template <int D>
-__global__ void __launch_bounds__(256) chunk_kernel(ChunkArgs a) {
+struct Sizes {
+    static constexpr int kChunk = kTile * 128;               // bytes of a chunk [128][64] f16
+    static constexpr int kOperand = kTile * D * 2;           // bytes of an operand tile
+    static constexpr int kQ = 2 * kOperand;
+};
+
+// Eight output columns (in the order the unpack leaves: 0 4 1 5 2 6 3 7) as 16 bytes in dimension order.
+__device__ __forceinline__ uint4 columns_to_halves(const float (&v)[8]) {
+    return make_uint4(pack_h2(v[0], v[2]), pack_h2(v[4], v[6]), pack_h2(v[1], v[3]), pack_h2(v[5], v[7]));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    using Z = Sizes<D>;
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t q_s = smem_u32(smem), ring_s = q_s + Z::kQ, packed_s = ring_s + kRing * Z::kOperand;
+    const int packed_bytes = (kTile >> p.lg_p) * p.L.bytes;
+    Ctl* ctl = reinterpret_cast<Ctl*>(smem + Z::kQ + kRing * Z::kOperand + kPacked * packed_bytes);
+    volatile int* stop = &ctl->stop;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kPacked; ++i) {
+            mbar_init(smem_u32(&ctl->pk_full[i]), 1);
+            mbar_init(smem_u32(&ctl->pk_empty[i]), 4);
+        }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(smem_u32(&ctl->kv_full[i]), 4);
+            mbar_init(smem_u32(&ctl->kv_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&ctl->q_full[i]), 4);
+            mbar_init(smem_u32(&ctl->s_full[i]), 1);
+            mbar_init(smem_u32(&ctl->p_full[i]), 4);
+            mbar_init(smem_u32(&ctl->o_done[i]), 1);
+        }
+        ctl->stop = 0;
+        fence_mbar_init();
+    }
+    if (warp == 12) tmem_alloc(smem_u32(&ctl->tmem), kTmem);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    tc_fence_before();
+    find_start(p, ctl);  // (has barriers of the CTA)
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem;
+    const Start st = ctl->start;
+
+    if (warp < 8) {
+        regs_more<192>();
+        // ---- softmax of stream sw, row `row` of the stream's row tile
+        const int sw = warp / 4;
+        const int row = threadIdx.x & 127;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+        const uint32_t s_t = tmem + lanes + 128u * sw, o_t = tmem + lanes + 256u;
+        const int tok_in = row / p.r, head_in = row - tok_in * p.r;  // of the row tile
+        uint32_t n_s = 0, n_o[2] = {0, 0};
+        Walk walk(p, st);
+        Segment g;
+        while (st.units > 0 && walk.next(g)) {
+            const int n = g.k1 - g.k0;
+            const int tile_of = g.two ? sw : 0;                       // the stream's row tile
+            const int tok = g.tok0 + tile_of * p.T + tok_in;          // token of the sequence
+            const bool valid = tok_in < p.T && tok < g.tok0 + g.tokens;
+            const long long at = (static_cast<long long>(g.s.row0 + tok) * p.Hq + g.h * p.r + head_in) * D;
+            const int limit = valid ? g.s.len - g.s.n + tok + 1 : 0;  // positions the row sees
+            if (g.two || sw == 0) {
+                // the row's query into shared memory, its dimensions in the order the unpack leaves
+                const uint32_t dst = q_s + sw * Z::kOperand;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (valid) x = __ldg(reinterpret_cast<const uint4*>(p.q + at) + i);
+                    const uint4 y = make_uint4(prmt(x.x, x.z, 0x5410) ^ p.q_flip, prmt(x.x, x.z, 0x7632) ^ p.q_flip,
+                                               prmt(x.y, x.w, 0x5410) ^ p.q_flip, prmt(x.y, x.w, 0x7632) ^ p.q_flip);
+                    const uint32_t a = dst + (i / 8) * Z::kChunk + swizzled(row, i % 8);
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                                 : "memory");
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full[sw]));
+            }
+            float m = -INFINITY, l = 0.f;  // the maximum the weights are taken against (of z / scale), their sum
+            bool begun = false;
+            for (int i = g.two ? 0 : sw; i < n; i += g.two ? 1 : 2) {
+                wait_or_stop(smem_u32(&ctl->s_full[sw]), n_s & 1, stop, p.status);
+                ++n_s;
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) tmem_ld32(s_t + 32 * x, s[x]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 4; ++x) tmem_touch(s[x]);
+                const int seen = limit - (g.k0 + i) * kTile;  // columns the row sees
+                if (__any_sync(0xffffffffu, seen < kTile)) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int y = 0; y < 32; ++y)
+                            if (32 * x + y >= seen) s[x][y] = 0xff800000u;
+                }
+                float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int y = 0; y < 32; y += 2) {
+                        top0 = fmaxf(top0, __uint_as_float(s[x][y]));
+                        top1 = fmaxf(top1, __uint_as_float(s[x][y + 1]));
+                    }
+                const float top = fmaxf(top0, top1);
+                // The reference follows the maximum only when that is more than 2^8 above it (weights then stay
+                // below 2^8, far inside f16): the output is rescaled a few times a row instead of every tile
+                const bool move = (top - m) * p.c > 8.f || m == -INFINITY;
+                const float m_new = move ? fmaxf(top, m) : m;
+                if (begun && __any_sync(0xffffffffu, move && m_new != m)) {
+                    const float a = m_new == -INFINITY ? 1.f : fast_exp2((m - m_new) * p.c);
+                    l *= a;
+#pragma unroll 1
+                    for (int x = 0; x < D / 32; ++x) {  // (the products into O that came before S are complete)
+                        uint32_t o[32];
+                        tmem_ld32(o_t + D * sw + 32 * x, o);
+                        tmem_wait_ld();
+                        tmem_touch(o);
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * a);
+                        tmem_st32(o_t + D * sw + 32 * x, o);
+                    }
+                }
+                m = m_new;
+                begun = true;
+                const float off = m == -INFINITY ? 0.f : -m * p.c;
+                float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) {
+                        const float p0 = fast_exp2(fmaf(__uint_as_float(s[2 * x + y / 16][2 * (y % 16)]), p.c, off));
+                        const float p1 = fast_exp2(fmaf(__uint_as_float(s[2 * x + y / 16][2 * (y % 16) + 1]), p.c, off));
+                        sum0 += p0;
+                        sum1 += p1;
+                        w[y] = pack_h2(p0, p1);
+                    }
+                    tmem_st32(s_t + 32 * x, w);
+                }
+                l += sum0 + sum1;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[sw]));
+            }
+            // ---- the segment's result
+            const bool whole = g.k0 == 0 && g.k1 == g.nt;
+            const int slot = 2 * blockIdx.x + (g.k0 == 0 ? 1 : 0);
+            const int prow = tile_of * kTile + row;  // row of a partial result
+            float* pml = p.part_ml + (static_cast<long long>(slot) * 256 + prow) * 2;
+            float* po = p.part_o + (static_cast<long long>(slot) * 256 + prow) * D;
+            if (g.two) {
+                wait_or_stop(smem_u32(&ctl->o_done[sw]), n_o[sw] & 1, stop, p.status);
+                ++n_o[0];
+                ++n_o[1];
+                tc_fence_after();
+                const float inv = l > 0.f ? 2.f / l : 0.f;
+#pragma unroll 1
+                for (int x = 0; x < D / 32; ++x) {
+                    uint32_t o[32];
+                    tmem_ld32(o_t + D * sw + 32 * x, o);
+                    tmem_wait_ld();
+                    tmem_touch(o);
+                    if (valid && whole) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            float v[8];
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) v[z] = __uint_as_float(o[8 * y + z]) * inv;
+                            reinterpret_cast<uint4*>(p.out + at)[4 * x + y] = columns_to_halves(v);
+                        }
+                    } else if (valid) {
+#pragma unroll
+                        for (int y = 0; y < 8; ++y)
+                            reinterpret_cast<uint4*>(po)[8 * x + y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (valid && !whole) {
+                    pml[0] = m * p.c;
+                    pml[1] = l;
+                }
+                tc_fence_before();
+            } else {
+                // both streams hold a part of the same rows: lane by lane the same tensor-memory lane
+                const bool both = n > 1;
+                wait_or_stop(smem_u32(&ctl->o_done[0]), n_o[0] & 1, stop, p.status);
+                ++n_o[0];
+                if (both) {
+                    wait_or_stop(smem_u32(&ctl->o_done[1]), n_o[1] & 1, stop, p.status);
+                    ++n_o[1];
+                }
+                tc_fence_after();
+                ctl->ml[sw][row][0] = m;
+                ctl->ml[sw][row][1] = l;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                const float m0 = ctl->ml[0][row][0], m1 = ctl->ml[1][row][0];
+                const float mm = fmaxf(m0, m1);
+                const float a0 = m0 == -INFINITY ? 0.f : fast_exp2((m0 - mm) * p.c);
+                const float a1 = m1 == -INFINITY ? 0.f : fast_exp2((m1 - mm) * p.c);
+                const float ll = ctl->ml[0][row][1] * a0 + ctl->ml[1][row][1] * a1;
+                const float f = whole ? (ll > 0.f ? 2.f / ll : 0.f) : 1.f;
+#pragma unroll 1
+                for (int x = sw * (D / 64); x < (sw + 1) * (D / 64); ++x) {  // each stream's warps half of the columns
+                    uint32_t o[32], u[32];
+                    tmem_ld32(o_t + 32 * x, o);
+                    if (both) tmem_ld32(o_t + D + 32 * x, u);
+                    tmem_wait_ld();
+                    tmem_touch(o);
+                    if (both) tmem_touch(u);
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) {
+                        float v = __uint_as_float(o[y]) * a0;
+                        if (both) v = fmaf(__uint_as_float(u[y]), a1, v);
+                        o[y] = __float_as_uint(v * f);
+                    }
+                    if (valid && whole) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            float v[8];
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) v[z] = __uint_as_float(o[8 * y + z]);
+                            reinterpret_cast<uint4*>(p.out + at)[4 * x + y] = columns_to_halves(v);
+                        }
+                    } else if (valid) {
+#pragma unroll
+                        for (int y = 0; y < 8; ++y)
+                            reinterpret_cast<uint4*>(po)[8 * x + y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (valid && !whole && sw == 0) {
+                    pml[0] = mm * p.c;
+                    pml[1] = ll;
+                }
+                tc_fence_before();
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+            }
+        }
+    } else if (warp < 12) {
+        regs_less<80>();
+        // ---- dequantize
+        constexpr int PARTS = D / 32;  // 16-byte pieces of a row's codes
+        const int dw = warp - 8;
+        uint32_t n_ring = 0, n_pk = 0;
+        Walk walk(p, st);
+        Segment g;
+        while (st.units > 0 && walk.next(g)) {
+            const int n = g.k1 - g.k0;
+            // tile i's keys (is_v 0) or values into the next operand tile
+            auto dequant = [&](int i, int is_v) {
+                const uint32_t stage = n_ring % kRing, phase = n_ring / kRing;
+                const uint32_t pk = (n_pk + i) % kPacked;
+                if (is_v == 0) wait_or_stop(smem_u32(&ctl->pk_full[pk]), ((n_pk + i) / kPacked) & 1, stop, p.status);
+                if (n_ring >= kRing) wait_or_stop(smem_u32(&ctl->kv_empty[stage]), (phase & 1) ^ 1, stop, p.status);
+                ++n_ring;
+                const uint8_t* src = smem + Z::kQ + kRing * Z::kOperand + pk * packed_bytes;
+                const uint32_t dst = ring_s + stage * Z::kOperand;
+                const int G = is_v ? p.L.Gv : p.L.Gk;
+                const int codes_off = is_v ? p.L.v_codes : 0, scales_off = is_v ? p.L.v_scales : p.L.k_scales;
+                const int end = g.vis - (g.k0 + i) * kTile;  // tokens of the tile that exist
+                const int mask = (1 << p.lg_p) - 1;
+#pragma unroll 2
+                for (int w = 0; w < kTile * PARTS / 128; ++w) {
+                    // 8 tokens x 4 pieces a warp: eight lanes of a piece read 128 bytes apart by rows (no bank
+                    // twice) and write 8 rows' swizzled pieces (no bank twice)
+                    const int job = (w * 4 + dw) * 32 + lane;
+                    const int t = (job / (8 * PARTS)) * 8 + (job & 7);
+                    const int part = ((job >> 3) + (t & 7) * PARTS / 8) % PARTS;
+                    const uint8_t* blk = src + (t >> p.lg_p) * p.L.bytes;
+                    const int slot = t & mask;
+                    uint4 w4 = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+                    uint32_t s2 = 0;
+                    if (t < end) {
+                        w4 = *reinterpret_cast<const uint4*>(blk + codes_off + slot * (D / 2) + part * 16);
+                        const uint32_t s = *reinterpret_cast<const uint16_t*>(blk + scales_off + (slot * (D / G) + part * 32 / G) * 2);
+                        // half the scale, so that 7 times it stays finite (exact but for the smallest subnormals)
+                        s2 = h2_mul(s | s << 16, 0x38003800u);
+                    }
+                    const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
+                    const uint32_t base = dst + (part / 2) * Z::kChunk;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t lo = ws[x], hi = ws[x] >> 8;
+                        const uint32_t a = base + swizzled(t, (part & 1) * 4 + x);
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(h2_mul(unpack_lo(lo), s2)),
+                                     "r"(h2_mul(unpack_hi(lo), s2)), "r"(h2_mul(unpack_lo(hi), s2)),
+                                     "r"(h2_mul(unpack_hi(hi), s2))
+                                     : "memory");
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&ctl->kv_full[stage]));
+                    if (is_v) mbar_arrive(smem_u32(&ctl->pk_empty[pk]));
+                }
+            };
+            if (g.two) {
+                for (int i = 0; i < n; ++i) {
+                    dequant(i, 0);
+                    dequant(i, 1);
+                }
+            } else {  // in the order of the products: a stream's next scores come before the other's output
+                dequant(0, 0);
+                if (n > 1) dequant(1, 0);
+                for (int i = 0; i < n; ++i) {
+                    dequant(i, 1);
+                    if (i + 2 < n) dequant(i + 2, 0);
+                }
+            }
+            n_pk += n;
+        }
+    } else {
+        regs_less<40>();
+        if (warp == 12) {
+            // ---- the products
+            constexpr uint32_t kIdS = mma_idesc(kTile, kTile, false, false), kIdO = mma_idesc(kTile, D, false, true);
+            uint32_t n_ring = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+            auto take = [&]() -> uint32_t {  // the next operand tile, in order
+                const uint32_t stage = n_ring % kRing;
+                wait_or_stop(smem_u32(&ctl->kv_full[stage]), (n_ring / kRing) & 1, stop, p.status);
+                ++n_ring;
+                return stage;
+            };
+            auto scores = [&](int s, int q_tile, uint32_t stage) {
+                tc_fence_after();
+                if (lane == 0 && !*stop) {
+                    const uint32_t a = q_s + q_tile * Z::kOperand, b = ring_s + stage * Z::kOperand;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = (k / 4) * Z::kChunk + (k % 4) * 32;
+                        mma_ss(tmem + 128u * s, smem_desc(a + off, 16, 1024), smem_desc(b + off, 16, 1024), kIdS, k > 0);
+                    }
+                    mma_commit(smem_u32(&ctl->s_full[s]));
+                }
+                __syncwarp();
+            };
+            auto output = [&](int s, uint32_t stage, bool first) {
+                wait_or_stop(smem_u32(&ctl->p_full[s]), n_p[s] & 1, stop, p.status);
+                ++n_p[s];
+                tc_fence_after();
+                if (lane == 0 && !*stop) {
+                    const uint32_t b = ring_s + stage * Z::kOperand;
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_ts(tmem + 256u + D * s, tmem + 128u * s + 8 * k, smem_desc(b + k * 2048, Z::kChunk, 1024), kIdO,
+                               !first || k > 0);
+                }
+                __syncwarp();
+            };
+            auto commit = [&](uint64_t* bar) {
+                if (lane == 0 && !*stop) mma_commit(smem_u32(bar));
+                __syncwarp();
+            };
+            auto wait_q = [&](int s) {
+                wait_or_stop(smem_u32(&ctl->q_full[s]), n_q[s] & 1, stop, p.status);
+                ++n_q[s];
+            };
+            Walk walk(p, st);
+            Segment g;
+            while (st.units > 0 && walk.next(g)) {
+                const int n = g.k1 - g.k0;
+                if (g.two) {
+                    uint32_t k = take();
+                    wait_q(0);
+                    scores(0, 0, k);
+                    wait_q(1);
+                    scores(1, 1, k);
+                    commit(&ctl->kv_empty[k]);
+                    for (int i = 0; i < n; ++i) {
+                        const uint32_t v = take();
+                        output(0, v, i == 0);
+                        if (i + 1 < n) {
+                            k = take();
+                            scores(0, 0, k);
+                        } else {
+                            commit(&ctl->o_done[0]);
+                        }
+                        output(1, v, i == 0);
+                        commit(&ctl->kv_empty[v]);
+                        if (i + 1 < n) {
+                            scores(1, 1, k);
+                            commit(&ctl->kv_empty[k]);
+                        } else {
+                            commit(&ctl->o_done[1]);
+                        }
+                    }
+                } else {
+                    wait_q(0);
+                    for (int i = 0; i < min(n, 2); ++i) {
+                        const uint32_t k = take();
+                        scores(i, 0, k);
+                        commit(&ctl->kv_empty[k]);
+                    }
+                    for (int i = 0; i < n; ++i) {
+                        const uint32_t v = take();
+                        output(i & 1, v, i < 2);
+                        commit(&ctl->kv_empty[v]);
+                        if (i + 2 < n) {
+                            const uint32_t k = take();
+                            scores(i & 1, 0, k);
+                            commit(&ctl->kv_empty[k]);
+                        } else {
+                            commit(&ctl->o_done[i & 1]);
+                        }
+                    }
+                }
+            }
+        } else if (warp == 13) {
+            // ---- packed pages
+            uint32_t n_pk = 0;
+            const int per = kTile >> p.lg_p;  // pages of a tile
+            Walk walk(p, st);
+            Segment g;
+            while (st.units > 0 && walk.next(g)) {
+                const int pages = (max(g.vis, 0) + (1 << p.lg_p) - 1) >> p.lg_p;  // the item's
+                const int32_t* table = p.block_table + static_cast<long long>(g.b) * p.max_blocks;
+                int base = g.k0 * per;  // lane l holds page base + l, and the one 32 later
+                auto look = [&](int at) -> int { return at < pages ? __ldg(table + at) : 0; };
+                int cur = look(base + lane), nxt = look(base + 32 + lane);
+                for (int i = g.k0; i < g.k1; ++i, ++n_pk) {
+                    const uint32_t pk = n_pk % kPacked;
+                    if (n_pk >= kPacked)
+                        wait_or_stop(smem_u32(&ctl->pk_empty[pk]), ((n_pk / kPacked) & 1) ^ 1, stop, p.status);
+                    const int first = i * per;
+                    if (first - base >= 32) {
+                        base += 32;
+                        cur = nxt;
+                        nxt = look(base + 32 + lane);
+                    }
+                    const int count = max(0, min(per, pages - first));
+                    const uint32_t bar = smem_u32(&ctl->pk_full[pk]);
+                    if (lane == 0 && !*stop) {
+                        if (count > 0) mbar_arrive_expect_tx(bar, count * p.L.bytes);
+                        else mbar_arrive(bar);
+                    }
+                    __syncwarp();
+                    int page = __shfl_sync(0xffffffffu, cur, (first - base + lane) & 31);
+                    if (lane < count && !*stop) {
+                        if (page < 0 || page >= p.num_pages) {
+                            raise_flag(p.status, KVQ_FLAG_BAD_PAGE);
+                            page = 0;
+                        }
+                        bulk_g2s(packed_s + pk * packed_bytes + lane * p.L.bytes,
+                                 p.pool + (static_cast<long long>(page) * p.Hkv + g.h) * p.L.bytes, p.L.bytes, bar);
+                    }
+                    __syncwarp();
+                }
+            }
+            // no copy of this CTA may be in flight when it leaves
+            for (uint32_t i = n_pk > kPacked ? n_pk - kPacked : 0; i < n_pk; ++i)
+                mbar_wait(smem_u32(&ctl->pk_full[i % kPacked]), (i / kPacked) & 1, 250000000ull);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_free(tmem, kTmem);
+    }
+}
+
+// The items cut between CTAs: blockIdx.x the CTA of the second part, a warp a row (one in 8 gridDim.y).
+template <int D>
+__global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const MergeDesc d = p.desc[blockIdx.x];
+    if (d.parts == 0) return;
     constexpr int E = D / 32;
-    uint32_t* status = reinterpret_cast<uint32_t*>(a.workspace);
     const int lane = threadIdx.x & 31;
-    const long long tasks = static_cast<long long>(a.rows) * a.Hq;
-    const long long warps = static_cast<long long>(gridDim.x) * 8;
-    for (long long task = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / 32; task < tasks; task += warps) {
-        const int row = static_cast<int>(task / a.Hq), hq = static_cast<int>(task % a.Hq), h = hq / (a.Hq / a.Hkv);
-        const int b = warp_find_seq(a.cu_rows, a.B, row, lane);
-        if (b < 0) continue;
-        const int most = static_cast<int>(min(static_cast<long long>(a.max_len), static_cast<long long>(a.max_blocks) << a.lg_p));
-        int len = a.seq_lens[b];
-        if (len > most) {
-            if (lane == 0) raise_flag(status, KVQ_FLAG_BAD_POSITION);
-            len = most;
-        }
-        // (offsets that do not ascend must not lead behind the sequence)
-        const int pos = min(max(len, 0) - 1, max(len, 0) - (a.cu_rows[b + 1] - a.cu_rows[b]) + (row - a.cu_rows[b]));
-        float q[E], o[E];
-        for (int i = 0; i < E; ++i) {
-            q[i] = __half2float(a.q[task * D + lane * E + i]) * a.softmax_scale;
-            o[i] = 0.f;
-        }
-        float m = -INFINITY, l = 0.f;
-        for (int t = 0; t <= pos; ++t) {
-            int page = a.block_table[static_cast<long long>(b) * a.max_blocks + (t >> a.lg_p)];
-            if (page < 0 || page >= a.num_pages) {
-                if (lane == 0) raise_flag(status, KVQ_FLAG_BAD_PAGE);
-                page = 0;
-            }
-            const int slot = t & ((1 << a.lg_p) - 1);
-            const uint8_t* blk = a.pool + (static_cast<long long>(page) * a.Hkv + h) * a.L.bytes;
-            const float sk = __half2float(reinterpret_cast<const __half*>(blk + a.L.k_scales)[slot * (D / a.L.Gk) + lane * E / a.L.Gk]);
-            const float sv = __half2float(reinterpret_cast<const __half*>(blk + a.L.v_scales)[slot * (D / a.L.Gv) + lane * E / a.L.Gv]);
-            float z = 0.f, v[E];
-            for (int i = 0; i < E; ++i) {
-                const int at = lane * E + i, sh = 4 * (at & 1);
-                z += q[i] * static_cast<float>(((blk[slot * (D / 2) + at / 2] >> sh) & 15) - 8) * sk;
-                v[i] = static_cast<float>(((blk[a.L.v_codes + slot * (D / 2) + at / 2] >> sh) & 15) - 8) * sv;
-            }
-            for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-            const float mn = fmaxf(m, z), al = expf(m - mn), p = expf(z - mn);
-            l = l * al + p;
-            for (int i = 0; i < E; ++i) o[i] = o[i] * al + p * v[i];
+    const int c = blockIdx.x;
+    for (int i = blockIdx.y * 8 + threadIdx.x / 32; i < d.tokens * p.r; i += 8 * gridDim.y) {
+        const int tok = i / p.r, g = i - tok * p.r;
+        const int prow = (tok / p.T) * kTile + (tok % p.T) * p.r + g;
+        float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+        for (int k = 0; k < d.parts; ++k) {
+            const long long at = static_cast<long long>(k == 0 ? 2 * (c - 1) + 1 : 2 * (c + k - 1)) * 256 + prow;
+            const float mk = p.part_ml[2 * at], lk = p.part_ml[2 * at + 1];
+            float ok[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) ok[e] = p.part_o[at * D + lane * E + e];
+            if (lk <= 0.f) continue;
+            const float mn = fmaxf(m, mk), a = fast_exp2(m - mn), ak = fast_exp2(mk - mn);
+            l = l * a + lk * ak;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = o[e] * a + ok[e] * ak;
             m = mn;
         }
-        for (int i = 0; i < E; ++i)
-            a.out[task * D + lane * E + i] = __float2half_rn(pos < 0 ? 0.f : o[i] / l);
+        const float inv = l > 0.f ? 2.f / l : 0.f;
+        // columns E lane .. of the 8 that share 16 bytes; dimension order 0 4 1 5 2 6 3 7
+        __half* out = p.out + (static_cast<long long>(d.row0 + tok) * p.Hq + d.h * p.r + g) * D;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int col = lane * E + e, x = col & 7;
+            out[(col & ~7) + (x >> 1) + 4 * (x & 1)] = __float2half_rn(o[e] * inv);
+        }
     }
+}
+
+int device_sms() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return sms;
+}
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+template <int D>
+cudaError_t launch(const ChunkParams& p, int ctas, cudaStream_t stream) {
+    const size_t smem = 1024 + Sizes<D>::kQ + kRing * Sizes<D>::kOperand +
+                        static_cast<size_t>(kPacked) * (kTile >> p.lg_p) * p.L.bytes + sizeof(Ctl);
+    cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, chunk_kernel<D>, p);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 8);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<D>, p);
 }
 
 }  // namespace
 
-size_t chunk_workspace_bytes(const ChunkArgs&) { return 256; }
+size_t chunk_workspace_bytes(const ChunkArgs& a) {
+    const size_t sms = static_cast<size_t>(device_sms());
+    if (sms == 0) return 0;
+    return 256 + round256(sms * sizeof(MergeDesc)) + 2 * sms * 256 * (2 + a.L.d) * sizeof(float);
+}
 
 cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t stream) {
-    int slices;
-    const int blocks = rows_grid(static_cast<long long>(a.rows) * a.Hq, 1, 32, &slices);
-    if (a.L.d == 64) chunk_kernel<64><<<blocks, 256, 0, stream>>>(a);
-    else chunk_kernel<128><<<blocks, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    const int sms = device_sms();
+    ChunkParams p{};
+    p.pool = a.pool;
+    p.q = a.q;
+    p.block_table = a.block_table;
+    p.seq_lens = a.seq_lens;
+    p.cu_rows = a.cu_rows;
+    p.out = a.out;
+    p.status = reinterpret_cast<uint32_t*>(a.workspace);
+    p.desc = reinterpret_cast<MergeDesc*>(a.workspace + 256);
+    p.part_ml = reinterpret_cast<float*>(a.workspace + 256 + round256(sms * sizeof(MergeDesc)));
+    p.part_o = p.part_ml + 2ll * sms * 256 * 2;
+    p.rows = a.rows;
+    p.B = a.B;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.r = a.Hq / a.Hkv;
+    p.T = kTile / p.r;
+    p.max_blocks = a.max_blocks;
+    p.num_pages = a.num_pages;
+    p.lg_p = a.lg_p;
+    const long long table = static_cast<long long>(a.max_blocks) << a.lg_p;
+    p.most = static_cast<int32_t>(table < a.max_len ? table : a.max_len);
+    // (at least 1e-30: a hidden score is -infinity, which zero times is not a number)
+    p.c = std::fmax(2.f * std::fabs(a.softmax_scale) * 1.4426950408889634f, 1e-30f);
+    p.q_flip = a.softmax_scale < 0.f ? 0x80008000u : 0u;
+    p.L = a.L;
+    return a.L.d == 64 ? launch<64>(p, sms, stream) : launch<128>(p, sms, stream);
 }
 
 }  // namespace kvq
