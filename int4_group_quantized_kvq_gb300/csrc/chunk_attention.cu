@@ -14,9 +14,10 @@
 // Warps of a CTA (one per SM):
 //   0-3, 4-7   softmax of stream 0 and 1: a thread has a row.  Scores come from tensor memory, weights go
 //              back there (as the f16 A operand of the second product, over the scores' columns).
-//   8-11       dequantize packed tiles into f16 operand tiles (shared memory, a ring of kRing).
-//   12         issues the MMAs: S = Q K^T (both from shared memory), O += P V (P from tensor memory).
-//   13         copies packed pages into shared memory (bulk copies, a ring of kPacked tiles).
+//   8-15       dequantize packed tiles into f16 operand tiles (shared memory, a ring of kRing).
+//   16         issues the MMAs: S = Q K^T (both from shared memory), O += P V (P from tensor memory).
+//   17         copies packed pages into shared memory (bulk copies, a ring of kPacked tiles).
+//   18, 19     the streams' query tiles into shared memory.
 #include <cuda_fp16.h>
 
 #include <cmath>
@@ -28,11 +29,13 @@
 namespace kvq {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
+constexpr int kDqWarps = 8;
 constexpr int kRing = 3;      // operand tiles (K or V) in shared memory
 constexpr int kPacked = 3;    // packed tiles in shared memory
 constexpr int kTile = 128;    // rows of M, positions of a tile
 constexpr uint32_t kTmem = 512;
+constexpr int kItemUnits = 2;  // what an item costs a CTA besides its tiles (queries in, output out), in units
 
 // Where a CTA's run of units starts, and how long it is.
 struct Start {
@@ -57,7 +60,7 @@ struct ChunkParams {
     MergeDesc* desc;  // [gridDim.x]
     float* part_ml;   // [2 gridDim.x][256][2]: maximum (of scale log2(e) z) and sum
     float* part_o;    // [2 gridDim.x][256][D]
-    int32_t rows, B, Hq, Hkv, r, T, max_blocks, num_pages, lg_p, most;  // T: tokens of a row tile; most: longest sequence
+    int32_t rows, B, Hq, Hkv, r, T, max_blocks, num_pages, lg_p, lg_gk, lg_gv, most;  // T: tokens of a row tile; most: longest sequence
     float c;          // 2 |scale| log2(e): keys are held halved
     uint32_t q_flip;  // sign bits of a negative scale
     BlockLayout L;
@@ -74,56 +77,71 @@ __device__ __forceinline__ Seq sequence(const ChunkParams& p, int b) {
     s.len = min(max(__ldg(p.seq_lens + b), 0), p.most);
     return s;
 }
-// Positions the last row of item j can see, and the item's units (one at least: rows that see nothing
+// Positions the last row of item j can see, and the item's tiles (one at least: rows that see nothing
 // are written too).
 __device__ __forceinline__ int visible(const ChunkParams& p, const Seq& s, int j) {
     return s.len - s.n + static_cast<int>(min(static_cast<long long>(j + 1) * 2 * p.T, static_cast<long long>(s.n)));
 }
-__device__ __forceinline__ int units_of(int vis) { return max(1, (vis + kTile - 1) / kTile); }
+__device__ __forceinline__ int tiles_of(int vis) { return max(1, (vis + kTile - 1) / kTile); }
 
-// A segment: the units [k0, k1) of one item.
+// A segment: the tiles [k0, k1) of one item.
 struct Segment {
-    int b, h, j, k0, k1, nt, vis, tokens, tok0;
-    Seq s;
-    bool two;  // a second row tile (else the streams alternate)
+    int b, h, k0, k1, nt, vis, tokens, tok0;
+    int row0, ahead;  // the sequence's first row, and positions before that row's
+    bool two;         // a second row tile (else the streams alternate)
 };
 
-// Walks a CTA's segments; every role of the CTA walks the same ones.
+// Walks a CTA's segments; every role walks the same ones.  The state lies in shared memory, a copy for
+// each warp: kept in registers it would cost the softmax warps two dozen.
 struct Walk {
-    const ChunkParams& p;
     long long left;
     int b, h, j, k;
     Seq s;
-    __device__ Walk(const ChunkParams& p_, const Start& st) : p(p_), left(st.units), b(st.b), h(st.h), j(st.j), k(st.k) {
+    Segment g;
+    __device__ __forceinline__ void begin(const ChunkParams& p, const Start& st) {
+        left = st.units;
+        b = st.b;
+        h = st.h;
+        j = st.j;
+        k = st.k;
         s = sequence(p, b);
+        __syncwarp();
     }
-    __device__ __forceinline__ bool next(Segment& g) {
-        if (left <= 0) return false;
+    __device__ __forceinline__ bool next(const ChunkParams& p) {
+        __syncwarp();
+        long long room = left;
+        int cj = j, ch = h, cb = b;
+        const int ck = k;
+        Seq cs = s;
+        if (room <= 0) return false;
         const int step = 2 * p.T;
-        if (j * static_cast<long long>(step) >= s.n) {  // the next head or sequence
-            j = 0;
-            if (++h == p.Hkv) {
-                h = 0;
+        if (cj * static_cast<long long>(step) >= cs.n) {  // the next head or sequence
+            cj = 0;
+            if (++ch == p.Hkv) {
+                ch = 0;
                 do {
-                    if (++b >= p.B) return false;
-                    s = sequence(p, b);
-                } while (s.n == 0);
+                    if (++cb >= p.B) return false;
+                    cs = sequence(p, cb);
+                } while (cs.n == 0);
             }
         }
-        g.b = b;
-        g.h = h;
-        g.j = j;
-        g.s = s;
-        g.vis = visible(p, s, j);
-        g.nt = units_of(g.vis);
-        g.k0 = k;
-        g.k1 = static_cast<int>(min(static_cast<long long>(g.nt), k + left));
-        g.tok0 = j * step;
-        g.tokens = min(step, s.n - g.tok0);
-        g.two = g.tokens > p.T;
-        left -= g.k1 - g.k0;
+        const int vis = visible(p, cs, cj), nt = tiles_of(vis);
+        if (ck == 0) room -= kItemUnits;
+        const int k1 = static_cast<int>(min(static_cast<long long>(nt), ck + room));
+        __syncwarp();
+        if (k1 <= ck) {  // not a tile of it
+            left = 0;
+            return false;
+        }
+        const int tok0 = cj * step, tokens = min(step, cs.n - tok0);
+        g = Segment{cb, ch, ck, k1, nt, vis, tokens, tok0, cs.row0, cs.len - cs.n, tokens > p.T};
+        left = room - (k1 - ck);
         k = 0;
-        ++j;
+        j = cj + 1;
+        h = ch;
+        b = cb;
+        s = cs;
+        __syncwarp();
         return true;
     }
 };
@@ -131,11 +149,12 @@ struct Walk {
 struct Ctl {
     uint64_t pk_full[kPacked], pk_empty[kPacked];
     uint64_t kv_full[kRing], kv_empty[kRing];
-    uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
+    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2];
     long long warp_sum[kThreads / 32];
     Start start;
     uint32_t tmem;
     int stop;
+    Walk walk[kThreads / 32];
     float ml[2][kTile][2];
 };
 
@@ -147,7 +166,7 @@ __device__ __forceinline__ void find_start(const ChunkParams& p, Ctl* ctl) {
         if (b >= p.B) return 0;
         const Seq s = sequence(p, b);
         long long u = 0;
-        for (int j = 0; j * 2ll * p.T < s.n; ++j) u += units_of(visible(p, s, j));
+        for (int j = 0; j * 2ll * p.T < s.n; ++j) u += tiles_of(visible(p, s, j)) + kItemUnits;
         if (u > 0 && blockIdx.x == 0 && __ldg(p.seq_lens + b) > p.most) raise_flag(p.status, KVQ_FLAG_BAD_POSITION);
         return u * p.Hkv;
     };
@@ -198,22 +217,22 @@ __device__ __forceinline__ void find_start(const ChunkParams& p, Ctl* ctl) {
             const long long per = v / p.Hkv;
             const int h = static_cast<int>((u0 - excl) / per);
             long long rem = u0 - excl - h * per;
-            int j = 0;
+            int j = 0, nt;
             while (true) {
-                const int nt = units_of(visible(p, s, j));
-                if (rem < nt) break;
-                rem -= nt;
+                nt = tiles_of(visible(p, s, j));
+                if (rem < nt + kItemUnits) break;
+                rem -= nt + kItemUnits;
                 ++j;
             }
-            ctl->start = Start{b, h, j, static_cast<int>(rem), u1 - u0};
+            // a boundary within an item's first kItemUnits leaves all its tiles to this CTA
+            const long long i0 = u0 - rem + kItemUnits;  // where the item's tiles start in the list
+            const int k = static_cast<int>(max(0ll, u0 - i0));
+            ctl->start = Start{b, h, j, k, u1 - (k > 0 ? u0 : i0 - kItemUnits)};
             // this CTA starts inside an item: is its part the item's second one?
-            if (rem > 0) {
-                const long long i0 = u0 - rem, i1 = i0 + units_of(visible(p, s, j));
-                if ((cta - 1) * U / C <= i0) {
-                    int parts = 1;
-                    for (long long c = cta; c < C && c * U / C < i1; ++c) ++parts;
-                    p.desc[cta] = MergeDesc{parts, s.row0 + j * 2 * p.T, min(2 * p.T, s.n - j * 2 * p.T), h};
-                }
+            if (k > 0 && (cta - 1) * U / C <= i0) {
+                int parts = 1;
+                for (long long c = cta; c < C && c * U / C < i0 + nt; ++c) ++parts;
+                p.desc[cta] = MergeDesc{parts, s.row0 + j * 2 * p.T, min(2 * p.T, s.n - j * 2 * p.T), h};
             }
         }
         base += total;
@@ -249,14 +268,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPacked; ++i) {
             mbar_init(smem_u32(&ctl->pk_full[i]), 1);
-            mbar_init(smem_u32(&ctl->pk_empty[i]), 4);
+            mbar_init(smem_u32(&ctl->pk_empty[i]), kDqWarps);
         }
         for (int i = 0; i < kRing; ++i) {
-            mbar_init(smem_u32(&ctl->kv_full[i]), 4);
+            mbar_init(smem_u32(&ctl->kv_full[i]), kDqWarps);
             mbar_init(smem_u32(&ctl->kv_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&ctl->q_full[i]), 4);
+            mbar_init(smem_u32(&ctl->q_full[i]), 1);
+            mbar_init(smem_u32(&ctl->q_free[i]), 1);
             mbar_init(smem_u32(&ctl->s_full[i]), 1);
             mbar_init(smem_u32(&ctl->p_full[i]), 4);
             mbar_init(smem_u32(&ctl->o_done[i]), 1);
@@ -264,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         ctl->stop = 0;
         fence_mbar_init();
     }
-    if (warp == 12) tmem_alloc(smem_u32(&ctl->tmem), kTmem);
+    if (warp == 16) tmem_alloc(smem_u32(&ctl->tmem), kTmem);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     tc_fence_before();
     find_start(p, ctl);  // (has barriers of the CTA)
@@ -272,105 +292,117 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const uint32_t tmem = ctl->tmem;
     const Start st = ctl->start;
 
+    Walk& walk = ctl->walk[warp];
+    if (st.units > 0) walk.begin(p, st);
+    const Segment& g = walk.g;
+
     if (warp < 8) {
-        regs_more<192>();
+        regs_more<152>();
         // ---- softmax of stream sw, row `row` of the stream's row tile
         const int sw = warp / 4;
         const int row = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
         const uint32_t s_t = tmem + lanes + 128u * sw, o_t = tmem + lanes + 256u;
-        const int tok_in = row / p.r, head_in = row - tok_in * p.r;  // of the row tile
+        const int tok_in = row / p.r;  // token within the row tile
         uint32_t n_s = 0, n_o[2] = {0, 0};
-        Walk walk(p, st);
-        Segment g;
-        while (st.units > 0 && walk.next(g)) {
+        while (st.units > 0 && walk.next(p)) {
             const int n = g.k1 - g.k0;
-            const int tile_of = g.two ? sw : 0;                       // the stream's row tile
-            const int tok = g.tok0 + tile_of * p.T + tok_in;          // token of the sequence
-            const bool valid = tok_in < p.T && tok < g.tok0 + g.tokens;
-            const long long at = (static_cast<long long>(g.s.row0 + tok) * p.Hq + g.h * p.r + head_in) * D;
-            const int limit = valid ? g.s.len - g.s.n + tok + 1 : 0;  // positions the row sees
-            if (g.two || sw == 0) {
-                // the row's query into shared memory, its dimensions in the order the unpack leaves
-                const uint32_t dst = q_s + sw * Z::kOperand;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (valid) x = __ldg(reinterpret_cast<const uint4*>(p.q + at) + i);
-                    const uint4 y = make_uint4(prmt(x.x, x.z, 0x5410) ^ p.q_flip, prmt(x.x, x.z, 0x7632) ^ p.q_flip,
-                                               prmt(x.y, x.w, 0x5410) ^ p.q_flip, prmt(x.y, x.w, 0x7632) ^ p.q_flip);
-                    const uint32_t a = dst + (i / 8) * Z::kChunk + swizzled(row, i % 8);
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
-                                 : "memory");
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full[sw]));
-            }
+            const int tok = (g.two ? sw * p.T : 0) + tok_in;          // token of the item
+            const bool valid = tok_in < p.T && tok < g.tokens;
+            int seen = valid ? g.ahead + g.tok0 + tok + 1 - g.k0 * kTile : 0;  // columns the row sees, from tile k0 on
             float m = -INFINITY, l = 0.f;  // the maximum the weights are taken against (of z / scale), their sum
             bool begun = false;
-            for (int i = g.two ? 0 : sw; i < n; i += g.two ? 1 : 2) {
+            if (!g.two && sw == 1) seen -= kTile;
+            for (int i = g.two ? 0 : sw; i < n; i += g.two ? 1 : 2, seen -= g.two ? kTile : 2 * kTile) {
                 wait_or_stop(smem_u32(&ctl->s_full[sw]), n_s & 1, stop, p.status);
                 ++n_s;
                 tc_fence_after();
-                uint32_t s[4][32];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) tmem_ld32(s_t + 32 * x, s[x]);
-                tmem_wait_ld();
-#pragma unroll
-                for (int x = 0; x < 4; ++x) tmem_touch(s[x]);
-                const int seen = limit - (g.k0 + i) * kTile;  // columns the row sees
-                if (__any_sync(0xffffffffu, seen < kTile)) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
+                // Two passes over the scores: the maximum, then the weights.  128 scores in registers spill (and a
+                // spill goes to L2, shared memory leaving no L1 to speak of), so half of them are read twice
+                const bool part = __any_sync(0xffffffffu, seen < kTile);
+                auto hide = [&](uint32_t (&v)[32], int x) {
+                    if (part) {
 #pragma unroll
                         for (int y = 0; y < 32; ++y)
-                            if (32 * x + y >= seen) s[x][y] = 0xff800000u;
-                }
-                float top0 = -INFINITY, top1 = -INFINITY;
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                    for (int y = 0; y < 32; y += 2) {
-                        top0 = fmaxf(top0, __uint_as_float(s[x][y]));
-                        top1 = fmaxf(top1, __uint_as_float(s[x][y + 1]));
+                            if (32 * x + y >= seen) v[y] = 0xff800000u;
                     }
+                };
+                float top0 = -INFINITY, top1 = -INFINITY;
+                auto top_of = [&](const uint32_t (&v)[32]) {
+#pragma unroll
+                    for (int y = 0; y < 32; y += 4) {
+                        top0 = fmaxf(fmaxf(top0, __uint_as_float(v[y])), __uint_as_float(v[y + 1]));
+                        top1 = fmaxf(fmaxf(top1, __uint_as_float(v[y + 2])), __uint_as_float(v[y + 3]));
+                    }
+                };
+                uint32_t a[32], b[32], c[32];
+                tmem_ld32(s_t, a);
+                tmem_ld32(s_t + 32, b);
+                tmem_wait_ld();
+                tmem_touch(a);
+                tmem_touch(b);
+                tmem_ld32(s_t + 64, c);
+                hide(a, 0);
+                top_of(a);
+                hide(b, 1);
+                top_of(b);
+                tmem_ld32(s_t + 96, a);
+                tmem_wait_ld();
+                tmem_touch(c);
+                tmem_touch(a);
+                hide(c, 2);
+                top_of(c);
+                hide(a, 3);
+                top_of(a);
                 const float top = fmaxf(top0, top1);
                 // The reference follows the maximum only when that is more than 2^8 above it (weights then stay
                 // below 2^8, far inside f16): the output is rescaled a few times a row instead of every tile
                 const bool move = (top - m) * p.c > 8.f || m == -INFINITY;
                 const float m_new = move ? fmaxf(top, m) : m;
                 if (begun && __any_sync(0xffffffffu, move && m_new != m)) {
-                    const float a = m_new == -INFINITY ? 1.f : fast_exp2((m - m_new) * p.c);
-                    l *= a;
+                    const float f = m_new == -INFINITY ? 1.f : fast_exp2((m - m_new) * p.c);
+                    l *= f;
 #pragma unroll 1
-                    for (int x = 0; x < D / 32; ++x) {  // (the products into O that came before S are complete)
-                        uint32_t o[32];
-                        tmem_ld32(o_t + D * sw + 32 * x, o);
+                    for (int x = 0; x < D / 16; ++x) {  // (the products into O that came before S are complete)
+                        uint32_t o[16];
+                        tmem_ld16(o_t + D * sw + 16 * x, o);
                         tmem_wait_ld();
                         tmem_touch(o);
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * a);
-                        tmem_st32(o_t + D * sw + 32 * x, o);
+                        for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                        tmem_st16(o_t + D * sw + 16 * x, o);
                     }
                 }
                 m = m_new;
                 begun = true;
                 const float off = m == -INFINITY ? 0.f : -m * p.c;
                 float sum0 = 0.f, sum1 = 0.f;
+                // weights of columns 32 x .. , two to a column, to columns 64 + 16 x ..: over scores that are in
+                // registers by now
+                auto weigh = [&](const uint32_t (&v)[32], int x) {
+                    uint32_t w[16];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int y = 0; y < 32; ++y) {
-                        const float p0 = fast_exp2(fmaf(__uint_as_float(s[2 * x + y / 16][2 * (y % 16)]), p.c, off));
-                        const float p1 = fast_exp2(fmaf(__uint_as_float(s[2 * x + y / 16][2 * (y % 16) + 1]), p.c, off));
+                    for (int y = 0; y < 16; ++y) {
+                        const float p0 = fast_exp2(fmaf(__uint_as_float(v[2 * y]), p.c, off));
+                        const float p1 = fast_exp2(fmaf(__uint_as_float(v[2 * y + 1]), p.c, off));
                         sum0 += p0;
                         sum1 += p1;
                         w[y] = pack_h2(p0, p1);
                     }
-                    tmem_st32(s_t + 32 * x, w);
-                }
+                    tmem_st16(s_t + 64 + 16 * x, w);
+                };
+                weigh(c, 2);
+                tmem_ld32(s_t, b);
+                weigh(a, 3);
+                tmem_wait_ld();
+                tmem_touch(b);
+                tmem_ld32(s_t + 32, c);
+                hide(b, 0);
+                weigh(b, 0);
+                tmem_wait_ld();
+                tmem_touch(c);
+                hide(c, 1);
+                weigh(c, 1);
                 l += sum0 + sum1;
                 tmem_wait_st();
                 tc_fence_before();
@@ -380,9 +412,26 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             // ---- the segment's result
             const bool whole = g.k0 == 0 && g.k1 == g.nt;
             const int slot = 2 * blockIdx.x + (g.k0 == 0 ? 1 : 0);
-            const int prow = tile_of * kTile + row;  // row of a partial result
+            const int prow = (g.two ? sw * kTile : 0) + row;  // row of a partial result
             float* pml = p.part_ml + (static_cast<long long>(slot) * 256 + prow) * 2;
             float* po = p.part_o + (static_cast<long long>(slot) * 256 + prow) * D;
+            __half* out = p.out + (static_cast<long long>(g.row0 + g.tok0 + tok) * p.Hq + g.h * p.r + (row - tok_in * p.r)) * D;
+            auto put = [&](const uint32_t (&o)[32], int x, float f) {  // 32 columns of the row
+                if (valid && whole) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        float v[8];
+#pragma unroll
+                        for (int z = 0; z < 8; ++z) v[z] = __uint_as_float(o[8 * y + z]) * f;
+                        reinterpret_cast<uint4*>(out)[4 * x + y] = columns_to_halves(v);
+                    }
+                } else if (valid) {
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        reinterpret_cast<uint4*>(po)[8 * x + y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                }
+                __syncwarp();
+            };
             if (g.two) {
                 wait_or_stop(smem_u32(&ctl->o_done[sw]), n_o[sw] & 1, stop, p.status);
                 ++n_o[0];
@@ -395,20 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     tmem_ld32(o_t + D * sw + 32 * x, o);
                     tmem_wait_ld();
                     tmem_touch(o);
-                    if (valid && whole) {
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            float v[8];
-#pragma unroll
-                            for (int z = 0; z < 8; ++z) v[z] = __uint_as_float(o[8 * y + z]) * inv;
-                            reinterpret_cast<uint4*>(p.out + at)[4 * x + y] = columns_to_halves(v);
-                        }
-                    } else if (valid) {
-#pragma unroll
-                        for (int y = 0; y < 8; ++y)
-                            reinterpret_cast<uint4*>(po)[8 * x + y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-                    }
-                    __syncwarp();
+                    put(o, x, inv);
                 }
                 if (valid && !whole) {
                     pml[0] = m * p.c;
@@ -446,22 +482,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     for (int y = 0; y < 32; ++y) {
                         float v = __uint_as_float(o[y]) * a0;
                         if (both) v = fmaf(__uint_as_float(u[y]), a1, v);
-                        o[y] = __float_as_uint(v * f);
+                        o[y] = __float_as_uint(v);
                     }
-                    if (valid && whole) {
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            float v[8];
-#pragma unroll
-                            for (int z = 0; z < 8; ++z) v[z] = __uint_as_float(o[8 * y + z]);
-                            reinterpret_cast<uint4*>(p.out + at)[4 * x + y] = columns_to_halves(v);
-                        }
-                    } else if (valid) {
-#pragma unroll
-                        for (int y = 0; y < 8; ++y)
-                            reinterpret_cast<uint4*>(po)[8 * x + y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-                    }
-                    __syncwarp();
+                    put(o, x, f);
                 }
                 if (valid && !whole && sw == 0) {
                     pml[0] = mm * p.c;
@@ -471,16 +494,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 asm volatile("bar.sync 1, 256;" ::: "memory");
             }
         }
-    } else if (warp < 12) {
-        regs_less<80>();
+    } else if (warp < 8 + kDqWarps) {
+        regs_less<48>();
         // ---- dequantize
         constexpr int PARTS = D / 32;  // 16-byte pieces of a row's codes
         const int dw = warp - 8;
         uint32_t n_ring = 0, n_pk = 0;
-        Walk walk(p, st);
-        Segment g;
-        while (st.units > 0 && walk.next(g)) {
+        while (st.units > 0 && walk.next(p)) {
             const int n = g.k1 - g.k0;
+            const int end0 = g.vis - g.k0 * kTile;
             // tile i's keys (is_v 0) or values into the next operand tile
             auto dequant = [&](int i, int is_v) {
                 const uint32_t stage = n_ring % kRing, phase = n_ring / kRing;
@@ -490,36 +512,45 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 ++n_ring;
                 const uint8_t* src = smem + Z::kQ + kRing * Z::kOperand + pk * packed_bytes;
                 const uint32_t dst = ring_s + stage * Z::kOperand;
-                const int G = is_v ? p.L.Gv : p.L.Gk;
+                const int lg_g = is_v ? p.lg_gv : p.lg_gk;
                 const int codes_off = is_v ? p.L.v_codes : 0, scales_off = is_v ? p.L.v_scales : p.L.k_scales;
-                const int end = g.vis - (g.k0 + i) * kTile;  // tokens of the tile that exist
+                const int end = end0 - i * kTile;  // tokens of the tile that exist
                 const int mask = (1 << p.lg_p) - 1;
-#pragma unroll 2
-                for (int w = 0; w < kTile * PARTS / 128; ++w) {
+                constexpr int JOBS = kTile * PARTS / (32 * kDqWarps);
+                uint4 w4[JOBS];
+                uint32_t s2[JOBS];
+#pragma unroll
+                for (int w = 0; w < JOBS; ++w) {
                     // 8 tokens x 4 pieces a warp: eight lanes of a piece read 128 bytes apart by rows (no bank
                     // twice) and write 8 rows' swizzled pieces (no bank twice)
-                    const int job = (w * 4 + dw) * 32 + lane;
+                    const int job = (w * kDqWarps + dw) * 32 + lane;
                     const int t = (job / (8 * PARTS)) * 8 + (job & 7);
                     const int part = ((job >> 3) + (t & 7) * PARTS / 8) % PARTS;
                     const uint8_t* blk = src + (t >> p.lg_p) * p.L.bytes;
                     const int slot = t & mask;
-                    uint4 w4 = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-                    uint32_t s2 = 0;
+                    w4[w] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+                    s2[w] = 0;
                     if (t < end) {
-                        w4 = *reinterpret_cast<const uint4*>(blk + codes_off + slot * (D / 2) + part * 16);
-                        const uint32_t s = *reinterpret_cast<const uint16_t*>(blk + scales_off + (slot * (D / G) + part * 32 / G) * 2);
-                        // half the scale, so that 7 times it stays finite (exact but for the smallest subnormals)
-                        s2 = h2_mul(s | s << 16, 0x38003800u);
+                        w4[w] = *reinterpret_cast<const uint4*>(blk + codes_off + slot * (D / 2) + part * 16);
+                        s2[w] = *reinterpret_cast<const uint16_t*>(blk + scales_off + (((slot * D + part * 32) >> lg_g) << 1));
                     }
-                    const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
-                    const uint32_t base = dst + (part / 2) * Z::kChunk;
+                }
+#pragma unroll
+                for (int w = 0; w < JOBS; ++w) {
+                    const int job = (w * kDqWarps + dw) * 32 + lane;
+                    const int t = (job / (8 * PARTS)) * 8 + (job & 7);
+                    const int part = ((job >> 3) + (t & 7) * PARTS / 8) % PARTS;
+                    // half the scale, so that 7 times it stays finite (exact but for the smallest subnormals)
+                    const uint32_t sc = h2_mul(s2[w] | s2[w] << 16, 0x38003800u);
+                    const uint32_t ws[4] = {w4[w].x, w4[w].y, w4[w].z, w4[w].w};
+                    const uint32_t base = dst + (part / 2) * Z::kChunk + t * 128;
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         const uint32_t lo = ws[x], hi = ws[x] >> 8;
-                        const uint32_t a = base + swizzled(t, (part & 1) * 4 + x);
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(h2_mul(unpack_lo(lo), s2)),
-                                     "r"(h2_mul(unpack_hi(lo), s2)), "r"(h2_mul(unpack_lo(hi), s2)),
-                                     "r"(h2_mul(unpack_hi(hi), s2))
+                        const uint32_t at = base + ((((part & 1) * 4 + x) ^ (t & 7)) << 4);
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(h2_mul(unpack_lo(lo), sc)),
+                                     "r"(h2_mul(unpack_hi(lo), sc)), "r"(h2_mul(unpack_lo(hi), sc)),
+                                     "r"(h2_mul(unpack_hi(hi), sc))
                                      : "memory");
                     }
                 }
@@ -530,24 +561,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     if (is_v) mbar_arrive(smem_u32(&ctl->pk_empty[pk]));
                 }
             };
-            if (g.two) {
-                for (int i = 0; i < n; ++i) {
-                    dequant(i, 0);
-                    dequant(i, 1);
-                }
-            } else {  // in the order of the products: a stream's next scores come before the other's output
+            if (!g.two) {  // in the order of the products: a stream's next scores come before the other's output
                 dequant(0, 0);
                 if (n > 1) dequant(1, 0);
-                for (int i = 0; i < n; ++i) {
-                    dequant(i, 1);
-                    if (i + 2 < n) dequant(i + 2, 0);
-                }
+            }
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                if (g.two) dequant(i, 0);
+                dequant(i, 1);
+                if (!g.two && i + 2 < n) dequant(i + 2, 0);
             }
             n_pk += n;
         }
     } else {
-        regs_less<40>();
-        if (warp == 12) {
+        regs_less<80>();
+        if (warp == 16) {
             // ---- the products
             constexpr uint32_t kIdS = mma_idesc(kTile, kTile, false, false), kIdO = mma_idesc(kTile, D, false, true);
             uint32_t n_ring = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
@@ -559,12 +587,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             };
             auto scores = [&](int s, int q_tile, uint32_t stage) {
                 tc_fence_after();
-                if (lane == 0 && !*stop) {
-                    const uint32_t a = q_s + q_tile * Z::kOperand, b = ring_s + stage * Z::kOperand;
+                if (elect_one() && !*stop) {
+                    const uint32_t a = desc_lo(q_s + q_tile * Z::kOperand, 16), b = desc_lo(ring_s + stage * Z::kOperand, 16);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (k / 4) * Z::kChunk + (k % 4) * 32;
-                        mma_ss(tmem + 128u * s, smem_desc(a + off, 16, 1024), smem_desc(b + off, 16, 1024), kIdS, k > 0);
+                        const uint32_t off = ((k / 4) * Z::kChunk + (k % 4) * 32) >> 4;
+                        mma_ss(tmem + 128u * s, smem_desc(a + off), smem_desc(b + off), kIdS, k > 0);
                     }
                     mma_commit(smem_u32(&ctl->s_full[s]));
                 }
@@ -574,40 +602,42 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 wait_or_stop(smem_u32(&ctl->p_full[s]), n_p[s] & 1, stop, p.status);
                 ++n_p[s];
                 tc_fence_after();
-                if (lane == 0 && !*stop) {
-                    const uint32_t b = ring_s + stage * Z::kOperand;
+                if (elect_one() && !*stop) {
+                    const uint32_t b = desc_lo(ring_s + stage * Z::kOperand, Z::kChunk);
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
-                        mma_ts(tmem + 256u + D * s, tmem + 128u * s + 8 * k, smem_desc(b + k * 2048, Z::kChunk, 1024), kIdO,
+                        mma_ts(tmem + 256u + D * s, tmem + 128u * s + 64 + 8 * k, smem_desc(b + (k * 2048 >> 4)), kIdO,
                                !first || k > 0);
                 }
                 __syncwarp();
             };
             auto commit = [&](uint64_t* bar) {
-                if (lane == 0 && !*stop) mma_commit(smem_u32(bar));
+                if (elect_one() && !*stop) mma_commit(smem_u32(bar));
                 __syncwarp();
             };
             auto wait_q = [&](int s) {
                 wait_or_stop(smem_u32(&ctl->q_full[s]), n_q[s] & 1, stop, p.status);
                 ++n_q[s];
             };
-            Walk walk(p, st);
-            Segment g;
-            while (st.units > 0 && walk.next(g)) {
+            while (st.units > 0 && walk.next(p)) {
                 const int n = g.k1 - g.k0;
                 if (g.two) {
                     uint32_t k = take();
                     wait_q(0);
                     scores(0, 0, k);
+                    if (n == 1) commit(&ctl->q_free[0]);
                     wait_q(1);
                     scores(1, 1, k);
                     commit(&ctl->kv_empty[k]);
+                    if (n == 1) commit(&ctl->q_free[1]);
+#pragma unroll 1
                     for (int i = 0; i < n; ++i) {
                         const uint32_t v = take();
                         output(0, v, i == 0);
                         if (i + 1 < n) {
                             k = take();
                             scores(0, 0, k);
+                            if (i + 2 == n) commit(&ctl->q_free[0]);
                         } else {
                             commit(&ctl->o_done[0]);
                         }
@@ -616,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         if (i + 1 < n) {
                             scores(1, 1, k);
                             commit(&ctl->kv_empty[k]);
+                            if (i + 2 == n) commit(&ctl->q_free[1]);
                         } else {
                             commit(&ctl->o_done[1]);
                         }
@@ -627,6 +658,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         scores(i, 0, k);
                         commit(&ctl->kv_empty[k]);
                     }
+                    if (n <= 2) commit(&ctl->q_free[0]);
+#pragma unroll 1
                     for (int i = 0; i < n; ++i) {
                         const uint32_t v = take();
                         output(i & 1, v, i < 2);
@@ -635,19 +668,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                             const uint32_t k = take();
                             scores(i & 1, 0, k);
                             commit(&ctl->kv_empty[k]);
+                            if (i + 3 == n) commit(&ctl->q_free[0]);
                         } else {
                             commit(&ctl->o_done[i & 1]);
                         }
                     }
                 }
             }
-        } else if (warp == 13) {
+        } else if (warp == 17) {
             // ---- packed pages
             uint32_t n_pk = 0;
             const int per = kTile >> p.lg_p;  // pages of a tile
-            Walk walk(p, st);
-            Segment g;
-            while (st.units > 0 && walk.next(g)) {
+            while (st.units > 0 && walk.next(p)) {
                 const int pages = (max(g.vis, 0) + (1 << p.lg_p) - 1) >> p.lg_p;  // the item's
                 const int32_t* table = p.block_table + static_cast<long long>(g.b) * p.max_blocks;
                 int base = g.k0 * per;  // lane l holds page base + l, and the one 32 later
@@ -685,11 +717,55 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             // no copy of this CTA may be in flight when it leaves
             for (uint32_t i = n_pk > kPacked ? n_pk - kPacked : 0; i < n_pk; ++i)
                 mbar_wait(smem_u32(&ctl->pk_full[i % kPacked]), (i / kPacked) & 1, 250000000ull);
+        } else {
+            // ---- the queries of stream qs, their dimensions in the order the unpack leaves
+            constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes of a row, rows a warp takes at a time
+            constexpr int BATCH = 8;
+            const int qs = warp - 18;
+            uint32_t n_q = 0;
+            while (st.units > 0 && walk.next(p)) {
+                if (!g.two && qs == 1) continue;
+                const int tok1 = g.tokens - qs * p.T;  // tokens of the stream's row tile: rows below r times that
+                const int rows = min(tok1, p.T) * p.r;
+                const __half* src = p.q + (static_cast<long long>(g.row0 + g.tok0 + qs * p.T) * p.Hq + g.h * p.r) * D;
+                const int piece = lane % LPR;
+                uint4 x[BATCH];
+                auto load = [&](int r0) {
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) {
+                        const int row = r0 + i * RPW + lane / LPR;
+                        const int tok = row / p.r;
+                        x[i] = make_uint4(0, 0, 0, 0);
+                        if (row < rows)
+                            x[i] = __ldg(reinterpret_cast<const uint4*>(src + (static_cast<long long>(tok) * p.Hq + row - tok * p.r) * D) +
+                                         piece);
+                    }
+                };
+                load(0);
+                if (n_q > 0) wait_or_stop(smem_u32(&ctl->q_free[qs]), (n_q - 1) & 1, stop, p.status);
+                ++n_q;
+#pragma unroll 1
+                for (int r0 = 0; r0 < kTile; r0 += BATCH * RPW) {
+                    if (r0 > 0) load(r0);
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) {
+                        const int row = r0 + i * RPW + lane / LPR;
+                        const uint32_t at = q_s + qs * Z::kOperand + (piece / 8) * Z::kChunk + swizzled(row, piece % 8);
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(prmt(x[i].x, x[i].z, 0x5410) ^ p.q_flip),
+                                     "r"(prmt(x[i].x, x[i].z, 0x7632) ^ p.q_flip), "r"(prmt(x[i].y, x[i].w, 0x5410) ^ p.q_flip),
+                                     "r"(prmt(x[i].y, x[i].w, 0x7632) ^ p.q_flip)
+                                     : "memory");
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full[qs]));
+            }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 16) {
         tc_fence_after();
         tmem_free(tmem, kTmem);
     }
@@ -797,6 +873,8 @@ cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t stream) {
     p.max_blocks = a.max_blocks;
     p.num_pages = a.num_pages;
     p.lg_p = a.lg_p;
+    p.lg_gk = a.L.Gk == 32 ? 5 : a.L.Gk == 64 ? 6 : 7;
+    p.lg_gv = a.L.Gv == 32 ? 5 : a.L.Gv == 64 ? 6 : 7;
     const long long table = static_cast<long long>(a.max_blocks) << a.lg_p;
     p.most = static_cast<int32_t>(table < a.max_len ? table : a.max_len);
     // (at least 1e-30: a hidden score is -infinity, which zero times is not a number)
