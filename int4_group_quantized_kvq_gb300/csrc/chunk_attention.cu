@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const Segment& g = walk.g;
 
     if (warp < 8) {
-        regs_more<152>();
+        regs_more<136>();
         // ---- softmax of stream sw, row `row` of the stream's row tile
         const int sw = warp / 4;
         const int row = threadIdx.x & 127;
@@ -317,43 +317,37 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 wait_or_stop(smem_u32(&ctl->s_full[sw]), n_s & 1, stop, p.status);
                 ++n_s;
                 tc_fence_after();
-                // Two passes over the scores: the maximum, then the weights.  128 scores in registers spill (and a
-                // spill goes to L2, shared memory leaving no L1 to speak of), so half of them are read twice
+                // Two passes over the scores, 64 columns at a time: the maximum, then the weights.  (128 scores in
+                // registers at once would spill, and a spill goes to L2, shared memory leaving no L1 to speak of.)
+                // The loops are not unrolled further: five warps with five programs share a scheduler, and longer
+                // code keeps them waiting for instructions
                 const bool part = __any_sync(0xffffffffu, seen < kTile);
-                auto hide = [&](uint32_t (&v)[32], int x) {
+                uint32_t a[32], b[32];
+                auto fetch = [&](int x) {
+                    tmem_ld32(s_t + 64 * x, a);
+                    tmem_ld32(s_t + 64 * x + 32, b);
+                    tmem_wait_ld();
+                    tmem_touch(a);
+                    tmem_touch(b);
                     if (part) {
+                        const int to = seen - 64 * x;
 #pragma unroll
-                        for (int y = 0; y < 32; ++y)
-                            if (32 * x + y >= seen) v[y] = 0xff800000u;
+                        for (int y = 0; y < 32; ++y) {
+                            if (y >= to) a[y] = 0xff800000u;
+                            if (32 + y >= to) b[y] = 0xff800000u;
+                        }
                     }
                 };
                 float top0 = -INFINITY, top1 = -INFINITY;
-                auto top_of = [&](const uint32_t (&v)[32]) {
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x) {
+                    fetch(x);
 #pragma unroll
-                    for (int y = 0; y < 32; y += 4) {
-                        top0 = fmaxf(fmaxf(top0, __uint_as_float(v[y])), __uint_as_float(v[y + 1]));
-                        top1 = fmaxf(fmaxf(top1, __uint_as_float(v[y + 2])), __uint_as_float(v[y + 3]));
+                    for (int y = 0; y < 32; y += 2) {
+                        top0 = fmaxf(fmaxf(top0, __uint_as_float(a[y])), __uint_as_float(a[y + 1]));
+                        top1 = fmaxf(fmaxf(top1, __uint_as_float(b[y])), __uint_as_float(b[y + 1]));
                     }
-                };
-                uint32_t a[32], b[32], c[32];
-                tmem_ld32(s_t, a);
-                tmem_ld32(s_t + 32, b);
-                tmem_wait_ld();
-                tmem_touch(a);
-                tmem_touch(b);
-                tmem_ld32(s_t + 64, c);
-                hide(a, 0);
-                top_of(a);
-                hide(b, 1);
-                top_of(b);
-                tmem_ld32(s_t + 96, a);
-                tmem_wait_ld();
-                tmem_touch(c);
-                tmem_touch(a);
-                hide(c, 2);
-                top_of(c);
-                hide(a, 3);
-                top_of(a);
+                }
                 const float top = fmaxf(top0, top1);
                 // The reference follows the maximum only when that is more than 2^8 above it (weights then stay
                 // below 2^8, far inside f16): the output is rescaled a few times a row instead of every tile
@@ -376,34 +370,34 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 m = m_new;
                 begun = true;
                 const float off = m == -INFINITY ? 0.f : -m * p.c;
-                float sum0 = 0.f, sum1 = 0.f;
-                // weights of columns 32 x .. , two to a column, to columns 64 + 16 x ..: over scores that are in
-                // registers by now
-                auto weigh = [&](const uint32_t (&v)[32], int x) {
-                    uint32_t w[16];
+                const uint64_t c2 = pair_of(p.c, p.c), off2 = pair_of(off, off);
+                uint64_t sums = 0, sums1 = 0;  // two sums each
+                // the second half first: the weights, two to a column, go to columns 64 .. 127, over scores that
+                // are in registers by now
+#pragma unroll 1
+                for (int x = 1; x >= 0; --x) {
+                    fetch(x);
+                    auto weigh = [&](uint32_t (&v)[32], uint64_t& sum, uint32_t to) {
+                        uint32_t w[16];
 #pragma unroll
-                    for (int y = 0; y < 16; ++y) {
-                        const float p0 = fast_exp2(fmaf(__uint_as_float(v[2 * y]), p.c, off));
-                        const float p1 = fast_exp2(fmaf(__uint_as_float(v[2 * y + 1]), p.c, off));
-                        sum0 += p0;
-                        sum1 += p1;
-                        w[y] = pack_h2(p0, p1);
-                    }
-                    tmem_st16(s_t + 64 + 16 * x, w);
-                };
-                weigh(c, 2);
-                tmem_ld32(s_t, b);
-                weigh(a, 3);
-                tmem_wait_ld();
-                tmem_touch(b);
-                tmem_ld32(s_t + 32, c);
-                hide(b, 0);
-                weigh(b, 0);
-                tmem_wait_ld();
-                tmem_touch(c);
-                hide(c, 1);
-                weigh(c, 1);
-                l += sum0 + sum1;
+                        for (int y = 0; y < 16; ++y) {
+                            const uint64_t z = fma_pair(pair_of(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1])), c2, off2);
+                            float p0, p1;
+                            split_pair(z, p0, p1);
+                            p0 = fast_exp2(p0);
+                            p1 = fast_exp2(p1);
+                            sum = add_pair(sum, pair_of(p0, p1));
+                            w[y] = pack_h2(p0, p1);
+                        }
+                        tmem_st16(to, w);
+                    };
+                    weigh(a, sums, s_t + 64 + 32 * x);
+                    weigh(b, sums1, s_t + 80 + 32 * x);
+                }
+                float l0, l1, l2, l3;
+                split_pair(sums, l0, l1);
+                split_pair(sums1, l2, l3);
+                l += (l0 + l1) + (l2 + l3);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -495,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             }
         }
     } else if (warp < 8 + kDqWarps) {
-        regs_less<48>();
+        regs_less<64>();
         // ---- dequantize
         constexpr int PARTS = D / 32;  // 16-byte pieces of a row's codes
         const int dw = warp - 8;
@@ -561,15 +555,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     if (is_v) mbar_arrive(smem_u32(&ctl->pk_empty[pk]));
                 }
             };
-            if (!g.two) {  // in the order of the products: a stream's next scores come before the other's output
-                dequant(0, 0);
-                if (n > 1) dequant(1, 0);
-            }
+            // in the order of the products.  Two row tiles: K0 V0 K1 V1 ..; one, whose streams' next scores come
+            // before the other's output: K0 K1 V0 K2 V1 ..
+            const bool two = g.two;
 #pragma unroll 1
-            for (int i = 0; i < n; ++i) {
-                if (g.two) dequant(i, 0);
-                dequant(i, 1);
-                if (!g.two && i + 2 < n) dequant(i + 2, 0);
+            for (int t = 0; t < 2 * n; ++t) {
+                int i = t >> 1, is_v = t & 1;
+                if (!two && t < 2 * n - 1) {
+                    is_v = t >= 2 && !(t & 1);
+                    i = t < 2 ? t : t & 1 ? (t + 1) >> 1 : (t - 2) >> 1;
+                }
+                dequant(i, is_v);
             }
             n_pk += n;
         }
@@ -587,12 +583,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             };
             auto scores = [&](int s, int q_tile, uint32_t stage) {
                 tc_fence_after();
+                const uint32_t a = uniform(desc_lo(q_s + q_tile * Z::kOperand, 16)), b = uniform(desc_lo(ring_s + stage * Z::kOperand, 16));
+                const uint32_t d = uniform(tmem + 128u * s);
                 if (elect_one() && !*stop) {
-                    const uint32_t a = desc_lo(q_s + q_tile * Z::kOperand, 16), b = desc_lo(ring_s + stage * Z::kOperand, 16);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t off = ((k / 4) * Z::kChunk + (k % 4) * 32) >> 4;
-                        mma_ss(tmem + 128u * s, smem_desc(a + off), smem_desc(b + off), kIdS, k > 0);
+                        mma_ss(d, smem_desc(a + off), smem_desc(b + off), kIdS, k > 0);
                     }
                     mma_commit(smem_u32(&ctl->s_full[s]));
                 }
@@ -602,11 +599,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 wait_or_stop(smem_u32(&ctl->p_full[s]), n_p[s] & 1, stop, p.status);
                 ++n_p[s];
                 tc_fence_after();
+                const uint32_t a = uniform(tmem + 128u * s + 64), d = uniform(tmem + 256u + D * s);
+                const uint32_t b = uniform(desc_lo(ring_s + stage * Z::kOperand, Z::kChunk));
                 if (elect_one() && !*stop) {
-                    const uint32_t b = desc_lo(ring_s + stage * Z::kOperand, Z::kChunk);
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
-                        mma_ts(tmem + 256u + D * s, tmem + 128u * s + 64 + 8 * k, smem_desc(b + (k * 2048 >> 4)), kIdO,
+                        mma_ts(d, a + 8 * k, smem_desc(b + (k * 2048 >> 4)), kIdO,
                                !first || k > 0);
                 }
                 __syncwarp();
