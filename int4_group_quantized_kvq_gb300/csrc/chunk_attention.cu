@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
         const uint32_t s_t = tmem + lanes + 128u * sw, o_t = tmem + lanes + 256u;
         const int tok_in = row / p.r;  // token within the row tile
-        uint32_t n_s = 0, n_o[2] = {0, 0};
+        uint32_t n_s = 0, par_o = 0;  // bit s: the phase of stream s's o_done
         while (st.units > 0 && walk.next(p)) {
             const int n = g.k1 - g.k0;
             const int tok = (g.two ? sw * p.T : 0) + tok_in;          // token of the item
@@ -427,9 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 __syncwarp();
             };
             if (g.two) {
-                wait_or_stop(smem_u32(&ctl->o_done[sw]), n_o[sw] & 1, stop, p.status);
-                ++n_o[0];
-                ++n_o[1];
+                wait_or_stop(smem_u32(&ctl->o_done[sw]), (par_o >> sw) & 1, stop, p.status);
+                par_o ^= 3u;
                 tc_fence_after();
                 const float inv = l > 0.f ? 2.f / l : 0.f;
 #pragma unroll 1
@@ -448,11 +447,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             } else {
                 // both streams hold a part of the same rows: lane by lane the same tensor-memory lane
                 const bool both = n > 1;
-                wait_or_stop(smem_u32(&ctl->o_done[0]), n_o[0] & 1, stop, p.status);
-                ++n_o[0];
+                wait_or_stop(smem_u32(&ctl->o_done[0]), par_o & 1, stop, p.status);
+                par_o ^= 1u;
                 if (both) {
-                    wait_or_stop(smem_u32(&ctl->o_done[1]), n_o[1] & 1, stop, p.status);
-                    ++n_o[1];
+                    wait_or_stop(smem_u32(&ctl->o_done[1]), par_o >> 1, stop, p.status);
+                    par_o ^= 2u;
                 }
                 tc_fence_after();
                 ctl->ml[sw][row][0] = m;
@@ -574,18 +573,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         if (warp == 16) {
             // ---- the products
             constexpr uint32_t kIdS = mma_idesc(kTile, kTile, false, false), kIdO = mma_idesc(kTile, D, false, true);
-            uint32_t n_ring = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+            // (The path between two products has as few trips to shared memory as can be: each takes 250 cycles in
+            // the traffic of the other warps, as long as the MMAs still queued.)
+            const uint32_t tm = uniform(tmem);
+            bool live = true;  // false once a wait has been given up: nothing more is issued
+            uint32_t n_ring = 0, par_q = 0, par_p = 0;  // bit s: the phase of stream s's barrier
             auto take = [&]() -> uint32_t {  // the next operand tile, in order
                 const uint32_t stage = n_ring % kRing;
-                wait_or_stop(smem_u32(&ctl->kv_full[stage]), (n_ring / kRing) & 1, stop, p.status);
+                live &= wait_or_stop(smem_u32(&ctl->kv_full[stage]), (n_ring / kRing) & 1, stop, p.status);
                 ++n_ring;
                 return stage;
             };
             auto scores = [&](int s, int q_tile, uint32_t stage) {
                 tc_fence_after();
-                const uint32_t a = uniform(desc_lo(q_s + q_tile * Z::kOperand, 16)), b = uniform(desc_lo(ring_s + stage * Z::kOperand, 16));
-                const uint32_t d = uniform(tmem + 128u * s);
-                if (elect_one() && !*stop) {
+                const uint32_t a = desc_lo(q_s + q_tile * Z::kOperand, 16), b = desc_lo(ring_s + stage * Z::kOperand, 16);
+                const uint32_t d = tm + 128u * s;
+                if (elect_one() && live) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t off = ((k / 4) * Z::kChunk + (k % 4) * 32) >> 4;
@@ -596,12 +599,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 __syncwarp();
             };
             auto output = [&](int s, uint32_t stage, bool first) {
-                wait_or_stop(smem_u32(&ctl->p_full[s]), n_p[s] & 1, stop, p.status);
-                ++n_p[s];
+                live &= wait_or_stop(smem_u32(&ctl->p_full[s]), (par_p >> s) & 1, stop, p.status);
+                par_p ^= 1u << s;
                 tc_fence_after();
-                const uint32_t a = uniform(tmem + 128u * s + 64), d = uniform(tmem + 256u + D * s);
-                const uint32_t b = uniform(desc_lo(ring_s + stage * Z::kOperand, Z::kChunk));
-                if (elect_one() && !*stop) {
+                const uint32_t a = tm + 128u * s + 64, d = tm + 256u + D * s;
+                const uint32_t b = desc_lo(ring_s + stage * Z::kOperand, Z::kChunk);
+                if (elect_one() && live) {
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
                         mma_ts(d, a + 8 * k, smem_desc(b + (k * 2048 >> 4)), kIdO,
@@ -610,66 +613,37 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 __syncwarp();
             };
             auto commit = [&](uint64_t* bar) {
-                if (elect_one() && !*stop) mma_commit(smem_u32(bar));
+                if (elect_one() && live) mma_commit(smem_u32(bar));
                 __syncwarp();
             };
             auto wait_q = [&](int s) {
-                wait_or_stop(smem_u32(&ctl->q_full[s]), n_q[s] & 1, stop, p.status);
-                ++n_q[s];
+                live &= wait_or_stop(smem_u32(&ctl->q_full[s]), (par_q >> s) & 1, stop, p.status);
+                par_q ^= 1u << s;
             };
-            while (st.units > 0 && walk.next(p)) {
-                const int n = g.k1 - g.k0;
-                if (g.two) {
-                    uint32_t k = take();
-                    wait_q(0);
-                    scores(0, 0, k);
-                    if (n == 1) commit(&ctl->q_free[0]);
-                    wait_q(1);
-                    scores(1, 1, k);
-                    commit(&ctl->kv_empty[k]);
-                    if (n == 1) commit(&ctl->q_free[1]);
+            while (uniform(st.units > 0 && walk.next(p))) {
+                const int n = uniform(g.k1 - g.k0);
+                const bool two = uniform(g.two);
+                // Two row tiles: turn (i, s) is the output of stream s with value tile i, then its scores with key tile
+                // i + 1.  One: turn i is stream i % 2's output with value tile i and its scores with key tile i + 2.
+                // (One loop, so one copy of the code; it starts with the turns that have scores alone.)
+                const int ahead = two ? 1 : 2;
+                uint32_t k = 0, v = 0;
 #pragma unroll 1
-                    for (int i = 0; i < n; ++i) {
-                        const uint32_t v = take();
-                        output(0, v, i == 0);
-                        if (i + 1 < n) {
-                            k = take();
-                            scores(0, 0, k);
-                            if (i + 2 == n) commit(&ctl->q_free[0]);
-                        } else {
-                            commit(&ctl->o_done[0]);
-                        }
-                        output(1, v, i == 0);
-                        commit(&ctl->kv_empty[v]);
-                        if (i + 1 < n) {
-                            scores(1, 1, k);
-                            commit(&ctl->kv_empty[k]);
-                            if (i + 2 == n) commit(&ctl->q_free[1]);
-                        } else {
-                            commit(&ctl->o_done[1]);
-                        }
+                for (int turn = -2; turn < (two ? 2 * n : n); ++turn) {
+                    const int i = two ? turn >> 1 : turn, s = turn & 1;
+                    const bool first = !two || s == 0, last = !two || s == 1;  // of the turns that share a tile
+                    if (i >= 0) {
+                        if (first) v = take();
+                        output(s, v, i < (two ? 1 : 2));
+                        if (last) commit(&ctl->kv_empty[v]);
+                        if (i + ahead >= n) commit(&ctl->o_done[s]);
                     }
-                } else {
-                    wait_q(0);
-                    for (int i = 0; i < min(n, 2); ++i) {
-                        const uint32_t k = take();
-                        scores(i, 0, k);
-                        commit(&ctl->kv_empty[k]);
-                    }
-                    if (n <= 2) commit(&ctl->q_free[0]);
-#pragma unroll 1
-                    for (int i = 0; i < n; ++i) {
-                        const uint32_t v = take();
-                        output(i & 1, v, i < 2);
-                        commit(&ctl->kv_empty[v]);
-                        if (i + 2 < n) {
-                            const uint32_t k = take();
-                            scores(i & 1, 0, k);
-                            commit(&ctl->kv_empty[k]);
-                            if (i + 3 == n) commit(&ctl->q_free[0]);
-                        } else {
-                            commit(&ctl->o_done[i & 1]);
-                        }
+                    if (i + ahead < n) {
+                        if (first) k = take();
+                        if (two ? i < 0 : turn == -2) wait_q(two ? s : 0);
+                        scores(s, two ? s : 0, k);
+                        if (last) commit(&ctl->kv_empty[k]);
+                        if (i + ahead + 1 == n) commit(&ctl->q_free[two ? s : 0]);
                     }
                 }
             }

@@ -51,8 +51,8 @@ __device__ __forceinline__ bool elect_one() {
     return one != 0;
 }
 
-// A value that is the same in the whole warp, made known as such: it is held in a uniform register from
-// here on, where each MMA would else convert its operands again (60 to 95 cycles an MMA to issue).
+// A value that is the same in the whole warp, made known as such to the compiler (what follows from such
+// values alone is computed in uniform registers, where the MMAs take their operands from).
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // D[tmem] (+)= A[smem] B[smem], 16 along K; by one thread.
@@ -154,10 +154,11 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
                  : "memory");
     return done != 0;
 }
-__device__ __forceinline__ void wait_or_stop(uint32_t bar, uint32_t parity, volatile int* stop, uint32_t* status) {
-    if (!mbar_try(bar, parity)) {
+__device__ __forceinline__ bool wait_or_stop(uint32_t bar, uint32_t parity, volatile int* stop, uint32_t* status) {
+    bool there = mbar_try(bar, parity);
+    if (!there) {
         uint64_t t0 = 0;
-        for (uint32_t tries = 1; !mbar_try(bar, parity); ++tries) {
+        for (uint32_t tries = 1; !(there = mbar_try(bar, parity)); ++tries) {
             if (tries % 64) continue;  // (the timer is slow to read: a short wait never does)
             if (*stop) break;
             const uint64_t t = global_timer_ns();
@@ -168,7 +169,7 @@ __device__ __forceinline__ void wait_or_stop(uint32_t bar, uint32_t parity, vola
             }
         }
     }
-    __syncwarp();
+    return __all_sync(0xffffffffu, there);  // false: given up
 }
 
 }  // namespace kvq
