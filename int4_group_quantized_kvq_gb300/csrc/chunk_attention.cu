@@ -14,10 +14,11 @@
 // Warps of a CTA (one per SM):
 //   0-3, 4-7   softmax of stream 0 and 1: a thread has a row.  Scores come from tensor memory, weights go
 //              back there (as the f16 A operand of the second product, over the scores' columns).
-//   8-15       dequantize packed tiles into f16 operand tiles (shared memory, a ring of kRing).
-//   16         issues the MMAs: S = Q K^T (both from shared memory), O += P V (P from tensor memory).
-//   17         copies packed pages into shared memory (bulk copies, a ring of kPacked tiles).
-//   18, 19     the streams' query tiles into shared memory.
+//   8-15       dequantize packed tiles into f16 operand tiles (shared memory, a ring of kRing), and bring the
+//              items' queries there.
+//   16, 17     issue the MMAs of stream 0 and 1: S = Q K^T (both from shared memory), O += P V (P from tensor
+//              memory).  A warp for each, so that one stream's waits and bookkeeping do not hold up the other.
+//   18         copies packed pages into shared memory (bulk copies, a ring of kPacked tiles).
 #include <cuda_fp16.h>
 
 #include <cmath>
@@ -272,11 +273,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(smem_u32(&ctl->kv_full[i]), kDqWarps);
-            mbar_init(smem_u32(&ctl->kv_empty[i]), 1);
+            mbar_init(smem_u32(&ctl->kv_empty[i]), 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&ctl->q_full[i]), 1);
-            mbar_init(smem_u32(&ctl->q_free[i]), 1);
+            mbar_init(smem_u32(&ctl->q_full[i]), kDqWarps);
+            mbar_init(smem_u32(&ctl->q_free[i]), 2 - i);
             mbar_init(smem_u32(&ctl->s_full[i]), 1);
             mbar_init(smem_u32(&ctl->p_full[i]), 4);
             mbar_init(smem_u32(&ctl->o_done[i]), 1);
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         // ---- dequantize
         constexpr int PARTS = D / 32;  // 16-byte pieces of a row's codes
         const int dw = warp - 8;
-        uint32_t n_ring = 0, n_pk = 0;
+        uint32_t n_ring = 0, n_pk = 0, n_q0 = 0, n_q1 = 0;
         while (st.units > 0 && walk.next(p)) {
             const int n = g.k1 - g.k0;
             const int end0 = g.vis - g.k0 * kTile;
@@ -554,6 +555,42 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     if (is_v) mbar_arrive(smem_u32(&ctl->pk_empty[pk]));
                 }
             };
+            // the item's row tile qs into shared memory, its dimensions in the order the unpack leaves (n_q: how many
+            // have been there before)
+            auto queries = [&](int qs, uint32_t n_q) {
+                constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes of a row, rows a warp takes at a time
+                constexpr int LOADS = kTile / (RPW * kDqWarps) / 2;
+                const int rows = min(g.tokens - qs * p.T, p.T) * p.r;
+                const __half* src = p.q + (static_cast<long long>(g.row0 + g.tok0 + qs * p.T) * p.Hq + g.h * p.r) * D;
+                const int piece = lane % LPR;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    const int row0 = half * (kTile / 2) + dw * RPW + lane / LPR;
+                    uint4 x[LOADS];
+#pragma unroll
+                    for (int i = 0; i < LOADS; ++i) {
+                        const int row = row0 + i * RPW * kDqWarps;
+                        const int tok = row / p.r;
+                        x[i] = make_uint4(0, 0, 0, 0);
+                        if (row < rows)
+                            x[i] = __ldg(reinterpret_cast<const uint4*>(src + (static_cast<long long>(tok) * p.Hq + row - tok * p.r) * D) +
+                                         piece);
+                    }
+                    if (n_q > 0 && half == 0) wait_or_stop(smem_u32(&ctl->q_free[qs]), (n_q - 1) & 1, stop, p.status);
+#pragma unroll
+                    for (int i = 0; i < LOADS; ++i) {
+                        const int row = row0 + i * RPW * kDqWarps;
+                        const uint32_t at = q_s + qs * Z::kOperand + (piece / 8) * Z::kChunk + swizzled(row, piece % 8);
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(prmt(x[i].x, x[i].z, 0x5410) ^ p.q_flip),
+                                     "r"(prmt(x[i].x, x[i].z, 0x7632) ^ p.q_flip), "r"(prmt(x[i].y, x[i].w, 0x5410) ^ p.q_flip),
+                                     "r"(prmt(x[i].y, x[i].w, 0x7632) ^ p.q_flip)
+                                     : "memory");
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full[qs]));
+            };
             // in the order of the products.  Two row tiles: K0 V0 K1 V1 ..; one, whose streams' next scores come
             // before the other's output: K0 K1 V0 K2 V1 ..
             const bool two = g.two;
@@ -565,89 +602,99 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     i = t < 2 ? t : t & 1 ? (t + 1) >> 1 : (t - 2) >> 1;
                 }
                 dequant(i, is_v);
+                if (t == 0) {
+                    queries(0, n_q0);
+                    ++n_q0;
+                    if (two) {
+                        queries(1, n_q1);
+                        ++n_q1;
+                    }
+                }
             }
             n_pk += n;
         }
     } else {
         regs_less<80>();
-        if (warp == 16) {
-            // ---- the products
+        if (warp < 18) {
+            // ---- the products of stream sw
             constexpr uint32_t kIdS = mma_idesc(kTile, kTile, false, false), kIdO = mma_idesc(kTile, D, false, true);
             // (The path between two products has as few trips to shared memory as can be: each takes 250 cycles in
             // the traffic of the other warps, as long as the MMAs still queued.)
-            const uint32_t tm = uniform(tmem);
+            const uint32_t tm = uniform(tmem), sw = uniform(warp - 16);
             bool live = true;  // false once a wait has been given up: nothing more is issued
-            uint32_t n_ring = 0, par_q = 0, par_p = 0;  // bit s: the phase of stream s's barrier
+            uint32_t n_ring = 0, n_q0 = 0, n_q1 = 0, n_p = 0;
             auto take = [&]() -> uint32_t {  // the next operand tile, in order
                 const uint32_t stage = n_ring % kRing;
                 live &= wait_or_stop(smem_u32(&ctl->kv_full[stage]), (n_ring / kRing) & 1, stop, p.status);
                 ++n_ring;
+                tc_fence_after();
                 return stage;
-            };
-            auto scores = [&](int s, int q_tile, uint32_t stage) {
-                tc_fence_after();
-                const uint32_t a = desc_lo(q_s + q_tile * Z::kOperand, 16), b = desc_lo(ring_s + stage * Z::kOperand, 16);
-                const uint32_t d = tm + 128u * s;
-                if (elect_one() && live) {
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = ((k / 4) * Z::kChunk + (k % 4) * 32) >> 4;
-                        mma_ss(d, smem_desc(a + off), smem_desc(b + off), kIdS, k > 0);
-                    }
-                    mma_commit(smem_u32(&ctl->s_full[s]));
-                }
-                __syncwarp();
-            };
-            auto output = [&](int s, uint32_t stage, bool first) {
-                live &= wait_or_stop(smem_u32(&ctl->p_full[s]), (par_p >> s) & 1, stop, p.status);
-                par_p ^= 1u << s;
-                tc_fence_after();
-                const uint32_t a = tm + 128u * s + 64, d = tm + 256u + D * s;
-                const uint32_t b = desc_lo(ring_s + stage * Z::kOperand, Z::kChunk);
-                if (elect_one() && live) {
-#pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        mma_ts(d, a + 8 * k, smem_desc(b + (k * 2048 >> 4)), kIdO,
-                               !first || k > 0);
-                }
-                __syncwarp();
-            };
-            auto commit = [&](uint64_t* bar) {
-                if (elect_one() && live) mma_commit(smem_u32(bar));
-                __syncwarp();
-            };
-            auto wait_q = [&](int s) {
-                live &= wait_or_stop(smem_u32(&ctl->q_full[s]), (par_q >> s) & 1, stop, p.status);
-                par_q ^= 1u << s;
             };
             while (uniform(st.units > 0 && walk.next(p))) {
                 const int n = uniform(g.k1 - g.k0);
                 const bool two = uniform(g.two);
-                // Two row tiles: turn (i, s) is the output of stream s with value tile i, then its scores with key tile
-                // i + 1.  One: turn i is stream i % 2's output with value tile i and its scores with key tile i + 2.
-                // (One loop, so one copy of the code; it starts with the turns that have scores alone.)
+                // Two row tiles: turn i is the output with value tile i and the scores with key tile i + 1.  One: the
+                // output with value tile i and the scores with key tile i + 2, of stream i % 2; the other stream lets
+                // the tiles go.  (One loop, so one copy of the code; it starts with turns that have scores alone.)
                 const int ahead = two ? 1 : 2;
-                uint32_t k = 0, v = 0;
+                live &= wait_or_stop(smem_u32(&ctl->q_full[0]), n_q0 & 1, stop, p.status);
+                ++n_q0;
+                if (two && sw == 1) {
+                    live &= wait_or_stop(smem_u32(&ctl->q_full[1]), n_q1 & 1, stop, p.status);
+                    ++n_q1;
+                }
 #pragma unroll 1
-                for (int turn = -2; turn < (two ? 2 * n : n); ++turn) {
-                    const int i = two ? turn >> 1 : turn, s = turn & 1;
-                    const bool first = !two || s == 0, last = !two || s == 1;  // of the turns that share a tile
+                for (int i = -ahead; i < n; ++i) {
+                    const bool mine = two || (i & 1) == static_cast<int>(sw);
                     if (i >= 0) {
-                        if (first) v = take();
-                        output(s, v, i < (two ? 1 : 2));
-                        if (last) commit(&ctl->kv_empty[v]);
-                        if (i + ahead >= n) commit(&ctl->o_done[s]);
+                        const uint32_t stage = take();
+                        if (mine) {
+                            live &= wait_or_stop(smem_u32(&ctl->p_full[sw]), n_p & 1, stop, p.status);
+                            ++n_p;
+                            tc_fence_after();
+                            const uint32_t a = tm + 128u * sw + 64, d = tm + 256u + D * sw;
+                            const uint32_t b = desc_lo(ring_s + stage * Z::kOperand, Z::kChunk);
+                            if (elect_one() && live) {
+                                const bool first = i < ahead;
+#pragma unroll
+                                for (int k = 0; k < kTile / 16; ++k)
+                                    mma_ts(d, a + 8 * k, smem_desc(b + (k * 2048 >> 4)), kIdO, !first || k > 0);
+                                mma_commit(smem_u32(&ctl->kv_empty[stage]));
+                                if (i + ahead >= n) mma_commit(smem_u32(&ctl->o_done[sw]));
+                            }
+                        } else if (elect_one()) {
+                            mbar_arrive(smem_u32(&ctl->kv_empty[stage]));
+                        }
+                        __syncwarp();
                     }
                     if (i + ahead < n) {
-                        if (first) k = take();
-                        if (two ? i < 0 : turn == -2) wait_q(two ? s : 0);
-                        scores(s, two ? s : 0, k);
-                        if (last) commit(&ctl->kv_empty[k]);
-                        if (i + ahead + 1 == n) commit(&ctl->q_free[two ? s : 0]);
+                        const uint32_t stage = take();
+                        if (mine) {
+                            const uint32_t a = desc_lo(q_s + (two ? sw : 0) * Z::kOperand, 16);
+                            const uint32_t b = desc_lo(ring_s + stage * Z::kOperand, 16);
+                            const uint32_t d = tm + 128u * sw;
+                            if (elect_one() && live) {
+#pragma unroll
+                                for (int k = 0; k < D / 16; ++k) {
+                                    const uint32_t off = ((k / 4) * Z::kChunk + (k % 4) * 32) >> 4;
+                                    mma_ss(d, smem_desc(a + off), smem_desc(b + off), kIdS, k > 0);
+                                }
+                                mma_commit(smem_u32(&ctl->s_full[sw]));
+                                mma_commit(smem_u32(&ctl->kv_empty[stage]));
+                            }
+                        } else if (elect_one()) {
+                            mbar_arrive(smem_u32(&ctl->kv_empty[stage]));
+                        }
+                        __syncwarp();
                     }
+                    if (i + ahead + 1 == n && elect_one() && live) {  // no more scores of the item
+                        mma_commit(smem_u32(&ctl->q_free[0]));
+                        if (two && sw == 1) mma_commit(smem_u32(&ctl->q_free[1]));
+                    }
+                    __syncwarp();
                 }
             }
-        } else if (warp == 17) {
+        } else if (warp == 18) {
             // ---- packed pages
             uint32_t n_pk = 0;
             const int per = kTile >> p.lg_p;  // pages of a tile
@@ -689,50 +736,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             // no copy of this CTA may be in flight when it leaves
             for (uint32_t i = n_pk > kPacked ? n_pk - kPacked : 0; i < n_pk; ++i)
                 mbar_wait(smem_u32(&ctl->pk_full[i % kPacked]), (i / kPacked) & 1, 250000000ull);
-        } else {
-            // ---- the queries of stream qs, their dimensions in the order the unpack leaves
-            constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes of a row, rows a warp takes at a time
-            constexpr int BATCH = 8;
-            const int qs = warp - 18;
-            uint32_t n_q = 0;
-            while (st.units > 0 && walk.next(p)) {
-                if (!g.two && qs == 1) continue;
-                const int tok1 = g.tokens - qs * p.T;  // tokens of the stream's row tile: rows below r times that
-                const int rows = min(tok1, p.T) * p.r;
-                const __half* src = p.q + (static_cast<long long>(g.row0 + g.tok0 + qs * p.T) * p.Hq + g.h * p.r) * D;
-                const int piece = lane % LPR;
-                uint4 x[BATCH];
-                auto load = [&](int r0) {
-#pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        const int row = r0 + i * RPW + lane / LPR;
-                        const int tok = row / p.r;
-                        x[i] = make_uint4(0, 0, 0, 0);
-                        if (row < rows)
-                            x[i] = __ldg(reinterpret_cast<const uint4*>(src + (static_cast<long long>(tok) * p.Hq + row - tok * p.r) * D) +
-                                         piece);
-                    }
-                };
-                load(0);
-                if (n_q > 0) wait_or_stop(smem_u32(&ctl->q_free[qs]), (n_q - 1) & 1, stop, p.status);
-                ++n_q;
-#pragma unroll 1
-                for (int r0 = 0; r0 < kTile; r0 += BATCH * RPW) {
-                    if (r0 > 0) load(r0);
-#pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        const int row = r0 + i * RPW + lane / LPR;
-                        const uint32_t at = q_s + qs * Z::kOperand + (piece / 8) * Z::kChunk + swizzled(row, piece % 8);
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(prmt(x[i].x, x[i].z, 0x5410) ^ p.q_flip),
-                                     "r"(prmt(x[i].x, x[i].z, 0x7632) ^ p.q_flip), "r"(prmt(x[i].y, x[i].w, 0x5410) ^ p.q_flip),
-                                     "r"(prmt(x[i].y, x[i].w, 0x7632) ^ p.q_flip)
-                                     : "memory");
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full[qs]));
-            }
         }
     }
     tc_fence_before();
