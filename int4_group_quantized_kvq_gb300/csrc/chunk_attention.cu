@@ -150,7 +150,7 @@ struct Walk {
 struct Ctl {
     uint64_t pk_full[kPacked], pk_empty[kPacked];
     uint64_t kv_full[kRing], kv_empty[kRing];
-    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2];
+    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], turn;
     long long warp_sum[kThreads / 32];
     Start start;
     uint32_t tmem;
@@ -282,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             mbar_init(smem_u32(&ctl->p_full[i]), 4);
             mbar_init(smem_u32(&ctl->o_done[i]), 1);
         }
+        mbar_init(smem_u32(&ctl->turn), 1);
         ctl->stop = 0;
         fence_mbar_init();
     }
@@ -622,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             // the traffic of the other warps, as long as the MMAs still queued.)
             const uint32_t tm = uniform(tmem), sw = uniform(warp - 16);
             bool live = true;  // false once a wait has been given up: nothing more is issued
-            uint32_t n_ring = 0, n_q0 = 0, n_q1 = 0, n_p = 0;
+            uint32_t n_ring = 0, n_q0 = 0, n_q1 = 0, n_p = 0, n_turn = 0;
             auto take = [&]() -> uint32_t {  // the next operand tile, in order
                 const uint32_t stage = n_ring % kRing;
                 live &= wait_or_stop(smem_u32(&ctl->kv_full[stage]), (n_ring / kRing) & 1, stop, p.status);
@@ -633,10 +634,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             while (uniform(st.units > 0 && walk.next(p))) {
                 const int n = uniform(g.k1 - g.k0);
                 const bool two = uniform(g.two);
-                // Two row tiles: turn i is the output with value tile i and the scores with key tile i + 1.  One: the
-                // output with value tile i and the scores with key tile i + 2, of stream i % 2; the other stream lets
-                // the tiles go.  (One loop, so one copy of the code; it starts with turns that have scores alone.)
-                const int ahead = two ? 1 : 2;
+                // Two row tiles: turn i is the output with value tile i and the scores with key tile i + 1, of both
+                // streams.  One: the output with value tile i and the scores with key tile i + 2, of stream i % 2; the
+                // other stream lets the tiles go.  (It starts with turns that have scores alone.)
+                // The streams issue in turn, a turn's products as one block: the streams' softmaxes then alternate
+                // with the products.  Mixed products would end together, and then both softmaxes run at once while
+                // the tensor cores wait.
+                // Turns alternate strictly (stream 1 takes an empty one behind an odd number of alternating tiles): a
+                // stream that waits for the other's turn has then seen the one before it.
+                const int ahead = two ? 1 : 2, turns = two ? n : n + (n & 1);
                 live &= wait_or_stop(smem_u32(&ctl->q_full[0]), n_q0 & 1, stop, p.status);
                 ++n_q0;
                 if (two && sw == 1) {
@@ -644,48 +650,46 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     ++n_q1;
                 }
 #pragma unroll 1
-                for (int i = -ahead; i < n; ++i) {
+                for (int i = -ahead; i < turns; ++i) {
                     const bool mine = two || (i & 1) == static_cast<int>(sw);
-                    if (i >= 0) {
-                        const uint32_t stage = take();
-                        if (mine) {
+                    const bool out = i >= 0 && i < n, in = i + ahead < n;
+                    const uint32_t v = out ? take() : 0, k = in ? take() : 0;
+                    if (mine) {
+                        if (out) {
                             live &= wait_or_stop(smem_u32(&ctl->p_full[sw]), n_p & 1, stop, p.status);
                             ++n_p;
-                            tc_fence_after();
-                            const uint32_t a = tm + 128u * sw + 64, d = tm + 256u + D * sw;
-                            const uint32_t b = desc_lo(ring_s + stage * Z::kOperand, Z::kChunk);
-                            if (elect_one() && live) {
+                        }
+                        const uint32_t turn = n_turn + (two ? 2 * (i + 1) + sw : i + 2);
+                        if (turn > 0) live &= wait_or_stop(smem_u32(&ctl->turn), (turn - 1) & 1, stop, p.status);
+                        tc_fence_after();
+                        if (elect_one()) {
+                            if (live && out) {
+                                const uint32_t a = tm + 128u * sw + 64, d = tm + 256u + D * sw;
+                                const uint32_t b = desc_lo(ring_s + v * Z::kOperand, Z::kChunk);
                                 const bool first = i < ahead;
 #pragma unroll
-                                for (int k = 0; k < kTile / 16; ++k)
-                                    mma_ts(d, a + 8 * k, smem_desc(b + (k * 2048 >> 4)), kIdO, !first || k > 0);
-                                mma_commit(smem_u32(&ctl->kv_empty[stage]));
-                                if (i + ahead >= n) mma_commit(smem_u32(&ctl->o_done[sw]));
+                                for (int x = 0; x < kTile / 16; ++x)
+                                    mma_ts(d, a + 8 * x, smem_desc(b + (x * 2048 >> 4)), kIdO, !first || x > 0);
+                                mma_commit(smem_u32(&ctl->kv_empty[v]));
+                                if (!in) mma_commit(smem_u32(&ctl->o_done[sw]));
                             }
-                        } else if (elect_one()) {
-                            mbar_arrive(smem_u32(&ctl->kv_empty[stage]));
-                        }
-                        __syncwarp();
-                    }
-                    if (i + ahead < n) {
-                        const uint32_t stage = take();
-                        if (mine) {
-                            const uint32_t a = desc_lo(q_s + (two ? sw : 0) * Z::kOperand, 16);
-                            const uint32_t b = desc_lo(ring_s + stage * Z::kOperand, 16);
-                            const uint32_t d = tm + 128u * sw;
-                            if (elect_one() && live) {
+                            if (live && in) {
+                                const uint32_t a = desc_lo(q_s + (two ? sw : 0) * Z::kOperand, 16);
+                                const uint32_t b = desc_lo(ring_s + k * Z::kOperand, 16);
+                                const uint32_t d = tm + 128u * sw;
 #pragma unroll
-                                for (int k = 0; k < D / 16; ++k) {
-                                    const uint32_t off = ((k / 4) * Z::kChunk + (k % 4) * 32) >> 4;
-                                    mma_ss(d, smem_desc(a + off), smem_desc(b + off), kIdS, k > 0);
+                                for (int x = 0; x < D / 16; ++x) {
+                                    const uint32_t off = ((x / 4) * Z::kChunk + (x % 4) * 32) >> 4;
+                                    mma_ss(d, smem_desc(a + off), smem_desc(b + off), kIdS, x > 0);
                                 }
                                 mma_commit(smem_u32(&ctl->s_full[sw]));
-                                mma_commit(smem_u32(&ctl->kv_empty[stage]));
+                                mma_commit(smem_u32(&ctl->kv_empty[k]));
                             }
-                        } else if (elect_one()) {
-                            mbar_arrive(smem_u32(&ctl->kv_empty[stage]));
+                            mbar_arrive(smem_u32(&ctl->turn));
                         }
-                        __syncwarp();
+                    } else if (elect_one()) {
+                        if (out) mbar_arrive(smem_u32(&ctl->kv_empty[v]));
+                        if (in) mbar_arrive(smem_u32(&ctl->kv_empty[k]));
                     }
                     if (i + ahead + 1 == n && elect_one() && live) {  // no more scores of the item
                         mma_commit(smem_u32(&ctl->q_free[0]));
@@ -693,6 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     }
                     __syncwarp();
                 }
+                n_turn += two ? 2 * (n + 1) : turns + 2;
             }
         } else if (warp == 18) {
             // ---- packed pages
