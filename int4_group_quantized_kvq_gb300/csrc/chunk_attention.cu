@@ -26,6 +26,7 @@
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
 #include "kvq_tcgen05.cuh"
+#include "kvq_units.cuh"
 
 namespace kvq {
 namespace {
@@ -34,117 +35,19 @@ constexpr int kThreads = 640;
 constexpr int kDqWarps = 8;
 constexpr int kRing = 3;      // operand tiles (K or V) in shared memory
 constexpr int kPacked = 3;    // packed tiles in shared memory
-constexpr int kTile = 128;    // rows of M, positions of a tile
 constexpr uint32_t kTmem = 512;
-constexpr int kItemUnits = 2;  // what an item costs a CTA besides its tiles (queries in, output out), in units
 
-// Where a CTA's run of units starts, and how long it is.
-struct Start {
-    int b, h, j, k;
-    long long units;
-};
-
-// Merging of an item whose units lie in several CTAs, described by the CTA of its second part.
-struct MergeDesc {
-    int32_t parts;  // 0: nothing to merge
-    int32_t row0, tokens, h;
-};
-
-struct ChunkParams {
+struct ChunkParams : Units {  // an item: the tokens of two row tiles
     const uint8_t* pool;
     const __half* q;
     const int32_t* block_table;
-    const int32_t* seq_lens;
-    const int32_t* cu_rows;
     __half* out;
-    uint32_t* status;
-    MergeDesc* desc;  // [gridDim.x]
     float* part_ml;   // [2 gridDim.x][256][2]: maximum (of scale log2(e) z) and sum
     float* part_o;    // [2 gridDim.x][256][D]
-    int32_t rows, B, Hq, Hkv, r, T, max_blocks, num_pages, lg_p, lg_gk, lg_gv, most;  // T: tokens of a row tile; most: longest sequence
+    int32_t Hq, Hkv, r, T, max_blocks, num_pages, lg_p, lg_gk, lg_gv;  // T: tokens of a row tile
     float c;          // 2 |scale| log2(e): keys are held halved
     uint32_t q_flip;  // sign bits of a negative scale
     BlockLayout L;
-};
-
-struct Seq {
-    int row0, n, len;  // first row, rows, positions
-};
-__device__ __forceinline__ Seq sequence(const ChunkParams& p, int b) {
-    Seq s;
-    const int c0 = min(max(__ldg(p.cu_rows + b), 0), p.rows), c1 = min(max(__ldg(p.cu_rows + b + 1), 0), p.rows);
-    s.row0 = c0;
-    s.n = max(0, c1 - c0);
-    s.len = min(max(__ldg(p.seq_lens + b), 0), p.most);
-    return s;
-}
-// Positions the last row of item j can see, and the item's tiles (one at least: rows that see nothing
-// are written too).
-__device__ __forceinline__ int visible(const ChunkParams& p, const Seq& s, int j) {
-    return s.len - s.n + static_cast<int>(min(static_cast<long long>(j + 1) * 2 * p.T, static_cast<long long>(s.n)));
-}
-__device__ __forceinline__ int tiles_of(int vis) { return max(1, (vis + kTile - 1) / kTile); }
-
-// A segment: the tiles [k0, k1) of one item.
-struct Segment {
-    int b, h, k0, k1, nt, vis, tokens, tok0;
-    int row0, ahead;  // the sequence's first row, and positions before that row's
-    bool two;         // a second row tile (else the streams alternate)
-};
-
-// Walks a CTA's segments; every role walks the same ones.  The state lies in shared memory, a copy for
-// each warp: kept in registers it would cost the softmax warps two dozen.
-struct Walk {
-    long long left;
-    int b, h, j, k;
-    Seq s;
-    Segment g;
-    __device__ __forceinline__ void begin(const ChunkParams& p, const Start& st) {
-        left = st.units;
-        b = st.b;
-        h = st.h;
-        j = st.j;
-        k = st.k;
-        s = sequence(p, b);
-        __syncwarp();
-    }
-    __device__ __forceinline__ bool next(const ChunkParams& p) {
-        __syncwarp();
-        long long room = left;
-        int cj = j, ch = h, cb = b;
-        const int ck = k;
-        Seq cs = s;
-        if (room <= 0) return false;
-        const int step = 2 * p.T;
-        if (cj * static_cast<long long>(step) >= cs.n) {  // the next head or sequence
-            cj = 0;
-            if (++ch == p.Hkv) {
-                ch = 0;
-                do {
-                    if (++cb >= p.B) return false;
-                    cs = sequence(p, cb);
-                } while (cs.n == 0);
-            }
-        }
-        const int vis = visible(p, cs, cj), nt = tiles_of(vis);
-        if (ck == 0) room -= kItemUnits;
-        const int k1 = static_cast<int>(min(static_cast<long long>(nt), ck + room));
-        __syncwarp();
-        if (k1 <= ck) {  // not a tile of it
-            left = 0;
-            return false;
-        }
-        const int tok0 = cj * step, tokens = min(step, cs.n - tok0);
-        g = Segment{cb, ch, ck, k1, nt, vis, tokens, tok0, cs.row0, cs.len - cs.n, tokens > p.T};
-        left = room - (k1 - ck);
-        k = 0;
-        j = cj + 1;
-        h = ch;
-        b = cb;
-        s = cs;
-        __syncwarp();
-        return true;
-    }
 };
 
 struct Ctl {
@@ -158,89 +61,6 @@ struct Ctl {
     Walk walk[kThreads / 32];
     float ml[2][kTile][2];
 };
-
-// The CTA's run of units: all threads.  The list is (sequence, kv head, item, tile); a thread counts the
-// units of a sequence per kv head.
-__device__ __forceinline__ void find_start(const ChunkParams& p, Ctl* ctl) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
-    auto count = [&](int b) -> long long {
-        if (b >= p.B) return 0;
-        const Seq s = sequence(p, b);
-        long long u = 0;
-        for (int j = 0; j * 2ll * p.T < s.n; ++j) u += tiles_of(visible(p, s, j)) + kItemUnits;
-        if (u > 0 && blockIdx.x == 0 && __ldg(p.seq_lens + b) > p.most) raise_flag(p.status, KVQ_FLAG_BAD_POSITION);
-        return u * p.Hkv;
-    };
-    long long mine = 0, first = 0;
-    for (int b = tid; b < p.B; b += kThreads) {
-        const long long u = count(b);
-        if (b == tid) first = u;
-        mine += u;
-    }
-    auto block_scan = [&](long long v, long long& total) -> long long {  // inclusive
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long t = __shfl_up_sync(0xffffffffu, v, off);
-            if (lane >= off) v += t;
-        }
-        if (lane == 31) ctl->warp_sum[warp] = v;
-        __syncthreads();
-        long long before = 0;
-        total = 0;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            const long long t = ctl->warp_sum[w];
-            if (w < warp) before += t;
-            total += t;
-        }
-        __syncthreads();
-        return v + before;
-    };
-    long long U;
-    block_scan(mine, U);
-    const long long C = min(static_cast<long long>(gridDim.x), U);
-    const long long cta = blockIdx.x;
-    if (tid == 0) {
-        ctl->start = Start{0, 0, 0, 0, 0};
-        p.desc[cta].parts = 0;
-    }
-    __syncthreads();
-    if (cta >= C) return;
-    const long long u0 = cta * U / C, u1 = (cta + 1) * U / C;
-    long long base = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-        const long long v = b0 == 0 ? first : count(b0 + tid);
-        long long total;
-        const long long incl = base + block_scan(v, total), excl = incl - v;
-        if (u0 >= excl && u0 < incl) {  // one thread
-            const int b = b0 + tid;
-            const Seq s = sequence(p, b);
-            const long long per = v / p.Hkv;
-            const int h = static_cast<int>((u0 - excl) / per);
-            long long rem = u0 - excl - h * per;
-            int j = 0, nt;
-            while (true) {
-                nt = tiles_of(visible(p, s, j));
-                if (rem < nt + kItemUnits) break;
-                rem -= nt + kItemUnits;
-                ++j;
-            }
-            // a boundary within an item's first kItemUnits leaves all its tiles to this CTA
-            const long long i0 = u0 - rem + kItemUnits;  // where the item's tiles start in the list
-            const int k = static_cast<int>(max(0ll, u0 - i0));
-            ctl->start = Start{b, h, j, k, u1 - (k > 0 ? u0 : i0 - kItemUnits)};
-            // this CTA starts inside an item: is its part the item's second one?
-            if (k > 0 && (cta - 1) * U / C <= i0) {
-                int parts = 1;
-                for (long long c = cta; c < C && c * U / C < i0 + nt; ++c) ++parts;
-                p.desc[cta] = MergeDesc{parts, s.row0 + j * 2 * p.T, min(2 * p.T, s.n - j * 2 * p.T), h};
-            }
-        }
-        base += total;
-        if (base > u0) break;
-    }
-    __syncthreads();
-}
 
 template <int D>
 struct Sizes {
@@ -289,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     if (warp == 16) tmem_alloc(smem_u32(&ctl->tmem), kTmem);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     tc_fence_before();
-    find_start(p, ctl);  // (has barriers of the CTA)
+    find_start<kThreads>(p, &ctl->start, ctl->warp_sum);  // (has barriers of the CTA)
     tc_fence_after();
     const uint32_t tmem = ctl->tmem;
     const Start st = ctl->start;
@@ -309,13 +129,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         uint32_t n_s = 0, par_o = 0;  // bit s: the phase of stream s's o_done
         while (st.units > 0 && walk.next(p)) {
             const int n = g.k1 - g.k0;
-            const int tok = (g.two ? sw * p.T : 0) + tok_in;          // token of the item
-            const bool valid = tok_in < p.T && tok < g.tokens;
-            int seen = valid ? g.ahead + g.tok0 + tok + 1 - g.k0 * kTile : 0;  // columns the row sees, from tile k0 on
+            const bool two = g.lines > p.T;                    // a second row tile (else the streams alternate)
+            const int tok = (two ? sw * p.T : 0) + tok_in;     // token of the item
+            const bool valid = tok_in < p.T && tok < g.lines;
+            int seen = valid ? g.ahead + g.line0 + tok + 1 - g.k0 * kTile : 0;  // columns the row sees, from tile k0 on
             float m = -INFINITY, l = 0.f;  // the maximum the weights are taken against (of z / scale), their sum
             bool begun = false;
-            if (!g.two && sw == 1) seen -= kTile;
-            for (int i = g.two ? 0 : sw; i < n; i += g.two ? 1 : 2, seen -= g.two ? kTile : 2 * kTile) {
+            if (!two && sw == 1) seen -= kTile;
+            for (int i = two ? 0 : sw; i < n; i += two ? 1 : 2, seen -= two ? kTile : 2 * kTile) {
                 wait_or_stop(smem_u32(&ctl->s_full[sw]), n_s & 1, stop, p.status);
                 ++n_s;
                 tc_fence_after();
@@ -407,11 +228,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             }
             // ---- the segment's result
             const bool whole = g.k0 == 0 && g.k1 == g.nt;
-            const int slot = 2 * blockIdx.x + (g.k0 == 0 ? 1 : 0);
-            const int prow = (g.two ? sw * kTile : 0) + row;  // row of a partial result
+            const int slot = partial_slot(g);
+            const int prow = (two ? sw * kTile : 0) + row;  // row of a partial result
             float* pml = p.part_ml + (static_cast<long long>(slot) * 256 + prow) * 2;
             float* po = p.part_o + (static_cast<long long>(slot) * 256 + prow) * D;
-            __half* out = p.out + (static_cast<long long>(g.row0 + g.tok0 + tok) * p.Hq + g.h * p.r + (row - tok_in * p.r)) * D;
+            __half* out = p.out + (static_cast<long long>(g.row0 + g.line0 + tok) * p.Hq + g.h * p.r + (row - tok_in * p.r)) * D;
             auto put = [&](const uint32_t (&o)[32], int x, float f) {  // 32 columns of the row
                 if (valid && whole) {
 #pragma unroll
@@ -428,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 }
                 __syncwarp();
             };
-            if (g.two) {
+            if (two) {
                 wait_or_stop(smem_u32(&ctl->o_done[sw]), (par_o >> sw) & 1, stop, p.status);
                 par_o ^= 3u;
                 tc_fence_after();
@@ -490,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             }
         }
     } else if (warp < 8 + kDqWarps) {
-        regs_less<64>();
+        regs_less<72>();
         // ---- dequantize
         constexpr int PARTS = D / 32;  // 16-byte pieces of a row's codes
         const int dw = warp - 8;
@@ -503,8 +324,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 const uint32_t stage = n_ring % kRing, phase = n_ring / kRing;
                 const uint32_t pk = (n_pk + i) % kPacked;
                 if (is_v == 0) wait_or_stop(smem_u32(&ctl->pk_full[pk]), ((n_pk + i) / kPacked) & 1, stop, p.status);
-                if (n_ring >= kRing) wait_or_stop(smem_u32(&ctl->kv_empty[stage]), (phase & 1) ^ 1, stop, p.status);
-                ++n_ring;
                 const uint8_t* src = smem + Z::kQ + kRing * Z::kOperand + pk * packed_bytes;
                 const uint32_t dst = ring_s + stage * Z::kOperand;
                 const int lg_g = is_v ? p.lg_gv : p.lg_gk;
@@ -512,40 +331,48 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 const int end = end0 - i * kTile;  // tokens of the tile that exist
                 const int mask = (1 << p.lg_p) - 1;
                 constexpr int JOBS = kTile * PARTS / (32 * kDqWarps);
-                uint4 w4[JOBS];
-                uint32_t s2[JOBS];
+                // 8 tokens x 4 pieces a warp: eight lanes of a piece read 128 bytes apart by rows (no bank twice)
+                // and write 8 rows' swizzled pieces (no bank twice)
+                uint32_t f[JOBS][16];
 #pragma unroll
                 for (int w = 0; w < JOBS; ++w) {
-                    // 8 tokens x 4 pieces a warp: eight lanes of a piece read 128 bytes apart by rows (no bank
-                    // twice) and write 8 rows' swizzled pieces (no bank twice)
                     const int job = (w * kDqWarps + dw) * 32 + lane;
                     const int t = (job / (8 * PARTS)) * 8 + (job & 7);
                     const int part = ((job >> 3) + (t & 7) * PARTS / 8) % PARTS;
                     const uint8_t* blk = src + (t >> p.lg_p) * p.L.bytes;
                     const int slot = t & mask;
-                    w4[w] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-                    s2[w] = 0;
+                    uint4 w4 = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+                    uint32_t s2 = 0;
                     if (t < end) {
-                        w4[w] = *reinterpret_cast<const uint4*>(blk + codes_off + slot * (D / 2) + part * 16);
-                        s2[w] = *reinterpret_cast<const uint16_t*>(blk + scales_off + (((slot * D + part * 32) >> lg_g) << 1));
+                        w4 = *reinterpret_cast<const uint4*>(blk + codes_off + slot * (D / 2) + part * 16);
+                        s2 = *reinterpret_cast<const uint16_t*>(blk + scales_off + (((slot * D + part * 32) >> lg_g) << 1));
+                    }
+                    // half the scale, so that 7 times it stays finite (exact but for the smallest subnormals)
+                    const uint32_t sc = h2_mul(s2 | s2 << 16, 0x38003800u);
+                    const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t lo = ws[x], hi = ws[x] >> 8;
+                        f[w][4 * x] = h2_mul(unpack_lo(lo), sc);
+                        f[w][4 * x + 1] = h2_mul(unpack_hi(lo), sc);
+                        f[w][4 * x + 2] = h2_mul(unpack_lo(hi), sc);
+                        f[w][4 * x + 3] = h2_mul(unpack_hi(hi), sc);
                     }
                 }
+                // only now the operand tile has to be free: the products wait for the stores alone
+                if (n_ring >= kRing) wait_or_stop(smem_u32(&ctl->kv_empty[stage]), (phase & 1) ^ 1, stop, p.status);
+                ++n_ring;
 #pragma unroll
                 for (int w = 0; w < JOBS; ++w) {
                     const int job = (w * kDqWarps + dw) * 32 + lane;
                     const int t = (job / (8 * PARTS)) * 8 + (job & 7);
                     const int part = ((job >> 3) + (t & 7) * PARTS / 8) % PARTS;
-                    // half the scale, so that 7 times it stays finite (exact but for the smallest subnormals)
-                    const uint32_t sc = h2_mul(s2[w] | s2[w] << 16, 0x38003800u);
-                    const uint32_t ws[4] = {w4[w].x, w4[w].y, w4[w].z, w4[w].w};
                     const uint32_t base = dst + (part / 2) * Z::kChunk + t * 128;
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const uint32_t lo = ws[x], hi = ws[x] >> 8;
                         const uint32_t at = base + ((((part & 1) * 4 + x) ^ (t & 7)) << 4);
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(h2_mul(unpack_lo(lo), sc)),
-                                     "r"(h2_mul(unpack_hi(lo), sc)), "r"(h2_mul(unpack_lo(hi), sc)),
-                                     "r"(h2_mul(unpack_hi(hi), sc))
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(f[w][4 * x]),
+                                     "r"(f[w][4 * x + 1]), "r"(f[w][4 * x + 2]), "r"(f[w][4 * x + 3])
                                      : "memory");
                     }
                 }
@@ -561,8 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             auto queries = [&](int qs, uint32_t n_q) {
                 constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes of a row, rows a warp takes at a time
                 constexpr int LOADS = kTile / (RPW * kDqWarps) / 2;
-                const int rows = min(g.tokens - qs * p.T, p.T) * p.r;
-                const __half* src = p.q + (static_cast<long long>(g.row0 + g.tok0 + qs * p.T) * p.Hq + g.h * p.r) * D;
+                const int rows = min(g.lines - qs * p.T, p.T) * p.r;
+                const __half* src = p.q + (static_cast<long long>(g.row0 + g.line0 + qs * p.T) * p.Hq + g.h * p.r) * D;
                 const int piece = lane % LPR;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
@@ -594,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             };
             // in the order of the products.  Two row tiles: K0 V0 K1 V1 ..; one, whose streams' next scores come
             // before the other's output: K0 K1 V0 K2 V1 ..
-            const bool two = g.two;
+            const bool two = g.lines > p.T;
 #pragma unroll 1
             for (int t = 0; t < 2 * n; ++t) {
                 int i = t >> 1, is_v = t & 1;
@@ -615,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             n_pk += n;
         }
     } else {
-        regs_less<80>();
+        regs_less<64>();
         if (warp < 18) {
             // ---- the products of stream sw
             constexpr uint32_t kIdS = mma_idesc(kTile, kTile, false, false), kIdO = mma_idesc(kTile, D, false, true);
@@ -633,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             };
             while (uniform(st.units > 0 && walk.next(p))) {
                 const int n = uniform(g.k1 - g.k0);
-                const bool two = uniform(g.two);
+                const bool two = uniform(g.lines > p.T);
                 // Two row tiles: turn i is the output with value tile i and the scores with key tile i + 1, of both
                 // streams.  One: the output with value tile i and the scores with key tile i + 2, of stream i % 2; the
                 // other stream lets the tiles go.  (It starts with turns that have scores alone.)
@@ -760,7 +587,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant_
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
     const int c = blockIdx.x;
-    for (int i = blockIdx.y * 8 + threadIdx.x / 32; i < d.tokens * p.r; i += 8 * gridDim.y) {
+    for (int i = blockIdx.y * 8 + threadIdx.x / 32; i < d.lines * p.r; i += 8 * gridDim.y) {
         const int tok = i / p.r, g = i - tok * p.r;
         const int prow = (tok / p.T) * kTile + (tok % p.T) * p.r + g;
         float m = -INFINITY, l = 0.f, o[E];
@@ -781,7 +608,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant_
         }
         const float inv = l > 0.f ? 2.f / l : 0.f;
         // columns E lane .. of the 8 that share 16 bytes; dimension order 0 4 1 5 2 6 3 7
-        __half* out = p.out + (static_cast<long long>(d.row0 + tok) * p.Hq + d.h * p.r + g) * D;
+        __half* out = p.out + (static_cast<long long>(d.line0 + tok) * p.Hq + d.h * p.r + g) * D;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const int col = lane * E + e, x = col & 7;
@@ -850,6 +677,9 @@ cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t stream) {
     p.Hkv = a.Hkv;
     p.r = a.Hq / a.Hkv;
     p.T = kTile / p.r;
+    p.heads = a.Hkv;
+    p.per_row = 1;
+    p.step = 2 * p.T;
     p.max_blocks = a.max_blocks;
     p.num_pages = a.num_pages;
     p.lg_p = a.lg_p;

@@ -1,0 +1,214 @@
+// kvq_units.cuh -- how the attention kernels over ragged batches of rows share their work out: equal runs
+// of units per CTA, items cut between CTAs, and where their partial results meet.
+//
+// A sequence has n rows (the last n of its len positions), each of per_row lines (query heads that read
+// one key/value head, where the kernel's items are counted in those); an item is `step` lines of one
+// (sequence, key/value head), and a unit one tile of 128 positions that an item attends to.  The list of
+// units is ordered (sequence, head, item, tile).
+#pragma once
+
+#include <cstdint>
+
+#include "kvq_device.cuh"
+
+namespace kvq {
+
+constexpr int kTile = 128;     // positions of a tile
+constexpr int kItemUnits = 2;  // what an item costs a CTA besides its tiles (queries in, output out), in units
+
+// Where a CTA's run of units starts, and how long it is.
+struct Start {
+    int b, h, j, k;
+    long long units;
+};
+
+// Merging of an item whose units lie in several CTAs, described by the CTA of its second part.
+struct MergeDesc {
+    int32_t parts;  // 0: nothing to merge
+    int32_t line0, lines, h;  // line0 counts all rows' lines
+};
+
+struct Units {
+    const int32_t* seq_lens;
+    const int32_t* cu_rows;
+    uint32_t* status;
+    MergeDesc* desc;  // [gridDim.x]
+    int32_t rows, B, heads, per_row, step;
+    int32_t most;  // the longest sequence
+};
+
+struct Seq {
+    int row0, n, len;  // first row, rows, positions
+};
+__device__ __forceinline__ Seq sequence(const Units& p, int b) {
+    Seq s;
+    const int c0 = min(max(__ldg(p.cu_rows + b), 0), p.rows), c1 = min(max(__ldg(p.cu_rows + b + 1), 0), p.rows);
+    s.row0 = c0;
+    s.n = max(0, c1 - c0);
+    s.len = min(max(__ldg(p.seq_lens + b), 0), p.most);
+    return s;
+}
+// (rows times lines are below 2^31)
+__device__ __forceinline__ uint32_t lines_of(const Units& p, const Seq& s) { return static_cast<uint32_t>(s.n) * p.per_row; }
+// Positions the last line of item j can see, and the item's tiles (one at least: rows that see nothing
+// are written too).
+__device__ __forceinline__ int visible(const Units& p, const Seq& s, uint32_t j) {
+    uint32_t end = min((j + 1) * p.step, lines_of(p, s));
+    if (p.per_row != 1) end = (end + p.per_row - 1) / p.per_row;
+    return s.len - s.n + static_cast<int>(end);
+}
+__device__ __forceinline__ int tiles_of(int vis) { return max(1, (vis + kTile - 1) / kTile); }
+
+// A segment: the tiles [k0, k1) of one item.
+struct Segment {
+    int b, h, k0, k1, nt, vis;
+    int line0, lines;  // within the sequence
+    int row0, ahead;   // the sequence's first row, and positions before that row's
+};
+
+// Walks a CTA's segments; every role walks the same ones.  The state lies in shared memory, a copy for
+// each warp: kept in registers it would cost each two dozen.
+struct Walk {
+    long long left;
+    int b, h, j, k;
+    Seq s;
+    Segment g;
+    __device__ __forceinline__ void begin(const Units& p, const Start& st) {
+        left = st.units;
+        b = st.b;
+        h = st.h;
+        j = st.j;
+        k = st.k;
+        s = sequence(p, b);
+        __syncwarp();
+    }
+    __device__ __forceinline__ bool next(const Units& p) {
+        __syncwarp();
+        long long room = left;
+        int cj = j, ch = h, cb = b;
+        const int ck = k;
+        Seq cs = s;
+        if (room <= 0) return false;
+        if (static_cast<uint32_t>(cj) * p.step >= lines_of(p, cs)) {  // the next head or sequence
+            cj = 0;
+            if (++ch == p.heads) {
+                ch = 0;
+                do {
+                    if (++cb >= p.B) return false;
+                    cs = sequence(p, cb);
+                } while (cs.n == 0);
+            }
+        }
+        const int vis = visible(p, cs, cj), nt = tiles_of(vis);
+        if (ck == 0) room -= kItemUnits;
+        const int k1 = static_cast<int>(min(static_cast<long long>(nt), ck + room));
+        __syncwarp();
+        if (k1 <= ck) {  // not a tile of it
+            left = 0;
+            return false;
+        }
+        const int line0 = cj * p.step;
+        g = Segment{cb, ch, ck, k1, nt, vis, line0, min(p.step, static_cast<int>(lines_of(p, cs)) - line0), cs.row0,
+                    cs.len - cs.n};
+        left = room - (k1 - ck);
+        k = 0;
+        j = cj + 1;
+        h = ch;
+        b = cb;
+        s = cs;
+        __syncwarp();
+        return true;
+    }
+};
+
+// The CTA's run of units: all threads (with barriers of the CTA).  A thread counts the units of a sequence
+// per head.  warp_sum: THREADS / 32 numbers in shared memory.
+template <int THREADS>
+__device__ __forceinline__ void find_start(const Units& p, Start* start, long long* warp_sum) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+    auto count = [&](int b) -> long long {
+        if (b >= p.B) return 0;
+        const Seq s = sequence(p, b);
+        long long u = 0;
+        for (uint32_t j = 0; j * p.step < lines_of(p, s); ++j) u += tiles_of(visible(p, s, j)) + kItemUnits;
+        if (u > 0 && blockIdx.x == 0 && __ldg(p.seq_lens + b) > p.most) raise_flag(p.status, KVQ_FLAG_BAD_POSITION);
+        return u * p.heads;
+    };
+    long long mine = 0, first = 0;
+    for (int b = tid; b < p.B; b += THREADS) {
+        const long long u = count(b);
+        if (b == tid) first = u;
+        mine += u;
+    }
+    auto block_scan = [&](long long v, long long& total) -> long long {  // inclusive
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, v, off);
+            if (lane >= off) v += t;
+        }
+        if (lane == 31) warp_sum[warp] = v;
+        __syncthreads();
+        long long before = 0;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) {
+            const long long t = warp_sum[w];
+            if (w < warp) before += t;
+            total += t;
+        }
+        __syncthreads();
+        return v + before;
+    };
+    long long U;
+    block_scan(mine, U);
+    const long long C = min(static_cast<long long>(gridDim.x), U);
+    const long long cta = blockIdx.x;
+    if (tid == 0) {
+        *start = Start{0, 0, 0, 0, 0};
+        p.desc[cta].parts = 0;
+    }
+    __syncthreads();
+    if (cta >= C) return;
+    const long long u0 = cta * U / C, u1 = (cta + 1) * U / C;
+    long long base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += THREADS) {
+        const long long v = b0 == 0 ? first : count(b0 + tid);
+        long long total;
+        const long long incl = base + block_scan(v, total), excl = incl - v;
+        if (u0 >= excl && u0 < incl) {  // one thread
+            const int b = b0 + tid;
+            const Seq s = sequence(p, b);
+            const long long per = v / p.heads;
+            const int h = static_cast<int>((u0 - excl) / per);
+            long long rem = u0 - excl - h * per;
+            int j = 0, nt;
+            while (true) {
+                nt = tiles_of(visible(p, s, j));
+                if (rem < nt + kItemUnits) break;
+                rem -= nt + kItemUnits;
+                ++j;
+            }
+            // a boundary within an item's first kItemUnits leaves all its tiles to this CTA
+            const long long i0 = u0 - rem + kItemUnits;  // where the item's tiles start in the list
+            const int k = static_cast<int>(max(0ll, u0 - i0));
+            *start = Start{b, h, j, k, u1 - (k > 0 ? u0 : i0 - kItemUnits)};
+            // this CTA starts inside an item: is its part the item's second one?
+            if (k > 0 && (cta - 1) * U / C <= i0) {
+                int parts = 1;
+                for (long long c = cta; c < C && c * U / C < i0 + nt; ++c) ++parts;
+                p.desc[cta] = MergeDesc{parts, s.row0 * p.per_row + j * p.step,
+                                        min(p.step, static_cast<int>(lines_of(p, s)) - j * p.step), h};
+            }
+        }
+        base += total;
+        if (base > u0) break;
+    }
+    __syncthreads();
+}
+
+// The slot of a CTA's partial result of a segment: slot 0 where it starts inside an item, else slot 1 (its
+// last segment).  The parts of a cut item are slot 1 of the CTA ahead of the descriptor's and slot 0 of
+// the descriptor's and those behind it.
+__device__ __forceinline__ int partial_slot(const Segment& g) { return 2 * blockIdx.x + (g.k0 == 0 ? 1 : 0); }
+
+}  // namespace kvq

@@ -1,81 +1,662 @@
 // latent_attention.cu -- attention whose keys and values are one shared latent vector per token
-// (absorbed form), over the packed latent cache.
+// (absorbed form), over the packed latent cache, on the tcgen05 tensor cores.
+//
+// For a line (a row's query head) at position p:  z_t = scale (q_l . c_t + q_r . k_t),
+// o = sum_{t <= p} softmax(z)_t c_t, with c_t the latent (4 bits, dequantized) and k_t the rotary key.
+//
+// Tiles.  Both products are formed transposed, positions and latent dimensions along M:
+//   S^T [128 positions, NC lines]  = [C R] [Q_l Q_r]^T        (K = latent and rotary dimensions)
+//   O^T [128 dimensions, NC lines] += C^T P^T, L / 128 times  (K = positions)
+// so that the lines are a column count of 16, 32 or 64 (a decode step of 16 heads fills 16 columns, not 16
+// of 128 rows), the output of 64 lines takes L / 128 x 64 = 256 of tensor memory's 512 columns, and one
+// dequantized tile serves both products: rows of 64 dimensions are a K-major operand of the first and an
+// MN-major one of the second.  A tile of 128 positions is 144 KB in shared memory and single: its groups
+// of 128 dimensions are refilled one by one as the second product lets them go.
+//
+// Warps of a CTA (one per SM):
+//   0-3    softmax: a thread has a position, its scores of all lines in registers.
+//   4-11   dequantize: two threads a position; packed rows go from memory to registers a tile ahead.
+//   12     issues the MMAs.
+// Work is shared out as in kvq_units.cuh; an item is NC lines of one sequence.
 #include <cuda_fp16.h>
 
 #include <cmath>
 
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
-#include "kvq_rows.cuh"
+#include "kvq_tcgen05.cuh"
+#include "kvq_units.cuh"
 
 namespace kvq {
 namespace {
 
-// One warp per (row, query head): a lane holds L / 32 latent values and two of the rotary part.
-template <int L>
-__global__ void __launch_bounds__(256) latent_kernel(LatentAttnArgs a) {
-    constexpr int E = L / 32, R = 64;
-    uint32_t* status = reinterpret_cast<uint32_t*>(a.workspace);
-    const int lane = threadIdx.x & 31;
-    const long long tasks = static_cast<long long>(a.rows) * a.H;
-    const long long warps = static_cast<long long>(gridDim.x) * 8;
-    for (long long task = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / 32; task < tasks; task += warps) {
-        const int row = static_cast<int>(task / a.H);
-        const int b = warp_find_seq(a.cu_rows, a.B, row, lane);
-        if (b < 0) continue;
-        const int most = static_cast<int>(min(static_cast<long long>(a.max_len), static_cast<long long>(a.max_blocks) << a.lg_p));
-        int len = a.seq_lens[b];
-        if (len > most) {
-            if (lane == 0) raise_flag(status, KVQ_FLAG_BAD_POSITION);
-            len = most;
+constexpr int kThreads = 512;
+constexpr int kDqWarps = 8;
+constexpr int kRope = 64;              // rotary dimensions
+constexpr int kChunk = kTile * 128;    // bytes of a chunk [128][64] f16
+
+struct LatentParams : Units {  // per_row: query heads
+    const uint8_t* pool;
+    const __half* q;
+    const int32_t* block_table;
+    __half* out;
+    float* part_ml;  // [2 gridDim.x][NC][2]: maximum (of scale log2(e) z) and sum
+    float* part_o;   // [2 gridDim.x][NC][L]
+    int32_t max_blocks, num_pages, lg_p, lg_g;
+    float c;          // 2 |scale| log2(e): latents are held halved, and so are the rotary queries
+    uint32_t q_flip;  // sign bits of a negative scale
+    LatentLayout lay;
+};
+
+template <int L, int NC>
+struct Shape {
+    static constexpr int kChunks = L / 64 + 1;             // the last one: rotary keys
+    static constexpr int kGroups = L / 128;                // pairs of latent chunks; the rotary chunk is one more
+    static constexpr int kQChunk = NC * 128;               // bytes of a chunk of queries [NC][64] f16
+    static constexpr int kQ = kChunks * kQChunk;
+    static constexpr int kK = kChunks * kChunk;
+    // weights [128][NC] f16 in rows of 128 bytes: in place of the rotary keys where memory is short (the scores are
+    // complete by the time there are weights)
+    static constexpr bool kOwnP = kQ + kK + kChunk + 8192 <= 231424;
+    static constexpr int kBytes = kQ + kK + (kOwnP ? kChunk : 0);
+    static constexpr uint32_t kS = kGroups * NC;           // tensor memory: outputs, then scores
+    static constexpr uint32_t kTmem = kS + NC <= 128 ? 128 : kS + NC <= 256 ? 256 : 512;
+};
+
+template <int NC>
+struct Ctl {
+    uint64_t full[5], free[5];  // groups of latent chunks, then the rotary chunk (the weights, where they share)
+    uint64_t q_full, q_free, s_full, p_full, o_done;
+    long long warp_sum[kThreads / 32];
+    Start start;
+    uint32_t tmem;
+    int stop;
+    Walk walk[13];
+    alignas(16) float off[NC];    // -(reference maximum) c, by line
+    alignas(16) float scale[NC];  // factors of a rescaling, or of the output
+    float m[NC];                  // reference maximum of the scores (of z / scale)
+    int lim[NC];                  // positions a line sees
+    float part[4][NC];            // by warp
+};
+
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Barrier of the softmax warps that tells whether any thread's x holds.
+__device__ __forceinline__ bool any_of_softmax(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, 2, 128, p; selp.u32 %0, 1, 0, q; }"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(x))
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void softmax_barrier() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
+// Sums over the warp's lanes of N values each: halving the values a lane keeps at each exchange, N - 1
+// shuffles and a few.  Afterwards v[0 .. max(1, N / 32)) of a lane belong to the columns from first_column.
+template <int N>
+__device__ __forceinline__ void warp_sums(float (&v)[N], int lane) {
+    int n = N;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        if (n > 1) {
+            n /= 2;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                if (i >= n) break;
+                const float keep = lane & off ? v[i + n] : v[i], send = lane & off ? v[i] : v[i + n];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+            }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
         }
-        // (offsets that do not ascend must not lead behind the sequence)
-        const int pos = min(max(len, 0) - 1, max(len, 0) - (a.cu_rows[b + 1] - a.cu_rows[b]) + (row - a.cu_rows[b]));
-        const __half* qr = a.q + task * (L + R);
-        float q[E], o[E], qp[2];
-        for (int i = 0; i < E; ++i) {
-            q[i] = __half2float(qr[lane * E + i]) * a.softmax_scale;
-            o[i] = 0.f;
+    }
+}
+template <int N>
+__device__ __forceinline__ int first_column(int lane) {
+    int n = N, c = 0;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        if (n > 1) {
+            n /= 2;
+            if (lane & off) c += n;
         }
-        for (int i = 0; i < 2; ++i) qp[i] = __half2float(qr[L + 2 * lane + i]) * a.softmax_scale;
-        float m = -INFINITY, l = 0.f;
-        for (int t = 0; t <= pos; ++t) {
-            int page = a.block_table[static_cast<long long>(b) * a.max_blocks + (t >> a.lg_p)];
-            if (page < 0 || page >= a.num_pages) {
-                if (lane == 0) raise_flag(status, KVQ_FLAG_BAD_PAGE);
+    return c;
+}
+
+template <int NC>
+__device__ __forceinline__ void load_columns(uint32_t addr, uint32_t (&v)[NC]) {
+    if constexpr (NC == 16) tmem_ld16(addr, v);
+    if constexpr (NC >= 32) tmem_ld32(addr, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+    if constexpr (NC == 64) tmem_ld32(addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[NC == 64 ? 32 : 0]));
+    tmem_wait_ld();
+    tmem_touch(v);
+}
+
+// The dimension at position x (of 8) in the order the unpack leaves.
+__device__ __forceinline__ int dim_of(int x) { return (x & ~7) + ((x & 7) >> 1) + 4 * (x & 1); }
+
+template <int L, int NC>
+__global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_constant__ LatentParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    using Z = Shape<L, NC>;
+    constexpr int G = Z::kGroups;
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t k_s = smem_u32(smem), q_s = k_s + Z::kK;
+    const uint32_t p_s = Z::kOwnP ? q_s + Z::kQ : k_s + (Z::kChunks - 1) * kChunk;
+    Ctl<NC>* ctl = reinterpret_cast<Ctl<NC>*>(smem + Z::kBytes);
+    volatile int* stop = &ctl->stop;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 5; ++i) {
+            mbar_init(smem_u32(&ctl->full[i]), kDqWarps);
+            mbar_init(smem_u32(&ctl->free[i]), 1);
+        }
+        mbar_init(smem_u32(&ctl->q_full), kDqWarps);
+        mbar_init(smem_u32(&ctl->q_free), 1);
+        mbar_init(smem_u32(&ctl->s_full), 1);
+        mbar_init(smem_u32(&ctl->p_full), 4);
+        mbar_init(smem_u32(&ctl->o_done), 1);
+        ctl->stop = 0;
+        fence_mbar_init();
+    }
+    if (warp == 12) tmem_alloc(smem_u32(&ctl->tmem), Z::kTmem);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    tc_fence_before();
+    find_start<kThreads>(p, &ctl->start, ctl->warp_sum);  // (has barriers of the CTA)
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem;
+    const Start st = ctl->start;
+    Walk& walk = ctl->walk[min(warp, 12)];
+    if (st.units > 0 && warp < 13) walk.begin(p, st);
+    const Segment& g = walk.g;
+
+    if (warp < 4) {
+        regs_more<200>();
+        // ---- softmax: position `t` of a tile; its tensor-memory lane is also a dimension of the outputs
+        const int t = threadIdx.x;
+        const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
+        const uint32_t s_t = tmem + lanes + Z::kS, o_t = tmem + lanes;
+        uint32_t n_tile = 0, n_seg = 0;
+        while (st.units > 0 && walk.next(p)) {
+            const int n = g.k1 - g.k0;
+            if (t < NC) {
+                ctl->lim[t] = g.ahead + (g.line0 + min(t, g.lines - 1)) / p.per_row + 1;
+                ctl->m[t] = -INFINITY;
+                ctl->off[t] = 0.f;
+            }
+            softmax_barrier();
+            const int lim0 = ctl->lim[0];  // the least
+            float l[NC];
+#pragma unroll
+            for (int i = 0; i < NC; ++i) l[i] = 0.f;
+#pragma unroll 1
+            for (int i = 0; i < n; ++i, ++n_tile) {
+                const int pos = (g.k0 + i) * kTile + t;
+                wait_or_stop(smem_u32(&ctl->s_full), n_tile & 1, stop, p.status);
+                tc_fence_after();
+                uint32_t s[NC];
+                load_columns<NC>(s_t, s);
+                if ((g.k0 + i + 1) * kTile > lim0) {
+#pragma unroll
+                    for (int x = 0; x < NC; ++x)
+                        if (pos >= ctl->lim[x]) s[x] = 0xff800000u;
+                }
+                // Are the references still within 2^8 of every score?  (Weights then stay below 2^8, far inside f16,
+                // and nothing is reduced over the positions: of a few hundred tiles a few move a reference)
+                float top = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < NC; x += 4) {
+                    const float4 off = *reinterpret_cast<const float4*>(&ctl->off[x]);
+                    const float a = fmaf(__uint_as_float(s[x]), p.c, off.x), b = fmaf(__uint_as_float(s[x + 1]), p.c, off.y);
+                    const float c = fmaf(__uint_as_float(s[x + 2]), p.c, off.z), d = fmaf(__uint_as_float(s[x + 3]), p.c, off.w);
+                    top = fmaxf(fmaxf(fmaxf(top, a), fmaxf(b, c)), d);
+                }
+                if (any_of_softmax(i == 0 || top > 8.f)) {
+#pragma unroll
+                    for (int x = 0; x < NC; ++x) {
+                        const float r = warp_max(__uint_as_float(s[x]));
+                        if (lane == (x & 31)) ctl->part[warp][x] = r;
+                    }
+                    softmax_barrier();
+                    if (t < NC) {
+                        const float most = fmaxf(fmaxf(ctl->part[0][t], ctl->part[1][t]), fmaxf(ctl->part[2][t], ctl->part[3][t]));
+                        const float m = ctl->m[t];
+                        const float to = m == -INFINITY || (most - m) * p.c > 8.f ? fmaxf(most, m) : m;
+                        ctl->scale[t] = to == m ? 1.f : fast_exp2((m - to) * p.c);
+                        ctl->m[t] = to;
+                        ctl->off[t] = to == -INFINITY ? 0.f : -to * p.c;
+                    }
+                    softmax_barrier();
+                    if (i > 0) {
+#pragma unroll
+                        for (int x = 0; x < NC; ++x) l[x] *= ctl->scale[x];
+#pragma unroll 1
+                        for (int x = 0; x < G * NC / 16; ++x) {  // (the products into O that came before S are complete)
+                            uint32_t o[16];
+                            tmem_ld16(o_t + 16 * x, o);
+                            tmem_wait_ld();
+                            tmem_touch(o);
+                            const float* f = &ctl->scale[16 * x % NC];
+#pragma unroll
+                            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f[y]);
+                            tmem_st16(o_t + 16 * x, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                // the weights, in rows of a position
+#pragma unroll
+                for (int x = 0; x < NC; x += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int y = 0; y < 8; y += 4) {
+                        const float4 off = *reinterpret_cast<const float4*>(&ctl->off[x + y]);
+                        const float a = fast_exp2(fmaf(__uint_as_float(s[x + y]), p.c, off.x));
+                        const float b = fast_exp2(fmaf(__uint_as_float(s[x + y + 1]), p.c, off.y));
+                        const float c = fast_exp2(fmaf(__uint_as_float(s[x + y + 2]), p.c, off.z));
+                        const float d = fast_exp2(fmaf(__uint_as_float(s[x + y + 3]), p.c, off.w));
+                        l[x + y] += a;
+                        l[x + y + 1] += b;
+                        l[x + y + 2] += c;
+                        l[x + y + 3] += d;
+                        w[y / 2] = pack_h2(a, b);
+                        w[y / 2 + 1] = pack_h2(c, d);
+                    }
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(p_s + swizzled(t, x / 8)), "r"(w[0]), "r"(w[1]),
+                                 "r"(w[2]), "r"(w[3])
+                                 : "memory");
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full));
+            }
+            // ---- the segment's result
+            const bool whole = g.k0 == 0 && g.k1 == g.nt;
+            warp_sums<NC>(l, lane);
+            const int col = first_column<NC>(lane);
+            if (NC == 64 || (NC == 32) || (lane & 1) == 0) {
+                ctl->part[warp][col] = l[0];
+                if (NC == 64) ctl->part[warp][col + 1] = l[1];
+            }
+            softmax_barrier();
+            const long long line0 = static_cast<long long>(g.row0) * p.per_row + g.line0;
+            const int slot = partial_slot(g);
+            if (t < NC) {
+                const float sum = (ctl->part[0][t] + ctl->part[1][t]) + (ctl->part[2][t] + ctl->part[3][t]);
+                ctl->scale[t] = !whole ? 1.f : sum > 0.f ? 2.f / sum : 0.f;
+                if (!whole) {
+                    p.part_ml[(static_cast<long long>(slot) * NC + t) * 2] = ctl->m[t] * p.c;
+                    p.part_ml[(static_cast<long long>(slot) * NC + t) * 2 + 1] = sum;
+                }
+            }
+            softmax_barrier();
+            wait_or_stop(smem_u32(&ctl->o_done), n_seg & 1, stop, p.status);
+            ++n_seg;
+            tc_fence_after();
+            const int dim = dim_of(t);
+#pragma unroll 1
+            for (int x = 0; x < G * NC / 16; ++x) {
+                uint32_t o[16];
+                tmem_ld16(o_t + 16 * x, o);
+                tmem_wait_ld();
+                tmem_touch(o);
+                const int c0 = 16 * x % NC, d = 16 * x / NC * 128 + dim;
+                if (whole) {
+#pragma unroll
+                    for (int y = 0; y < 16; ++y)
+                        if (c0 + y < g.lines)
+                            p.out[(line0 + c0 + y) * L + d] = __float2half_rn(__uint_as_float(o[y]) * ctl->scale[c0 + y]);
+                } else {
+                    float* to = p.part_o + (static_cast<long long>(slot) * NC + c0) * L + d;
+#pragma unroll
+                    for (int y = 0; y < 16; ++y)
+                        if (c0 + y < g.lines) to[y * L] = __uint_as_float(o[y]);
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            softmax_barrier();
+        }
+    } else if (warp < 4 + kDqWarps) {
+        regs_less<120>();
+        // ---- dequantize: position `t` of a tile, half `hf` of every 64 dimensions
+        const int tid = threadIdx.x - 128, t = tid >> 1, hf = tid & 1;
+        struct Tile {
+            const int32_t* table;
+            const __half* q;  // the item's queries, where the tile is its first of this CTA (else nullptr)
+            int tile, vis, lines;
+            bool there;
+        };
+        int k = 0, k1 = 0;
+        auto next_tile = [&](Tile& x) {
+            x.q = nullptr;
+            if (++k >= k1) {
+                x.there = walk.next(p);
+                if (!x.there) return;
+                k = g.k0;
+                k1 = g.k1;
+                x.vis = g.vis;
+                x.lines = g.lines;
+                x.table = p.block_table + static_cast<long long>(g.b) * p.max_blocks;
+                x.q = p.q + (static_cast<long long>(g.row0) * p.per_row + g.line0) * (L + kRope);
+            }
+            x.tile = k;
+        };
+        auto page_of = [&](const Tile& x) -> int {  // of this thread's position; -1: behind the sequence
+            const int pos = x.tile * kTile + t;
+            return x.there && pos < x.vis ? __ldg(x.table + (pos >> p.lg_p)) : -1;
+        };
+        // the packed row of a position
+        uint4 codes[L / 64], keys[4];
+        uint32_t scales[L / 128];  // of chunks 2 i and 2 i + 1
+        const uint8_t* src = nullptr;
+        int slot = 0;
+        auto find = [&](const Tile& x, int page) {
+            src = nullptr;
+            if (!x.there || x.tile * kTile + t >= x.vis) return;
+            if (page < 0 || page >= p.num_pages) {
+                raise_flag(p.status, KVQ_FLAG_BAD_PAGE);
                 page = 0;
             }
-            const int slot = t & ((1 << a.lg_p) - 1);
-            const uint8_t* blk = a.pool + static_cast<long long>(page) * a.lay.bytes;
-            const float s = __half2float(reinterpret_cast<const __half*>(blk + a.lay.scales)[slot * (L / a.lay.G) + lane * E / a.lay.G]);
-            const __half* rope = reinterpret_cast<const __half*>(blk + a.lay.rope) + slot * R;
-            float z = qp[0] * __half2float(rope[2 * lane]) + qp[1] * __half2float(rope[2 * lane + 1]), v[E];
-            for (int i = 0; i < E; ++i) {
-                const int at = lane * E + i;
-                v[i] = static_cast<float>(((blk[slot * (L / 2) + at / 2] >> (4 * (at & 1))) & 15) - 8) * s;
-                z += q[i] * v[i];
+            slot = (x.tile * kTile + t) & ((1 << p.lg_p) - 1);
+            src = p.pool + static_cast<long long>(page) * p.lay.bytes;
+        };
+        auto load_group = [&](int i) {  // chunks 2 i and 2 i + 1
+            codes[2 * i] = codes[2 * i + 1] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+            scales[i] = 0;
+            if (src != nullptr) {
+                const uint4* row = reinterpret_cast<const uint4*>(src + slot * (L / 2)) + hf;
+                codes[2 * i] = __ldg(row + 4 * i);
+                codes[2 * i + 1] = __ldg(row + 4 * i + 2);
+                const uint16_t* sc = reinterpret_cast<const uint16_t*>(src + p.lay.scales) + ((slot * L) >> p.lg_g);
+                scales[i] = __ldg(sc + ((128 * i + 32 * hf) >> p.lg_g)) |
+                            static_cast<uint32_t>(__ldg(sc + ((128 * i + 64 + 32 * hf) >> p.lg_g))) << 16;
             }
-            for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-            const float mn = fmaxf(m, z), al = expf(m - mn), p = expf(z - mn);
-            l = l * al + p;
-            for (int i = 0; i < E; ++i) o[i] = o[i] * al + p * v[i];
+        };
+        auto load_keys = [&]() {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                keys[i] = make_uint4(0, 0, 0, 0);
+                if (src != nullptr) keys[i] = __ldg(reinterpret_cast<const uint4*>(src + p.lay.rope + slot * (2 * kRope)) + 4 * hf + i);
+            }
+        };
+        auto store = [&](uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+        };
+        uint32_t n_tile = 0, n_q = 0;
+        Tile cur{}, nxt{};
+        cur.there = false;
+        if (st.units > 0) {
+            next_tile(cur);
+            nxt = cur;
+            find(cur, page_of(cur));
+#pragma unroll
+            for (int i = 0; i < G; ++i) load_group(i);
+            load_keys();
+            if (cur.there) next_tile(nxt);
+        }
+        int page = page_of(nxt);
+#pragma unroll 1
+        while (cur.there) {
+            if (cur.q != nullptr) {
+                // the item's queries, latent dimensions in the order the unpack leaves, the rotary part halved
+                if (n_q > 0) wait_or_stop(smem_u32(&ctl->q_free), (n_q - 1) & 1, stop, p.status);
+                ++n_q;
+                constexpr int PIECES = (L + kRope) / 8;
+#pragma unroll 4
+                for (int i = tid; i < NC * PIECES; i += 32 * kDqWarps) {
+                    const int line = i / PIECES, piece = i - line * PIECES;
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (line < cur.lines) x = __ldg(reinterpret_cast<const uint4*>(cur.q + static_cast<long long>(line) * (L + kRope)) + piece);
+                    x.x ^= p.q_flip;
+                    x.y ^= p.q_flip;
+                    x.z ^= p.q_flip;
+                    x.w ^= p.q_flip;
+                    const uint32_t at = q_s + (piece / 8) * Z::kQChunk + swizzled(line, piece % 8);
+                    if (piece < L / 8)
+                        store(at, prmt(x.x, x.z, 0x5410), prmt(x.x, x.z, 0x7632), prmt(x.y, x.w, 0x5410), prmt(x.y, x.w, 0x7632));
+                    else
+                        store(at, h2_mul(x.x, 0x38003800u), h2_mul(x.y, 0x38003800u), h2_mul(x.z, 0x38003800u),
+                              h2_mul(x.w, 0x38003800u));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full));
+            }
+            find(nxt, page);  // the next tile's rows are on their way while this one is dequantized
+            Tile far = nxt;
+            if (nxt.there) next_tile(far);
+            page = page_of(far);
+            const uint32_t row_s = k_s + t * 128;
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                uint32_t f[2][16];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    // half the scale, so that 7 times it stays finite (exact but for the smallest subnormals)
+                    const uint32_t sc = h2_mul(prmt(scales[i], 0, c ? 0x3232 : 0x1010), 0x38003800u);
+                    const uint32_t ws[4] = {codes[2 * i + c].x, codes[2 * i + c].y, codes[2 * i + c].z, codes[2 * i + c].w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t lo = ws[x], hi = ws[x] >> 8;
+                        f[c][4 * x] = h2_mul(unpack_lo(lo), sc);
+                        f[c][4 * x + 1] = h2_mul(unpack_hi(lo), sc);
+                        f[c][4 * x + 2] = h2_mul(unpack_lo(hi), sc);
+                        f[c][4 * x + 3] = h2_mul(unpack_hi(hi), sc);
+                    }
+                }
+                load_group(i);
+                if (n_tile > 0) wait_or_stop(smem_u32(&ctl->free[i]), (n_tile - 1) & 1, stop, p.status);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        store(row_s + (2 * i + c) * kChunk + (((4 * hf + x) ^ (t & 7)) << 4), f[c][4 * x], f[c][4 * x + 1],
+                              f[c][4 * x + 2], f[c][4 * x + 3]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->full[i]));
+            }
+            if (n_tile > 0) wait_or_stop(smem_u32(&ctl->free[4]), (n_tile - 1) & 1, stop, p.status);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                store(row_s + (Z::kChunks - 1) * kChunk + (((4 * hf + x) ^ (t & 7)) << 4), keys[x].x, keys[x].y, keys[x].z,
+                      keys[x].w);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->full[4]));
+            load_keys();
+            ++n_tile;
+            cur = nxt;
+            nxt = far;
+        }
+    } else {
+        regs_less<72>();
+        if (warp == 12) {
+            // ---- the products
+            constexpr uint32_t kIdS = mma_idesc(kTile, NC, false, false), kIdO = mma_idesc(128, NC, true, true);
+            const uint32_t tm = uniform(tmem);
+            bool live = true;  // false once a wait has been given up: nothing more is issued
+            uint32_t n_tile = 0, n_seg = 0;
+            while (uniform(st.units > 0 && walk.next(p))) {
+                const int n = uniform(g.k1 - g.k0);
+                live &= wait_or_stop(smem_u32(&ctl->q_full), n_seg & 1, stop, p.status);
+                ++n_seg;
+#pragma unroll 1
+                for (int i = 0; i < n; ++i, ++n_tile) {
+#pragma unroll 1
+                    for (int c = 0; c <= G; ++c) {  // pairs of chunks, then the rotary one
+                        live &= wait_or_stop(smem_u32(&ctl->full[c < G ? c : 4]), n_tile & 1, stop, p.status);
+                        tc_fence_after();
+                        const uint32_t a = desc_lo(k_s + 2 * c * kChunk, 16), b = desc_lo(q_s + 2 * c * Z::kQChunk, 16);
+                        if (elect_one() && live) {
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                if (x < 4 || c < G)
+                                    mma_ss(tm + Z::kS, smem_desc(a + (((x / 4) * kChunk + (x % 4) * 32) >> 4)),
+                                           smem_desc(b + (((x / 4) * Z::kQChunk + (x % 4) * 32) >> 4)), kIdS, c > 0 || x > 0);
+                        }
+                        __syncwarp();
+                    }
+                    if (elect_one() && live) {
+                        mma_commit(smem_u32(&ctl->s_full));
+                        if (i + 1 == n) mma_commit(smem_u32(&ctl->q_free));
+                    }
+                    __syncwarp();
+                    live &= wait_or_stop(smem_u32(&ctl->p_full), n_tile & 1, stop, p.status);
+                    tc_fence_after();
+                    if (elect_one() && live) {
+#pragma unroll 1
+                        for (int m = 0; m < G; ++m) {
+                            const uint32_t a = desc_lo(k_s + 2 * m * kChunk, kChunk), b = desc_lo(p_s, kChunk);
+#pragma unroll
+                            for (int x = 0; x < kTile / 16; ++x)
+                                mma_ss(tm + m * NC, smem_desc(a + (x * 2048 >> 4)), smem_desc(b + (x * 2048 >> 4)), kIdO,
+                                       i > 0 || x > 0);
+                            mma_commit(smem_u32(&ctl->free[m]));
+                        }
+                        mma_commit(smem_u32(&ctl->free[4]));
+                        if (i + 1 == n) mma_commit(smem_u32(&ctl->o_done));
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_free(tmem, Z::kTmem);
+    }
+}
+
+// The items cut between CTAs: blockIdx.x the CTA of the second part, a warp a line (one in 8 gridDim.y).
+template <int L, int NC>
+__global__ void __launch_bounds__(256) latent_merge_kernel(const __grid_constant__ LatentParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const MergeDesc d = p.desc[blockIdx.x];
+    if (d.parts == 0) return;
+    constexpr int E = L / 128;  // runs of 4 dimensions a lane holds, 128 apart
+    const int lane = threadIdx.x & 31;
+    const int c = blockIdx.x;
+    for (int i = blockIdx.y * 8 + threadIdx.x / 32; i < d.lines; i += 8 * gridDim.y) {
+        float m = -INFINITY, l = 0.f;
+        float4 o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (int k = 0; k < d.parts; ++k) {
+            const long long at = static_cast<long long>(k == 0 ? 2 * (c - 1) + 1 : 2 * (c + k - 1)) * NC + i;
+            const float mk = p.part_ml[2 * at], lk = p.part_ml[2 * at + 1];
+            float4 ok[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) ok[e] = reinterpret_cast<const float4*>(p.part_o + at * L)[32 * e + lane];
+            if (lk <= 0.f) continue;
+            const float mn = fmaxf(m, mk), a = fast_exp2(m - mn), ak = fast_exp2(mk - mn);
+            l = l * a + lk * ak;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                o[e].x = o[e].x * a + ok[e].x * ak;
+                o[e].y = o[e].y * a + ok[e].y * ak;
+                o[e].z = o[e].z * a + ok[e].z * ak;
+                o[e].w = o[e].w * a + ok[e].w * ak;
+            }
             m = mn;
         }
-        for (int i = 0; i < E; ++i)
-            a.out[task * L + lane * E + i] = __float2half_rn(pos < 0 ? 0.f : o[i] / l);
+        const float inv = l > 0.f ? 2.f / l : 0.f;
+        __half* out = p.out + (static_cast<long long>(d.line0) + i) * L;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            reinterpret_cast<uint2*>(out)[32 * e + lane] =
+                make_uint2(pack_h2(o[e].x * inv, o[e].y * inv), pack_h2(o[e].z * inv, o[e].w * inv));
     }
+}
+
+int device_sms() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return sms;
+}
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+template <int L, int NC>
+cudaError_t launch(LatentParams p, int ctas, cudaStream_t stream) {
+    p.step = NC;
+    const size_t smem = 1024 + Shape<L, NC>::kBytes + sizeof(Ctl<NC>);
+    cudaError_t e =
+        cudaFuncSetAttribute(latent_kernel<L, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, latent_kernel<L, NC>, p);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), NC / 8);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, latent_merge_kernel<L, NC>, p);
 }
 
 }  // namespace
 
-size_t latent_workspace_bytes(const LatentAttnArgs&) { return 256; }
+size_t latent_workspace_bytes(const LatentAttnArgs& a) {
+    const size_t sms = static_cast<size_t>(device_sms());
+    if (sms == 0) return 0;
+    return 256 + round256(sms * sizeof(MergeDesc)) + 2 * sms * 64 * (2 + a.lay.L) * sizeof(float);
+}
 
 cudaError_t launch_latent_attention(const LatentAttnArgs& a, cudaStream_t stream) {
-    int slices;
-    const int blocks = rows_grid(static_cast<long long>(a.rows) * a.H, 1, 32, &slices);
-    if (a.lay.L == 256) latent_kernel<256><<<blocks, 256, 0, stream>>>(a);
-    else latent_kernel<512><<<blocks, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    const int sms = device_sms();
+    LatentParams p{};
+    p.pool = a.pool;
+    p.q = a.q;
+    p.block_table = a.block_table;
+    p.seq_lens = a.seq_lens;
+    p.cu_rows = a.cu_rows;
+    p.out = a.out;
+    p.status = reinterpret_cast<uint32_t*>(a.workspace);
+    p.desc = reinterpret_cast<MergeDesc*>(a.workspace + 256);
+    p.part_ml = reinterpret_cast<float*>(a.workspace + 256 + round256(sms * sizeof(MergeDesc)));
+    p.part_o = p.part_ml + 2ll * sms * 64 * 2;
+    p.rows = a.rows;
+    p.B = a.B;
+    p.heads = 1;
+    p.per_row = a.H;
+    p.max_blocks = a.max_blocks;
+    p.num_pages = a.num_pages;
+    p.lg_p = a.lg_p;
+    p.lg_g = a.lay.G == 32 ? 5 : a.lay.G == 64 ? 6 : 7;
+    const long long table = static_cast<long long>(a.max_blocks) << a.lg_p;
+    p.most = static_cast<int32_t>(table < a.max_len ? table : a.max_len);
+    // (at least 1e-30: a hidden score is -infinity, which zero times is not a number)
+    p.c = std::fmax(2.f * std::fabs(a.softmax_scale) * 1.4426950408889634f, 1e-30f);
+    p.q_flip = a.softmax_scale < 0.f ? 0x80008000u : 0u;
+    p.lay = a.lay;
+    // As many lines to an item as a sequence has on average: an MMA of 16, 32 and 64 columns takes 40, 41 and 48
+    // cycles, but unused columns cost shared memory for their queries and the softmax's time
+    const long long lines = static_cast<long long>(a.rows) * a.H / a.B;
+    const int nc = lines <= 16 ? 16 : lines <= 32 ? 32 : 64;
+    if (a.lay.L == 256)
+        return nc == 16 ? launch<256, 16>(p, sms, stream) : nc == 32 ? launch<256, 32>(p, sms, stream) : launch<256, 64>(p, sms, stream);
+    return nc == 16 ? launch<512, 16>(p, sms, stream) : nc == 32 ? launch<512, 32>(p, sms, stream) : launch<512, 64>(p, sms, stream);
 }
 
 }  // namespace kvq
