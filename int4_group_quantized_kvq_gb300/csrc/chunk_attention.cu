@@ -578,53 +578,36 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
 }
 
-// The items cut between CTAs: blockIdx.x the CTA of the second part, a warp a row (one in 8 gridDim.y).
+// The items cut between CTAs.
 template <int D>
-__global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant__ ChunkParams p, int ctas) {
+    __shared__ MergeShare share;
+    __shared__ float4 sums[8][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const MergeDesc d = p.desc[blockIdx.x];
-    if (d.parts == 0) return;
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int c = blockIdx.x;
-    for (int i = blockIdx.y * 8 + threadIdx.x / 32; i < d.lines * p.r; i += 8 * gridDim.y) {
-        const int tok = i / p.r, g = i - tok * p.r;
-        const int prow = (tok / p.T) * kTile + (tok % p.T) * p.r + g;
-        float m = -INFINITY, l = 0.f, o[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = 0.f;
-        for (int k = 0; k < d.parts; ++k) {
-            const long long at = static_cast<long long>(k == 0 ? 2 * (c - 1) + 1 : 2 * (c + k - 1)) * 256 + prow;
-            const float mk = p.part_ml[2 * at], lk = p.part_ml[2 * at + 1];
-            float ok[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) ok[e] = p.part_o[at * D + lane * E + e];
-            if (lk <= 0.f) continue;
-            const float mn = fmaxf(m, mk), a = fast_exp2(m - mn), ak = fast_exp2(mk - mn);
-            l = l * a + lk * ak;
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = o[e] * a + ok[e] * ak;
-            m = mn;
-        }
-        const float inv = l > 0.f ? 2.f / l : 0.f;
-        // columns E lane .. of the 8 that share 16 bytes; dimension order 0 4 1 5 2 6 3 7
-        __half* out = p.out + (static_cast<long long>(d.line0 + tok) * p.Hq + d.h * p.r + g) * D;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int col = lane * E + e, x = col & 7;
-            out[(col & ~7) + (x >> 1) + 4 * (x & 1)] = __float2half_rn(o[e] * inv);
-        }
-    }
+    // lanes hold 4 columns of a row each (D = 64: half of the lanes)
+    merge_items<1>(
+        p, ctas, p.r, &share, &sums[0][0],
+        [&](long long slot, int line, float& m, float& l, float4 (&o)[1], int lane) {
+            const int tok = line / p.r;
+            const long long at = slot * 256 + (tok / p.T) * kTile + (tok % p.T) * p.r + line - tok * p.r;
+            m = p.part_ml[2 * at];
+            l = p.part_ml[2 * at + 1];
+            o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (4 * lane < D) o[0] = reinterpret_cast<const float4*>(p.part_o + at * D)[lane];
+        },
+        [&](const MergeDesc& d, int line, float l, const float4 (&o)[1], int lane) {
+            if (4 * lane >= D) return;
+            const float inv = l > 0.f ? 2.f / l : 0.f;
+            const int tok = line / p.r;
+            // columns 4 lane .. of the 8 that share 16 bytes: dimensions 0 4 1 5 or 2 6 3 7
+            __half* out = p.out + (static_cast<long long>(d.line0 + tok) * p.Hq + d.h * p.r + line - tok * p.r) * D + (lane & ~1) * 4 +
+                          (lane & 1) * 2;
+            *reinterpret_cast<uint32_t*>(out) = pack_h2(o[0].x * inv, o[0].z * inv);
+            *reinterpret_cast<uint32_t*>(out + 4) = pack_h2(o[0].y * inv, o[0].w * inv);
+        });
 }
 
-int device_sms() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return sms;
-}
-
-size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 template <int D>
 cudaError_t launch(const ChunkParams& p, int ctas, cudaStream_t stream) {
@@ -644,22 +627,29 @@ cudaError_t launch(const ChunkParams& p, int ctas, cudaStream_t stream) {
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, chunk_kernel<D>, p);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 8);
+    cfg.gridDim = dim3(static_cast<unsigned>(4 * ctas));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<D>, p);
+    return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<D>, p, ctas);
 }
 
 }  // namespace
 
+int attention_ctas() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return sms < kMaxCtas ? sms : kMaxCtas;
+}
+
 size_t chunk_workspace_bytes(const ChunkArgs& a) {
-    const size_t sms = static_cast<size_t>(device_sms());
+    const size_t sms = static_cast<size_t>(attention_ctas());
     if (sms == 0) return 0;
-    return 256 + round256(sms * sizeof(MergeDesc)) + 2 * sms * 256 * (2 + a.L.d) * sizeof(float);
+    return 256 + align256(sms * sizeof(MergeDesc)) + 2 * sms * 256 * (2 + a.L.d) * sizeof(float);
 }
 
 cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t stream) {
-    const int sms = device_sms();
+    const int sms = attention_ctas();
     ChunkParams p{};
     p.pool = a.pool;
     p.q = a.q;
@@ -669,7 +659,7 @@ cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t stream) {
     p.out = a.out;
     p.status = reinterpret_cast<uint32_t*>(a.workspace);
     p.desc = reinterpret_cast<MergeDesc*>(a.workspace + 256);
-    p.part_ml = reinterpret_cast<float*>(a.workspace + 256 + round256(sms * sizeof(MergeDesc)));
+    p.part_ml = reinterpret_cast<float*>(a.workspace + 256 + align256(sms * sizeof(MergeDesc)));
     p.part_o = p.part_ml + 2ll * sms * 256 * 2;
     p.rows = a.rows;
     p.B = a.B;

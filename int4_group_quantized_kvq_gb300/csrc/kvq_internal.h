@@ -351,6 +351,8 @@ struct ChunkArgs {
     float softmax_scale;
     BlockLayout L;
 };
+// CTAs of the attention kernels on ragged batches: one per SM (0: no device).
+int attention_ctas();
 size_t chunk_workspace_bytes(const ChunkArgs& a);
 cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t stream);
 

@@ -211,4 +211,98 @@ __device__ __forceinline__ void find_start(const Units& p, Start* start, long lo
 // the descriptor's and those behind it.
 __device__ __forceinline__ int partial_slot(const Segment& g) { return 2 * blockIdx.x + (g.k0 == 0 ? 1 : 0); }
 
+constexpr int kMaxCtas = 256;  // of an attention grid
+
+// The merges of a call, shared out over a grid of 256-thread CTAs: a warp merges a line of an item of few
+// parts, a CTA one of many (its warps take the parts in turn).  `first` counts the pieces of work ahead of
+// each descriptor's.
+struct MergeShare {
+    int first[kMaxCtas + 1];
+    int warp_sum[8];
+    float ml[8][2];
+};
+constexpr int kFewParts = 8;
+
+// E float4 of a line per lane.  fetch(slot, line, m, l, o, lane) reads a part, put(desc, line, l, o, lane)
+// writes the merged line; lines: `mult` times the descriptor's.  sums: shared memory, [8][32 E] float4.
+template <int E, class FETCH, class PUT>
+__device__ __forceinline__ void merge_items(const Units& p, int ctas, int mult, MergeShare* share, float4* sums, FETCH fetch,
+                                            PUT put) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+    int mine = 0;
+    if (tid < ctas) {
+        const MergeDesc d = p.desc[tid];
+        if (d.parts > 0) mine = d.parts > kFewParts ? d.lines * mult : (d.lines * mult + 7) / 8;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += t;
+    }
+    if (lane == 31) share->warp_sum[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += share->warp_sum[w];
+    share->first[tid] = incl - mine;
+    if (tid == 255) share->first[256] = incl;
+    __syncthreads();
+    const int total = share->first[256];
+    auto add = [&](float& m, float& l, float4 (&o)[E], float mk, float lk, const float4 (&ok)[E]) {
+        if (lk <= 0.f) return;
+        const float mn = fmaxf(m, mk), a = fast_exp2(m - mn), ak = fast_exp2(mk - mn);
+        l = l * a + lk * ak;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            o[e].x = o[e].x * a + ok[e].x * ak;
+            o[e].y = o[e].y * a + ok[e].y * ak;
+            o[e].z = o[e].z * a + ok[e].z * ak;
+            o[e].w = o[e].w * a + ok[e].w * ak;
+        }
+        m = mn;
+    };
+    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+        int lo = 0, hi = 255;  // the last descriptor whose pieces start at or before u: it has some
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (share->first[mid] <= u) lo = mid;
+            else hi = mid - 1;
+        }
+        const MergeDesc d = p.desc[lo];
+        const bool wide = d.parts > kFewParts;
+        const int line = wide ? u - share->first[lo] : (u - share->first[lo]) * 8 + warp;
+        float m = -INFINITY, l = 0.f;
+        float4 o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (line < d.lines * mult) {
+#pragma unroll 2
+            for (int k = wide ? warp : 0; k < d.parts; k += wide ? 8 : 1) {
+                float mk, lk;
+                float4 ok[E];
+                fetch(k == 0 ? 2 * (lo - 1) + 1 : 2 * (lo + k - 1), line, mk, lk, ok, lane);
+                add(m, l, o, mk, lk, ok);
+            }
+            if (!wide) put(d, line, l, o, lane);
+        }
+        if (!wide) continue;
+#pragma unroll
+        for (int e = 0; e < E; ++e) sums[(warp * E + e) * 32 + lane] = o[e];
+        if (lane == 0) {
+            share->ml[warp][0] = m;
+            share->ml[warp][1] = l;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            for (int w = 1; w < 8; ++w) {
+                float4 ok[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) ok[e] = sums[(w * E + e) * 32 + lane];
+                add(m, l, o, share->ml[w][0], share->ml[w][1], ok);
+            }
+            put(d, line, l, o, lane);
+        }
+        __syncthreads();
+    }
+}
+
 }  // namespace kvq

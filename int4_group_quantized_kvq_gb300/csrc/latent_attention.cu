@@ -14,9 +14,9 @@
 // of 128 dimensions are refilled one by one as the second product lets them go.
 //
 // Warps of a CTA (one per SM):
-//   0-3    softmax: a thread has a position, its scores of all lines in registers.
-//   4-11   dequantize: two threads a position; packed rows go from memory to registers a tile ahead.
-//   12     issues the MMAs.
+//   0-7    softmax: two threads have a position, half of the lines' scores each in registers.
+//   8-15   dequantize: two threads a position; packed rows go from memory to registers a tile ahead.
+//   16     issues the MMAs.
 // Work is shared out as in kvq_units.cuh; an item is NC lines of one sequence.
 #include <cuda_fp16.h>
 
@@ -30,8 +30,8 @@
 namespace kvq {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kDqWarps = 8;
+constexpr int kThreads = 640;
+constexpr int kSmWarps = 8, kDqWarps = 8, kMmaWarp = 16;
 constexpr int kRope = 64;              // rotary dimensions
 constexpr int kChunk = kTile * 128;    // bytes of a chunk [128][64] f16
 
@@ -71,7 +71,7 @@ struct Ctl {
     Start start;
     uint32_t tmem;
     int stop;
-    Walk walk[13];
+    Walk walk[kMmaWarp + 1];
     alignas(16) float off[NC];    // -(reference maximum) c, by line
     alignas(16) float scale[NC];  // factors of a rescaling, or of the output
     float m[NC];                  // reference maximum of the scores (of z / scale)
@@ -88,16 +88,16 @@ __device__ __forceinline__ float warp_max(float x) {
 __device__ __forceinline__ bool any_of_softmax(bool x) {
     uint32_t r;
     asm volatile(
-        "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, 2, 128, p; selp.u32 %0, 1, 0, q; }"
+        "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, 2, 256, p; selp.u32 %0, 1, 0, q; }"
         : "=r"(r)
         : "r"(static_cast<uint32_t>(x))
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void softmax_barrier() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void softmax_barrier() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
 
 // Sums over the warp's lanes of N values each: halving the values a lane keeps at each exchange, N - 1
-// shuffles and a few.  Afterwards v[0 .. max(1, N / 32)) of a lane belong to the columns from first_column.
+// shuffles and a few.  Afterwards v[0] of a lane is the sum of column first_column (N up to 32).
 template <int N>
 __device__ __forceinline__ void warp_sums(float (&v)[N], int lane) {
     int n = N;
@@ -128,11 +128,11 @@ __device__ __forceinline__ int first_column(int lane) {
     return c;
 }
 
-template <int NC>
-__device__ __forceinline__ void load_columns(uint32_t addr, uint32_t (&v)[NC]) {
-    if constexpr (NC == 16) tmem_ld16(addr, v);
-    if constexpr (NC >= 32) tmem_ld32(addr, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-    if constexpr (NC == 64) tmem_ld32(addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[NC == 64 ? 32 : 0]));
+template <int N>
+__device__ __forceinline__ void load_columns(uint32_t addr, uint32_t (&v)[N]) {
+    if constexpr (N == 8) tmem_ld8(addr, v);
+    if constexpr (N == 16) tmem_ld16(addr, v);
+    if constexpr (N == 32) tmem_ld32(addr, v);
     tmem_wait_ld();
     tmem_touch(v);
 }
@@ -161,71 +161,73 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
         mbar_init(smem_u32(&ctl->q_full), kDqWarps);
         mbar_init(smem_u32(&ctl->q_free), 1);
         mbar_init(smem_u32(&ctl->s_full), 1);
-        mbar_init(smem_u32(&ctl->p_full), 4);
+        mbar_init(smem_u32(&ctl->p_full), kSmWarps);
         mbar_init(smem_u32(&ctl->o_done), 1);
         ctl->stop = 0;
         fence_mbar_init();
     }
-    if (warp == 12) tmem_alloc(smem_u32(&ctl->tmem), Z::kTmem);
+    if (warp == kMmaWarp) tmem_alloc(smem_u32(&ctl->tmem), Z::kTmem);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     tc_fence_before();
     find_start<kThreads>(p, &ctl->start, ctl->warp_sum);  // (has barriers of the CTA)
     tc_fence_after();
     const uint32_t tmem = ctl->tmem;
     const Start st = ctl->start;
-    Walk& walk = ctl->walk[min(warp, 12)];
-    if (st.units > 0 && warp < 13) walk.begin(p, st);
+    Walk& walk = ctl->walk[min(warp, kMmaWarp)];
+    if (st.units > 0 && warp <= kMmaWarp) walk.begin(p, st);
     const Segment& g = walk.g;
 
-    if (warp < 4) {
-        regs_more<200>();
-        // ---- softmax: position `t` of a tile; its tensor-memory lane is also a dimension of the outputs
-        const int t = threadIdx.x;
-        const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
-        const uint32_t s_t = tmem + lanes + Z::kS, o_t = tmem + lanes;
+    if (warp < kSmWarps) {
+        regs_more<104>();
+        // ---- softmax: position `t` of a tile, columns c0 .. c0 + HC - 1; the thread's tensor-memory lane is also a
+        // dimension of the outputs
+        constexpr int HC = NC / 2;
+        const int t = threadIdx.x & 127, side = warp / 4, c0 = side * HC;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+        const uint32_t s_t = tmem + lanes + Z::kS + c0, o_t = tmem + lanes;
         uint32_t n_tile = 0, n_seg = 0;
         while (st.units > 0 && walk.next(p)) {
             const int n = g.k1 - g.k0;
-            if (t < NC) {
+            if (side == 0 && t < NC) {
                 ctl->lim[t] = g.ahead + (g.line0 + min(t, g.lines - 1)) / p.per_row + 1;
                 ctl->m[t] = -INFINITY;
                 ctl->off[t] = 0.f;
             }
             softmax_barrier();
             const int lim0 = ctl->lim[0];  // the least
-            float l[NC];
+            float l[HC];
 #pragma unroll
-            for (int i = 0; i < NC; ++i) l[i] = 0.f;
+            for (int i = 0; i < HC; ++i) l[i] = 0.f;
 #pragma unroll 1
             for (int i = 0; i < n; ++i, ++n_tile) {
                 const int pos = (g.k0 + i) * kTile + t;
                 wait_or_stop(smem_u32(&ctl->s_full), n_tile & 1, stop, p.status);
                 tc_fence_after();
-                uint32_t s[NC];
-                load_columns<NC>(s_t, s);
+                uint32_t s[HC];
+                load_columns<HC>(s_t, s);
                 if ((g.k0 + i + 1) * kTile > lim0) {
 #pragma unroll
-                    for (int x = 0; x < NC; ++x)
-                        if (pos >= ctl->lim[x]) s[x] = 0xff800000u;
+                    for (int x = 0; x < HC; ++x)
+                        if (pos >= ctl->lim[c0 + x]) s[x] = 0xff800000u;
                 }
                 // Are the references still within 2^8 of every score?  (Weights then stay below 2^8, far inside f16,
                 // and nothing is reduced over the positions: of a few hundred tiles a few move a reference)
                 float top = -INFINITY;
 #pragma unroll
-                for (int x = 0; x < NC; x += 4) {
-                    const float4 off = *reinterpret_cast<const float4*>(&ctl->off[x]);
+                for (int x = 0; x < HC; x += 4) {
+                    const float4 off = *reinterpret_cast<const float4*>(&ctl->off[c0 + x]);
                     const float a = fmaf(__uint_as_float(s[x]), p.c, off.x), b = fmaf(__uint_as_float(s[x + 1]), p.c, off.y);
                     const float c = fmaf(__uint_as_float(s[x + 2]), p.c, off.z), d = fmaf(__uint_as_float(s[x + 3]), p.c, off.w);
                     top = fmaxf(fmaxf(fmaxf(top, a), fmaxf(b, c)), d);
                 }
                 if (any_of_softmax(i == 0 || top > 8.f)) {
 #pragma unroll
-                    for (int x = 0; x < NC; ++x) {
+                    for (int x = 0; x < HC; ++x) {
                         const float r = warp_max(__uint_as_float(s[x]));
-                        if (lane == (x & 31)) ctl->part[warp][x] = r;
+                        if (lane == x) ctl->part[warp & 3][c0 + x] = r;
                     }
                     softmax_barrier();
-                    if (t < NC) {
+                    if (side == 0 && t < NC) {
                         const float most = fmaxf(fmaxf(ctl->part[0][t], ctl->part[1][t]), fmaxf(ctl->part[2][t], ctl->part[3][t]));
                         const float m = ctl->m[t];
                         const float to = m == -INFINITY || (most - m) * p.c > 8.f ? fmaxf(most, m) : m;
@@ -236,9 +238,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                     softmax_barrier();
                     if (i > 0) {
 #pragma unroll
-                        for (int x = 0; x < NC; ++x) l[x] *= ctl->scale[x];
+                        for (int x = 0; x < HC; ++x) l[x] *= ctl->scale[c0 + x];
 #pragma unroll 1
-                        for (int x = 0; x < G * NC / 16; ++x) {  // (the products into O that came before S are complete)
+                        for (int x = side; x < G * NC / 16; x += 2) {  // (the products into O that came before S are complete)
                             uint32_t o[16];
                             tmem_ld16(o_t + 16 * x, o);
                             tmem_wait_ld();
@@ -253,11 +255,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 }
                 // the weights, in rows of a position
 #pragma unroll
-                for (int x = 0; x < NC; x += 8) {
+                for (int x = 0; x < HC; x += 8) {
                     uint32_t w[4];
 #pragma unroll
                     for (int y = 0; y < 8; y += 4) {
-                        const float4 off = *reinterpret_cast<const float4*>(&ctl->off[x + y]);
+                        const float4 off = *reinterpret_cast<const float4*>(&ctl->off[c0 + x + y]);
                         const float a = fast_exp2(fmaf(__uint_as_float(s[x + y]), p.c, off.x));
                         const float b = fast_exp2(fmaf(__uint_as_float(s[x + y + 1]), p.c, off.y));
                         const float c = fast_exp2(fmaf(__uint_as_float(s[x + y + 2]), p.c, off.z));
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                         w[y / 2] = pack_h2(a, b);
                         w[y / 2 + 1] = pack_h2(c, d);
                     }
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(p_s + swizzled(t, x / 8)), "r"(w[0]), "r"(w[1]),
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(p_s + swizzled(t, (c0 + x) / 8)), "r"(w[0]), "r"(w[1]),
                                  "r"(w[2]), "r"(w[3])
                                  : "memory");
                 }
@@ -280,16 +282,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             }
             // ---- the segment's result
             const bool whole = g.k0 == 0 && g.k1 == g.nt;
-            warp_sums<NC>(l, lane);
-            const int col = first_column<NC>(lane);
-            if (NC == 64 || (NC == 32) || (lane & 1) == 0) {
-                ctl->part[warp][col] = l[0];
-                if (NC == 64) ctl->part[warp][col + 1] = l[1];
-            }
+            warp_sums<HC>(l, lane);
+            ctl->part[warp & 3][c0 + first_column<HC>(lane)] = l[0];
             softmax_barrier();
             const long long line0 = static_cast<long long>(g.row0) * p.per_row + g.line0;
             const int slot = partial_slot(g);
-            if (t < NC) {
+            if (side == 0 && t < NC) {
                 const float sum = (ctl->part[0][t] + ctl->part[1][t]) + (ctl->part[2][t] + ctl->part[3][t]);
                 ctl->scale[t] = !whole ? 1.f : sum > 0.f ? 2.f / sum : 0.f;
                 if (!whole) {
@@ -303,32 +301,32 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             tc_fence_after();
             const int dim = dim_of(t);
 #pragma unroll 1
-            for (int x = 0; x < G * NC / 16; ++x) {
+            for (int x = side; x < G * NC / 16; x += 2) {
                 uint32_t o[16];
                 tmem_ld16(o_t + 16 * x, o);
                 tmem_wait_ld();
                 tmem_touch(o);
-                const int c0 = 16 * x % NC, d = 16 * x / NC * 128 + dim;
+                const int c = 16 * x % NC, d = 16 * x / NC * 128 + dim;
                 if (whole) {
 #pragma unroll
                     for (int y = 0; y < 16; ++y)
-                        if (c0 + y < g.lines)
-                            p.out[(line0 + c0 + y) * L + d] = __float2half_rn(__uint_as_float(o[y]) * ctl->scale[c0 + y]);
+                        if (c + y < g.lines)
+                            p.out[(line0 + c + y) * L + d] = __float2half_rn(__uint_as_float(o[y]) * ctl->scale[c + y]);
                 } else {
-                    float* to = p.part_o + (static_cast<long long>(slot) * NC + c0) * L + d;
+                    float* to = p.part_o + (static_cast<long long>(slot) * NC + c) * L + d;
 #pragma unroll
                     for (int y = 0; y < 16; ++y)
-                        if (c0 + y < g.lines) to[y * L] = __uint_as_float(o[y]);
+                        if (c + y < g.lines) to[y * L] = __uint_as_float(o[y]);
                 }
                 __syncwarp();
             }
             tc_fence_before();
             softmax_barrier();
         }
-    } else if (warp < 4 + kDqWarps) {
-        regs_less<120>();
+    } else if (warp < kSmWarps + kDqWarps) {
+        regs_more<104>();
         // ---- dequantize: position `t` of a tile, half `hf` of every 64 dimensions
-        const int tid = threadIdx.x - 128, t = tid >> 1, hf = tid & 1;
+        const int tid = threadIdx.x - 32 * kSmWarps, t = tid >> 1, hf = tid & 1;
         struct Tile {
             const int32_t* table;
             const __half* q;  // the item's queries, where the tile is its first of this CTA (else nullptr)
@@ -411,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 if (n_q > 0) wait_or_stop(smem_u32(&ctl->q_free), (n_q - 1) & 1, stop, p.status);
                 ++n_q;
                 constexpr int PIECES = (L + kRope) / 8;
-#pragma unroll 4
+#pragma unroll 6
                 for (int i = tid; i < NC * PIECES; i += 32 * kDqWarps) {
                     const int line = i / PIECES, piece = i - line * PIECES;
                     uint4 x = make_uint4(0, 0, 0, 0);
@@ -431,10 +429,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full));
             }
-            find(nxt, page);  // the next tile's rows are on their way while this one is dequantized
-            Tile far = nxt;
-            if (nxt.there) next_tile(far);
-            page = page_of(far);
             const uint32_t row_s = k_s + t * 128;
 #pragma unroll
             for (int i = 0; i < G; ++i) {
@@ -453,7 +447,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                         f[c][4 * x + 3] = h2_mul(unpack_hi(hi), sc);
                     }
                 }
-                load_group(i);
                 if (n_tile > 0) wait_or_stop(smem_u32(&ctl->free[i]), (n_tile - 1) & 1, stop, p.status);
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
@@ -473,14 +466,21 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ctl->full[4]));
+            // the next tile's rows (here and not between the stores: the fences above would wait for loads in flight)
+            find(nxt, page);
+            Tile far = nxt;
+            if (nxt.there) next_tile(far);
+            page = page_of(far);
+#pragma unroll
+            for (int i = 0; i < G; ++i) load_group(i);
             load_keys();
             ++n_tile;
             cur = nxt;
             nxt = far;
         }
     } else {
-        regs_less<72>();
-        if (warp == 12) {
+        regs_less<64>();
+        if (warp == kMmaWarp) {
             // ---- the products
             constexpr uint32_t kIdS = mma_idesc(kTile, NC, false, false), kIdO = mma_idesc(128, NC, true, true);
             const uint32_t tm = uniform(tmem);
@@ -533,62 +533,39 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_free(tmem, Z::kTmem);
     }
 }
 
-// The items cut between CTAs: blockIdx.x the CTA of the second part, a warp a line (one in 8 gridDim.y).
+// The items cut between CTAs.
 template <int L, int NC>
-__global__ void __launch_bounds__(256) latent_merge_kernel(const __grid_constant__ LatentParams p) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const MergeDesc d = p.desc[blockIdx.x];
-    if (d.parts == 0) return;
+__global__ void __launch_bounds__(256) latent_merge_kernel(const __grid_constant__ LatentParams p, int ctas) {
     constexpr int E = L / 128;  // runs of 4 dimensions a lane holds, 128 apart
-    const int lane = threadIdx.x & 31;
-    const int c = blockIdx.x;
-    for (int i = blockIdx.y * 8 + threadIdx.x / 32; i < d.lines; i += 8 * gridDim.y) {
-        float m = -INFINITY, l = 0.f;
-        float4 o[E];
+    __shared__ MergeShare share;
+    __shared__ float4 sums[8][L / 4];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    merge_items<E>(
+        p, ctas, 1, &share, &sums[0][0],
+        [&](long long slot, int line, float& m, float& l, float4 (&o)[E], int lane) {
+            const long long at = slot * NC + line;
+            m = p.part_ml[2 * at];
+            l = p.part_ml[2 * at + 1];
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-        for (int k = 0; k < d.parts; ++k) {
-            const long long at = static_cast<long long>(k == 0 ? 2 * (c - 1) + 1 : 2 * (c + k - 1)) * NC + i;
-            const float mk = p.part_ml[2 * at], lk = p.part_ml[2 * at + 1];
-            float4 ok[E];
+            for (int e = 0; e < E; ++e) o[e] = reinterpret_cast<const float4*>(p.part_o + at * L)[32 * e + lane];
+        },
+        [&](const MergeDesc& d, int line, float l, const float4 (&o)[E], int lane) {
+            const float inv = l > 0.f ? 2.f / l : 0.f;
+            __half* out = p.out + (static_cast<long long>(d.line0) + line) * L;
 #pragma unroll
-            for (int e = 0; e < E; ++e) ok[e] = reinterpret_cast<const float4*>(p.part_o + at * L)[32 * e + lane];
-            if (lk <= 0.f) continue;
-            const float mn = fmaxf(m, mk), a = fast_exp2(m - mn), ak = fast_exp2(mk - mn);
-            l = l * a + lk * ak;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                o[e].x = o[e].x * a + ok[e].x * ak;
-                o[e].y = o[e].y * a + ok[e].y * ak;
-                o[e].z = o[e].z * a + ok[e].z * ak;
-                o[e].w = o[e].w * a + ok[e].w * ak;
-            }
-            m = mn;
-        }
-        const float inv = l > 0.f ? 2.f / l : 0.f;
-        __half* out = p.out + (static_cast<long long>(d.line0) + i) * L;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            reinterpret_cast<uint2*>(out)[32 * e + lane] =
-                make_uint2(pack_h2(o[e].x * inv, o[e].y * inv), pack_h2(o[e].z * inv, o[e].w * inv));
-    }
+            for (int e = 0; e < E; ++e)
+                reinterpret_cast<uint2*>(out)[32 * e + lane] =
+                    make_uint2(pack_h2(o[e].x * inv, o[e].y * inv), pack_h2(o[e].z * inv, o[e].w * inv));
+        });
 }
 
-int device_sms() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return sms;
-}
-
-size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 template <int L, int NC>
 cudaError_t launch(LatentParams p, int ctas, cudaStream_t stream) {
@@ -609,22 +586,22 @@ cudaError_t launch(LatentParams p, int ctas, cudaStream_t stream) {
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, latent_kernel<L, NC>, p);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas), NC / 8);
+    cfg.gridDim = dim3(static_cast<unsigned>(4 * ctas));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, latent_merge_kernel<L, NC>, p);
+    return cudaLaunchKernelEx(&cfg, latent_merge_kernel<L, NC>, p, ctas);
 }
 
 }  // namespace
 
 size_t latent_workspace_bytes(const LatentAttnArgs& a) {
-    const size_t sms = static_cast<size_t>(device_sms());
+    const size_t sms = static_cast<size_t>(attention_ctas());
     if (sms == 0) return 0;
-    return 256 + round256(sms * sizeof(MergeDesc)) + 2 * sms * 64 * (2 + a.lay.L) * sizeof(float);
+    return 256 + align256(sms * sizeof(MergeDesc)) + 2 * sms * 64 * (2 + a.lay.L) * sizeof(float);
 }
 
 cudaError_t launch_latent_attention(const LatentAttnArgs& a, cudaStream_t stream) {
-    const int sms = device_sms();
+    const int sms = attention_ctas();
     LatentParams p{};
     p.pool = a.pool;
     p.q = a.q;
@@ -634,7 +611,7 @@ cudaError_t launch_latent_attention(const LatentAttnArgs& a, cudaStream_t stream
     p.out = a.out;
     p.status = reinterpret_cast<uint32_t*>(a.workspace);
     p.desc = reinterpret_cast<MergeDesc*>(a.workspace + 256);
-    p.part_ml = reinterpret_cast<float*>(a.workspace + 256 + round256(sms * sizeof(MergeDesc)));
+    p.part_ml = reinterpret_cast<float*>(a.workspace + 256 + align256(sms * sizeof(MergeDesc)));
     p.part_o = p.part_ml + 2ll * sms * 64 * 2;
     p.rows = a.rows;
     p.B = a.B;
