@@ -10,12 +10,12 @@
 // so that the lines are a column count of 16, 32 or 64 (a decode step of 16 heads fills 16 columns, not 16
 // of 128 rows), the output of 64 lines takes L / 128 x 64 = 256 of tensor memory's 512 columns, and one
 // dequantized tile serves both products: rows of 64 dimensions are a K-major operand of the first and an
-// MN-major one of the second.  A tile of 128 positions is 144 KB in shared memory and single: its groups
-// of 128 dimensions are refilled one by one as the second product lets them go.
+// MN-major one of the second.  A tile of 128 positions is 144 KB in shared memory and single: its halves
+// of 256 dimensions are refilled as the second product lets them go.
 //
 // Warps of a CTA (one per SM):
 //   0-7    softmax: two threads have a position, half of the lines' scores each in registers.
-//   8-15   dequantize: two threads a position; packed rows go from memory to registers a tile ahead.
+//   8-15   dequantize: packed rows go from memory to registers a tile ahead, eight lanes 128 bytes of a row.
 //   16     issues the MMAs.
 // Work is shared out as in kvq_units.cuh; an item is NC lines of one sequence.
 #include <cuda_fp16.h>
@@ -51,7 +51,8 @@ struct LatentParams : Units {  // per_row: query heads
 template <int L, int NC>
 struct Shape {
     static constexpr int kChunks = L / 64 + 1;             // the last one: rotary keys
-    static constexpr int kGroups = L / 128;                // pairs of latent chunks; the rotary chunk is one more
+    static constexpr int kGroups = L / 128;                // outputs of 128 dimensions
+    static constexpr int kHalves = L / 256;                // runs of four latent chunks, refilled together
     static constexpr int kQChunk = NC * 128;               // bytes of a chunk of queries [NC][64] f16
     static constexpr int kQ = kChunks * kQChunk;
     static constexpr int kK = kChunks * kChunk;
@@ -65,7 +66,7 @@ struct Shape {
 
 template <int NC>
 struct Ctl {
-    uint64_t full[5], free[5];  // groups of latent chunks, then the rotary chunk (the weights, where they share)
+    uint64_t full[3], free[3];  // halves of the latent chunks; [2]: the rotary chunk (the weights, where they share)
     uint64_t q_full, q_free, s_full, p_full, o_done;
     long long warp_sum[kThreads / 32];
     Start start;
@@ -154,8 +155,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
 
     asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 5; ++i) {
-            mbar_init(smem_u32(&ctl->full[i]), kDqWarps);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(smem_u32(&ctl->full[i]), i < 2 ? kDqWarps / Z::kHalves : kDqWarps);
             mbar_init(smem_u32(&ctl->free[i]), 1);
         }
         mbar_init(smem_u32(&ctl->q_full), kDqWarps);
@@ -325,8 +326,22 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
         }
     } else if (warp < kSmWarps + kDqWarps) {
         regs_more<104>();
-        // ---- dequantize: position `t` of a tile, half `hf` of every 64 dimensions
-        const int tid = threadIdx.x - 32 * kSmWarps, t = tid >> 1, hf = tid & 1;
+        // ---- dequantize.  A warp takes four positions of one half (256 dimensions) at a time: eight lanes read 128
+        // bytes of a row's codes, 16 each (32 dimensions, half of a chunk)
+        constexpr int WPH = kDqWarps / Z::kHalves;   // warps of a half
+        constexpr int JOBS = kTile / (4 * WPH);      // positions of a lane
+        const int tid = threadIdx.x - 32 * kSmWarps, dw = warp - kSmWarps;
+        const int half = dw / WPH, q = lane & 7, hf = q & 1;
+        const int t0 = (dw % WPH) * 4 + (lane >> 3);  // the lane's positions: t0 + 4 WPH job
+        const int r0 = dw * 4 + (lane >> 3);          // of the rotary keys: r0 + 32 job, 16 bytes each
+        const int per = kTile >> p.lg_p, lg_p = p.lg_p;
+        // A lane's four 16-byte pieces of f16 lie in one chunk; the eight lanes' chunks start on the same banks, so each
+        // pair of lanes starts with another piece (its words turned accordingly) and no bank is met twice
+        const int turn = q >> 1;
+        uint32_t to[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            to[x] = k_s + (4 * half + (q >> 1)) * kChunk + t0 * 128 + (((4 * hf + ((x + turn) & 3)) ^ (t0 & 7)) << 4);
         struct Tile {
             const int32_t* table;
             const __half* q;  // the item's queries, where the tile is its first of this CTA (else nullptr)
@@ -348,42 +363,39 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             }
             x.tile = k;
         };
-        auto page_of = [&](const Tile& x) -> int {  // of this thread's position; -1: behind the sequence
-            const int pos = x.tile * kTile + t;
-            return x.there && pos < x.vis ? __ldg(x.table + (pos >> p.lg_p)) : -1;
+        auto pages_of = [&](const Tile& x) -> int {  // lane l: page l of the tile
+            const int first = x.tile * per + lane;
+            return x.there && lane < per && (first << lg_p) < x.vis ? __ldg(x.table + first) : 0;
         };
-        // the packed row of a position
-        uint4 codes[L / 64], keys[4];
-        uint32_t scales[L / 128];  // of chunks 2 i and 2 i + 1
-        const uint8_t* src = nullptr;
-        int slot = 0;
-        auto find = [&](const Tile& x, int page) {
-            src = nullptr;
-            if (!x.there || x.tile * kTile + t >= x.vis) return;
-            if (page < 0 || page >= p.num_pages) {
+        // the packed rows of a tile
+        uint4 codes[JOBS], keys[4];
+        uint32_t scales[JOBS];
+        auto load = [&](const Tile& x, int pages) {
+            const int end = x.there ? x.vis - x.tile * kTile : 0;  // positions that exist
+            if (x.there && (pages < 0 || pages >= p.num_pages)) {
                 raise_flag(p.status, KVQ_FLAG_BAD_PAGE);
-                page = 0;
+                pages = 0;
             }
-            slot = (x.tile * kTile + t) & ((1 << p.lg_p) - 1);
-            src = p.pool + static_cast<long long>(page) * p.lay.bytes;
-        };
-        auto load_group = [&](int i) {  // chunks 2 i and 2 i + 1
-            codes[2 * i] = codes[2 * i + 1] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-            scales[i] = 0;
-            if (src != nullptr) {
-                const uint4* row = reinterpret_cast<const uint4*>(src + slot * (L / 2)) + hf;
-                codes[2 * i] = __ldg(row + 4 * i);
-                codes[2 * i + 1] = __ldg(row + 4 * i + 2);
-                const uint16_t* sc = reinterpret_cast<const uint16_t*>(src + p.lay.scales) + ((slot * L) >> p.lg_g);
-                scales[i] = __ldg(sc + ((128 * i + 32 * hf) >> p.lg_g)) |
-                            static_cast<uint32_t>(__ldg(sc + ((128 * i + 64 + 32 * hf) >> p.lg_g))) << 16;
-            }
-        };
-        auto load_keys = [&]() {
+            const int mask = (1 << lg_p) - 1;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                keys[i] = make_uint4(0, 0, 0, 0);
-                if (src != nullptr) keys[i] = __ldg(reinterpret_cast<const uint4*>(src + p.lay.rope + slot * (2 * kRope)) + 4 * hf + i);
+            for (int j = 0; j < JOBS; ++j) {
+                const int t = t0 + 4 * WPH * j;
+                const uint8_t* src = p.pool + static_cast<long long>(__shfl_sync(0xffffffffu, pages, t >> lg_p)) * p.lay.bytes;
+                codes[j] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+                scales[j] = 0;
+                if (t < end) {
+                    const int slot = t & mask;
+                    codes[j] = __ldg(reinterpret_cast<const uint4*>(src + slot * (L / 2)) + 8 * half + q);
+                    scales[j] = __ldg(reinterpret_cast<const uint16_t*>(src + p.lay.scales) +
+                                      ((slot * L + 256 * half + 32 * q) >> p.lg_g));
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = r0 + 32 * j;
+                const uint8_t* src = p.pool + static_cast<long long>(__shfl_sync(0xffffffffu, pages, t >> lg_p)) * p.lay.bytes;
+                keys[j] = make_uint4(0, 0, 0, 0);
+                if (t < end) keys[j] = __ldg(reinterpret_cast<const uint4*>(src + p.lay.rope + (t & mask) * (2 * kRope)) + q);
             }
         };
         auto store = [&](uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -395,13 +407,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
         if (st.units > 0) {
             next_tile(cur);
             nxt = cur;
-            find(cur, page_of(cur));
-#pragma unroll
-            for (int i = 0; i < G; ++i) load_group(i);
-            load_keys();
+            load(cur, pages_of(cur));
             if (cur.there) next_tile(nxt);
         }
-        int page = page_of(nxt);
+        int pages = pages_of(nxt);
 #pragma unroll 1
         while (cur.there) {
             if (cur.q != nullptr) {
@@ -429,51 +438,37 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full));
             }
-            const uint32_t row_s = k_s + t * 128;
+            if (n_tile > 0) wait_or_stop(smem_u32(&ctl->free[half]), (n_tile - 1) & 1, stop, p.status);
 #pragma unroll
-            for (int i = 0; i < G; ++i) {
-                uint32_t f[2][16];
+            for (int j = 0; j < JOBS; ++j) {
+                // half the scale, so that 7 times it stays finite (exact but for the smallest subnormals)
+                const uint32_t sc = h2_mul(scales[j] | scales[j] << 16, 0x38003800u);
+                const bool one = turn & 1, two = turn & 2;
+                const uint32_t a = one ? codes[j].y : codes[j].x, b = one ? codes[j].z : codes[j].y;
+                const uint32_t c = one ? codes[j].w : codes[j].z, d = one ? codes[j].x : codes[j].w;
+                const uint32_t ws[4] = {two ? c : a, two ? d : b, two ? a : c, two ? b : d};
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    // half the scale, so that 7 times it stays finite (exact but for the smallest subnormals)
-                    const uint32_t sc = h2_mul(prmt(scales[i], 0, c ? 0x3232 : 0x1010), 0x38003800u);
-                    const uint32_t ws[4] = {codes[2 * i + c].x, codes[2 * i + c].y, codes[2 * i + c].z, codes[2 * i + c].w};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t lo = ws[x], hi = ws[x] >> 8;
-                        f[c][4 * x] = h2_mul(unpack_lo(lo), sc);
-                        f[c][4 * x + 1] = h2_mul(unpack_hi(lo), sc);
-                        f[c][4 * x + 2] = h2_mul(unpack_lo(hi), sc);
-                        f[c][4 * x + 3] = h2_mul(unpack_hi(hi), sc);
-                    }
+                for (int x = 0; x < 4; ++x) {
+                    const uint32_t lo = ws[x], hi = ws[x] >> 8;
+                    store(to[x] + 4 * WPH * 128 * j, h2_mul(unpack_lo(lo), sc), h2_mul(unpack_hi(lo), sc), h2_mul(unpack_lo(hi), sc),
+                          h2_mul(unpack_hi(hi), sc));
                 }
-                if (n_tile > 0) wait_or_stop(smem_u32(&ctl->free[i]), (n_tile - 1) & 1, stop, p.status);
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        store(row_s + (2 * i + c) * kChunk + (((4 * hf + x) ^ (t & 7)) << 4), f[c][4 * x], f[c][4 * x + 1],
-                              f[c][4 * x + 2], f[c][4 * x + 3]);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ctl->full[i]));
             }
-            if (n_tile > 0) wait_or_stop(smem_u32(&ctl->free[4]), (n_tile - 1) & 1, stop, p.status);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                store(row_s + (Z::kChunks - 1) * kChunk + (((4 * hf + x) ^ (t & 7)) << 4), keys[x].x, keys[x].y, keys[x].z,
-                      keys[x].w);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ctl->full[4]));
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->full[half]));
+            if (n_tile > 0) wait_or_stop(smem_u32(&ctl->free[2]), (n_tile - 1) & 1, stop, p.status);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                store(k_s + (Z::kChunks - 1) * kChunk + swizzled(r0 + 32 * j, q), keys[j].x, keys[j].y, keys[j].z, keys[j].w);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->full[2]));
             // the next tile's rows (here and not between the stores: the fences above would wait for loads in flight)
-            find(nxt, page);
+            load(nxt, pages);
             Tile far = nxt;
             if (nxt.there) next_tile(far);
-            page = page_of(far);
-#pragma unroll
-            for (int i = 0; i < G; ++i) load_group(i);
-            load_keys();
+            pages = pages_of(far);
             ++n_tile;
             cur = nxt;
             nxt = far;
@@ -493,14 +488,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
 #pragma unroll 1
                 for (int i = 0; i < n; ++i, ++n_tile) {
 #pragma unroll 1
-                    for (int c = 0; c <= G; ++c) {  // pairs of chunks, then the rotary one
-                        live &= wait_or_stop(smem_u32(&ctl->full[c < G ? c : 4]), n_tile & 1, stop, p.status);
+                    for (int c = 0; c <= Z::kHalves; ++c) {  // four chunks, four chunks, the rotary one
+                        live &= wait_or_stop(smem_u32(&ctl->full[c < Z::kHalves ? c : 2]), n_tile & 1, stop, p.status);
                         tc_fence_after();
-                        const uint32_t a = desc_lo(k_s + 2 * c * kChunk, 16), b = desc_lo(q_s + 2 * c * Z::kQChunk, 16);
+                        const uint32_t a = desc_lo(k_s + 4 * c * kChunk, 16), b = desc_lo(q_s + 4 * c * Z::kQChunk, 16);
                         if (elect_one() && live) {
 #pragma unroll
-                            for (int x = 0; x < 8; ++x)
-                                if (x < 4 || c < G)
+                            for (int x = 0; x < 16; ++x)
+                                if (x < 4 || c < Z::kHalves)
                                     mma_ss(tm + Z::kS, smem_desc(a + (((x / 4) * kChunk + (x % 4) * 32) >> 4)),
                                            smem_desc(b + (((x / 4) * Z::kQChunk + (x % 4) * 32) >> 4)), kIdS, c > 0 || x > 0);
                         }
@@ -521,9 +516,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                             for (int x = 0; x < kTile / 16; ++x)
                                 mma_ss(tm + m * NC, smem_desc(a + (x * 2048 >> 4)), smem_desc(b + (x * 2048 >> 4)), kIdO,
                                        i > 0 || x > 0);
-                            mma_commit(smem_u32(&ctl->free[m]));
+                            if (m & 1) mma_commit(smem_u32(&ctl->free[m / 2]));
                         }
-                        mma_commit(smem_u32(&ctl->free[4]));
+                        mma_commit(smem_u32(&ctl->free[2]));
                         if (i + 1 == n) mma_commit(smem_u32(&ctl->o_done));
                     }
                     __syncwarp();
