@@ -582,28 +582,28 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 template <int D>
 __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant__ ChunkParams p, int ctas) {
     __shared__ MergeShare share;
-    __shared__ float4 sums[8][32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // lanes hold 4 columns of a row each (D = 64: half of the lanes)
     merge_items<1>(
-        p, ctas, p.r, &share, &sums[0][0],
-        [&](long long slot, int line, float& m, float& l, float4 (&o)[1], int lane) {
+        p, ctas, p.r, &share,
+        [&](long long slot, int line, int, float& m, float& l, float4& o, int lane) {
             const int tok = line / p.r;
             const long long at = slot * 256 + (tok / p.T) * kTile + (tok % p.T) * p.r + line - tok * p.r;
-            m = p.part_ml[2 * at];
-            l = p.part_ml[2 * at + 1];
-            o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (4 * lane < D) o[0] = reinterpret_cast<const float4*>(p.part_o + at * D)[lane];
+            const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
+            m = ml.x;
+            l = ml.y;
+            o = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (4 * lane < D) o = reinterpret_cast<const float4*>(p.part_o + at * D)[lane];
         },
-        [&](const MergeDesc& d, int line, float l, const float4 (&o)[1], int lane) {
+        [&](const MergeDesc& d, int line, int, float l, const float4& o, int lane) {
             if (4 * lane >= D) return;
             const float inv = l > 0.f ? 2.f / l : 0.f;
             const int tok = line / p.r;
             // columns 4 lane .. of the 8 that share 16 bytes: dimensions 0 4 1 5 or 2 6 3 7
             __half* out = p.out + (static_cast<long long>(d.line0 + tok) * p.Hq + d.h * p.r + line - tok * p.r) * D + (lane & ~1) * 4 +
                           (lane & 1) * 2;
-            *reinterpret_cast<uint32_t*>(out) = pack_h2(o[0].x * inv, o[0].z * inv);
-            *reinterpret_cast<uint32_t*>(out + 4) = pack_h2(o[0].y * inv, o[0].w * inv);
+            *reinterpret_cast<uint32_t*>(out) = pack_h2(o.x * inv, o.z * inv);
+            *reinterpret_cast<uint32_t*>(out + 4) = pack_h2(o.y * inv, o.w * inv);
         });
 }
 

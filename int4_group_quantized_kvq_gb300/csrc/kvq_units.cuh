@@ -121,11 +121,18 @@ struct Walk {
     }
 };
 
+// c U / C (in 32 bits where that is enough: a 64-bit division takes a microsecond's fifth).
+__device__ __forceinline__ long long slice(long long c, long long U, long long C) {
+    if (U < (1 << 23) && C < 512) return static_cast<uint32_t>(c) * static_cast<uint32_t>(U) / static_cast<uint32_t>(C);
+    return c * U / C;
+}
+
 // The CTA's run of units: all threads (with barriers of the CTA).  A thread counts the units of a sequence
 // per head.  warp_sum: THREADS / 32 numbers in shared memory.
 template <int THREADS>
 __device__ __forceinline__ void find_start(const Units& p, Start* start, long long* warp_sum) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+    const long long cta = blockIdx.x;
     auto count = [&](int b) -> long long {
         if (b >= p.B) return 0;
         const Seq s = sequence(p, b);
@@ -140,6 +147,10 @@ __device__ __forceinline__ void find_start(const Units& p, Start* start, long lo
         if (b == tid) first = u;
         mine += u;
     }
+    if (tid == 0) {
+        *start = Start{0, 0, 0, 0, 0};
+        p.desc[cta].parts = 0;
+    }
     auto block_scan = [&](long long v, long long& total) -> long long {  // inclusive
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -150,37 +161,39 @@ __device__ __forceinline__ void find_start(const Units& p, Start* start, long lo
         __syncthreads();
         long long before = 0;
         total = 0;
-#pragma unroll
+#pragma unroll 4
         for (int w = 0; w < THREADS / 32; ++w) {
             const long long t = warp_sum[w];
             if (w < warp) before += t;
             total += t;
         }
-        __syncthreads();
         return v + before;
     };
     long long U;
-    block_scan(mine, U);
+    long long incl = block_scan(mine, U);
     const long long C = min(static_cast<long long>(gridDim.x), U);
-    const long long cta = blockIdx.x;
-    if (tid == 0) {
-        *start = Start{0, 0, 0, 0, 0};
-        p.desc[cta].parts = 0;
-    }
-    __syncthreads();
-    if (cta >= C) return;
-    const long long u0 = cta * U / C, u1 = (cta + 1) * U / C;
+    if (cta >= C) return;  // (the whole CTA)
+    const long long u0 = slice(cta, U, C), u1 = slice(cta + 1, U, C);
     long long base = 0;
     for (int b0 = 0; b0 < p.B; b0 += THREADS) {
         const long long v = b0 == 0 ? first : count(b0 + tid);
-        long long total;
-        const long long incl = base + block_scan(v, total), excl = incl - v;
+        if (p.B > THREADS) {  // (else the first scan has it)
+            long long total;
+            __syncthreads();
+            incl = base + block_scan(v, total);
+            base += total;
+        }
+        const long long excl = incl - v;
         if (u0 >= excl && u0 < incl) {  // one thread
             const int b = b0 + tid;
             const Seq s = sequence(p, b);
-            const long long per = v / p.heads;
-            const int h = static_cast<int>((u0 - excl) / per);
-            long long rem = u0 - excl - h * per;
+            int h = 0;
+            long long rem = u0 - excl;
+            if (p.heads > 1) {
+                const long long per = v / p.heads;
+                h = static_cast<int>(rem < (1ll << 31) ? static_cast<uint32_t>(rem) / static_cast<uint32_t>(per) : rem / per);
+                rem -= h * per;
+            }
             int j = 0, nt;
             while (true) {
                 nt = tiles_of(visible(p, s, j));
@@ -193,14 +206,16 @@ __device__ __forceinline__ void find_start(const Units& p, Start* start, long lo
             const int k = static_cast<int>(max(0ll, u0 - i0));
             *start = Start{b, h, j, k, u1 - (k > 0 ? u0 : i0 - kItemUnits)};
             // this CTA starts inside an item: is its part the item's second one?
-            if (k > 0 && (cta - 1) * U / C <= i0) {
-                int parts = 1;
-                for (long long c = cta; c < C && c * U / C < i0 + nt; ++c) ++parts;
-                p.desc[cta] = MergeDesc{parts, s.row0 * p.per_row + j * p.step,
+            if (k > 0 && slice(cta - 1, U, C) <= i0) {
+                // the CTAs that start before the item's end (an estimate, and at most a step or two from it)
+                long long c = cta + 1;
+                if (U < (1 << 23) && C < 512) c = max(c, static_cast<long long>(static_cast<uint32_t>(i0 + nt) * static_cast<uint32_t>(C) / static_cast<uint32_t>(U)));
+                while (c > cta + 1 && slice(c - 1, U, C) >= i0 + nt) --c;
+                while (c < C && slice(c, U, C) < i0 + nt) ++c;
+                p.desc[cta] = MergeDesc{static_cast<int>(c - cta) + 1, s.row0 * p.per_row + j * p.step,
                                         min(p.step, static_cast<int>(lines_of(p, s)) - j * p.step), h};
             }
         }
-        base += total;
         if (base > u0) break;
     }
     __syncthreads();
@@ -213,26 +228,26 @@ __device__ __forceinline__ int partial_slot(const Segment& g) { return 2 * block
 
 constexpr int kMaxCtas = 256;  // of an attention grid
 
-// The merges of a call, shared out over a grid of 256-thread CTAs: a warp merges a line of an item of few
-// parts, a CTA one of many (its warps take the parts in turn).  `first` counts the pieces of work ahead of
-// each descriptor's.
+// The merges of a call, shared out over a grid of 256-thread CTAs in pieces of 128 dimensions of a line: a
+// warp merges a piece of an item of few parts, a CTA one of many (its warps take the parts in turn).
+// `first` counts the units of work ahead of each descriptor's: eight pieces, or one.
 struct MergeShare {
     int first[kMaxCtas + 1];
     int warp_sum[8];
     float ml[8][2];
+    float4 sums[8][32];
 };
 constexpr int kFewParts = 8;
 
-// E float4 of a line per lane.  fetch(slot, line, m, l, o, lane) reads a part, put(desc, line, l, o, lane)
-// writes the merged line; lines: `mult` times the descriptor's.  sums: shared memory, [8][32 E] float4.
+// A line has E pieces, four dimensions of one to a lane.  fetch(slot, line, e, m, l, o, lane) reads a part,
+// put(desc, line, e, l, o, lane) writes what is merged; lines: `mult` times the descriptor's.
 template <int E, class FETCH, class PUT>
-__device__ __forceinline__ void merge_items(const Units& p, int ctas, int mult, MergeShare* share, float4* sums, FETCH fetch,
-                                            PUT put) {
+__device__ __forceinline__ void merge_items(const Units& p, int ctas, int mult, MergeShare* share, FETCH fetch, PUT put) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     int mine = 0;
     if (tid < ctas) {
         const MergeDesc d = p.desc[tid];
-        if (d.parts > 0) mine = d.parts > kFewParts ? d.lines * mult : (d.lines * mult + 7) / 8;
+        if (d.parts > 0) mine = d.parts > kFewParts ? d.lines * mult * E : (d.lines * mult * E + 7) / 8;
     }
     int incl = mine;
 #pragma unroll
@@ -247,21 +262,18 @@ __device__ __forceinline__ void merge_items(const Units& p, int ctas, int mult, 
     if (tid == 255) share->first[256] = incl;
     __syncthreads();
     const int total = share->first[256];
-    auto add = [&](float& m, float& l, float4 (&o)[E], float mk, float lk, const float4 (&ok)[E]) {
-        if (lk <= 0.f) return;
-        const float mn = fmaxf(m, mk), a = fast_exp2(m - mn), ak = fast_exp2(mk - mn);
+    auto add = [&](float& m, float& l, float4& o, float mk, float lk, const float4& ok) {
+        const float mn = fmaxf(m, mk), at = mn == -INFINITY ? 0.f : mn;  // (a part that saw nothing: weight 0)
+        const float a = fast_exp2(m - at), ak = fast_exp2(mk - at);
         l = l * a + lk * ak;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            o[e].x = o[e].x * a + ok[e].x * ak;
-            o[e].y = o[e].y * a + ok[e].y * ak;
-            o[e].z = o[e].z * a + ok[e].z * ak;
-            o[e].w = o[e].w * a + ok[e].w * ak;
-        }
+        o.x = o.x * a + ok.x * ak;
+        o.y = o.y * a + ok.y * ak;
+        o.z = o.z * a + ok.z * ak;
+        o.w = o.w * a + ok.w * ak;
         m = mn;
     };
     for (int u = blockIdx.x; u < total; u += gridDim.x) {
-        int lo = 0, hi = 255;  // the last descriptor whose pieces start at or before u: it has some
+        int lo = 0, hi = 255;  // the last descriptor whose units start at or before u: it has some
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
             if (share->first[mid] <= u) lo = mid;
@@ -269,37 +281,31 @@ __device__ __forceinline__ void merge_items(const Units& p, int ctas, int mult, 
         }
         const MergeDesc d = p.desc[lo];
         const bool wide = d.parts > kFewParts;
-        const int line = wide ? u - share->first[lo] : (u - share->first[lo]) * 8 + warp;
+        const int piece = wide ? u - share->first[lo] : (u - share->first[lo]) * 8 + warp;
+        const int line = piece / E, e = piece - line * E;
         float m = -INFINITY, l = 0.f;
-        float4 o[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         if (line < d.lines * mult) {
-#pragma unroll 2
+#pragma unroll 4
             for (int k = wide ? warp : 0; k < d.parts; k += wide ? 8 : 1) {
                 float mk, lk;
-                float4 ok[E];
-                fetch(k == 0 ? 2 * (lo - 1) + 1 : 2 * (lo + k - 1), line, mk, lk, ok, lane);
+                float4 ok;
+                fetch(k == 0 ? 2 * (lo - 1) + 1 : 2 * (lo + k - 1), line, e, mk, lk, ok, lane);
                 add(m, l, o, mk, lk, ok);
             }
-            if (!wide) put(d, line, l, o, lane);
+            if (!wide) put(d, line, e, l, o, lane);
         }
         if (!wide) continue;
-#pragma unroll
-        for (int e = 0; e < E; ++e) sums[(warp * E + e) * 32 + lane] = o[e];
+        share->sums[warp][lane] = o;
         if (lane == 0) {
             share->ml[warp][0] = m;
             share->ml[warp][1] = l;
         }
         __syncthreads();
         if (warp == 0) {
-            for (int w = 1; w < 8; ++w) {
-                float4 ok[E];
 #pragma unroll
-                for (int e = 0; e < E; ++e) ok[e] = sums[(w * E + e) * 32 + lane];
-                add(m, l, o, share->ml[w][0], share->ml[w][1], ok);
-            }
-            put(d, line, l, o, lane);
+            for (int w = 1; w < 8; ++w) add(m, l, o, share->ml[w][0], share->ml[w][1], share->sums[w][lane]);
+            put(d, line, e, l, o, lane);
         }
         __syncthreads();
     }

@@ -537,26 +537,21 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
 // The items cut between CTAs.
 template <int L, int NC>
 __global__ void __launch_bounds__(256) latent_merge_kernel(const __grid_constant__ LatentParams p, int ctas) {
-    constexpr int E = L / 128;  // runs of 4 dimensions a lane holds, 128 apart
     __shared__ MergeShare share;
-    __shared__ float4 sums[8][L / 4];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    merge_items<E>(
-        p, ctas, 1, &share, &sums[0][0],
-        [&](long long slot, int line, float& m, float& l, float4 (&o)[E], int lane) {
+    merge_items<L / 128>(
+        p, ctas, 1, &share,
+        [&](long long slot, int line, int e, float& m, float& l, float4& o, int lane) {
             const long long at = slot * NC + line;
-            m = p.part_ml[2 * at];
-            l = p.part_ml[2 * at + 1];
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = reinterpret_cast<const float4*>(p.part_o + at * L)[32 * e + lane];
+            const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
+            m = ml.x;
+            l = ml.y;
+            o = reinterpret_cast<const float4*>(p.part_o + at * L)[32 * e + lane];
         },
-        [&](const MergeDesc& d, int line, float l, const float4 (&o)[E], int lane) {
+        [&](const MergeDesc& d, int line, int e, float l, const float4& o, int lane) {
             const float inv = l > 0.f ? 2.f / l : 0.f;
-            __half* out = p.out + (static_cast<long long>(d.line0) + line) * L;
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                reinterpret_cast<uint2*>(out)[32 * e + lane] =
-                    make_uint2(pack_h2(o[e].x * inv, o[e].y * inv), pack_h2(o[e].z * inv, o[e].w * inv));
+            reinterpret_cast<uint2*>(p.out + (static_cast<long long>(d.line0) + line) * L)[32 * e + lane] =
+                make_uint2(pack_h2(o.x * inv, o.y * inv), pack_h2(o.z * inv, o.w * inv));
         });
 }
 
