@@ -18,6 +18,15 @@ by that measure to a budget of positions, each KV head keeping its own
 differential attention, for a cache made with ``diff`` (``kvq_diff_decode_attention`` /
 ``kvq_diff_decode_step``); they know no window and add nothing to the weights.
 
+Prompts, parts of prompts and drafted tokens (any number of new rows per sequence, ``cu_rows``), in a cache made
+with ``rows``:
+``append_rotary`` turns queries and keys by their positions and quantizes the rows into the pages
+(``kvq_rope_append``), ``attend_rows`` attends with them (``kvq_chunk_attention``), ``prompt_step`` does both,
+and ``read_rows`` dequantizes rows (``kvq_dequantize_varlen``).
+
+``LatentKVCache`` holds one layer's latent cache: ``step`` appends new rows (``kvq_latent_append``) and
+attends in the absorbed form (``kvq_latent_attention``), for single tokens and prompts alike.
+
 ``decode_step_host`` is the same step driven from pinned host buffers (``HostStaging``)
 in one kvq_decode_step_host call: the step's q, K and V are copied in with one transfer
 and the output copied back, on the same stream; ``HostPipeline`` overlaps those copies
@@ -35,8 +44,13 @@ from . import binding as B
 class PagedKVCache:
     def __init__(self, cfg: B.CacheConfig, block_table: torch.Tensor, num_q_heads: int, max_len: int,
                  device="cuda", pool: torch.Tensor | None = None, window: int = 0, sinks: int = 0,
-                 track_weights: bool = False, decay: float = 1.0, diff: bool = False):
+                 track_weights: bool = False, decay: float = 1.0, diff: bool = False,
+                 rows: bool = False, rope: B.RopeConfig | None = None, cos_sin: torch.Tensor | None = None):
         self.cfg = cfg
+        if (rope is None) != (cos_sin is None):
+            raise ValueError("rotary positions need both rope and its table cos_sin")
+        self.rope = rope
+        self.cos_sin = cos_sin
         self.window = int(window)
         self.sinks = int(sinks)
         self.device = torch.device(device)
@@ -56,6 +70,10 @@ class PagedKVCache:
             raise ValueError("differential attention attends to every position (no window)")
         self.diff_workspace = B.new_diff_workspace(cfg, self.batch, self.num_q_heads, self.max_len,
                                                    device=self.device) if diff else None
+        if rows and (self.window > 0 or track_weights):
+            raise ValueError("attention of many rows attends to every position (no window) and tracks no weights")
+        self.rows_workspace = B.new_chunk_workspace(cfg, self.batch, self.num_q_heads, self.max_len,
+                                                    device=self.device) if rows else None
         if track_weights:
             if self.window > 0:
                 raise ValueError("a cache with a window does not track weights")
@@ -159,6 +177,39 @@ class PagedKVCache:
                                self.max_len, self.softmax_scale * math.sqrt(2.0), lam, norm_weight, norm_eps,
                                out_scale, out, self.diff_workspace, stream=stream)
 
+    def append_rotary(self, q, k, v, q_out, start_pos, cu_rows, positions=None, stream=None) -> None:
+        """Turn q into q_out (both fp16 [T, Hq, d]; the same tensor: in place) and k, and quantize k, v (fp16
+        [T, Hkv, d]) into positions start_pos[b] .. of every sequence: rows cu_rows[b] .. cu_rows[b + 1] - 1 are its
+        new ones.  positions (int32 [axes, T]): where the angles are taken, if not at the rows' places in the cache.
+        For a cache made with rope and cos_sin."""
+        if self.rope is None:
+            raise ValueError("append_rotary needs a cache made with rope and cos_sin")
+        B.kvq_rope_append(self.cfg, self.rope, self.pool, q, k, v, q_out, self.cos_sin, self.block_table, start_pos, cu_rows,
+                          positions=positions, status=self.status, stream=stream)
+
+    def attend_rows(self, q, seq_lens, cu_rows, out, stream=None) -> None:
+        """Causal attention of the last rows of every sequence: q fp16 [T, Hq, d] at the last positions of seq_lens
+        (which include them) into out (fp16 [T, Hq, d]).  For a cache made with `rows`."""
+        if self.rows_workspace is None:
+            raise ValueError("attend_rows needs a cache made with rows")
+        B.kvq_chunk_attention(self.cfg, self.pool, q, self.block_table, seq_lens, cu_rows, self.max_len, self.softmax_scale,
+                              out, self.rows_workspace, stream=stream)
+
+    def prompt_step(self, q, k, v, start_pos, seq_lens, cu_rows, out, positions=None, stream=None) -> None:
+        """New rows of every sequence, a prompt or a part of one: append_rotary (q in place), then attend_rows;
+        without rope, kvq_quantize_append_varlen in its place.  seq_lens[b] = start_pos[b] + new rows."""
+        if self.rope is not None:
+            self.append_rotary(q, k, v, q, start_pos, cu_rows, positions, stream)
+        else:
+            B.kvq_quantize_append_varlen(self.cfg, self.pool, k, v, self.block_table, start_pos, cu_rows, status=self.status,
+                                         stream=stream)
+        self.attend_rows(q, seq_lens, cu_rows, out, stream)
+
+    def read_rows(self, start_pos, cu_rows, out_k, out_v, stream=None) -> None:
+        """Positions start_pos[b] .. of every sequence, dequantized into out_k, out_v (fp16 or fp32 [T, Hkv, d])."""
+        B.kvq_dequantize_varlen(self.cfg, self.pool, self.block_table, start_pos, cu_rows, out_k, out_v,
+                                status=self.status, stream=stream)
+
     def decode_step_host(self, staging: "HostStaging", append_pos, seq_lens, stream=None) -> None:
         """The decode step from pinned host memory in one kvq_decode_step_host call: one H2D copy of
         the step's q, K and V (staged back to back), the step, one D2H copy of the output, all
@@ -174,7 +225,57 @@ class PagedKVCache:
     def flags(self) -> int:
         """Status flags of the last calls (synchronizes)."""
         f = B.kvq_read_status(self.status) | B.kvq_read_status(self.workspace)
+        if self.rows_workspace is not None:
+            f |= B.kvq_read_status(self.rows_workspace)
         return f if self.diff_workspace is None else f | B.kvq_read_status(self.diff_workspace)
+
+
+class LatentKVCache:
+    """One layer's latent cache: pages of 4-bit latents and fp16 rotary keys, one row per token for all heads."""
+
+    def __init__(self, cfg: B.LatentConfig, block_table: torch.Tensor, num_heads: int, max_len: int, rope: B.RopeConfig,
+                 cos_sin: torch.Tensor, softmax_scale: float, norm_weight: torch.Tensor | None = None,
+                 norm_eps: float = 1e-6, device="cuda", pool: torch.Tensor | None = None):
+        self.cfg = cfg
+        self.device = torch.device(device)
+        self.block_table = block_table.to(self.device, torch.int32).contiguous()
+        self.batch = int(self.block_table.shape[0])
+        self.num_heads = int(num_heads)
+        self.max_len = int(max_len)
+        self.rope, self.cos_sin = rope, cos_sin
+        self.softmax_scale = float(softmax_scale)
+        self.norm_weight, self.norm_eps = norm_weight, float(norm_eps)
+        nbytes = B.kvq_latent_pool_bytes(cfg)
+        self.pool = torch.zeros(nbytes, dtype=torch.uint8, device=self.device) if pool is None else pool
+        if self.pool.numel() < nbytes:
+            raise ValueError(f"pool has {self.pool.numel()} bytes, needs {nbytes}")
+        self.workspace = B.new_latent_workspace(cfg, self.batch, self.num_heads, self.max_len, device=self.device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def append(self, rows, q_pe, q, start_pos, cu_rows, positions=None, stream=None) -> None:
+        """New rows (fp16 [T, L + R]: latent, rotary key) of every sequence into positions start_pos[b] ..; q_pe (fp16
+        [T, H, R]) turned into the last R values of q (fp16 [T, H, L + R]), or both None."""
+        B.kvq_latent_append(self.cfg, self.rope, self.pool, rows, self.norm_weight, self.norm_eps, q_pe, q, self.cos_sin,
+                            self.block_table, start_pos, cu_rows, positions=positions, status=self.status, stream=stream)
+
+    def attend(self, q, seq_lens, cu_rows, out, stream=None) -> None:
+        """Attention in the absorbed form: q fp16 [T, H, L + R] at the last positions of seq_lens, out fp16 [T, H, L]."""
+        B.kvq_latent_attention(self.cfg, self.pool, q, self.block_table, seq_lens, cu_rows, self.max_len,
+                               self.softmax_scale, out, self.workspace, stream=stream)
+
+    def step(self, rows, q_pe, q, start_pos, seq_lens, cu_rows, out, positions=None, stream=None) -> None:
+        """append, then attend: a decode step with one row per sequence, a prompt with many."""
+        self.append(rows, q_pe, q, start_pos, cu_rows, positions, stream)
+        self.attend(q, seq_lens, cu_rows, out, stream)
+
+    def read_rows(self, start_pos, cu_rows, out, stream=None) -> None:
+        """Rows read back into out (fp16 [T, L + R]), for the expanded form's matrix products."""
+        B.kvq_latent_dequantize(self.cfg, self.pool, self.block_table, start_pos, cu_rows, out, status=self.status,
+                                stream=stream)
+
+    def flags(self) -> int:
+        """Status flags of the last calls (synchronizes)."""
+        return B.kvq_read_status(self.status) | B.kvq_read_status(self.workspace)
 
 
 class HostStaging:
