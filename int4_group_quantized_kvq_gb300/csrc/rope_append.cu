@@ -46,6 +46,19 @@ __global__ void __launch_bounds__(256, 3) rope_append_kernel(RopeAppendArgs a) {
         const int row = static_cast<int>(task / a.slices);
         const int h0 = static_cast<int>(task - static_cast<long long>(row) * a.slices) * per;
         const int h1 = min(heads, h0 + per);
+        const __half* qr = a.q + row * a.q_stride;
+        const __half* kr = a.k + row * a.k_stride;
+        const __half* vr = a.v + row * a.v_stride;
+        auto load = [&](int h, uint4 (&r)[2]) {
+            r[0] = r[1] = make_uint4(0, 0, 0, 0);
+            if (h >= h1) return;
+            const __half* src = h < a.Hq ? qr + h * D : h < a.Hq + a.Hkv ? kr + (h - a.Hq) * D : vr + (h - a.Hq - a.Hkv) * D;
+            r[0] = __ldcs(reinterpret_cast<const uint4*>(src + o0));
+            r[1] = __ldcs(reinterpret_cast<const uint4*>(src + o1));
+        };
+        // the first values are on their way while the row's place is looked up (a chain of dependent loads)
+        uint4 raw[2], nxt[2];
+        load(h0 + team, raw);
         const int b = warp_find_seq(a.cu_rows, a.B, row, lane);
         if (b < 0) continue;  // behind the last sequence
         const long long pos = static_cast<long long>(__ldg(a.start_pos + b)) + (row - __ldg(a.cu_rows + b));
@@ -70,13 +83,24 @@ __global__ void __launch_bounds__(256, 3) rope_append_kernel(RopeAppendArgs a) {
                 if (x < a.axes) p[x] = __ldg(a.positions + static_cast<long long>(x) * a.rows + row);
                 bad |= p[x] < 0 || p[x] >= a.table_len;
             }
+            auto axis_of = [&](int pair) { return pair < a.bound0 ? p[0] : pair < a.bound1 ? p[1] : p[2]; };
+            const int at0 = axis_of(8 * tl);
             if (turned && !bad) {
+                const float* t = a.table + static_cast<long long>(at0) * a.rot + 8 * tl;
+                const bool one = (8 * tl < a.bound0) == (8 * tl + 7 < a.bound0) && (8 * tl < a.bound1) == (8 * tl + 7 < a.bound1);
+                if (one) {  // the lane's pairs turn with one axis
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int pair = 8 * tl + i;
-                    const int at = pair < a.bound0 ? p[0] : pair < a.bound1 ? p[1] : p[2];
-                    c[i] = __ldg(a.table + static_cast<long long>(at) * a.rot + pair);
-                    n[i] = __ldg(a.table + static_cast<long long>(at) * a.rot + half + pair);
+                    for (int i = 0; i < 2; ++i) {
+                        reinterpret_cast<float4*>(c)[i] = __ldg(reinterpret_cast<const float4*>(t) + i);
+                        reinterpret_cast<float4*>(n)[i] = __ldg(reinterpret_cast<const float4*>(t + half) + i);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float* ti = a.table + static_cast<long long>(axis_of(8 * tl + i)) * a.rot + 8 * tl + i;
+                        c[i] = __ldg(ti);
+                        n[i] = __ldg(ti + half);
+                    }
                 }
             }
         }
@@ -100,18 +124,6 @@ __global__ void __launch_bounds__(256, 3) rope_append_kernel(RopeAppendArgs a) {
                 }
             }
         }
-        const __half* qr = a.q + row * a.q_stride;
-        const __half* kr = a.k + row * a.k_stride;
-        const __half* vr = a.v + row * a.v_stride;
-        auto load = [&](int h, uint4 (&r)[2]) {
-            r[0] = r[1] = make_uint4(0, 0, 0, 0);
-            if (h >= h1 || (h >= a.Hq && blk == nullptr)) return;
-            const __half* src = h < a.Hq ? qr + h * D : h < a.Hq + a.Hkv ? kr + (h - a.Hq) * D : vr + (h - a.Hq - a.Hkv) * D;
-            r[0] = __ldcs(reinterpret_cast<const uint4*>(src + o0));
-            r[1] = __ldcs(reinterpret_cast<const uint4*>(src + o1));
-        };
-        uint4 raw[2], nxt[2];
-        load(h0 + team, raw);
 #pragma unroll 1
         for (int hb = h0; hb < h1; hb += TEAMS) {  // (the warp's teams take heads hb .. hb + TEAMS - 1)
             const int h = hb + team;
