@@ -25,34 +25,21 @@
 
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
-#include "kvq_tcgen05.cuh"
-#include "kvq_units.cuh"
+#include "chunk_shared.cuh"
 
 namespace kvq {
 namespace {
 
 constexpr int kThreads = 640;
-constexpr int kDqWarps = 8;
-constexpr int kRing = 3;      // operand tiles (K or V) in shared memory
-constexpr int kPacked = 3;    // packed tiles in shared memory
 constexpr uint32_t kTmem = 512;
-
-struct ChunkParams : Units {  // an item: the tokens of two row tiles
-    const uint8_t* pool;
-    const __half* q;
-    const int32_t* block_table;
-    __half* out;
-    float* part_ml;   // [2 gridDim.x][256][2]: maximum (of scale log2(e) z) and sum
-    float* part_o;    // [2 gridDim.x][256][D]
-    int32_t Hq, Hkv, r, T, max_blocks, num_pages, lg_p, lg_gk, lg_gv;  // T: tokens of a row tile
-    float c;          // 2 |scale| log2(e): keys are held halved
-    uint32_t q_flip;  // sign bits of a negative scale
-    BlockLayout L;
-};
+// Up to so many lines to a sequence, on average, lines are columns (chunk_few.cu).  Both sides, in us, lines
+// as columns first: four sequences of 32761 positions, 8 kv heads of 128, with 4 lines 88 and 108, with 32 lines
+// 94 and 109, with 64 (items of 64) 107 and 110, with 128 195 and 107; 24 short sequences of 3 to 12 lines, 25 and 31.
+// At 64 lines there is nothing to gain, and a long prompt among single tokens would pay for it.
+constexpr int kFewLines = 32;
 
 struct Ctl {
-    uint64_t pk_full[kPacked], pk_empty[kPacked];
-    uint64_t kv_full[kRing], kv_empty[kRing];
+    TileBars tiles;
     uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], turn;
     long long warp_sum[kThreads / 32];
     Start start;
@@ -64,7 +51,6 @@ struct Ctl {
 
 template <int D>
 struct Sizes {
-    static constexpr int kChunk = kTile * 128;               // bytes of a chunk [128][64] f16
     static constexpr int kOperand = kTile * D * 2;           // bytes of an operand tile
     static constexpr int kQ = 2 * kOperand;
 };
@@ -88,12 +74,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPacked; ++i) {
-            mbar_init(smem_u32(&ctl->pk_full[i]), 1);
-            mbar_init(smem_u32(&ctl->pk_empty[i]), kDqWarps);
+            mbar_init(smem_u32(&ctl->tiles.pk_full[i]), 1);
+            mbar_init(smem_u32(&ctl->tiles.pk_empty[i]), kDqWarps);
         }
         for (int i = 0; i < kRing; ++i) {
-            mbar_init(smem_u32(&ctl->kv_full[i]), kDqWarps);
-            mbar_init(smem_u32(&ctl->kv_empty[i]), 2);
+            mbar_init(smem_u32(&ctl->tiles.kv_full[i]), kDqWarps);
+            mbar_init(smem_u32(&ctl->tiles.kv_empty[i]), 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&ctl->q_full[i]), kDqWarps);
@@ -313,75 +299,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     } else if (warp < 8 + kDqWarps) {
         regs_less<72>();
         // ---- dequantize
-        constexpr int PARTS = D / 32;  // 16-byte pieces of a row's codes
         const int dw = warp - 8;
         uint32_t n_ring = 0, n_pk = 0, n_q0 = 0, n_q1 = 0;
         while (st.units > 0 && walk.next(p)) {
             const int n = g.k1 - g.k0;
             const int end0 = g.vis - g.k0 * kTile;
-            // tile i's keys (is_v 0) or values into the next operand tile
             auto dequant = [&](int i, int is_v) {
-                const uint32_t stage = n_ring % kRing, phase = n_ring / kRing;
-                const uint32_t pk = (n_pk + i) % kPacked;
-                if (is_v == 0) wait_or_stop(smem_u32(&ctl->pk_full[pk]), ((n_pk + i) / kPacked) & 1, stop, p.status);
-                const uint8_t* src = smem + Z::kQ + kRing * Z::kOperand + pk * packed_bytes;
-                const uint32_t dst = ring_s + stage * Z::kOperand;
-                const int lg_g = is_v ? p.lg_gv : p.lg_gk;
-                const int codes_off = is_v ? p.L.v_codes : 0, scales_off = is_v ? p.L.v_scales : p.L.k_scales;
-                const int end = end0 - i * kTile;  // tokens of the tile that exist
-                const int mask = (1 << p.lg_p) - 1;
-                constexpr int JOBS = kTile * PARTS / (32 * kDqWarps);
-                // 8 tokens x 4 pieces a warp: eight lanes of a piece read 128 bytes apart by rows (no bank twice)
-                // and write 8 rows' swizzled pieces (no bank twice)
-                uint32_t f[JOBS][16];
-#pragma unroll
-                for (int w = 0; w < JOBS; ++w) {
-                    const int job = (w * kDqWarps + dw) * 32 + lane;
-                    const int t = (job / (8 * PARTS)) * 8 + (job & 7);
-                    const int part = ((job >> 3) + (t & 7) * PARTS / 8) % PARTS;
-                    const uint8_t* blk = src + (t >> p.lg_p) * p.L.bytes;
-                    const int slot = t & mask;
-                    uint4 w4 = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-                    uint32_t s2 = 0;
-                    if (t < end) {
-                        w4 = *reinterpret_cast<const uint4*>(blk + codes_off + slot * (D / 2) + part * 16);
-                        s2 = *reinterpret_cast<const uint16_t*>(blk + scales_off + (((slot * D + part * 32) >> lg_g) << 1));
-                    }
-                    // half the scale, so that 7 times it stays finite (exact but for the smallest subnormals)
-                    const uint32_t sc = h2_mul(s2 | s2 << 16, 0x38003800u);
-                    const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t lo = ws[x], hi = ws[x] >> 8;
-                        f[w][4 * x] = h2_mul(unpack_lo(lo), sc);
-                        f[w][4 * x + 1] = h2_mul(unpack_hi(lo), sc);
-                        f[w][4 * x + 2] = h2_mul(unpack_lo(hi), sc);
-                        f[w][4 * x + 3] = h2_mul(unpack_hi(hi), sc);
-                    }
-                }
-                // only now the operand tile has to be free: the products wait for the stores alone
-                if (n_ring >= kRing) wait_or_stop(smem_u32(&ctl->kv_empty[stage]), (phase & 1) ^ 1, stop, p.status);
-                ++n_ring;
-#pragma unroll
-                for (int w = 0; w < JOBS; ++w) {
-                    const int job = (w * kDqWarps + dw) * 32 + lane;
-                    const int t = (job / (8 * PARTS)) * 8 + (job & 7);
-                    const int part = ((job >> 3) + (t & 7) * PARTS / 8) % PARTS;
-                    const uint32_t base = dst + (part / 2) * Z::kChunk + t * 128;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t at = base + ((((part & 1) * 4 + x) ^ (t & 7)) << 4);
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(f[w][4 * x]),
-                                     "r"(f[w][4 * x + 1]), "r"(f[w][4 * x + 2]), "r"(f[w][4 * x + 3])
-                                     : "memory");
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&ctl->kv_full[stage]));
-                    if (is_v) mbar_arrive(smem_u32(&ctl->pk_empty[pk]));
-                }
+                dequantize_tile<D>(p, ctl->tiles, smem + Z::kQ + kRing * Z::kOperand, packed_bytes, ring_s, n_pk + i,
+                                   end0 - i * kTile, is_v, dw, n_ring, stop);
             };
             // the item's row tile qs into shared memory, its dimensions in the order the unpack leaves (n_q: how many
             // have been there before)
@@ -408,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 #pragma unroll
                     for (int i = 0; i < LOADS; ++i) {
                         const int row = row0 + i * RPW * kDqWarps;
-                        const uint32_t at = q_s + qs * Z::kOperand + (piece / 8) * Z::kChunk + swizzled(row, piece % 8);
+                        const uint32_t at = q_s + qs * Z::kOperand + (piece / 8) * kChunk + swizzled(row, piece % 8);
                         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(prmt(x[i].x, x[i].z, 0x5410) ^ p.q_flip),
                                      "r"(prmt(x[i].x, x[i].z, 0x7632) ^ p.q_flip), "r"(prmt(x[i].y, x[i].w, 0x5410) ^ p.q_flip),
                                      "r"(prmt(x[i].y, x[i].w, 0x7632) ^ p.q_flip)
@@ -453,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             uint32_t n_ring = 0, n_q0 = 0, n_q1 = 0, n_p = 0, n_turn = 0;
             auto take = [&]() -> uint32_t {  // the next operand tile, in order
                 const uint32_t stage = n_ring % kRing;
-                live &= wait_or_stop(smem_u32(&ctl->kv_full[stage]), (n_ring / kRing) & 1, stop, p.status);
+                live &= wait_or_stop(smem_u32(&ctl->tiles.kv_full[stage]), (n_ring / kRing) & 1, stop, p.status);
                 ++n_ring;
                 tc_fence_after();
                 return stage;
@@ -492,12 +417,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         if (elect_one()) {
                             if (live && out) {
                                 const uint32_t a = tm + 128u * sw + 64, d = tm + 256u + D * sw;
-                                const uint32_t b = desc_lo(ring_s + v * Z::kOperand, Z::kChunk);
+                                const uint32_t b = desc_lo(ring_s + v * Z::kOperand, kChunk);
                                 const bool first = i < ahead;
 #pragma unroll
                                 for (int x = 0; x < kTile / 16; ++x)
                                     mma_ts(d, a + 8 * x, smem_desc(b + (x * 2048 >> 4)), kIdO, !first || x > 0);
-                                mma_commit(smem_u32(&ctl->kv_empty[v]));
+                                mma_commit(smem_u32(&ctl->tiles.kv_empty[v]));
                                 if (!in) mma_commit(smem_u32(&ctl->o_done[sw]));
                             }
                             if (live && in) {
@@ -506,17 +431,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                                 const uint32_t d = tm + 128u * sw;
 #pragma unroll
                                 for (int x = 0; x < D / 16; ++x) {
-                                    const uint32_t off = ((x / 4) * Z::kChunk + (x % 4) * 32) >> 4;
+                                    const uint32_t off = ((x / 4) * kChunk + (x % 4) * 32) >> 4;
                                     mma_ss(d, smem_desc(a + off), smem_desc(b + off), kIdS, x > 0);
                                 }
                                 mma_commit(smem_u32(&ctl->s_full[sw]));
-                                mma_commit(smem_u32(&ctl->kv_empty[k]));
+                                mma_commit(smem_u32(&ctl->tiles.kv_empty[k]));
                             }
                             mbar_arrive(smem_u32(&ctl->turn));
                         }
                     } else if (elect_one()) {
-                        if (out) mbar_arrive(smem_u32(&ctl->kv_empty[v]));
-                        if (in) mbar_arrive(smem_u32(&ctl->kv_empty[k]));
+                        if (out) mbar_arrive(smem_u32(&ctl->tiles.kv_empty[v]));
+                        if (in) mbar_arrive(smem_u32(&ctl->tiles.kv_empty[k]));
                     }
                     if (i + ahead + 1 == n && elect_one() && live) {  // no more scores of the item
                         mma_commit(smem_u32(&ctl->q_free[0]));
@@ -528,46 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             }
         } else if (warp == 18) {
             // ---- packed pages
-            uint32_t n_pk = 0;
-            const int per = kTile >> p.lg_p;  // pages of a tile
-            while (st.units > 0 && walk.next(p)) {
-                const int pages = (max(g.vis, 0) + (1 << p.lg_p) - 1) >> p.lg_p;  // the item's
-                const int32_t* table = p.block_table + static_cast<long long>(g.b) * p.max_blocks;
-                int base = g.k0 * per;  // lane l holds page base + l, and the one 32 later
-                auto look = [&](int at) -> int { return at < pages ? __ldg(table + at) : 0; };
-                int cur = look(base + lane), nxt = look(base + 32 + lane);
-                for (int i = g.k0; i < g.k1; ++i, ++n_pk) {
-                    const uint32_t pk = n_pk % kPacked;
-                    if (n_pk >= kPacked)
-                        wait_or_stop(smem_u32(&ctl->pk_empty[pk]), ((n_pk / kPacked) & 1) ^ 1, stop, p.status);
-                    const int first = i * per;
-                    if (first - base >= 32) {
-                        base += 32;
-                        cur = nxt;
-                        nxt = look(base + 32 + lane);
-                    }
-                    const int count = max(0, min(per, pages - first));
-                    const uint32_t bar = smem_u32(&ctl->pk_full[pk]);
-                    if (lane == 0 && !*stop) {
-                        if (count > 0) mbar_arrive_expect_tx(bar, count * p.L.bytes);
-                        else mbar_arrive(bar);
-                    }
-                    __syncwarp();
-                    int page = __shfl_sync(0xffffffffu, cur, (first - base + lane) & 31);
-                    if (lane < count && !*stop) {
-                        if (page < 0 || page >= p.num_pages) {
-                            raise_flag(p.status, KVQ_FLAG_BAD_PAGE);
-                            page = 0;
-                        }
-                        bulk_g2s(packed_s + pk * packed_bytes + lane * p.L.bytes,
-                                 p.pool + (static_cast<long long>(page) * p.Hkv + g.h) * p.L.bytes, p.L.bytes, bar);
-                    }
-                    __syncwarp();
-                }
-            }
-            // no copy of this CTA may be in flight when it leaves
-            for (uint32_t i = n_pk > kPacked ? n_pk - kPacked : 0; i < n_pk; ++i)
-                mbar_wait(smem_u32(&ctl->pk_full[i % kPacked]), (i / kPacked) & 1, 250000000ull);
+            load_pages(p, ctl->tiles, walk, packed_s, packed_bytes, st.units > 0, stop);
         }
     }
     tc_fence_before();
@@ -681,6 +567,9 @@ cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t stream) {
     p.c = std::fmax(2.f * std::fabs(a.softmax_scale) * 1.4426950408889634f, 1e-30f);
     p.q_flip = a.softmax_scale < 0.f ? 0x80008000u : 0u;
     p.L = a.L;
+    // Few lines to a sequence (on average): lines as columns instead of rows of 128
+    const long long lines = static_cast<long long>(a.rows) * p.r / a.B;
+    if (lines <= kFewLines) return launch_chunk_few(p, a.L.d, static_cast<int>(lines), sms, stream);
     return a.L.d == 64 ? launch<64>(p, sms, stream) : launch<128>(p, sms, stream);
 }
 
