@@ -31,6 +31,7 @@ namespace kvq {
 namespace {
 
 constexpr int kThreads = 640;
+constexpr int kRing = 3;  // operand tiles
 constexpr uint32_t kTmem = 512;
 // Up to so many lines to a sequence, on average, lines are columns (chunk_few.cu).  Both sides, in us, lines
 // as columns first: four sequences of 32761 positions, 8 kv heads of 128, with 4 lines 88 and 108, with 32 lines
@@ -305,8 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             const int n = g.k1 - g.k0;
             const int end0 = g.vis - g.k0 * kTile;
             auto dequant = [&](int i, int is_v) {
-                dequantize_tile<D>(p, ctl->tiles, smem + Z::kQ + kRing * Z::kOperand, packed_bytes, ring_s, n_pk + i,
-                                   end0 - i * kTile, is_v, dw, n_ring, stop);
+                dequantize_tile<D, false>(p, ctl->tiles, smem + Z::kQ + kRing * Z::kOperand, packed_bytes, ring_s, n_pk + i,
+                                          end0 - i * kTile, is_v, dw, n_ring % kRing, n_ring / kRing, stop);
+                ++n_ring;
             };
             // the item's row tile qs into shared memory, its dimensions in the order the unpack leaves (n_q: how many
             // have been there before)

@@ -11,8 +11,8 @@
 // The codes and scales are 140 MB, 20.8 us at the copy rate: it is the dequantization and its stores into
 // shared memory that bound it, not the copies.
 //
-// Warps of a CTA (one per SM): 0-7 softmax, 8-15 dequantize (and bring the queries), 16 the products, 17 the
-// packed pages.
+// Warps of a CTA (one per SM): 0-7 softmax, 8-15 dequantize the keys (and bring the queries), 16-23 the
+// values, 24 the products, 25 the packed pages.
 #include <cmath>
 
 #include "chunk_shared.cuh"
@@ -21,8 +21,9 @@
 namespace kvq {
 namespace {
 
-constexpr int kThreads = 640;
-constexpr int kSmWarps = 8, kMmaWarp = 16, kPageWarp = 17;
+constexpr int kThreads = 896;
+constexpr int kSmWarps = 8, kMmaWarp = 24, kPageWarp = 25;
+constexpr int kRing = 2;  // operand tiles of keys, and as many of values
 constexpr uint32_t kTmem = 256;  // columns: outputs from 0, two score tiles from 64
 
 template <int D, int NC>
@@ -31,7 +32,7 @@ struct Shape {
     static constexpr int kQChunk = NC * 128;                     // [NC][64] f16
     static constexpr int kQ = (D / 64) * kQChunk;
     // operand tiles, weights of two tiles ([128][NC] f16 in rows of 128 bytes), queries, packed tiles
-    static constexpr int kP = kRing * kOperand, kQAt = kP + 2 * kChunk, kPackedAt = kQAt + kQ;
+    static constexpr int kP = 2 * kRing * kOperand, kQAt = kP + 2 * kChunk, kPackedAt = kQAt + kQ;
 };
 
 template <int NC>
@@ -67,9 +68,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPacked; ++i) {
             mbar_init(smem_u32(&ctl->tiles.pk_full[i]), 1);
-            mbar_init(smem_u32(&ctl->tiles.pk_empty[i]), kDqWarps);
+            mbar_init(smem_u32(&ctl->tiles.pk_empty[i]), 2 * kDqWarps);
         }
-        for (int i = 0; i < kRing; ++i) {
+        for (int i = 0; i < 2 * kRing; ++i) {
             mbar_init(smem_u32(&ctl->tiles.kv_full[i]), kDqWarps);
             mbar_init(smem_u32(&ctl->tiles.kv_empty[i]), 1);
         }
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
     const Segment& g = walk.g;
 
     if (warp < kSmWarps) {
-        regs_more<104>();
+        regs_more<96>();
         // ---- softmax: position `t` of a tile, columns c0 .. c0 + HC - 1; the thread's tensor-memory lane is also a
         // dimension of the output
         constexpr int HC = NC / 2;
@@ -243,24 +244,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
             tc_fence_before();
             softmax_barrier();
         }
-    } else if (warp < kSmWarps + kDqWarps) {
-        regs_more<104>();
-        // ---- dequantize
-        const int dw = warp - kSmWarps, tid = threadIdx.x - 32 * kSmWarps;
-        uint32_t n_ring = 0, n_pk = 0, n_q = 0;
+    } else if (warp < kSmWarps + 2 * kDqWarps) {
+        regs_less<64>();
+        // ---- dequantize: eight warps the keys (and the queries), eight the values
+        const int is_v = warp >= kSmWarps + kDqWarps, dw = (warp - kSmWarps) % kDqWarps, tid = threadIdx.x - 32 * kSmWarps;
+        uint32_t n_pk = 0, n_q = 0;
         while (st.units > 0 && walk.next(p)) {
             const int n = g.k1 - g.k0, end0 = g.vis - g.k0 * kTile;
-            // in the order of the products, whose scores run a tile ahead: K0 K1 V0 K2 V1 ..
 #pragma unroll 1
-            for (int i = 0; i < 2 * n; ++i) {
-                int tile = i >> 1, is_v = i & 1;
-                if (i < 2 * n - 1) {
-                    is_v = i >= 2 && !(i & 1);
-                    tile = i < 2 ? i : i & 1 ? (i + 1) >> 1 : (i - 2) >> 1;
-                }
-                dequantize_tile<D>(p, ctl->tiles, smem + Z::kPackedAt, packed_bytes, ring_s, n_pk + tile, end0 - tile * kTile, is_v,
-                                   dw, n_ring, stop);
-                if (i > 0) continue;
+            for (int i = 0; i < n; ++i, ++n_pk) {
+                dequantize_tile<D, true>(p, ctl->tiles, smem + Z::kPackedAt, packed_bytes, ring_s, n_pk, end0 - i * kTile, is_v, dw,
+                                         kRing * is_v + n_pk % kRing, n_pk / kRing, stop);
+                if (i > 0 || is_v) continue;
                 // the item's queries, their dimensions in the order the unpack leaves
                 if (n_q > 0) wait_or_stop(smem_u32(&ctl->q_free), (n_q - 1) & 1, stop, p.status);
                 ++n_q;
@@ -282,20 +277,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full));
             }
-            n_pk += n;
         }
     } else {
-        regs_less<64>();
+        regs_less<56>();
         if (warp == kMmaWarp) {
             // ---- the products
             constexpr uint32_t kIdS = mma_idesc(kTile, NC, false, false), kIdO = mma_idesc(128, NC, true, true);
             const uint32_t tm = uniform(tmem);
             bool live = true;  // false once a wait has been given up: nothing more is issued
-            uint32_t n_ring = 0, n_seg = 0, n_b0 = 0, n_b1 = 0;
-            auto take = [&]() -> uint32_t {  // the next operand tile, in order
-                const uint32_t stage = n_ring % kRing;
-                live &= wait_or_stop(smem_u32(&ctl->tiles.kv_full[stage]), (n_ring / kRing) & 1, stop, p.status);
-                ++n_ring;
+            uint32_t n_k = 0, n_v = 0, n_seg = 0, n_b0 = 0, n_b1 = 0;
+            auto take = [&](uint32_t& n, uint32_t first) -> uint32_t {  // the next operand tile of keys or values
+                const uint32_t stage = first + n % kRing;
+                live &= wait_or_stop(smem_u32(&ctl->tiles.kv_full[stage]), (n / kRing) & 1, stop, p.status);
+                ++n;
                 return stage;
             };
             while (uniform(st.units > 0 && walk.next(p))) {
@@ -307,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
                 for (int i = -2; i < n; ++i) {
                     const int buf = i & 1;
                     if (i >= 0) {
-                        const uint32_t v = take();
+                        const uint32_t v = take(n_v, kRing);
                         live &= wait_or_stop(smem_u32(&ctl->p_full[buf]), ((buf ? n_b1 : n_b0) + (i >> 1)) & 1, stop, p.status);
                         tc_fence_after();
                         // (64 dimensions: the second half of M is the next operand tile's bytes, whatever they are; the
@@ -323,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
                         __syncwarp();
                     }
                     if (i + 2 < n) {
-                        const uint32_t k = take();
+                        const uint32_t k = take(n_k, 0);
                         tc_fence_after();
                         const uint32_t a = desc_lo(ring_s + k * Z::kOperand, 16), b = desc_lo(q_s, 16);
                         if (elect_one() && live) {
@@ -382,6 +376,7 @@ template <int D, int NC>
 cudaError_t launch(ChunkParams p, int ctas, cudaStream_t stream) {
     p.per_row = p.r;
     p.step = NC;
+    static_assert(1024 + Shape<D, NC>::kPackedAt + kPacked * kTile * (D + D / 8) + sizeof(Ctl<NC>) <= 232448, "");  // groups of 32
     const size_t smem = 1024 + Shape<D, NC>::kPackedAt + static_cast<size_t>(kPacked) * (kTile >> p.lg_p) * p.L.bytes + sizeof(Ctl<NC>);
     cudaError_t e = cudaFuncSetAttribute(chunk_few_kernel<D, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;

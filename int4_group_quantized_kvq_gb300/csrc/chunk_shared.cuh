@@ -12,7 +12,7 @@
 namespace kvq {
 
 constexpr int kDqWarps = 8;
-constexpr int kRing = 3;             // operand tiles (K or V) in shared memory
+constexpr int kMaxRing = 4;          // operand tiles (K or V) in shared memory, at most
 constexpr int kPacked = 3;           // packed tiles in shared memory
 constexpr int kChunk = kTile * 128;  // bytes of a chunk [128][64] f16
 
@@ -32,21 +32,25 @@ struct ChunkParams : Units {  // an item: the tokens of two row tiles
 // The barriers of the rings: packed tiles (copied, read), operand tiles (written, multiplied).
 struct TileBars {
     uint64_t pk_full[kPacked], pk_empty[kPacked];
-    uint64_t kv_full[kRing], kv_empty[kRing];
+    uint64_t kv_full[kMaxRing], kv_empty[kMaxRing];
 };
 
-// The keys (is_v 0) or values of packed tile n_tile into the next operand tile, `end` of whose positions
-// exist; by warp dw of kDqWarps.  n_ring counts the operand tiles.
-template <int D>
+// The keys (is_v 0) or values of packed tile n_tile, `end` of whose positions exist, into operand tile
+// `stage`, which was written `use` times before; by warp dw of kDqWarps.  APART: keys and values have
+// warps of their own (else the same ones dequantize a tile's keys, later its values).
+//
+// code x scale has 15 significant bits and is rounded to the 11 of f16, the operands' type: a relative
+// 2^-12 at most on average over a key's dimensions, which moves a score by about 2^-12 of its own spread.
+// (Exact operands would take a second product for the scales' lower bits, or one product per group.)
+template <int D, bool APART>
 __device__ __forceinline__ void dequantize_tile(const ChunkParams& p, TileBars& tiles, const uint8_t* packed, int packed_bytes,
-                                                uint32_t ring_s, uint32_t n_tile, int end, int is_v, int dw, uint32_t& n_ring,
-                                                volatile int* stop) {
+                                                uint32_t ring_s, uint32_t n_tile, int end, int is_v, int dw, uint32_t stage,
+                                                uint32_t use, volatile int* stop) {
     constexpr int PARTS = D / 32;  // 16-byte pieces of a row's codes
     constexpr int kOperand = kTile * D * 2;
     const int lane = threadIdx.x & 31;
-    const uint32_t stage = n_ring % kRing, phase = n_ring / kRing;
     const uint32_t pk = n_tile % kPacked;
-    if (is_v == 0) wait_or_stop(smem_u32(&tiles.pk_full[pk]), (n_tile / kPacked) & 1, stop, p.status);
+    if (APART || is_v == 0) wait_or_stop(smem_u32(&tiles.pk_full[pk]), (n_tile / kPacked) & 1, stop, p.status);
     const uint8_t* src = packed + pk * packed_bytes;
     const uint32_t dst = ring_s + stage * kOperand;
     const int lg_g = is_v ? p.lg_gv : p.lg_gk;
@@ -82,8 +86,7 @@ __device__ __forceinline__ void dequantize_tile(const ChunkParams& p, TileBars& 
         }
     }
     // only now the operand tile has to be free: the products wait for the stores alone
-    if (n_ring >= kRing) wait_or_stop(smem_u32(&tiles.kv_empty[stage]), (phase & 1) ^ 1, stop, p.status);
-    ++n_ring;
+    if (use > 0) wait_or_stop(smem_u32(&tiles.kv_empty[stage]), (use & 1) ^ 1, stop, p.status);
 #pragma unroll
     for (int w = 0; w < JOBS; ++w) {
         const int job = (w * kDqWarps + dw) * 32 + lane;
@@ -102,7 +105,7 @@ __device__ __forceinline__ void dequantize_tile(const ChunkParams& p, TileBars& 
     __syncwarp();
     if (lane == 0) {
         mbar_arrive(smem_u32(&tiles.kv_full[stage]));
-        if (is_v) mbar_arrive(smem_u32(&tiles.pk_empty[pk]));
+        if (APART || is_v) mbar_arrive(smem_u32(&tiles.pk_empty[pk]));
     }
 }
 
