@@ -640,7 +640,10 @@ int kvq_dequantize_varlen(const kvq_cache_config *cfg, const void *pool, const i
  *              word (zero it before the first call).  Nothing else in it has to be kept or cleared
  *              between calls; calls that share one must not overlap on the GPU.
  *   num_q_heads / num_kv_heads at most 8, head_dim 64 or 128.  A bad page reads as page 0 (flagged).
+ *   softmax_scale   any sign, at most 2^64 in size.
  *   Slots behind a sequence may hold any bytes; rows inside it must be finite.
+ * A copy or a product that does not complete in time raises KVQ_FLAG_WAIT_TIMEOUT; out is then not the
+ * attention.
  * Repeated calls agree bit for bit.
  * Returns KVQ_OK, KVQ_EINVAL, KVQ_EUNSUPPORTED, KVQ_EWORKSPACE or KVQ_ECUDA.
  */

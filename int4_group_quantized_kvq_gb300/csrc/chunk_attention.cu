@@ -34,9 +34,9 @@ constexpr int kThreads = 640;
 constexpr int kRing = 3;  // operand tiles
 constexpr uint32_t kTmem = 512;
 // Up to so many lines to a sequence, on average, lines are columns (chunk_few.cu).  Both sides, in us, lines
-// as columns first: four sequences of 32761 positions, 8 kv heads of 128, with 4 lines 88 and 108, with 32 lines
-// 94 and 109, with 64 (items of 64) 107 and 110, with 128 195 and 107; 24 short sequences of 3 to 12 lines, 25 and 31.
-// At 64 lines there is nothing to gain, and a long prompt among single tokens would pay for it.
+// as columns first: four sequences of 32761 positions, 8 kv heads of 128, with 4 lines 71 and 108, with 32 lines
+// 80 and 109, with 36 (two items) 136 and 110, with 64 138 and 110; 16 of 8000 positions with 32 lines 79 and 108;
+// 24 short sequences of 3 to 12 lines, 26 and 31.
 constexpr int kFewLines = 32;
 
 struct Ctl {
@@ -179,8 +179,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 }
                 m = m_new;
                 begun = true;
-                const float off = m == -INFINITY ? 0.f : -m * p.c;
-                const uint64_t c2 = pair_of(p.c, p.c), off2 = pair_of(off, off);
+                // The difference before the product: exact at the maximum however large the scores are, where a fused
+                // s c - m c would leave the rounding of m c (2% of a long prompt's time; a branch for large scores alone
+                // took the same)
+                const float ref = m == -INFINITY ? 0.f : -m;
+                const uint64_t c2 = pair_of(p.c, p.c), ref2 = pair_of(ref, ref);
                 uint64_t sums = 0, sums1 = 0;  // two sums each
                 // the second half first: the weights, two to a column, go to columns 64 .. 127, over scores that
                 // are in registers by now
@@ -191,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         uint32_t w[16];
 #pragma unroll
                         for (int y = 0; y < 16; ++y) {
-                            const uint64_t z = fma_pair(pair_of(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1])), c2, off2);
+                            const uint64_t z = mul_pair(add_pair(pair_of(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1])), ref2), c2);
                             float p0, p1;
                             split_pair(z, p0, p1);
                             p0 = fast_exp2(p0);

@@ -95,7 +95,8 @@ int check_table(const float* cos_sin, int32_t table_len, const int32_t* position
 
 int check_attention(const void* q, const void* out, int32_t max_len, float softmax_scale) {
     if (max_len < 0 || max_len > kMaxLen) return fail(KVQ_EINVAL, "max_len %d not in 0 .. 2^30", max_len);
-    if (!std::isfinite(softmax_scale)) return fail(KVQ_EINVAL, "softmax_scale is not finite");
+    // (2^64: fp16 queries and keys then keep every score, in powers of two, below fp32's largest)
+    if (!(std::fabs(softmax_scale) <= 1.8446744e19f)) return fail(KVQ_EINVAL, "softmax_scale is not finite or above 2^64");
     if (!q || !out) return fail(KVQ_EINVAL, "NULL device pointer");
     if (!aligned(q, 16) || !aligned(out, 16)) return fail(KVQ_EINVAL, "q and out must be 16-byte aligned");
     return KVQ_OK;

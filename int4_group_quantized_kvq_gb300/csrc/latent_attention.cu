@@ -74,7 +74,7 @@ struct Ctl {
     uint32_t tmem;
     int stop;
     Walk walk[kMmaWarp + 1];
-    alignas(16) float off[NC];    // -(reference maximum) c, by line
+    alignas(16) float ref[NC];    // the reference maximum, or 0 where nothing is seen yet
     alignas(16) float scale[NC];  // factors of a rescaling, or of the output
     float m[NC];                  // reference maximum of the scores (of z / scale)
     int lim[NC];                  // positions a line sees
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             if (side == 0 && t < NC) {
                 ctl->lim[t] = g.ahead + (g.line0 + min(t, g.lines - 1)) / p.per_row + 1;
                 ctl->m[t] = -INFINITY;
-                ctl->off[t] = 0.f;
+                ctl->ref[t] = 0.f;
             }
             softmax_barrier();
             const int lim0 = ctl->lim[0];  // the least
@@ -145,23 +145,36 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 wait_or_stop(smem_u32(&ctl->s_full), n_tile & 1, stop, p.status);
                 tc_fence_after();
                 uint32_t s[HC];
-                load_columns<HC>(s_t, s);
-                if ((g.k0 + i + 1) * kTile > lim0) {
+                auto fetch = [&]() {
+                    load_columns<HC>(s_t, s);
+                    if ((g.k0 + i + 1) * kTile > lim0) {
 #pragma unroll
-                    for (int x = 0; x < HC; ++x)
-                        if (pos >= ctl->lim[c0 + x]) s[x] = 0xff800000u;
-                }
+                        for (int x = 0; x < HC; ++x)
+                            if (pos >= ctl->lim[c0 + x]) s[x] = 0xff800000u;
+                    }
+                };
+                // The scores less their references.  (The difference before the product: exact at the maximum, however
+                // large the scores are; a fused s c - m c would leave the rounding of m c)
+                auto less = [&]() -> float {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int x = 0; x < HC; x += 4) {
+                        const float4 r = *reinterpret_cast<const float4*>(&ctl->ref[c0 + x]);
+                        const float a = __uint_as_float(s[x]) - r.x, b = __uint_as_float(s[x + 1]) - r.y;
+                        const float c = __uint_as_float(s[x + 2]) - r.z, d = __uint_as_float(s[x + 3]) - r.w;
+                        top = fmaxf(fmaxf(fmaxf(top, a), fmaxf(b, c)), d);
+                        s[x] = __float_as_uint(a);
+                        s[x + 1] = __float_as_uint(b);
+                        s[x + 2] = __float_as_uint(c);
+                        s[x + 3] = __float_as_uint(d);
+                    }
+                    return top;
+                };
+                fetch();
                 // Are the references still within 2^8 of every score?  (Weights then stay below 2^8, far inside f16,
                 // and nothing is reduced over the positions: of a few hundred tiles a few move a reference)
-                float top = -INFINITY;
-#pragma unroll
-                for (int x = 0; x < HC; x += 4) {
-                    const float4 off = *reinterpret_cast<const float4*>(&ctl->off[c0 + x]);
-                    const float a = fmaf(__uint_as_float(s[x]), p.c, off.x), b = fmaf(__uint_as_float(s[x + 1]), p.c, off.y);
-                    const float c = fmaf(__uint_as_float(s[x + 2]), p.c, off.z), d = fmaf(__uint_as_float(s[x + 3]), p.c, off.w);
-                    top = fmaxf(fmaxf(fmaxf(top, a), fmaxf(b, c)), d);
-                }
-                if (any_of_softmax(i == 0 || top > 8.f)) {
+                if (any_of_softmax(less() * p.c > 8.f || i == 0)) {
+                    fetch();
 #pragma unroll
                     for (int x = 0; x < HC; ++x) {
                         const float r = warp_max(__uint_as_float(s[x]));
@@ -174,9 +187,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                         const float to = m == -INFINITY || (most - m) * p.c > 8.f ? fmaxf(most, m) : m;
                         ctl->scale[t] = to == m ? 1.f : fast_exp2((m - to) * p.c);
                         ctl->m[t] = to;
-                        ctl->off[t] = to == -INFINITY ? 0.f : -to * p.c;
+                        ctl->ref[t] = to == -INFINITY ? 0.f : to;
                     }
                     softmax_barrier();
+                    less();
                     if (i > 0) {
 #pragma unroll
                         for (int x = 0; x < HC; ++x) l[x] *= ctl->scale[c0 + x];
@@ -200,11 +214,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                     uint32_t w[4];
 #pragma unroll
                     for (int y = 0; y < 8; y += 4) {
-                        const float4 off = *reinterpret_cast<const float4*>(&ctl->off[c0 + x + y]);
-                        const float a = fast_exp2(fmaf(__uint_as_float(s[x + y]), p.c, off.x));
-                        const float b = fast_exp2(fmaf(__uint_as_float(s[x + y + 1]), p.c, off.y));
-                        const float c = fast_exp2(fmaf(__uint_as_float(s[x + y + 2]), p.c, off.z));
-                        const float d = fast_exp2(fmaf(__uint_as_float(s[x + y + 3]), p.c, off.w));
+                        const float a = fast_exp2(__uint_as_float(s[x + y]) * p.c);
+                        const float b = fast_exp2(__uint_as_float(s[x + y + 1]) * p.c);
+                        const float c = fast_exp2(__uint_as_float(s[x + y + 2]) * p.c);
+                        const float d = fast_exp2(__uint_as_float(s[x + y + 3]) * p.c);
                         l[x + y] += a;
                         l[x + y + 1] += b;
                         l[x + y + 2] += c;

@@ -160,6 +160,37 @@ def test_large_scores_and_sharp_softmax(kvq):
         c.check(rows=[0, 7, 19])
 
 
+@pytest.mark.parametrize("case", ["few", "many", "latent"])
+def test_enormous_scores_pick_one_position(kvq, case):
+    """Scores of 2^30 and more: the softmax is 1 at the largest.  Rows whose two largest are closer than four times what
+    the scores may be off by are left out.  The weight is rounded to fp16, so are the value and the output: half a step each."""
+    new, total = [3, 1, 2], [3, 129, 700]
+    if case == "latent":
+        c = Latent(kvq, 256, 5, 32, 64, new, total, seed=3, size=1000.0)
+    else:
+        c = Chunk(kvq, 2, 2, 128, 16, 64, 128, new if case == "few" else [150, 40], total if case == "few" else [700, 40],
+                  seed=3, size=1000.0)
+    c.scale = 65536.0
+    got = c.run().cpu().numpy().astype(np.float64)
+    assert np.isfinite(got).all() and kvq.kvq_read_status(c.ws) == 0
+    q, seen, clear, largest = c.q.astype(np.float64), 0, 0, 0.0
+    for b, (m, n) in enumerate(zip(c.new, c.total)):
+        kv = [(x, x[:, :c.pool.L]) for x in [c.pool.rows(b, n)]] if case == "latent" else list(zip(*c.pool.values(b, n)))
+        for h in range(q.shape[1]):
+            K, V = kv[0] if case == "latent" else kv[h // c.r]
+            for i in range(m):
+                end = n - m + i + 1
+                z = K[:end] @ q[c.cu[b] + i, h] * c.scale
+                dz = (np.abs(K[:end]) @ np.abs(q[c.cu[b] + i, h])).max() * c.scale * (2.0 ** -11 + K.shape[1] * 2.0 ** -23)
+                top, seen, largest = int(z.argmax()), seen + 1, max(largest, float(z.max()))
+                if end > 1 and np.sort(z)[-1] - np.sort(z)[-2] < 4 * dz:
+                    continue
+                clear += 1
+                err = np.abs(got[c.cu[b] + i, h] - V[top])
+                assert (err <= 3.2 * 2.0 ** -11 * np.abs(V[top]) + 2.0 ** -24).all(), (b, h, i, float(err.max()))
+    assert 2 * clear > seen and largest > 2.0 ** 30
+
+
 def test_negative_scale(kvq):
     for c in both(kvq, [5], [300]):
         c.scale = -c.scale

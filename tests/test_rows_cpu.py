@@ -74,6 +74,8 @@ def test_attention_refuses(kvq, latent):
         assert call(**bad) == kvq.KVQ_EINVAL, bad
         assert kvq.kvq_last_error()
     assert call(B=70000) == kvq.KVQ_EUNSUPPORTED
+    for scale in (2.1e19, -3e38):
+        assert call(scale=scale) == kvq.KVQ_EINVAL
     assert call(T=0, pool=None, ws=None) == kvq.KVQ_OK
     if latent:
         assert call(H=1025) == kvq.KVQ_EINVAL
