@@ -19,6 +19,19 @@
 //   16, 17     issue the MMAs of stream 0 and 1: S = Q K^T (both from shared memory), O += P V (P from tensor
 //              memory).  A warp for each, so that one stream's waits and bookkeeping do not hold up the other.
 //   18         copies packed pages into shared memory (bulk copies, a ring of kPacked tiles).
+//
+// Rounding.  Operands are f16: code x scale (chunk_shared.cuh) and the weights (11 of their bits; the sum
+// that divides takes them unrounded).  Scores, maxima, sums and outputs are fp32 throughout.
+//
+// What bounds it.  A pair of tiles (one key/value tile, both streams) takes the tensor cores 32 MMAs of 64
+// cycles, 2048; the exponential unit 32768 values at 32 a cycle, 1024; the half-rate pipe (64 lanes a cycle)
+// about 1500 for the maxima, the conversions and the unpacking of keys and values.  It takes about 5000 in
+// all.  Measured (8192 tokens of one prompt, 32 heads on 8 kv heads of 128): 600 us, 916 TFLOP/s, tensor
+// cores 40% busy, 55% of the issue slots.  A stream's scores, softmax and output follow one
+// another, and with two streams (tensor memory has room for no third) the waits between them are not filled.
+// Tried and not kept: 64-position steps with two score buffers a stream (848 -> 991 us at the time); the
+// softmax loops unrolled whole (848 instead of 703: instruction fetch); 128 scores in registers at once
+// (spills, which go to L2).
 #include <cuda_fp16.h>
 
 #include <cmath>

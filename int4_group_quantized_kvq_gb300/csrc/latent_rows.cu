@@ -42,6 +42,12 @@ __device__ __forceinline__ float rsqrt_two(const TwoFloat& m) {
     return fmaf(0.5f * r, t, r);
 }
 
+// A warp takes a row: its latent values, L / 32 to a lane, are read once, summed, normalised, quantized and
+// stored, its rotary key and the row's query heads turned in between; with few rows the heads are shared
+// out over further warps.  A stream of bytes: 18 000 rows of L = 512 with 32 heads, 178 MB, take 43 us
+// (4.1 TB/s) at 40% of the issue slots; what is missing is the chain of lookups and of the sum over the row
+// ahead of its stores.  Rows in runs, their lookups side by side in the lanes of a warp, took 73 us instead
+// of 54 for the whole case.
 template <int L, bool INTER>
 __global__ void __launch_bounds__(256, 3) latent_append_kernel(LatentAppendArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // (and no early start of the next kernel: q_out may be its q)
@@ -179,6 +185,7 @@ __global__ void __launch_bounds__(256, 3) latent_append_kernel(LatentAppendArgs 
     }
 }
 
+// The way back, a warp a row: 28 MB in 12 us, of which the launch and one chain of lookups are half.
 template <int L>
 __global__ void __launch_bounds__(256) latent_dequantize_kernel(LatentDequantArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");

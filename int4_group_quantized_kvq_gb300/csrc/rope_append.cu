@@ -21,6 +21,12 @@ namespace {
 // rotary pairs in registers.  LPR = D / 16 lanes hold a head, two pieces of 8 values each; a lane of
 // the rotary part of a head split in halves holds both halves of its pairs (so no value moves
 // between lanes), any other lane 16 values in a row.
+//
+// A stream of bytes: 668 MB take 147 us (4.5 TB/s, two thirds of the copy rate) for 32768 rows of 32 + 8 + 8
+// heads of 128, at 56% of the issue slots.  What is missing is the chain of lookups ahead of a row's loads
+// and the scattered stores of the codes (4 bytes a lane).  Three CTAs an SM: with four, or 16 warps, the
+// registers spill or the loads in flight get fewer (232 us).  Runs of rows a warp, their lookups side by
+// side in its lanes, took 211 to 302 us for both kernels of the case instead of 200.
 template <int D, bool INTER>
 __global__ void __launch_bounds__(256, 3) rope_append_kernel(RopeAppendArgs a) {
     // Starts while the kernel ahead drains, and touches nothing before that one has finished.  It does
@@ -189,7 +195,8 @@ __global__ void __launch_bounds__(256, 3) rope_append_kernel(RopeAppendArgs a) {
 }
 
 // The way back: a warp takes a row (or a part of its heads), a lane 16 values of a head's K or V row
-// at a time.
+// at a time.  The same 32768 rows of 8 heads take 46 us: 35 MB read and 134 MB written (of which L2 keeps a
+// part), at 61% of the issue slots.
 template <bool F32>
 __global__ void __launch_bounds__(256) dequantize_rows_kernel(DequantRowsArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
