@@ -11,7 +11,7 @@
 // Measured on four sequences over 32761 positions, 32 heads on 8 kv heads of 128 (in brackets the kernel of
 // chunk_attention.cu): one row each 71 us (108), 8 rows 80 (109).  The pages are 140 MB, 20.8 us at the copy
 // rate: a tile of 128 positions takes 2500 cycles of an SM where its copy would take 700.  It is bounded by
-// the work on a tile (half of the issue slots; unpack and multiply at half rate, 64 KB of stores into shared
+// the work on a tile (two thirds of the issue slots; unpack and multiply at half rate, 64 KB of stores into shared
 // memory, the softmax's barriers) and by shared memory, which leaves room for three packed tiles in flight:
 // with two it took 90.  Keys and values by the same eight warps took 94.
 //
