@@ -635,7 +635,7 @@ int kvq_dequantize_varlen(const kvq_cache_config *cfg, const void *pool, const i
  *              table, raises KVQ_FLAG_BAD_POSITION and is cut to it.
  *   out        device fp16 [total_rows, num_q_heads, head_dim], 16-byte aligned: sums and softmax
  *              statistics in fp32; a dequantized element and a softmax weight are rounded to fp16
- *              before their products, the output once.
+ *              before their products, the output once.  It must share no memory with the inputs.
  *   workspace  >= kvq_chunk_workspace_bytes(...) bytes, 256-byte aligned; its first word is the status
  *              word (zero it before the first call).  Nothing else in it has to be kept or cleared
  *              between calls; calls that share one must not overlap on the GPU.

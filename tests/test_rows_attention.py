@@ -160,6 +160,17 @@ def test_large_scores_and_sharp_softmax(kvq):
         c.check(rows=[0, 7, 19])
 
 
+@pytest.mark.parametrize("d,r", [(128, 4), (64, 1), (64, 7)])
+def test_a_prompt_among_single_tokens(kvq, d, r):
+    """Few lines a sequence on average, one of them with many: items of one sequence share its tiles, and the last is short."""
+    new = [0, 1, 97 if r < 7 else 41, 1, 1] + [1] * 11
+    total = [3, 1, 650, 128, 129] + [40 * i + 1 for i in range(11)]
+    assert sum(new) * r <= 32 * len(new)
+    c = Chunk(kvq, 2, r, d, 32, 32, 64, new, total, pad=3, seed=r)
+    c.run()
+    c.check()
+
+
 @pytest.mark.parametrize("case", ["few", "many", "latent"])
 def test_enormous_scores_pick_one_position(kvq, case):
     """Scores of 2^30 and more: the softmax is 1 at the largest.  Rows whose two largest are closer than four times what
