@@ -776,6 +776,25 @@ int kvq_test_decode_weights_wait_timeout(const kvq_cache_config *cfg, const void
                                          kvq_stream_t stream);
 
 /*
+ * The same test of kvq_chunk_attention and kvq_latent_attention (same arguments): every wait is bounded by
+ * wait_limit_ns (in [1 us, 10 ms]) instead of 250 ms, and one operand tile's barrier of every CTA waits for an
+ * arrival that nobody makes.  The kernels raise KVQ_FLAG_WAIT_TIMEOUT in the workspace's status word and stop
+ * waiting (out is not the attention; rows behind the last sequence keep what they held), and leave once the
+ * copies and products they have issued are complete.  Later calls run normally.
+ * Return as the calls tested, or KVQ_EINVAL for a limit outside the range.
+ */
+int kvq_test_chunk_wait_timeout(const kvq_cache_config *cfg, const void *pool, const void *q,
+                                const int32_t *block_table, int32_t max_blocks, const int32_t *seq_lens,
+                                const int32_t *cu_rows, int32_t batch, int32_t total_rows, int32_t num_q_heads,
+                                int32_t max_len, float softmax_scale, void *out, void *workspace,
+                                size_t workspace_bytes, uint64_t wait_limit_ns, kvq_stream_t stream);
+int kvq_test_latent_wait_timeout(const kvq_latent_config *cfg, const void *pool, const void *q,
+                                 const int32_t *block_table, int32_t max_blocks, const int32_t *seq_lens,
+                                 const int32_t *cu_rows, int32_t batch, int32_t total_rows, int32_t num_heads,
+                                 int32_t max_len, float softmax_scale, void *out, void *workspace,
+                                 size_t workspace_bytes, uint64_t wait_limit_ns, kvq_stream_t stream);
+
+/*
  * Dequantize positions [start, start + n) of sequence b (section 2.1 of the 4-bit
  * page: value = code * scale, exact in fp32).
  *   out_k, out_v  device [n, num_kv_heads, head_dim]; out_dtype 0 = fp16 (the fp32

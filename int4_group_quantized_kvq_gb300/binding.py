@@ -35,7 +35,8 @@ ABI_SYMBOLS = ("kvq_block_bytes", "kvq_pool_bytes", "kvq_quantize_append", "kvq_
                "kvq_diff_decode_attention", "kvq_diff_decode_step", "kvq_test_decode_weights_wait_timeout",
                "kvq_rope_append", "kvq_dequantize_varlen", "kvq_chunk_workspace_bytes", "kvq_chunk_attention",
                "kvq_latent_block_bytes", "kvq_latent_pool_bytes", "kvq_latent_append", "kvq_latent_dequantize",
-               "kvq_latent_workspace_bytes", "kvq_latent_attention")
+               "kvq_latent_workspace_bytes", "kvq_latent_attention", "kvq_test_chunk_wait_timeout",
+               "kvq_test_latent_wait_timeout")
 
 
 class KvqError(RuntimeError):
@@ -186,8 +187,11 @@ def lib() -> C.CDLL:
                                         P]
         L.kvq_latent_dequantize.argtypes = [lcp, P, P, I32, P, P, I32, I32, P, P, P]
         L.kvq_latent_attention.argtypes = [lcp, P, P, P, I32, P, P, I32, I32, I32, I32, F, P, P, SZ, P]
+        L.kvq_test_chunk_wait_timeout.argtypes = [cfgp, P, P, P, I32, P, P, I32, I32, I32, I32, F, P, P, SZ, C.c_uint64, P]
+        L.kvq_test_latent_wait_timeout.argtypes = [lcp, P, P, P, I32, P, P, I32, I32, I32, I32, F, P, P, SZ, C.c_uint64, P]
         for name in ("kvq_rope_append", "kvq_dequantize_varlen", "kvq_chunk_attention", "kvq_latent_append",
-                     "kvq_latent_dequantize", "kvq_latent_attention"):
+                     "kvq_latent_dequantize", "kvq_latent_attention", "kvq_test_chunk_wait_timeout",
+                     "kvq_test_latent_wait_timeout"):
             getattr(L, name).restype = C.c_int
         L.kvq_chunk_workspace_bytes.argtypes = [cfgp, I32, I32, I32]
         L.kvq_latent_workspace_bytes.argtypes = [lcp, I32, I32, I32]
@@ -1122,6 +1126,19 @@ def kvq_chunk_attention(cfg: CacheConfig, pool: torch.Tensor, q: torch.Tensor, b
                  max_len, softmax_scale, out, cfg.head_dim, workspace, stream, torch.cuda.current_device())
 
 
+def kvq_test_chunk_wait_timeout(cfg: CacheConfig, pool: torch.Tensor, q: torch.Tensor, block_table: torch.Tensor,
+                                seq_lens: torch.Tensor, cu_rows: torch.Tensor, max_len: int, softmax_scale: float,
+                                out: torch.Tensor, workspace: torch.Tensor, wait_limit_ns: int, stream=None) -> None:
+    """The bounded-wait test of kvq_chunk_attention (the test suite's): its waits run out."""
+    L, ref = lib(), C.byref(cfg)
+
+    def fn(*args):
+        return L.kvq_test_chunk_wait_timeout(*args[:-1], int(wait_limit_ns), args[-1])
+
+    _attend_rows(fn, ref, pool, L.kvq_pool_bytes(ref), q, cfg.head_dim, block_table, seq_lens, cu_rows, max_len,
+                 softmax_scale, out, cfg.head_dim, workspace, stream, torch.cuda.current_device())
+
+
 def kvq_latent_block_bytes(cfg: LatentConfig) -> int:
     n = lib().kvq_latent_block_bytes(C.byref(cfg))
     if n == 0:
@@ -1197,3 +1214,16 @@ def kvq_latent_attention(cfg: LatentConfig, pool: torch.Tensor, q: torch.Tensor,
     _attend_rows(L.kvq_latent_attention, ref, pool, L.kvq_latent_pool_bytes(ref), q, cfg.latent_dim + cfg.rope_dim,
                  block_table, seq_lens, cu_rows, max_len, softmax_scale, out, cfg.latent_dim, workspace, stream,
                  torch.cuda.current_device())
+
+
+def kvq_test_latent_wait_timeout(cfg: LatentConfig, pool: torch.Tensor, q: torch.Tensor, block_table: torch.Tensor,
+                                 seq_lens: torch.Tensor, cu_rows: torch.Tensor, max_len: int, softmax_scale: float,
+                                 out: torch.Tensor, workspace: torch.Tensor, wait_limit_ns: int, stream=None) -> None:
+    """The bounded-wait test of kvq_latent_attention (the test suite's): its waits run out."""
+    L, ref = lib(), C.byref(cfg)
+
+    def fn(*args):
+        return L.kvq_test_latent_wait_timeout(*args[:-1], int(wait_limit_ns), args[-1])
+
+    _attend_rows(fn, ref, pool, L.kvq_latent_pool_bytes(ref), q, cfg.latent_dim + cfg.rope_dim, block_table, seq_lens,
+                 cu_rows, max_len, softmax_scale, out, cfg.latent_dim, workspace, stream, torch.cuda.current_device())

@@ -54,7 +54,7 @@ constexpr int kFewLines = 32;
 
 struct Ctl {
     TileBars tiles;
-    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], turn;
+    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], turn, last[2];
     long long warp_sum[kThreads / 32];
     Start start;
     uint32_t tmem;
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             mbar_init(smem_u32(&ctl->tiles.pk_empty[i]), kDqWarps);
         }
         for (int i = 0; i < kRing; ++i) {
-            mbar_init(smem_u32(&ctl->tiles.kv_full[i]), kDqWarps);
+            mbar_init(smem_u32(&ctl->tiles.kv_full[i]), kDqWarps + (i == 1 ? p.withheld : 0));
             mbar_init(smem_u32(&ctl->tiles.kv_empty[i]), 2);
         }
         for (int i = 0; i < 2; ++i) {
@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             mbar_init(smem_u32(&ctl->s_full[i]), 1);
             mbar_init(smem_u32(&ctl->p_full[i]), 4);
             mbar_init(smem_u32(&ctl->o_done[i]), 1);
+            mbar_init(smem_u32(&ctl->last[i]), 1);
         }
         mbar_init(smem_u32(&ctl->turn), 1);
         ctl->stop = 0;
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             bool begun = false;
             if (!two && sw == 1) seen -= kTile;
             for (int i = two ? 0 : sw; i < n; i += two ? 1 : 2, seen -= two ? kTile : 2 * kTile) {
-                wait_or_stop(smem_u32(&ctl->s_full[sw]), n_s & 1, stop, p.status);
+                wait_or_stop(smem_u32(&ctl->s_full[sw]), n_s & 1, stop, p);
                 ++n_s;
                 tc_fence_after();
                 // Two passes over the scores, 64 columns at a time: the maximum, then the weights.  (128 scores in
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 __syncwarp();
             };
             if (two) {
-                wait_or_stop(smem_u32(&ctl->o_done[sw]), (par_o >> sw) & 1, stop, p.status);
+                wait_or_stop(smem_u32(&ctl->o_done[sw]), (par_o >> sw) & 1, stop, p);
                 par_o ^= 3u;
                 tc_fence_after();
                 const float inv = l > 0.f ? 2.f / l : 0.f;
@@ -273,10 +274,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             } else {
                 // both streams hold a part of the same rows: lane by lane the same tensor-memory lane
                 const bool both = n > 1;
-                wait_or_stop(smem_u32(&ctl->o_done[0]), par_o & 1, stop, p.status);
+                wait_or_stop(smem_u32(&ctl->o_done[0]), par_o & 1, stop, p);
                 par_o ^= 1u;
                 if (both) {
-                    wait_or_stop(smem_u32(&ctl->o_done[1]), par_o >> 1, stop, p.status);
+                    wait_or_stop(smem_u32(&ctl->o_done[1]), par_o >> 1, stop, p);
                     par_o ^= 2u;
                 }
                 tc_fence_after();
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                             x[i] = __ldg(reinterpret_cast<const uint4*>(src + (static_cast<long long>(tok) * p.Hq + row - tok * p.r) * D) +
                                          piece);
                     }
-                    if (n_q > 0 && half == 0) wait_or_stop(smem_u32(&ctl->q_free[qs]), (n_q - 1) & 1, stop, p.status);
+                    if (n_q > 0 && half == 0) wait_or_stop(smem_u32(&ctl->q_free[qs]), (n_q - 1) & 1, stop, p);
 #pragma unroll
                     for (int i = 0; i < LOADS; ++i) {
                         const int row = row0 + i * RPW * kDqWarps;
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             uint32_t n_ring = 0, n_q0 = 0, n_q1 = 0, n_p = 0, n_turn = 0;
             auto take = [&]() -> uint32_t {  // the next operand tile, in order
                 const uint32_t stage = n_ring % kRing;
-                live &= wait_or_stop(smem_u32(&ctl->tiles.kv_full[stage]), (n_ring / kRing) & 1, stop, p.status);
+                live &= wait_or_stop(smem_u32(&ctl->tiles.kv_full[stage]), (n_ring / kRing) & 1, stop, p);
                 ++n_ring;
                 tc_fence_after();
                 return stage;
@@ -413,10 +414,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 // Turns alternate strictly (stream 1 takes an empty one behind an odd number of alternating tiles): a
                 // stream that waits for the other's turn has then seen the one before it.
                 const int ahead = two ? 1 : 2, turns = two ? n : n + (n & 1);
-                live &= wait_or_stop(smem_u32(&ctl->q_full[0]), n_q0 & 1, stop, p.status);
+                live &= wait_or_stop(smem_u32(&ctl->q_full[0]), n_q0 & 1, stop, p);
                 ++n_q0;
                 if (two && sw == 1) {
-                    live &= wait_or_stop(smem_u32(&ctl->q_full[1]), n_q1 & 1, stop, p.status);
+                    live &= wait_or_stop(smem_u32(&ctl->q_full[1]), n_q1 & 1, stop, p);
                     ++n_q1;
                 }
 #pragma unroll 1
@@ -426,11 +427,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     const uint32_t v = out ? take() : 0, k = in ? take() : 0;
                     if (mine) {
                         if (out) {
-                            live &= wait_or_stop(smem_u32(&ctl->p_full[sw]), n_p & 1, stop, p.status);
+                            live &= wait_or_stop(smem_u32(&ctl->p_full[sw]), n_p & 1, stop, p);
                             ++n_p;
                         }
                         const uint32_t turn = n_turn + (two ? 2 * (i + 1) + sw : i + 2);
-                        if (turn > 0) live &= wait_or_stop(smem_u32(&ctl->turn), (turn - 1) & 1, stop, p.status);
+                        if (turn > 0) live &= wait_or_stop(smem_u32(&ctl->turn), (turn - 1) & 1, stop, p);
                         tc_fence_after();
                         if (elect_one()) {
                             if (live && out) {
@@ -476,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
+    finish_products(warp == 16 || warp == 17, smem_u32(&ctl->last[warp & 1]), stop);
     if (warp == 16) {
         tc_fence_after();
         tmem_free(tmem, kTmem);
@@ -581,6 +583,8 @@ cudaError_t launch_chunk_attention(const ChunkArgs& a, cudaStream_t stream) {
     p.lg_gv = a.L.Gv == 32 ? 5 : a.L.Gv == 64 ? 6 : 7;
     const long long table = static_cast<long long>(a.max_blocks) << a.lg_p;
     p.most = static_cast<int32_t>(table < a.max_len ? table : a.max_len);
+    p.wait_ns = a.wait_limit_ns > 0 ? a.wait_limit_ns : kWaitNs;
+    p.withheld = a.wait_limit_ns > 0;
     // (at least 1e-30: a hidden score is -infinity, which zero times is not a number)
     p.c = std::fmax(2.f * std::fabs(a.softmax_scale) * 1.4426950408889634f, 1e-30f);
     p.q_flip = a.softmax_scale < 0.f ? 0x80008000u : 0u;

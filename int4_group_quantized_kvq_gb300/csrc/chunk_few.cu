@@ -44,7 +44,7 @@ struct Ctl {
     TileBars tiles;
     // scores and weights by buffer; the output with tile i in o_done[i % 2], so that whoever waits for it has seen
     // the phase before (scores of tile i complete: the output with tile i - 2, too)
-    uint64_t q_full, q_free, s_full[2], p_full[2], o_done[2];
+    uint64_t q_full, q_free, s_full[2], p_full[2], o_done[2], last;
     long long warp_sum[kThreads / 32];
     Start start;
     uint32_t tmem;
@@ -75,11 +75,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
             mbar_init(smem_u32(&ctl->tiles.pk_empty[i]), 2 * kDqWarps);
         }
         for (int i = 0; i < 2 * kRing; ++i) {
-            mbar_init(smem_u32(&ctl->tiles.kv_full[i]), kDqWarps);
+            mbar_init(smem_u32(&ctl->tiles.kv_full[i]), kDqWarps + (i == kRing ? p.withheld : 0));
             mbar_init(smem_u32(&ctl->tiles.kv_empty[i]), 1);
         }
         mbar_init(smem_u32(&ctl->q_full), kDqWarps);
         mbar_init(smem_u32(&ctl->q_free), 1);
+        mbar_init(smem_u32(&ctl->last), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&ctl->s_full[i]), 1);
             mbar_init(smem_u32(&ctl->p_full[i]), kSmWarps);
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 const int pos = (g.k0 + i) * kTile + t, buf = i & 1;
-                wait_or_stop(smem_u32(&ctl->s_full[buf]), phase(i), stop, p.status);
+                wait_or_stop(smem_u32(&ctl->s_full[buf]), phase(i), stop, p);
                 tc_fence_after();
                 uint32_t s[HC];
                 auto fetch = [&]() {
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
                     softmax_barrier();
                     less();
                     if (i > 0) {
-                        wait_or_stop(smem_u32(&ctl->o_done[buf ^ 1]), phase(i - 1), stop, p.status);  // the output so far
+                        wait_or_stop(smem_u32(&ctl->o_done[buf ^ 1]), phase(i - 1), stop, p);  // the output so far
                         tc_fence_after();
 #pragma unroll
                         for (int x = 0; x < HC; ++x) l[x] *= ctl->scale[c0 + x];
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
                 }
             }
             softmax_barrier();
-            wait_or_stop(smem_u32(&ctl->o_done[(n - 1) & 1]), phase(n - 1), stop, p.status);
+            wait_or_stop(smem_u32(&ctl->o_done[(n - 1) & 1]), phase(n - 1), stop, p);
             tc_fence_after();
             n_b0 += (n + 1) / 2;
             n_b1 += n / 2;
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
                                          kRing * is_v + n_pk % kRing, n_pk / kRing, stop);
                 if (i > 0 || is_v) continue;
                 // the item's queries, their dimensions in the order the unpack leaves
-                if (n_q > 0) wait_or_stop(smem_u32(&ctl->q_free), (n_q - 1) & 1, stop, p.status);
+                if (n_q > 0) wait_or_stop(smem_u32(&ctl->q_free), (n_q - 1) & 1, stop, p);
                 ++n_q;
 #pragma unroll 4
                 for (int j = tid; j < NC * (D / 8); j += 32 * kDqWarps) {
@@ -305,13 +306,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
             uint32_t n_k = 0, n_v = 0, n_seg = 0, n_b0 = 0, n_b1 = 0;
             auto take = [&](uint32_t& n, uint32_t first) -> uint32_t {  // the next operand tile of keys or values
                 const uint32_t stage = first + n % kRing;
-                live &= wait_or_stop(smem_u32(&ctl->tiles.kv_full[stage]), (n / kRing) & 1, stop, p.status);
+                live &= wait_or_stop(smem_u32(&ctl->tiles.kv_full[stage]), (n / kRing) & 1, stop, p);
                 ++n;
                 return stage;
             };
             while (uniform(st.units > 0 && walk.next(p))) {
                 const int n = uniform(g.k1 - g.k0);
-                live &= wait_or_stop(smem_u32(&ctl->q_full), n_seg & 1, stop, p.status);
+                live &= wait_or_stop(smem_u32(&ctl->q_full), n_seg & 1, stop, p);
                 ++n_seg;
                 // turn i: the output with value tile i, then the scores with key tile i + 2 (it starts with scores alone)
 #pragma unroll 1
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
                     const int buf = i & 1;
                     if (i >= 0) {
                         const uint32_t v = take(n_v, kRing);
-                        live &= wait_or_stop(smem_u32(&ctl->p_full[buf]), ((buf ? n_b1 : n_b0) + (i >> 1)) & 1, stop, p.status);
+                        live &= wait_or_stop(smem_u32(&ctl->p_full[buf]), ((buf ? n_b1 : n_b0) + (i >> 1)) & 1, stop, p);
                         tc_fence_after();
                         // (64 dimensions: the second half of M is the next operand tile's bytes, whatever they are; the
                         // rows of the output it gives are not read)
@@ -358,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
     }
     tc_fence_before();
     __syncthreads();
+    finish_products(warp == kMmaWarp, smem_u32(&ctl->last), stop);
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_free(tmem, kTmem);

@@ -50,7 +50,7 @@ __device__ __forceinline__ void dequantize_tile(const ChunkParams& p, TileBars& 
     constexpr int kOperand = kTile * D * 2;
     const int lane = threadIdx.x & 31;
     const uint32_t pk = n_tile % kPacked;
-    if (APART || is_v == 0) wait_or_stop(smem_u32(&tiles.pk_full[pk]), (n_tile / kPacked) & 1, stop, p.status);
+    if (APART || is_v == 0) wait_or_stop(smem_u32(&tiles.pk_full[pk]), (n_tile / kPacked) & 1, stop, p);
     const uint8_t* src = packed + pk * packed_bytes;
     const uint32_t dst = ring_s + stage * kOperand;
     const int lg_g = is_v ? p.lg_gv : p.lg_gk;
@@ -86,7 +86,7 @@ __device__ __forceinline__ void dequantize_tile(const ChunkParams& p, TileBars& 
         }
     }
     // only now the operand tile has to be free: the products wait for the stores alone
-    if (use > 0) wait_or_stop(smem_u32(&tiles.kv_empty[stage]), (use & 1) ^ 1, stop, p.status);
+    if (use > 0) wait_or_stop(smem_u32(&tiles.kv_empty[stage]), (use & 1) ^ 1, stop, p);
 #pragma unroll
     for (int w = 0; w < JOBS; ++w) {
         const int job = (w * kDqWarps + dw) * 32 + lane;
@@ -113,7 +113,7 @@ __device__ __forceinline__ void dequantize_tile(const ChunkParams& p, TileBars& 
 __device__ __forceinline__ void load_pages(const ChunkParams& p, TileBars& tiles, Walk& walk, uint32_t packed_s, int packed_bytes,
                                            bool any, volatile int* stop) {
     const int lane = threadIdx.x & 31;
-    uint32_t n_pk = 0;
+    uint32_t n_pk = 0, n_copied = 0;
     const int per = kTile >> p.lg_p;  // pages of a tile
     const Segment& g = walk.g;
     while (any && walk.next(p)) {
@@ -125,7 +125,7 @@ __device__ __forceinline__ void load_pages(const ChunkParams& p, TileBars& tiles
         for (int i = g.k0; i < g.k1; ++i, ++n_pk) {
             const uint32_t pk = n_pk % kPacked;
             if (n_pk >= kPacked)
-                wait_or_stop(smem_u32(&tiles.pk_empty[pk]), ((n_pk / kPacked) & 1) ^ 1, stop, p.status);
+                wait_or_stop(smem_u32(&tiles.pk_empty[pk]), ((n_pk / kPacked) & 1) ^ 1, stop, p);
             const int first = i * per;
             if (first - base >= 32) {
                 base += 32;
@@ -134,13 +134,15 @@ __device__ __forceinline__ void load_pages(const ChunkParams& p, TileBars& tiles
             }
             const int count = max(0, min(per, pages - first));
             const uint32_t bar = smem_u32(&tiles.pk_full[pk]);
-            if (lane == 0 && !*stop) {
+            const bool go = !__shfl_sync(0xffffffffu, *stop, 0);  // one answer: what is announced is copied
+            if (go) n_copied = n_pk + 1;
+            if (lane == 0 && go) {
                 if (count > 0) mbar_arrive_expect_tx(bar, count * p.L.bytes);
                 else mbar_arrive(bar);
             }
             __syncwarp();
             int page = __shfl_sync(0xffffffffu, cur, (first - base + lane) & 31);
-            if (lane < count && !*stop) {
+            if (lane < count && go) {
                 if (page < 0 || page >= p.num_pages) {
                     raise_flag(p.status, KVQ_FLAG_BAD_PAGE);
                     page = 0;
@@ -151,9 +153,10 @@ __device__ __forceinline__ void load_pages(const ChunkParams& p, TileBars& tiles
             __syncwarp();
         }
     }
-    // no copy of this CTA may be in flight when it leaves
-    for (uint32_t i = n_pk > kPacked ? n_pk - kPacked : 0; i < n_pk; ++i)
-        mbar_wait(smem_u32(&tiles.pk_full[i % kPacked]), (i / kPacked) & 1, 250000000ull);
+    // No copy of this CTA may be in flight when it leaves.  (Given up: of the tiles that were copied, whose phases
+    // alone tell the last copies apart from those before)
+    for (uint32_t i = n_copied > kPacked ? n_copied - kPacked : 0; i < n_copied; ++i)
+        mbar_wait(smem_u32(&tiles.pk_full[i % kPacked]), (i / kPacked) & 1, kWaitNs);
 }
 
 // Chunk attention where a sequence has few lines (rows times the query heads of a kv head): chunk_few.cu.

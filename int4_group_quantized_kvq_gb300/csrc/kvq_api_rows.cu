@@ -126,6 +126,79 @@ int check_latent_shape(const kvq_latent_config* cfg, int32_t num_heads) {
     return KVQ_OK;
 }
 
+int check_wait_limit(uint64_t ns) {
+    if (ns < 1000 || ns > 10000000)
+        return fail(KVQ_EINVAL, "wait_limit_ns %llu outside [1 us, 10 ms]", static_cast<unsigned long long>(ns));
+    return KVQ_OK;
+}
+
+int chunk_attention_impl(const kvq_cache_config* cfg, const void* pool, const void* q, const int32_t* block_table,
+                         int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_rows, int32_t batch,
+                         int32_t total_rows, int32_t num_q_heads, int32_t max_len, float softmax_scale, void* out,
+                         void* workspace, size_t workspace_bytes, kvq_stream_t stream, uint64_t wait_limit_ns = 0) {
+    if (int e = check_chunk_shape(cfg, num_q_heads)) return e;
+    bool none;
+    if (int e = check_rows(batch, total_rows, num_q_heads, &none)) return e;
+    if (none) return ok();
+    if (int e = check_places(pool, block_table, max_blocks, seq_lens, cu_rows, nullptr)) return e;
+    if (int e = check_attention(q, out, max_len, softmax_scale)) return e;
+    kvq::ChunkArgs a{};
+    a.pool = static_cast<const uint8_t*>(pool);
+    a.q = static_cast<const __half*>(q);
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.cu_rows = cu_rows;
+    a.out = static_cast<__half*>(out);
+    a.workspace = static_cast<uint8_t*>(workspace);
+    a.rows = total_rows;
+    a.B = batch;
+    a.Hq = num_q_heads;
+    a.Hkv = cfg->num_kv_heads;
+    a.max_blocks = max_blocks;
+    a.num_pages = cfg->num_pages;
+    a.lg_p = lg(cfg->page_size);
+    a.max_len = max_len;
+    a.softmax_scale = softmax_scale;
+    a.wait_limit_ns = static_cast<uint32_t>(wait_limit_ns);
+    a.L = kvq::block_layout(*cfg);
+    if (int e = check_workspace(workspace, workspace_bytes, kvq::chunk_workspace_bytes(a))) return e;
+    const cudaError_t e = kvq::launch_chunk_attention(a, reinterpret_cast<cudaStream_t>(stream));
+    return e != cudaSuccess ? cuda_fail(e, "kvq_chunk_attention launch") : ok();
+}
+
+int latent_attention_impl(const kvq_latent_config* cfg, const void* pool, const void* q, const int32_t* block_table,
+                          int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_rows, int32_t batch,
+                          int32_t total_rows, int32_t num_heads, int32_t max_len, float softmax_scale, void* out,
+                          void* workspace, size_t workspace_bytes, kvq_stream_t stream, uint64_t wait_limit_ns = 0) {
+    if (int e = check_latent_shape(cfg, num_heads)) return e;
+    bool none;
+    if (int e = check_rows(batch, total_rows, num_heads, &none)) return e;
+    if (none) return ok();
+    if (int e = check_places(pool, block_table, max_blocks, seq_lens, cu_rows, nullptr)) return e;
+    if (int e = check_attention(q, out, max_len, softmax_scale)) return e;
+    kvq::LatentAttnArgs a{};
+    a.pool = static_cast<const uint8_t*>(pool);
+    a.q = static_cast<const __half*>(q);
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.cu_rows = cu_rows;
+    a.out = static_cast<__half*>(out);
+    a.workspace = static_cast<uint8_t*>(workspace);
+    a.rows = total_rows;
+    a.B = batch;
+    a.H = num_heads;
+    a.max_blocks = max_blocks;
+    a.num_pages = cfg->num_pages;
+    a.lg_p = lg(cfg->page_size);
+    a.max_len = max_len;
+    a.softmax_scale = softmax_scale;
+    a.wait_limit_ns = static_cast<uint32_t>(wait_limit_ns);
+    a.lay = kvq::latent_layout(*cfg);
+    if (int e = check_workspace(workspace, workspace_bytes, kvq::latent_workspace_bytes(a))) return e;
+    const cudaError_t e = kvq::launch_latent_attention(a, reinterpret_cast<cudaStream_t>(stream));
+    return e != cudaSuccess ? cuda_fail(e, "kvq_latent_attention launch") : ok();
+}
+
 }  // namespace
 
 extern "C" {
@@ -240,33 +313,18 @@ int kvq_chunk_attention(const kvq_cache_config* cfg, const void* pool, const voi
                         int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_rows, int32_t batch,
                         int32_t total_rows, int32_t num_q_heads, int32_t max_len, float softmax_scale, void* out,
                         void* workspace, size_t workspace_bytes, kvq_stream_t stream) {
-    if (int e = check_chunk_shape(cfg, num_q_heads)) return e;
-    bool none;
-    if (int e = check_rows(batch, total_rows, num_q_heads, &none)) return e;
-    if (none) return ok();
-    if (int e = check_places(pool, block_table, max_blocks, seq_lens, cu_rows, nullptr)) return e;
-    if (int e = check_attention(q, out, max_len, softmax_scale)) return e;
-    kvq::ChunkArgs a{};
-    a.pool = static_cast<const uint8_t*>(pool);
-    a.q = static_cast<const __half*>(q);
-    a.block_table = block_table;
-    a.seq_lens = seq_lens;
-    a.cu_rows = cu_rows;
-    a.out = static_cast<__half*>(out);
-    a.workspace = static_cast<uint8_t*>(workspace);
-    a.rows = total_rows;
-    a.B = batch;
-    a.Hq = num_q_heads;
-    a.Hkv = cfg->num_kv_heads;
-    a.max_blocks = max_blocks;
-    a.num_pages = cfg->num_pages;
-    a.lg_p = lg(cfg->page_size);
-    a.max_len = max_len;
-    a.softmax_scale = softmax_scale;
-    a.L = kvq::block_layout(*cfg);
-    if (int e = check_workspace(workspace, workspace_bytes, kvq::chunk_workspace_bytes(a))) return e;
-    const cudaError_t e = kvq::launch_chunk_attention(a, reinterpret_cast<cudaStream_t>(stream));
-    return e != cudaSuccess ? cuda_fail(e, "kvq_chunk_attention launch") : ok();
+    return chunk_attention_impl(cfg, pool, q, block_table, max_blocks, seq_lens, cu_rows, batch, total_rows, num_q_heads, max_len,
+                                softmax_scale, out, workspace, workspace_bytes, stream);
+}
+
+int kvq_test_chunk_wait_timeout(const kvq_cache_config* cfg, const void* pool, const void* q, const int32_t* block_table,
+                                int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_rows, int32_t batch,
+                                int32_t total_rows, int32_t num_q_heads, int32_t max_len, float softmax_scale, void* out,
+                                void* workspace, size_t workspace_bytes, uint64_t wait_limit_ns,
+                                kvq_stream_t stream) {
+    if (int e = check_wait_limit(wait_limit_ns)) return e;
+    return chunk_attention_impl(cfg, pool, q, block_table, max_blocks, seq_lens, cu_rows, batch, total_rows, num_q_heads, max_len,
+                                softmax_scale, out, workspace, workspace_bytes, stream, wait_limit_ns);
 }
 
 size_t kvq_latent_block_bytes(const kvq_latent_config* cfg) {
@@ -379,32 +437,18 @@ int kvq_latent_attention(const kvq_latent_config* cfg, const void* pool, const v
                          int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_rows, int32_t batch,
                          int32_t total_rows, int32_t num_heads, int32_t max_len, float softmax_scale, void* out,
                          void* workspace, size_t workspace_bytes, kvq_stream_t stream) {
-    if (int e = check_latent_shape(cfg, num_heads)) return e;
-    bool none;
-    if (int e = check_rows(batch, total_rows, num_heads, &none)) return e;
-    if (none) return ok();
-    if (int e = check_places(pool, block_table, max_blocks, seq_lens, cu_rows, nullptr)) return e;
-    if (int e = check_attention(q, out, max_len, softmax_scale)) return e;
-    kvq::LatentAttnArgs a{};
-    a.pool = static_cast<const uint8_t*>(pool);
-    a.q = static_cast<const __half*>(q);
-    a.block_table = block_table;
-    a.seq_lens = seq_lens;
-    a.cu_rows = cu_rows;
-    a.out = static_cast<__half*>(out);
-    a.workspace = static_cast<uint8_t*>(workspace);
-    a.rows = total_rows;
-    a.B = batch;
-    a.H = num_heads;
-    a.max_blocks = max_blocks;
-    a.num_pages = cfg->num_pages;
-    a.lg_p = lg(cfg->page_size);
-    a.max_len = max_len;
-    a.softmax_scale = softmax_scale;
-    a.lay = kvq::latent_layout(*cfg);
-    if (int e = check_workspace(workspace, workspace_bytes, kvq::latent_workspace_bytes(a))) return e;
-    const cudaError_t e = kvq::launch_latent_attention(a, reinterpret_cast<cudaStream_t>(stream));
-    return e != cudaSuccess ? cuda_fail(e, "kvq_latent_attention launch") : ok();
+    return latent_attention_impl(cfg, pool, q, block_table, max_blocks, seq_lens, cu_rows, batch, total_rows, num_heads, max_len,
+                                 softmax_scale, out, workspace, workspace_bytes, stream);
+}
+
+int kvq_test_latent_wait_timeout(const kvq_latent_config* cfg, const void* pool, const void* q, const int32_t* block_table,
+                                 int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_rows, int32_t batch,
+                                 int32_t total_rows, int32_t num_heads, int32_t max_len, float softmax_scale, void* out,
+                                 void* workspace, size_t workspace_bytes, uint64_t wait_limit_ns,
+                                 kvq_stream_t stream) {
+    if (int e = check_wait_limit(wait_limit_ns)) return e;
+    return latent_attention_impl(cfg, pool, q, block_table, max_blocks, seq_lens, cu_rows, batch, total_rows, num_heads, max_len,
+                                 softmax_scale, out, workspace, workspace_bytes, stream, wait_limit_ns);
 }
 
 }  // extern "C"

@@ -349,6 +349,7 @@ struct ChunkArgs {
     uint8_t* workspace;
     int32_t rows, B, Hq, Hkv, max_blocks, num_pages, lg_p, max_len;
     float softmax_scale;
+    uint32_t wait_limit_ns = 0;  // not 0: a test of the bounded waits
     BlockLayout L;
 };
 // CTAs of the attention kernels on ragged batches: one per SM (0: no device).
@@ -366,6 +367,7 @@ struct LatentAttnArgs {
     uint8_t* workspace;
     int32_t rows, B, H, max_blocks, num_pages, lg_p, max_len;
     float softmax_scale;
+    uint32_t wait_limit_ns = 0;  // not 0: a test of the bounded waits
     LatentLayout lay;
 };
 size_t latent_workspace_bytes(const LatentAttnArgs& a);

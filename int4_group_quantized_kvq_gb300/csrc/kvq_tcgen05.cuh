@@ -149,9 +149,11 @@ __device__ __forceinline__ void regs_less() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// A wait of these kernels on an mbarrier, by a whole warp: bounded, and over at once when any thread of
-// the CTA has given up (*stop).  A thread that gives up raises the flag and goes on through its loops
-// without waiting, so the CTA's barriers stay matched; the issuers of copies and MMAs issue nothing more.
+// A wait of these kernels on an mbarrier, by a whole warp: bounded (by p.wait_ns), and over at once when any
+// thread of the CTA has given up (*stop).  A thread that gives up raises the flag and goes on through its loops
+// without waiting, so the CTA's barriers stay matched; the issuers of copies and MMAs issue nothing more, and
+// wait for what they have issued before the CTA leaves (finish_products; load_pages in chunk_shared.cuh).
+constexpr uint32_t kWaitNs = 250000000;
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
@@ -160,22 +162,40 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
                  : "memory");
     return done != 0;
 }
-__device__ __forceinline__ bool wait_or_stop(uint32_t bar, uint32_t parity, volatile int* stop, uint32_t* status) {
+template <class P>
+__device__ __forceinline__ bool wait_or_stop(uint32_t bar, uint32_t parity, volatile int* stop, const P& p) {
     bool there = mbar_try(bar, parity);
     if (!there) {
         uint64_t t0 = 0;
         for (uint32_t tries = 1; !(there = mbar_try(bar, parity)); ++tries) {
-            if (tries % 64) continue;  // (the timer is slow to read: a short wait never does)
+            // (a short wait reads neither: *stop on each third try took 4% of a call of drafted tokens)
+            if (tries % 4) continue;
             if (*stop) break;
+            if (tries % 64) continue;
             const uint64_t t = global_timer_ns();
             if (t0 == 0) t0 = t;
-            if (t - t0 > 250000000ull) {
+            if (t - t0 > p.wait_ns) {
                 *stop = 1;
-                raise_flag(status, KVQ_FLAG_WAIT_TIMEOUT);
+                raise_flag(p.status, KVQ_FLAG_WAIT_TIMEOUT);
+                break;
             }
         }
     }
     return __all_sync(0xffffffffu, there);  // false: given up
+}
+
+// The end of a CTA, behind a barrier of all its threads (which all call this).  Once a wait has been given up,
+// nobody has waited for the last products: they may still read shared memory, write tensor memory and arrive on
+// barriers.  Each warp that issued some waits for all of its own (`bar`: a barrier of its own, of one arrival;
+// the elected thread is the same every time), and nobody leaves before.
+__device__ __forceinline__ void finish_products(bool issuer, uint32_t bar, volatile int* stop) {
+    if (!*stop) return;
+    if (issuer) {
+        if (elect_one()) mma_commit(bar);
+        __syncwarp();
+        mbar_wait(bar, 0, kWaitNs);
+    }
+    __syncthreads();
 }
 
 }  // namespace kvq

@@ -34,7 +34,10 @@ struct Units {
     uint32_t* status;
     MergeDesc* desc;  // [gridDim.x]
     int32_t rows, B, heads, per_row, step;
-    int32_t most;  // the longest sequence
+    int32_t most;      // the longest sequence
+    uint32_t wait_ns;  // bound of every wait
+    // A test of that bound: 1 adds an arrival that nobody makes to what an operand tile's barrier waits for
+    uint32_t withheld;
 };
 
 struct Seq {

@@ -76,7 +76,7 @@ struct Shape {
 template <int NC>
 struct Ctl {
     uint64_t full[3], free[3];  // halves of the latent chunks; [2]: the rotary chunk (the weights, where they share)
-    uint64_t q_full, q_free, s_full, p_full, o_done;
+    uint64_t q_full, q_free, s_full, p_full, o_done, last;
     long long warp_sum[kThreads / 32];
     Start start;
     uint32_t tmem;
@@ -104,11 +104,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
     asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 0) {
         for (int i = 0; i < 3; ++i) {
-            mbar_init(smem_u32(&ctl->full[i]), i < 2 ? kDqWarps / Z::kHalves : kDqWarps);
+            mbar_init(smem_u32(&ctl->full[i]), i < 2 ? kDqWarps / Z::kHalves : kDqWarps + p.withheld);
             mbar_init(smem_u32(&ctl->free[i]), 1);
         }
         mbar_init(smem_u32(&ctl->q_full), kDqWarps);
         mbar_init(smem_u32(&ctl->q_free), 1);
+        mbar_init(smem_u32(&ctl->last), 1);
         mbar_init(smem_u32(&ctl->s_full), 1);
         mbar_init(smem_u32(&ctl->p_full), kSmWarps);
         mbar_init(smem_u32(&ctl->o_done), 1);
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
 #pragma unroll 1
             for (int i = 0; i < n; ++i, ++n_tile) {
                 const int pos = (g.k0 + i) * kTile + t;
-                wait_or_stop(smem_u32(&ctl->s_full), n_tile & 1, stop, p.status);
+                wait_or_stop(smem_u32(&ctl->s_full), n_tile & 1, stop, p);
                 tc_fence_after();
                 uint32_t s[HC];
                 auto fetch = [&]() {
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 }
             }
             softmax_barrier();
-            wait_or_stop(smem_u32(&ctl->o_done), n_seg & 1, stop, p.status);
+            wait_or_stop(smem_u32(&ctl->o_done), n_seg & 1, stop, p);
             ++n_seg;
             tc_fence_after();
             const int dim = dim_of(t);
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
         while (cur.there) {
             if (cur.q != nullptr) {
                 // the item's queries, latent dimensions in the order the unpack leaves, the rotary part halved
-                if (n_q > 0) wait_or_stop(smem_u32(&ctl->q_free), (n_q - 1) & 1, stop, p.status);
+                if (n_q > 0) wait_or_stop(smem_u32(&ctl->q_free), (n_q - 1) & 1, stop, p);
                 ++n_q;
                 constexpr int PIECES = (L + kRope) / 8;
 #pragma unroll 6
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full));
             }
-            if (n_tile > 0) wait_or_stop(smem_u32(&ctl->free[half]), (n_tile - 1) & 1, stop, p.status);
+            if (n_tile > 0) wait_or_stop(smem_u32(&ctl->free[half]), (n_tile - 1) & 1, stop, p);
 #pragma unroll
             for (int j = 0; j < JOBS; ++j) {
                 // half the scale, so that 7 times it stays finite (exact but for the smallest subnormals)
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ctl->full[half]));
-            if (n_tile > 0) wait_or_stop(smem_u32(&ctl->free[2]), (n_tile - 1) & 1, stop, p.status);
+            if (n_tile > 0) wait_or_stop(smem_u32(&ctl->free[2]), (n_tile - 1) & 1, stop, p);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 store(k_s + (Z::kChunks - 1) * kChunk + swizzled(r0 + 32 * j, q), keys[j].x, keys[j].y, keys[j].z, keys[j].w);
@@ -444,13 +445,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             uint32_t n_tile = 0, n_seg = 0;
             while (uniform(st.units > 0 && walk.next(p))) {
                 const int n = uniform(g.k1 - g.k0);
-                live &= wait_or_stop(smem_u32(&ctl->q_full), n_seg & 1, stop, p.status);
+                live &= wait_or_stop(smem_u32(&ctl->q_full), n_seg & 1, stop, p);
                 ++n_seg;
 #pragma unroll 1
                 for (int i = 0; i < n; ++i, ++n_tile) {
 #pragma unroll 1
                     for (int c = 0; c <= Z::kHalves; ++c) {  // four chunks, four chunks, the rotary one
-                        live &= wait_or_stop(smem_u32(&ctl->full[c < Z::kHalves ? c : 2]), n_tile & 1, stop, p.status);
+                        live &= wait_or_stop(smem_u32(&ctl->full[c < Z::kHalves ? c : 2]), n_tile & 1, stop, p);
                         tc_fence_after();
                         const uint32_t a = desc_lo(k_s + 4 * c * kChunk, 16), b = desc_lo(q_s + 4 * c * Z::kQChunk, 16);
                         if (elect_one() && live) {
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                         if (i + 1 == n) mma_commit(smem_u32(&ctl->q_free));
                     }
                     __syncwarp();
-                    live &= wait_or_stop(smem_u32(&ctl->p_full), n_tile & 1, stop, p.status);
+                    live &= wait_or_stop(smem_u32(&ctl->p_full), n_tile & 1, stop, p);
                     tc_fence_after();
                     if (elect_one() && live) {
 #pragma unroll 1
@@ -489,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
+    finish_products(warp == kMmaWarp, smem_u32(&ctl->last), stop);
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_free(tmem, Z::kTmem);
@@ -574,6 +576,8 @@ cudaError_t launch_latent_attention(const LatentAttnArgs& a, cudaStream_t stream
     p.lg_g = a.lay.G == 32 ? 5 : a.lay.G == 64 ? 6 : 7;
     const long long table = static_cast<long long>(a.max_blocks) << a.lg_p;
     p.most = static_cast<int32_t>(table < a.max_len ? table : a.max_len);
+    p.wait_ns = a.wait_limit_ns > 0 ? a.wait_limit_ns : kWaitNs;
+    p.withheld = a.wait_limit_ns > 0;
     // (at least 1e-30: a hidden score is -infinity, which zero times is not a number)
     p.c = std::fmax(2.f * std::fabs(a.softmax_scale) * 1.4426950408889634f, 1e-30f);
     p.q_flip = a.softmax_scale < 0.f ? 0x80008000u : 0u;
