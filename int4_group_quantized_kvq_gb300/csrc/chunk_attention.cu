@@ -54,7 +54,10 @@ constexpr int kFewLines = 32;
 
 struct Ctl {
     TileBars tiles;
-    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], turn, last[2];
+    // o_done: a stream's output of a segment of two row tiles, for that stream alone; o_both: both streams' of a segment
+    // of one, for both.  (A stream that waited for the other's o_done in some segments would skip phases of it, and
+    // a wait by parity knows a phase only from the one before)
+    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_done[2], o_both, turn, last[2];
     long long warp_sum[kThreads / 32];
     Start start;
     uint32_t tmem;
@@ -103,6 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             mbar_init(smem_u32(&ctl->o_done[i]), 1);
             mbar_init(smem_u32(&ctl->last[i]), 1);
         }
+        mbar_init(smem_u32(&ctl->o_both), 2);
         mbar_init(smem_u32(&ctl->turn), 1);
         ctl->stop = 0;
         fence_mbar_init();
@@ -127,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
         const uint32_t s_t = tmem + lanes + 128u * sw, o_t = tmem + lanes + 256u;
         const int tok_in = row / p.r;  // token within the row tile
-        uint32_t n_s = 0, par_o = 0;  // bit s: the phase of stream s's o_done
+        uint32_t n_s = 0, n_two = 0, n_one = 0;  // score tiles; segments of two row tiles, and of one
         while (st.units > 0 && walk.next(p)) {
             const int n = g.k1 - g.k0;
             const bool two = g.lines > p.T;                    // a second row tile (else the streams alternate)
@@ -254,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 __syncwarp();
             };
             if (two) {
-                wait_or_stop(smem_u32(&ctl->o_done[sw]), (par_o >> sw) & 1, stop, p);
-                par_o ^= 3u;
+                wait_or_stop(smem_u32(&ctl->o_done[sw]), n_two & 1, stop, p);
+                ++n_two;
                 tc_fence_after();
                 const float inv = l > 0.f ? 2.f / l : 0.f;
 #pragma unroll 1
@@ -274,12 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             } else {
                 // both streams hold a part of the same rows: lane by lane the same tensor-memory lane
                 const bool both = n > 1;
-                wait_or_stop(smem_u32(&ctl->o_done[0]), par_o & 1, stop, p);
-                par_o ^= 1u;
-                if (both) {
-                    wait_or_stop(smem_u32(&ctl->o_done[1]), par_o >> 1, stop, p);
-                    par_o ^= 2u;
-                }
+                wait_or_stop(smem_u32(&ctl->o_both), n_one & 1, stop, p);
+                ++n_one;
                 tc_fence_after();
                 ctl->ml[sw][row][0] = m;
                 ctl->ml[sw][row][1] = l;
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                                 for (int x = 0; x < kTile / 16; ++x)
                                     mma_ts(d, a + 8 * x, smem_desc(b + (x * 2048 >> 4)), kIdO, !first || x > 0);
                                 mma_commit(smem_u32(&ctl->tiles.kv_empty[v]));
-                                if (!in) mma_commit(smem_u32(&ctl->o_done[sw]));
+                                if (two && !in) mma_commit(smem_u32(&ctl->o_done[sw]));
                             }
                             if (live && in) {
                                 const uint32_t a = desc_lo(q_s + (two ? sw : 0) * Z::kOperand, 16);
@@ -456,6 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                                 mma_commit(smem_u32(&ctl->s_full[sw]));
                                 mma_commit(smem_u32(&ctl->tiles.kv_empty[k]));
                             }
+                            if (live && !two && i + 2 >= turns) mma_commit(smem_u32(&ctl->o_both));  // the stream's last turn
                             mbar_arrive(smem_u32(&ctl->turn));
                         }
                     } else if (elect_one()) {
