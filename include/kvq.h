@@ -634,8 +634,9 @@ int kvq_dequantize_varlen(const kvq_cache_config *cfg, const void *pool, const i
  *   max_len    host bound on every seq_lens[b] (at most 2^30); a longer one, or one beyond the block
  *              table, raises KVQ_FLAG_BAD_POSITION and is cut to it.
  *   out        device fp16 [total_rows, num_q_heads, head_dim], 16-byte aligned: sums and softmax
- *              statistics in fp32; a dequantized element and a softmax weight are rounded to fp16
- *              before their products, the output once.  It must share no memory with the inputs.
+ *              statistics in fp32; a dequantized element (below 2^-13 in size: to a multiple of 2^-23)
+ *              and a softmax weight are rounded to fp16 before their products, the output once.  It must
+ *              share no memory with the inputs.
  *   workspace  >= kvq_chunk_workspace_bytes(...) bytes, 256-byte aligned; its first word is the status
  *              word (zero it before the first call).  Nothing else in it has to be kept or cleared
  *              between calls; calls that share one must not overlap on the GPU.
@@ -711,7 +712,7 @@ int kvq_latent_dequantize(const kvq_latent_config *cfg, const void *pool, const 
  * token's key for all heads is its row [latent, rotary key], its value the latent:
  *   out[i][h] = sum_t softmax_t(softmax_scale * (q_latent . c_t + q_rotary . k_t)) c_t.
  * Rows, masks, max_len, workspace, precision and errors as in kvq_chunk_attention (one row per
- * sequence: a decode step).
+ * sequence: a decode step); the queries' rotary part is rounded as dequantized elements are.
  *   q    device fp16 [total_rows, num_heads, L + R], 16-byte aligned, num_heads 1 to 1024.
  *   out  device fp16 [total_rows, num_heads, L], 16-byte aligned.
  */

@@ -41,7 +41,9 @@ struct TileBars {
 //
 // code x scale has 15 significant bits and is rounded to the 11 of f16, the operands' type: a relative
 // 2^-12 at most on average over a key's dimensions, which moves a score by about 2^-12 of its own spread.
-// (Exact operands would take a second product for the scales' lower bits, or one product per group.)
+// (Exact operands would take a second product for the scales' lower bits, or one product per group.)  Half of
+// it is what is held (7 scales may pass fp16's largest), so elements below 2^-13 in size are rounded to multiples of
+// 2^-23; the scale itself is not rounded.
 template <int D, bool APART>
 __device__ __forceinline__ void dequantize_tile(const ChunkParams& p, TileBars& tiles, const uint8_t* packed, int packed_bytes,
                                                 uint32_t ring_s, uint32_t n_tile, int end, int is_v, int dw, uint32_t stage,
@@ -73,16 +75,16 @@ __device__ __forceinline__ void dequantize_tile(const ChunkParams& p, TileBars& 
             w4 = *reinterpret_cast<const uint4*>(blk + codes_off + slot * (D / 2) + part * 16);
             s2 = *reinterpret_cast<const uint16_t*>(blk + scales_off + (((slot * D + part * 32) >> lg_g) << 1));
         }
-        // half the scale, so that 7 times it stays finite (exact but for the smallest subnormals)
-        const uint32_t sc = h2_mul(s2 | s2 << 16, 0x38003800u);
+        // half of the codes, so that 7 scales stay finite
+        const uint32_t sc = s2 | s2 << 16;
         const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             const uint32_t lo = ws[x], hi = ws[x] >> 8;
-            f[w][4 * x] = h2_mul(unpack_lo(lo), sc);
-            f[w][4 * x + 1] = h2_mul(unpack_hi(lo), sc);
-            f[w][4 * x + 2] = h2_mul(unpack_lo(hi), sc);
-            f[w][4 * x + 3] = h2_mul(unpack_hi(hi), sc);
+            f[w][4 * x] = h2_mul(unpack_lo_half(lo), sc);
+            f[w][4 * x + 1] = h2_mul(unpack_hi_half(lo), sc);
+            f[w][4 * x + 2] = h2_mul(unpack_lo_half(hi), sc);
+            f[w][4 * x + 3] = h2_mul(unpack_hi_half(hi), sc);
         }
     }
     // only now the operand tile has to be free: the products wait for the stores alone

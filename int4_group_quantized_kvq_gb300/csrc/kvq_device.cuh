@@ -147,6 +147,14 @@ __device__ __forceinline__ uint32_t unpack_hi(uint32_t w) {
     return h2_fma(lop3_and_or(w, 0x00F000F0u, 0x64006400u), 0x2C002C00u /* 1/16 */, 0xD480D480u /* -72 */);
 }
 
+// Halves of those codes, exact as well: (1024 + n) / 2 - 516 and (1024 + 16 n) / 32 - 36 are (n - 8) / 2.
+__device__ __forceinline__ uint32_t unpack_lo_half(uint32_t w) {
+    return h2_fma(lop3_and_or(w, 0x000F000Fu, 0x64006400u), 0x38003800u /* 1/2 */, 0xE008E008u /* -516 */);
+}
+__device__ __forceinline__ uint32_t unpack_hi_half(uint32_t w) {
+    return h2_fma(lop3_and_or(w, 0x00F000F0u, 0x64006400u), 0x28002800u /* 1/32 */, 0xD080D080u /* -36 */);
+}
+
 // max(a, |b|), NaN when either is NaN (max.NaN), so one instruction can track both the
 // largest magnitude and any NaN among a run of values.
 __device__ __forceinline__ float max_abs_nan(float a, float b) {

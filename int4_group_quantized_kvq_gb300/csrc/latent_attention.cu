@@ -19,7 +19,9 @@
 //   16     issues the MMAs.
 // Work is shared out as in kvq_units.cuh; an item is NC lines of one sequence.
 //
-// Rounding.  As in chunk_attention.cu: latents and weights are f16 operands, everything else fp32.
+// Rounding.  As in chunk_attention.cu: latents and weights are f16 operands, everything else fp32.  Latents are held
+// halved (chunk_shared.cuh), so the rotary queries are too: below 2^-13 in size, to multiples of 2^-23 (2^-24 of a
+// key's size in a score, where the rounding of the latents is 2^-12 of a query's).
 //
 // What bounds it.  One tile is in shared memory, so its steps stand in a row: refill of the halves (the
 // unpacking of 128 x 512 values), 36 MMAs for the scores, the softmax, 32 for the output.  Measured, L =
@@ -403,8 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
             if (n_tile > 0) wait_or_stop(smem_u32(&ctl->free[half]), (n_tile - 1) & 1, stop, p);
 #pragma unroll
             for (int j = 0; j < JOBS; ++j) {
-                // half the scale, so that 7 times it stays finite (exact but for the smallest subnormals)
-                const uint32_t sc = h2_mul(scales[j] | scales[j] << 16, 0x38003800u);
+                // half of the codes, so that 7 scales stay finite
+                const uint32_t sc = scales[j] | scales[j] << 16;
                 const bool one = turn & 1, two = turn & 2;
                 const uint32_t a = one ? codes[j].y : codes[j].x, b = one ? codes[j].z : codes[j].y;
                 const uint32_t c = one ? codes[j].w : codes[j].z, d = one ? codes[j].x : codes[j].w;
@@ -412,8 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const uint32_t lo = ws[x], hi = ws[x] >> 8;
-                    store(to[x] + 4 * WPH * 128 * j, h2_mul(unpack_lo(lo), sc), h2_mul(unpack_hi(lo), sc), h2_mul(unpack_lo(hi), sc),
-                          h2_mul(unpack_hi(hi), sc));
+                    store(to[x] + 4 * WPH * 128 * j, h2_mul(unpack_lo_half(lo), sc), h2_mul(unpack_hi_half(lo), sc),
+                          h2_mul(unpack_lo_half(hi), sc), h2_mul(unpack_hi_half(hi), sc));
                 }
             }
             fence_proxy_async_smem();
