@@ -177,9 +177,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     }
                 }
                 const float top = fmaxf(top0, top1);
-                // The reference follows the maximum only when that is more than 2^8 above it (weights then stay
-                // below 2^8, far inside f16): the output is rescaled a few times a row instead of every tile
-                const bool move = (top - m) * p.c > 8.f || m == -INFINITY;
+                // (kvq_units.cuh: when the reference follows the maximum)
+                const bool move = (top - m) * p.c > kLag || m == -INFINITY;
                 const float m_new = move ? fmaxf(top, m) : m;
                 if (begun && __any_sync(0xffffffffu, move && m_new != m)) {
                     const float f = m_new == -INFINITY ? 1.f : fast_exp2((m - m_new) * p.c);
@@ -201,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 // s c - m c would leave the rounding of m c (2% of a long prompt's time; a branch for large scores alone
                 // took the same)
                 const float ref = m == -INFINITY ? 0.f : -m;
-                const uint64_t c2 = pair_of(p.c, p.c), ref2 = pair_of(ref, ref);
+                const uint64_t c2 = pair_of(p.c, p.c), ref2 = pair_of(ref, ref), up2 = pair_of(kUp, kUp);
                 uint64_t sums = 0, sums1 = 0;  // two sums each
                 // the second half first: the weights, two to a column, go to columns 64 .. 127, over scores that
                 // are in registers by now
@@ -212,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                         uint32_t w[16];
 #pragma unroll
                         for (int y = 0; y < 16; ++y) {
-                            const uint64_t z = mul_pair(add_pair(pair_of(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1])), ref2), c2);
+                            const uint64_t z = fma_pair(add_pair(pair_of(__uint_as_float(v[2 * y]), __uint_as_float(v[2 * y + 1])), ref2), c2, up2);
                             float p0, p1;
                             split_pair(z, p0, p1);
                             p0 = fast_exp2(p0);

@@ -154,8 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
                     return top;
                 };
                 fetch();
-                // are the references still within 2^8 of every score? (see latent_attention.cu)
-                if (any_of_softmax(less() * p.c > 8.f || i == 0)) {
+                // are the references still within 2^kLag of every score? (see latent_attention.cu)
+                if (any_of_softmax(less() * p.c > kLag || i == 0)) {
                     fetch();
 #pragma unroll
                     for (int x = 0; x < HC; ++x) {
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
                     if (side == 0 && t < NC) {
                         const float most = fmaxf(fmaxf(ctl->part[0][t], ctl->part[1][t]), fmaxf(ctl->part[2][t], ctl->part[3][t]));
                         const float m = ctl->m[t];
-                        const float to = m == -INFINITY || (most - m) * p.c > 8.f ? fmaxf(most, m) : m;
+                        const float to = m == -INFINITY || (most - m) * p.c > kLag ? fmaxf(most, m) : m;
                         ctl->scale[t] = to == m ? 1.f : fast_exp2((m - to) * p.c);
                         ctl->m[t] = to;
                         ctl->ref[t] = to == -INFINITY ? 0.f : to;
@@ -198,10 +198,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
                     uint32_t w[4];
 #pragma unroll
                     for (int y = 0; y < 8; y += 4) {
-                        const float a = fast_exp2(__uint_as_float(s[x + y]) * p.c);
-                        const float b = fast_exp2(__uint_as_float(s[x + y + 1]) * p.c);
-                        const float c = fast_exp2(__uint_as_float(s[x + y + 2]) * p.c);
-                        const float d = fast_exp2(__uint_as_float(s[x + y + 3]) * p.c);
+                        const float a = fast_exp2(fmaf(__uint_as_float(s[x + y]), p.c, kUp));
+                        const float b = fast_exp2(fmaf(__uint_as_float(s[x + y + 1]), p.c, kUp));
+                        const float c = fast_exp2(fmaf(__uint_as_float(s[x + y + 2]), p.c, kUp));
+                        const float d = fast_exp2(fmaf(__uint_as_float(s[x + y + 3]), p.c, kUp));
                         l[x + y] += a;
                         l[x + y + 1] += b;
                         l[x + y + 2] += c;
