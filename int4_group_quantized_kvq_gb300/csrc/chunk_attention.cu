@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     put(o, x, inv);
                 }
                 if (valid && !whole) {
-                    pml[0] = m * p.c;
+                    pml[0] = m;
                     pml[1] = l;
                 }
                 tc_fence_before();
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                     put(o, x, f);
                 }
                 if (valid && !whole && sw == 0) {
-                    pml[0] = mm * p.c;
+                    pml[0] = mm;
                     pml[1] = ll;
                 }
                 tc_fence_before();
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant_
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // lanes hold 4 columns of a row each (D = 64: half of the lanes)
     merge_items<1>(
-        p, ctas, p.r, &share,
+        p, p.c, ctas, p.r, &share,
         [&](long long slot, int line, int, float& m, float& l, float4& o, int lane) {
             const int tok = line / p.r;
             const long long at = slot * 256 + (tok / p.T) * kTile + (tok % p.T) * p.r + line - tok * p.r;

@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_few_kernel(const __grid_con
                 const float sum = (ctl->part[0][t] + ctl->part[1][t]) + (ctl->part[2][t] + ctl->part[3][t]);
                 ctl->scale[t] = !whole ? 1.f : sum > 0.f ? 2.f / sum : 0.f;
                 if (!whole) {
-                    p.part_ml[(static_cast<long long>(slot) * NC + t) * 2] = ctl->m[t] * p.c;
+                    p.part_ml[(static_cast<long long>(slot) * NC + t) * 2] = ctl->m[t];
                     p.part_ml[(static_cast<long long>(slot) * NC + t) * 2 + 1] = sum;
                 }
             }
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(256) chunk_few_merge_kernel(const __grid_const
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // lanes hold 4 dimensions of a line each (D = 64: half of the lanes)
     merge_items<1>(
-        p, ctas, 1, &share,
+        p, p.c, ctas, 1, &share,
         [&](long long slot, int line, int, float& m, float& l, float4& o, int lane) {
             const long long at = slot * NC + line;
             const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);

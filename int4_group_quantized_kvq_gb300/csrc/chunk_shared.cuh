@@ -21,7 +21,7 @@ struct ChunkParams : Units {  // an item: the tokens of two row tiles
     const __half* q;
     const int32_t* block_table;
     __half* out;
-    float* part_ml;   // [2 gridDim.x][256][2]: maximum (of scale log2(e) z) and sum
+    float* part_ml;   // [2 gridDim.x][256][2]: reference maximum (of the scores) and sum
     float* part_o;    // [2 gridDim.x][256][D]
     int32_t Hq, Hkv, r, T, max_blocks, num_pages, lg_p, lg_gk, lg_gv;  // T: tokens of a row tile
     float c;          // 2 |scale| log2(e): keys are held halved

@@ -251,9 +251,10 @@ struct MergeShare {
 constexpr int kFewParts = 8;
 
 // A line has E pieces, four dimensions of one to a lane.  fetch(slot, line, e, m, l, o, lane) reads a part,
-// put(desc, line, e, l, o, lane) writes what is merged; lines: `mult` times the descriptor's.
+// put(desc, line, e, l, o, lane) writes what is merged; lines: `mult` times the descriptor's.  c: a maximum's factor
+// to powers of two, which the difference of two maxima takes (that is exact or nearly, however large they are).
 template <int E, class FETCH, class PUT>
-__device__ __forceinline__ void merge_items(const Units& p, int ctas, int mult, MergeShare* share, FETCH fetch, PUT put) {
+__device__ __forceinline__ void merge_items(const Units& p, float c, int ctas, int mult, MergeShare* share, FETCH fetch, PUT put) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     int mine = 0;
     if (tid < ctas) {
@@ -275,7 +276,7 @@ __device__ __forceinline__ void merge_items(const Units& p, int ctas, int mult, 
     const int total = share->first[256];
     auto add = [&](float& m, float& l, float4& o, float mk, float lk, const float4& ok) {
         const float mn = fmaxf(m, mk), at = mn == -INFINITY ? 0.f : mn;  // (a part that saw nothing: weight 0)
-        const float a = fast_exp2(m - at), ak = fast_exp2(mk - at);
+        const float a = fast_exp2((m - at) * c), ak = fast_exp2((mk - at) * c);
         l = l * a + lk * ak;
         o.x = o.x * a + ok.x * ak;
         o.y = o.y * a + ok.y * ak;

@@ -51,7 +51,7 @@ struct LatentParams : Units {  // per_row: query heads
     const __half* q;
     const int32_t* block_table;
     __half* out;
-    float* part_ml;  // [2 gridDim.x][NC][2]: maximum (of scale log2(e) z) and sum
+    float* part_ml;  // [2 gridDim.x][NC][2]: reference maximum (of the scores) and sum
     float* part_o;   // [2 gridDim.x][NC][L]
     int32_t max_blocks, num_pages, lg_p, lg_g;
     float c;          // 2 |scale| log2(e): latents are held halved, and so are the rotary queries
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_kernel(const __grid_consta
                 const float sum = (ctl->part[0][t] + ctl->part[1][t]) + (ctl->part[2][t] + ctl->part[3][t]);
                 ctl->scale[t] = !whole ? 1.f : sum > 0.f ? 2.f / sum : 0.f;
                 if (!whole) {
-                    p.part_ml[(static_cast<long long>(slot) * NC + t) * 2] = ctl->m[t] * p.c;
+                    p.part_ml[(static_cast<long long>(slot) * NC + t) * 2] = ctl->m[t];
                     p.part_ml[(static_cast<long long>(slot) * NC + t) * 2 + 1] = sum;
                 }
             }
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const __grid_constant
     __shared__ MergeShare share;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     merge_items<L / 128>(
-        p, ctas, 1, &share,
+        p, p.c, ctas, 1, &share,
         [&](long long slot, int line, int e, float& m, float& l, float4& o, int lane) {
             const long long at = slot * NC + line;
             const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
