@@ -23,6 +23,10 @@ with ``rows``:
 ``append_rotary`` turns queries and keys by their positions and quantizes the rows into the pages
 (``kvq_rope_append``), ``attend_rows`` attends with them (``kvq_chunk_attention``), ``prompt_step`` does both,
 and ``read_rows`` dequantizes rows (``kvq_dequantize_varlen``).
+In a cache made with ``rope`` these two, ``append_rotary`` and ``prompt_step``, are the calls that turn anything.  Every
+other one (``append``, ``decode_step`` and its kin, ``HostPipeline``) stores k and uses q as they are given, so there
+both must have been turned by their positions already; a decode step over projections not turned yet is
+``append_rotary`` with one row per sequence (q in place), then ``attend``.
 
 ``LatentKVCache`` holds one layer's latent cache: ``step`` appends new rows (``kvq_latent_append``) and
 attends in the absorbed form (``kvq_latent_attention``), for single tokens and prompts alike.
@@ -87,7 +91,8 @@ class PagedKVCache:
         self.softmax_scale = 1.0 / math.sqrt(cfg.head_dim)
 
     def append(self, k: torch.Tensor, v: torch.Tensor, start_pos: torch.Tensor, stream=None) -> None:
-        """Quantize k, v [B, n, Hkv, d] fp16 into positions start_pos[b] .. start_pos[b] + n - 1."""
+        """Quantize k, v [B, n, Hkv, d] fp16 into positions start_pos[b] .. start_pos[b] + n - 1 (k as it is given: where
+        keys have rotary positions, turned already)."""
         B.kvq_quantize_append(self.cfg, self.pool, k, v, self.block_table, start_pos, status=self.status,
                               stream=stream)
 
@@ -107,7 +112,8 @@ class PagedKVCache:
 
     def decode_step(self, q, k_new, v_new, append_pos, seq_lens, out, stream=None) -> None:
         """Append one token per sequence at append_pos, then attend over seq_lens (which include it):
-        one kvq_decode_step call."""
+        one kvq_decode_step call.  q and k_new are taken as they are given: where they have rotary positions, turned
+        already (for those that are not: append_rotary, then attend)."""
         if self.weights is not None:
             B.kvq_decode_step_weights(self.cfg, self.pool, k_new, v_new, append_pos, q, self.block_table, seq_lens,
                                       self.max_len, self.softmax_scale, self.decay, self.weights, out, self.workspace,
@@ -170,7 +176,8 @@ class PagedKVCache:
 
     def decode_step_diff(self, q, k_new, v_new, lam, append_pos, seq_lens, out, norm_weight=None,
                          norm_eps: float = 1e-5, out_scale: float = 1.0, stream=None) -> None:
-        """Append one token per sequence at append_pos, then attend_diff over seq_lens: one kvq_diff_decode_step."""
+        """Append one token per sequence at append_pos, then attend_diff over seq_lens: one kvq_diff_decode_step.  q and
+        k_new are taken as they are given, as in decode_step."""
         if self.diff_workspace is None:
             raise ValueError("decode_step_diff needs a cache made with diff")
         B.kvq_diff_decode_step(self.cfg, self.pool, k_new, v_new, append_pos, q, self.block_table, seq_lens,
@@ -181,7 +188,7 @@ class PagedKVCache:
         """Turn q into q_out (both fp16 [T, Hq, d]; the same tensor: in place) and k, and quantize k, v (fp16
         [T, Hkv, d]) into positions start_pos[b] .. of every sequence: rows cu_rows[b] .. cu_rows[b + 1] - 1 are its
         new ones.  positions (int32 [axes, T]): where the angles are taken, if not at the rows' places in the cache.
-        For a cache made with rope and cos_sin."""
+        For a cache made with rope and cos_sin.  One row per sequence, then attend: a decode step."""
         if self.rope is None:
             raise ValueError("append_rotary needs a cache made with rope and cos_sin")
         B.kvq_rope_append(self.cfg, self.rope, self.pool, q, k, v, q_out, self.cos_sin, self.block_table, start_pos, cu_rows,
@@ -212,8 +219,8 @@ class PagedKVCache:
 
     def decode_step_host(self, staging: "HostStaging", append_pos, seq_lens, stream=None) -> None:
         """The decode step from pinned host memory in one kvq_decode_step_host call: one H2D copy of
-        the step's q, K and V (staged back to back), the step, one D2H copy of the output, all
-        asynchronous on the step's stream."""
+        the step's q, K and V (staged back to back, taken as they are given: decode_step), the step, one
+        D2H copy of the output, all asynchronous on the step's stream."""
         if self.window > 0:
             raise ValueError("the host step attends to every position (no window)")
         if self.weights is not None:
