@@ -169,10 +169,10 @@ __device__ __forceinline__ bool wait_or_stop(uint32_t bar, uint32_t parity, vola
     if (!there) {
         uint64_t t0 = 0;
         for (uint32_t tries = 1; !(there = mbar_try(bar, parity)); ++tries) {
-            // (a short wait reads neither: *stop on each third try took 4% of a call of drafted tokens)
-            if (tries % 4) continue;
+            // (a short wait reads neither: *stop behind the first try took 4% of a call of drafted tokens, every fourth one
+            // 1% of a part of a prompt)
+            if (tries % 16) continue;
             if (*stop) break;
-            if (tries % 64) continue;
             const uint64_t t = global_timer_ns();
             if (t0 == 0) t0 = t;
             if (t - t0 > p.wait_ns) {
