@@ -26,9 +26,10 @@
 // What bounds it.  A pair of tiles (one key/value tile, both streams) takes the tensor cores 32 MMAs of 64
 // cycles, 2048; the exponential unit 32768 values at 32 a cycle, 1024; the half-rate pipe (64 lanes a cycle)
 // about 1500 for the maxima, the conversions and the unpacking of keys and values.  It takes about 5000 in
-// all.  Measured (8192 tokens of one prompt, 32 heads on 8 kv heads of 128): 600 us, 916 TFLOP/s, tensor
-// cores 40% busy, 55% of the issue slots.  A stream's scores, softmax and output follow one
-// another, and with two streams (tensor memory has room for no third) the waits between them are not filled.
+// all.  Measured (8192 tokens of one prompt, 32 heads on 8 kv heads of 128): 609 us, 903 TFLOP/s, tensor
+// cores 39% busy, 56% of the issue slots.  A stream's scores, softmax and output follow one another, and with two
+// streams the waits between them are not filled: neither pipe is full.  (At head_dim 128 tensor memory has no room
+// for a third buffer of scores; at 64, where half of the products wait for the same softmax, 128 columns are free.)
 // Tried and not kept: 64-position steps with two score buffers a stream (848 -> 991 us at the time); the
 // softmax loops unrolled whole (848 instead of 703: instruction fetch); 128 scores in registers at once
 // (spills, which go to L2).
@@ -46,10 +47,13 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kRing = 3;  // operand tiles
 constexpr uint32_t kTmem = 512;
-// Up to so many lines to a sequence, on average, lines are columns (chunk_few.cu).  Both sides, in us, lines
-// as columns first: four sequences of 32761 positions, 8 kv heads of 128, with 4 lines 71 and 108, with 32 lines
-// 80 and 109, with 36 (two items) 136 and 110, with 64 138 and 110; 16 of 8000 positions with 32 lines 79 and 108;
-// 24 short sequences of 3 to 12 lines, 26 and 31.
+// Up to so many lines to a sequence, on average, lines are columns (chunk_few.cu).  Both sides for even batches, in
+// us, lines as columns first: four sequences of 32761 positions, 8 kv heads of 128, with 4 lines 69 and 111, with 32
+// lines 76 and 112, with 36 (two items) 134 and 113, with 64 134 and 114; 16 of 8000 positions with 32 lines 77 and
+// 112; 24 short sequences of 4 to 12 lines, 21 and 24.  The average is what the host knows: all rows of the arrays,
+// those behind the last sequence too, over the batch.  It is a poor guide where they are uneven: 16 single tokens over
+// 4096 positions take 42, in arrays padded to 2048 rows 64; 64 of them and a prompt of 2048 rows 342, where apart they
+// take 127 and 83; 63 and a part of 400 rows 241, apart 125 and 58.
 constexpr int kFewLines = 32;
 
 struct Ctl {

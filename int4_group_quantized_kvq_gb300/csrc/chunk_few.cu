@@ -9,7 +9,8 @@
 // the products of two tiles in flight.
 //
 // Measured on four sequences over 32761 positions, 32 heads on 8 kv heads of 128 (in brackets the kernel of
-// chunk_attention.cu): one row each 71 us (108), 8 rows 80 (109).  The pages are 140 MB, 20.8 us at the copy
+// chunk_attention.cu): one row each 69 us (111), 8 rows 76 (112); 80 where four channels of the keys are 20 times
+// larger and references move.  The pages are 140 MB, 20.8 us at the copy
 // rate: a tile of 128 positions takes 2500 cycles of an SM where its copy would take 700.  It is bounded by
 // the work on a tile (two thirds of the issue slots; unpack and multiply at half rate, 64 KB of stores into shared
 // memory, the softmax's barriers) and by shared memory, which leaves room for three packed tiles in flight:

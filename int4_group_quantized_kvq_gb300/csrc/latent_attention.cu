@@ -25,9 +25,11 @@
 //
 // What bounds it.  One tile is in shared memory, so its steps stand in a row: refill of the halves (the
 // unpacking of 128 x 512 values), 36 MMAs for the scores, the softmax, 32 for the output.  Measured, L =
-// 512: 32 sequences of 1024 to 8192 positions with 128 heads 87 us (41 GFLOP, 68 MB: tensor cores 20%
-// busy, 35% of the issue slots); one of 131072 positions with 16 heads 38 us (52 MB, 1.4 TB/s), of which the
-// merge of 152 parts is 5.  A second tile in shared memory would take the place of 144 KB that are not there.
+// 512, the cache in memory (in brackets: in L2, from the call before): 32 sequences of 1024 to 8192 positions with 128
+// heads 96 us (86; 41 GFLOP, 68 MB: tensor cores 20% busy, 35% of the issue slots); one of 131072 positions with 16
+// heads 47 us (39; 52 MB), of which the merge of 152 parts is 5.  A second tile of 128 positions would take 144 KB that
+// are not there at L = 512; at L = 256 (72 KB) there is room for one, and at 512 for two of 64 positions, which has
+// not been tried.
 #include <cuda_fp16.h>
 
 #include <cmath>

@@ -24,9 +24,9 @@ namespace {
 //
 // A stream of bytes: 668 MB take 147 us (4.5 TB/s, two thirds of the copy rate) for 32768 rows of 32 + 8 + 8
 // heads of 128, at 56% of the issue slots.  What is missing is the chain of lookups ahead of a row's loads
-// and the scattered stores of the codes (4 bytes a lane).  Three CTAs an SM: with four, or 16 warps, the
-// registers spill or the loads in flight get fewer (232 us).  Runs of rows a warp, their lookups side by
-// side in its lanes, took 211 to 302 us for both kernels of the case instead of 200.
+// and the scattered stores of the codes (4 bytes a lane).  Three CTAs an SM (80 registers, of which 52 to 60 bytes
+// spill): with four, or 16 warps, more spills or fewer loads are in flight (232 us).  Runs of rows a warp, their
+// lookups side by side in its lanes, took 211 to 302 us for both kernels of the case instead of 200.
 template <int D, bool INTER>
 __global__ void __launch_bounds__(256, 3) rope_append_kernel(RopeAppendArgs a) {
     // Starts while the kernel ahead drains, and touches nothing before that one has finished.  It does
